@@ -1,6 +1,7 @@
 /*
- * moe.h -- C ABI of libmoe: the forward pass of one mixture-of-experts layer
- * on one GPU (router -> token dispatch -> grouped SwiGLU experts -> combine).
+ * moe.h -- C ABI of libmoe: one mixture-of-experts layer on one GPU: its
+ * forward pass (router -> token dispatch -> grouped SwiGLU experts ->
+ * combine), its backward pass, and the clipping of gradients by their norm.
  *
  * Sources, by page title and section:
  *   [EP]       Transformers docs, "Expert parallelism" (intro): a router sends
@@ -320,6 +321,158 @@ moe_status_t moe_forward_host(const moe_config_t *cfg, const void *x_host,
                               const void *W_gate_up, const void *W_down,
                               void *out_host, void *x_dev, void *out_dev,
                               void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------ backward pass ------------------------------
+ *
+ * The gradients of the four steps above and of the whole layer, for a caller
+ * that trains it.  Conventions as above, and:
+ *   - gradients of activations and expert weights have the act dtype, those
+ *     of routing weights, logits, the router weight and bias are fp32; every
+ *     sum is fp32 in an order fixed by the sizes, so results repeat bit for
+ *     bit; each output is rounded once at its end (see
+ *     moe_grouped_swiglu_backward for its one rounded intermediate);
+ *   - outputs are written, not added to; an output may not overlap an input
+ *     unless the entry says so;
+ *   - T == 0 launches no kernel, but weight gradients (sums over no rows) are
+ *     cleared: their buffers are set to zero on `stream`;
+ *   - a pair dropped by the dispatch (pos == -1) contributes nothing and has
+ *     a zero weight gradient.
+ */
+
+/*
+ * Gradient of moe_combine:
+ *   dy_perm[pos[t*k+j]][:] = topk_w[t][j] * dout[t][:]
+ *   dtopk_w[t][j]          = <dout[t], y_perm[pos[t*k+j]]>
+ * With cfg->scale_inputs the combine sums unweighted: dy_perm's rows are
+ * dout's, and y_perm, topk_w and dtopk_w are not used (may be NULL; the
+ * weights' gradient then comes from moe_dispatch_backward).
+ * dout [T][d], y_perm [P][d], pos [P], topk_w [T][k]; dy_perm [P][d] and
+ * dtopk_w [T][k] written.
+ */
+moe_status_t moe_combine_backward(const moe_config_t *cfg, const void *dout, const void *y_perm,
+                                  const int32_t *pos, const float *topk_w, void *dy_perm,
+                                  float *dtopk_w, void *stream);
+
+/*
+ * Gradient of moe_dispatch's rows:
+ *   dx[t][:] = sum_j dx_perm[pos[t*k+j]][:]
+ * summed in slot order.  With cfg->scale_inputs
+ *   dx[t][:]      = sum_j topk_w[t][j] * dx_perm[pos[t*k+j]][:]
+ *   dtopk_w[t][j] = <x[t], dx_perm[pos[t*k+j]]>
+ * else topk_w, x and dtopk_w are not used (may be NULL).
+ * dx_perm [P][d], pos [P], topk_w [T][k], x [T][d]; dx [T][d] and dtopk_w
+ * [T][k] written.
+ */
+moe_status_t moe_dispatch_backward(const moe_config_t *cfg, const void *dx_perm,
+                                   const int32_t *pos, const float *topk_w, const void *x,
+                                   void *dx, float *dtopk_w, void *stream);
+
+/* Bytes of workspace moe_grouped_swiglu_backward needs for `cfg`. */
+size_t moe_grouped_swiglu_backward_workspace_size(const moe_config_t *cfg);
+
+/*
+ * Gradient of moe_grouped_swiglu.  For expert e and row r of its segment,
+ * with the gate and up products (g, u) = x_perm[r] @ W_gate_up[e] formed
+ * again (the forward pass does not keep them), s = 1 / (1 + exp(-g)) and
+ * dh = dy_perm[r] @ W_down[e]^T:
+ *   dgu          = [ dh u s (1 + g (1 - s)),  dh g s ]                   [2f]
+ *   dx_perm[r]   = dgu @ W_gate_up[e]^T
+ *   dW_gate_up[e] = sum over the segment's rows of x_perm[r]^T dgu[r]
+ *   dW_down[e]    = sum over the segment's rows of h_perm[r]^T dy_perm[r]
+ * An expert without rows has zero weight gradients.
+ * x_perm, h_perm, offsets: as the forward pass left them.  bf16: fp32
+ * accumulation on the tensor cores; g, u and dh stay fp32, and dgu is rounded
+ * to bf16 where it becomes an operand of the last products.
+ * x_perm [P][d], offsets [E+1], W_gate_up [E][d][2f], W_down [E][f][d],
+ * h_perm [P][f], dy_perm [P][d]; dx_perm [P][d], dW_gate_up [E][d][2f] and
+ * dW_down [E][f][d] written (rows of dx_perm past offsets[E] are not).
+ * ws: at least moe_grouped_swiglu_backward_workspace_size(cfg) bytes, 256-byte
+ * aligned.
+ */
+moe_status_t moe_grouped_swiglu_backward(const moe_config_t *cfg, const void *x_perm,
+                                         const int32_t *offsets, const void *W_gate_up,
+                                         const void *W_down, const void *h_perm,
+                                         const void *dy_perm, void *dx_perm, void *dW_gate_up,
+                                         void *dW_down, void *ws, size_t ws_bytes, void *stream);
+
+/* Bytes of workspace moe_route_backward needs for `cfg`. */
+size_t moe_route_backward_workspace_size(const moe_config_t *cfg);
+
+/*
+ * Gradient of moe_route.  With S = sum_j topk_w[t][j] dtopk_w[t][j]:
+ *   renormalize: the weights are a softmax over the chosen logits alone:
+ *     dlogits[t][topk_idx[t][j]] = topk_w[t][j] (dtopk_w[t][j] - S), 0 elsewhere;
+ *   else, with p = softmax over all E logits of row t and g[e] = dtopk_w[t][j]
+ *     where e = topk_idx[t][j], 0 elsewhere:
+ *     dlogits[t][e] = p[e] (g[e] - S);
+ *   dWr         = dlogits^T @ x,   dlogit_bias = column sums of dlogits
+ *   dx          = dx_in + dlogits @ Wr     (dx_in NULL: no first term)
+ * The selection itself has no gradient.  logits (read only without
+ * renormalize; NULL allowed with it), topk_idx and topk_w: as moe_route wrote
+ * them.  An expert id outside [0, E) sets MOE_ERR_BAD_ROUTING in the device
+ * error word and that slot contributes nothing.
+ * x [T][d] act dtype, Wr [E][d], logits [T][E], topk_idx, topk_w, dtopk_w
+ * [T][k], dx_in [T][d] act dtype or NULL (may be dx itself); dlogits [T][E],
+ * dWr [E][d], dlogit_bias [E] (or NULL), dx [T][d] written.
+ * ws: at least moe_route_backward_workspace_size(cfg) bytes, 256-byte aligned.
+ */
+moe_status_t moe_route_backward(const moe_config_t *cfg, const void *x, const float *Wr,
+                                const float *logits, const int32_t *topk_idx,
+                                const float *topk_w, const float *dtopk_w, const void *dx_in,
+                                float *dlogits, float *dWr, float *dlogit_bias, void *dx, void *ws,
+                                size_t ws_bytes, void *stream);
+
+/* Bytes of workspace moe_backward needs for `cfg` (0 when T == 0). */
+size_t moe_backward_workspace_size(const moe_config_t *cfg);
+
+/*
+ * The whole layer's gradient, one stream, no host synchronisation: from dout
+ * = dLoss/dout to the gradients of x and of every parameter, by the four
+ * entries above.  fwd_ws is the workspace of the moe_forward call whose
+ * gradient is taken, with the same cfg, x and weights, unchanged since (its
+ * routing, h_perm and y_perm are read; where moe_forward formed no permuted
+ * copy of x, the rows are copied here into ws).
+ * x, dout, dx [T][d]; Wr, dWr [E][d]; W_gate_up, dW_gate_up [E][d][2f];
+ * W_down, dW_down [E][f][d]; dlogit_bias [E] or NULL.
+ * ws: at least moe_backward_workspace_size(cfg) bytes, 256-byte aligned, not
+ * fwd_ws.
+ */
+moe_status_t moe_backward(const moe_config_t *cfg, const void *x, const float *Wr,
+                          const void *W_gate_up, const void *W_down, const void *fwd_ws,
+                          size_t fwd_ws_bytes, const void *dout, void *dx, float *dWr,
+                          float *dlogit_bias, void *dW_gate_up, void *dW_down, void *ws,
+                          size_t ws_bytes, void *stream);
+
+/* One gradient tensor of moe_clip_grad_norm. */
+typedef struct {
+    const void *grad;  /* numel elements, aligned to its element size */
+    void *out;         /* clipped copy, same type; may be grad itself; NULL: norm only */
+    int64_t numel;     /* >= 0 */
+    int32_t dtype;     /* moe_dtype_t */
+    int32_t reserved;  /* 0 */
+} moe_grad_t;
+
+/* Bytes of workspace moe_clip_grad_norm needs, for any list. */
+size_t moe_clip_grad_norm_workspace_size(void);
+
+/*
+ * The global 2-norm of n gradient tensors, and the tensors scaled so that it
+ * is at most max_norm (no counterpart on the pages: the step between a
+ * layer's gradients and its optimizer):
+ *   norm = sqrt(sum over all tensors and elements of g^2)
+ *   out  = g * min(1, max_norm / (norm + 1e-6)),  rounded once
+ * Squares are summed in fp32 within 16384 elements and in fp64 across, in a
+ * fixed order; the norm never leaves the device.  A NaN or infinite gradient
+ * gives a NaN or infinite norm, and the scale follows the formula (an
+ * infinite norm scales finite gradients to 0): a caller that wants to skip
+ * such a step reads `norm`.
+ * grads: HOST array of n >= 0 entries, read before the call returns; `norm`:
+ * one float on the device, written (0 for no elements).  max_norm >= 0.
+ * ws: at least moe_clip_grad_norm_workspace_size() bytes, 256-byte aligned.
+ * Tensors may overlap only where out == grad.
+ */
+moe_status_t moe_clip_grad_norm(const moe_grad_t *grads, int64_t n, float max_norm, float *norm,
+                                void *ws, size_t ws_bytes, void *stream);
 
 /*
  * Synchronises `stream`, then reads and clears the current device's error

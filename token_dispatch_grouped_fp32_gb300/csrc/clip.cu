@@ -1,0 +1,184 @@
+// clip.cu -- the global norm of many gradient tensors, and their clipped
+// copies:  N = sqrt(sum of all squares),  out = g * min(1, max_norm / (N + 1e-6)).
+//
+// Launch 1 (norm_kernel): the tensors are cut into chunks of kChunk elements;
+// block b sums the squares of chunks b, b + grid, ... (fp32 inside a chunk,
+// doubles across chunks) and writes one double.  Launch 2 (scale_kernel):
+// every block adds the partial sums of launch 1 in the same order, so each
+// has the same norm and no block waits for another, and scales its chunks.
+// The tensors' addresses and sizes travel as kernel parameters: no copy to
+// the device, and the calls can be captured in a graph.
+#include <algorithm>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kChunk = 16384;
+constexpr int kBlocks = 152 * 6;
+constexpr int kTable = 512;  // tensors per launch
+
+struct Table {
+    const void *src[kTable];
+    void *dst[kTable];
+    int64_t numel[kTable];
+    int end[kTable];  // chunks of tensors 0 .. i; bit 31 of none (chunks < 2^31)
+    uint8_t bf16[kTable];
+    int n;
+};
+
+__device__ __forceinline__ double block_sum(double v) {
+    __shared__ double s[kThreads / 32];
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+    __syncthreads();
+    double t = 0.0;
+    for (int i = 0; i < kThreads / 32; ++i) t += s[i];
+    __syncthreads();
+    return t;
+}
+
+struct Chunk {
+    int tensor;
+    int64_t first;
+    int count;
+};
+__device__ __forceinline__ Chunk find_chunk(const Table &t, int c) {
+    int lo = 0, hi = t.n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (t.end[mid] > c) hi = mid; else lo = mid + 1;
+    }
+    Chunk k;
+    k.tensor = lo;
+    k.first = (int64_t)(c - (lo ? t.end[lo - 1] : 0)) * kChunk;
+    k.count = (int)min((int64_t)kChunk, t.numel[lo] - k.first);
+    return k;
+}
+
+template <typename TA> __device__ __forceinline__ float chunk_squares(const TA *p, int n) {
+    constexpr int EPV = 16 / sizeof(TA);
+    const int head = min(n, (int)((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / (int)sizeof(TA));
+    float s = 0.f;
+    if ((int)threadIdx.x < head) {
+        const float v = Act<TA>::to_f(p[threadIdx.x]);
+        s = v * v;
+    }
+    const int nv = (n - head) / EPV;
+    const TA *q = p + head;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < nv; i += kThreads) {
+        float v[EPV];
+        unpack16(ldg16(q + (int64_t)i * EPV), v, static_cast<const TA *>(nullptr));
+#pragma unroll
+        for (int j = 0; j < EPV; ++j) s = fmaf(v[j], v[j], s);
+    }
+    const int tail = head + nv * EPV + threadIdx.x;
+    if (tail < n) {
+        const float v = Act<TA>::to_f(p[tail]);
+        s = fmaf(v, v, s);
+    }
+    return s;
+}
+
+template <typename TA>
+__device__ __forceinline__ void chunk_scale(const TA *p, TA *o, int n, float coef) {
+    constexpr int EPV = 16 / sizeof(TA);
+    const unsigned mp = reinterpret_cast<uintptr_t>(p) & 15, mo = reinterpret_cast<uintptr_t>(o) & 15;
+    if (mp != mo) {  // no common 16-byte boundary
+        for (int i = threadIdx.x; i < n; i += kThreads)
+            o[i] = Act<TA>::from_f(Act<TA>::to_f(p[i]) * coef);
+        return;
+    }
+    const int head = min(n, (int)((16 - mp) & 15) / (int)sizeof(TA));
+    if ((int)threadIdx.x < head) o[threadIdx.x] = Act<TA>::from_f(Act<TA>::to_f(p[threadIdx.x]) * coef);
+    const int nv = (n - head) / EPV;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < nv; i += kThreads) {
+        float v[EPV];
+        unpack16(*reinterpret_cast<const uint4 *>(p + head + (int64_t)i * EPV), v, static_cast<const TA *>(nullptr));
+#pragma unroll
+        for (int j = 0; j < EPV; ++j) v[j] *= coef;
+        stg16(o + head + (int64_t)i * EPV, pack16(v, static_cast<const TA *>(nullptr)));
+    }
+    const int tail = head + nv * EPV + threadIdx.x;
+    if (tail < n) o[tail] = Act<TA>::from_f(Act<TA>::to_f(p[tail]) * coef);
+}
+
+__global__ void __launch_bounds__(kThreads)
+norm_kernel(const __grid_constant__ Table t, int add, double *__restrict__ part) {
+    pdl_entry();
+    double sum = 0.0;
+    const int chunks = t.n ? t.end[t.n - 1] : 0;
+    for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
+        const Chunk k = find_chunk(t, c);
+        sum += t.bf16[k.tensor]
+                   ? chunk_squares(static_cast<const __nv_bfloat16 *>(t.src[k.tensor]) + k.first, k.count)
+                   : chunk_squares(static_cast<const float *>(t.src[k.tensor]) + k.first, k.count);
+    }
+    sum = block_sum(sum);
+    if (threadIdx.x == 0) part[blockIdx.x] = add ? part[blockIdx.x] + sum : sum;
+}
+
+__global__ void __launch_bounds__(kThreads)
+scale_kernel(const __grid_constant__ Table t, const double *__restrict__ part, float max_norm,
+             float *__restrict__ norm) {
+    pdl_entry();
+    double sum = 0.0;
+    for (int i = threadIdx.x; i < kBlocks; i += kThreads) sum += part[i];
+    const float nrm = (float)sqrt(block_sum(sum));
+    if (blockIdx.x == 0 && threadIdx.x == 0) *norm = nrm;
+    float coef = max_norm / (nrm + 1e-6f);
+    coef = coef > 1.f ? 1.f : coef;  // a NaN norm stays NaN
+    const int chunks = t.n ? t.end[t.n - 1] : 0;
+    for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
+        const Chunk k = find_chunk(t, c);
+        if (t.dst[k.tensor] == nullptr) continue;
+        if (t.bf16[k.tensor])
+            chunk_scale(static_cast<const __nv_bfloat16 *>(t.src[k.tensor]) + k.first,
+                        static_cast<__nv_bfloat16 *>(t.dst[k.tensor]) + k.first, k.count, coef);
+        else
+            chunk_scale(static_cast<const float *>(t.src[k.tensor]) + k.first,
+                        static_cast<float *>(t.dst[k.tensor]) + k.first, k.count, coef);
+    }
+}
+
+void fill(const moe_grad_t *g, int64_t n, Table *t) {
+    int end = 0;
+    for (int64_t i = 0; i < n; ++i) {
+        t->src[i] = g[i].grad;
+        t->dst[i] = g[i].out;
+        t->numel[i] = g[i].numel;
+        t->bf16[i] = g[i].dtype == MOE_BF16;
+        end += (int)((g[i].numel + kChunk - 1) / kChunk);
+        t->end[i] = end;
+    }
+    t->n = (int)n;
+}
+
+}  // namespace
+
+size_t clip_scratch_bytes() { return sizeof(double) * kBlocks; }
+int64_t clip_chunk() { return kChunk; }
+
+cudaError_t launch_clip(const moe_grad_t *g, int64_t n, float max_norm, float *norm, void *ws,
+                        cudaStream_t st) {
+    Table t;
+    double *part = static_cast<double *>(ws);
+    for (int64_t i = 0; i == 0 || i < n; i += kTable) {
+        fill(g + i, std::min<int64_t>(kTable, n - i), &t);
+        launch_pdl(norm_kernel, dim3(kBlocks), dim3(kThreads), 0, st, t, i > 0 ? 1 : 0, part);
+    }
+    for (int64_t i = 0; i == 0 || i < n; i += kTable) {
+        if (n > kTable || i > 0) fill(g + i, std::min<int64_t>(kTable, n - i), &t);
+        launch_pdl(scale_kernel, dim3(kBlocks), dim3(kThreads), 0, st, t, (const double *)part, max_norm,
+                   norm);
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace moe

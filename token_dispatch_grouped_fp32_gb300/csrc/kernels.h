@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "common.cuh"
+#include "moe.h"
 
 namespace moe {
 
@@ -115,6 +116,48 @@ cudaError_t launch_dispatch_all_experts(const Shape &s, const int32_t *idx, int3
 // unweighted sum).
 cudaError_t launch_combine(const Shape &s, const void *y_perm, const int32_t *pos, const float *w,
                            void *out, cudaStream_t st);
+
+// ------------------------------ backward pass ------------------------------
+// dst[pos[q]] = w[q] * src[q / k] for every pair q (w == nullptr: unscaled),
+// and with dw (not null) dw[q] = <src[q / k], y_perm[pos[q]]>: the gradient of
+// the combine (src = dout), or the permuted copy of x (dw == nullptr).
+cudaError_t launch_scatter_rows(const Shape &s, const void *src, const void *y_perm,
+                                const int32_t *pos, const float *w, void *dst, float *dw,
+                                cudaStream_t st);
+// dx[t] = sum_j dx_perm[pos[t*k+j]] (w == nullptr), or weighted by w with
+// dw[t*k+j] = <x[t], dx_perm[pos[t*k+j]]>.
+cudaError_t launch_dispatch_backward(const Shape &s, const void *dx_perm, const int32_t *pos,
+                                     const float *w, const void *x, void *dx, float *dw,
+                                     cudaStream_t st);
+
+// Operands of the grouped SwiGLU's gradient (see moe_grouped_swiglu_backward).
+struct ExpertsBwd {
+    const void *x_perm;
+    const int32_t *offsets;
+    const void *Wgu, *Wd, *h_perm, *dy_perm;
+    void *dx_perm, *dWgu, *dWd, *ws;
+};
+cudaError_t launch_experts_backward_f32(const Shape &s, const ExpertsBwd &a, cudaStream_t st);
+
+// Operands of the router's gradient (see moe_route_backward).
+struct RouteBwd {
+    const void *x;
+    const float *Wr, *logits;
+    const int32_t *idx;
+    const float *w, *dw;
+    const void *dx_in;
+    float *dlogits, *dWr, *dbias;
+    void *dx, *ws;
+};
+size_t route_backward_scratch_bytes(const Shape &s);
+cudaError_t launch_route_backward(const Shape &s, const RouteBwd &a, const DevStatus &ds,
+                                  cudaStream_t st);
+
+// Global norm of n gradient tensors and their clipped copies.
+size_t clip_scratch_bytes();
+int64_t clip_chunk();  // elements per unit of work (the library's limit is 2^31 units)
+cudaError_t launch_clip(const moe_grad_t *g, int64_t n, float max_norm, float *norm, void *ws,
+                        cudaStream_t st);
 
 // Streaming multiprocessors of the current device (queried once per device).
 // Without a usable device (sizing a workspace on a host with no GPU) it is

@@ -6,9 +6,7 @@
 
 #include <atomic>
 
-#include "moe.h"
-#include "common.cuh"
-#include "kernels.h"
+#include "api.h"
 
 namespace moe {
 
@@ -68,6 +66,8 @@ struct DevState {
     unsigned *err_word = nullptr;
 };
 DevState g_dev[kMaxDevices];
+
+}  // namespace
 
 // First use on a device: check the architecture and fetch the error word's
 // device address.  Both are cached; later calls launch without queries.
@@ -196,13 +196,6 @@ bool rows_scaled_in_gemm(const Shape &s) {
 bool forward_uses_x_perm(const Shape &s) { return !all_experts_path(s) && !gather_path(s); }
 
 // ----- workspace layout of moe_forward (256-byte aligned sub-buffers) -----
-struct WsLayout {
-    size_t logits, idx, w, counts, offsets, pos, src, hist, route, row_scale, x_perm, h_perm,
-        y_perm, total;
-};
-
-size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
-
 WsLayout ws_layout(const Shape &s) {
     WsLayout L;
     const size_t P = (size_t)s.P(), T = (size_t)s.T, es = s.bf16 ? 2 : 4;
@@ -230,9 +223,7 @@ WsLayout ws_layout(const Shape &s) {
     return L;
 }
 
-template <typename T> T *at(void *ws, size_t off) {
-    return reinterpret_cast<T *>(static_cast<uint8_t *>(ws) + off);
-}
+namespace {
 
 // Router: tensor-core logits (split weight, K-split partials summed by the
 // top-k kernel) when the shape allows, else the SIMT logits kernel.

@@ -52,6 +52,11 @@ class moe_workspace_layout_t(ctypes.Structure):
                                                "total")]
 
 
+class moe_grad_t(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -74,6 +79,17 @@ def _load():
         "moe_combine": ([cfgp, vp, vp, vp, vp, vp], st),
         "moe_forward": ([cfgp, vp, vp, vp, vp, vp, vp, vp, sz, vp], st),
         "moe_forward_host": ([cfgp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp], st),
+        "moe_combine_backward": ([cfgp] + [vp] * 7, st),
+        "moe_dispatch_backward": ([cfgp] + [vp] * 7, st),
+        "moe_grouped_swiglu_backward_workspace_size": ([cfgp], sz),
+        "moe_grouped_swiglu_backward": ([cfgp] + [vp] * 10 + [sz, vp], st),
+        "moe_route_backward_workspace_size": ([cfgp], sz),
+        "moe_route_backward": ([cfgp] + [vp] * 12 + [sz, vp], st),
+        "moe_backward_workspace_size": ([cfgp], sz),
+        "moe_backward": ([cfgp] + [vp] * 5 + [sz] + [vp] * 7 + [sz, vp], st),
+        "moe_clip_grad_norm_workspace_size": ([], sz),
+        "moe_clip_grad_norm": ([ctypes.POINTER(moe_grad_t), ctypes.c_int64, ctypes.c_float, vp, vp,
+                                sz, vp], st),
         "moe_last_device_error": ([vp], st),
         "moe_set_wait_limit_ns": ([ctypes.c_uint64], None),
         "moe_wait_limit_ns": ([], ctypes.c_uint64),
@@ -232,6 +248,101 @@ def moe_forward_host(cfg, x_host, Wr, logit_bias, W_gate_up, W_down, out_host, x
     return _check(s, "moe_forward_host", raise_on_error)
 
 
+def _bytes(ws, ws_bytes):
+    if ws_bytes is not None:
+        return int(ws_bytes)
+    return 0 if ws is None or isinstance(ws, int) else ws.numel() * ws.element_size()
+
+
+def moe_combine_backward(cfg, dout, y_perm, pos, topk_w, dy_perm, dtopk_w, stream=None,
+                         raise_on_error=True):
+    s = _lib.moe_combine_backward(ctypes.byref(cfg), _ptr(dout), _ptr(y_perm), _ptr(pos),
+                                  _ptr(topk_w), _ptr(dy_perm), _ptr(dtopk_w), _stream(stream))
+    return _check(s, "moe_combine_backward", raise_on_error)
+
+
+def moe_dispatch_backward(cfg, dx_perm, pos, topk_w, x, dx, dtopk_w, stream=None,
+                          raise_on_error=True):
+    s = _lib.moe_dispatch_backward(ctypes.byref(cfg), _ptr(dx_perm), _ptr(pos), _ptr(topk_w),
+                                   _ptr(x), _ptr(dx), _ptr(dtopk_w), _stream(stream))
+    return _check(s, "moe_dispatch_backward", raise_on_error)
+
+
+def moe_grouped_swiglu_backward_workspace_size(cfg: moe_config_t) -> int:
+    return int(_lib.moe_grouped_swiglu_backward_workspace_size(ctypes.byref(cfg)))
+
+
+def moe_grouped_swiglu_backward(cfg, x_perm, offsets, W_gate_up, W_down, h_perm, dy_perm, dx_perm,
+                                dW_gate_up, dW_down, ws, ws_bytes=None, stream=None,
+                                raise_on_error=True):
+    s = _lib.moe_grouped_swiglu_backward(
+        ctypes.byref(cfg), _ptr(x_perm), _ptr(offsets), _ptr(W_gate_up), _ptr(W_down),
+        _ptr(h_perm), _ptr(dy_perm), _ptr(dx_perm), _ptr(dW_gate_up), _ptr(dW_down), _ptr(ws),
+        _bytes(ws, ws_bytes), _stream(stream))
+    return _check(s, "moe_grouped_swiglu_backward", raise_on_error)
+
+
+def moe_route_backward_workspace_size(cfg: moe_config_t) -> int:
+    return int(_lib.moe_route_backward_workspace_size(ctypes.byref(cfg)))
+
+
+def moe_route_backward(cfg, x, Wr, logits, topk_idx, topk_w, dtopk_w, dx_in, dlogits, dWr,
+                       dlogit_bias, dx, ws, ws_bytes=None, stream=None, raise_on_error=True):
+    s = _lib.moe_route_backward(
+        ctypes.byref(cfg), _ptr(x), _ptr(Wr), _ptr(logits), _ptr(topk_idx), _ptr(topk_w),
+        _ptr(dtopk_w), _ptr(dx_in), _ptr(dlogits), _ptr(dWr), _ptr(dlogit_bias), _ptr(dx), _ptr(ws),
+        _bytes(ws, ws_bytes), _stream(stream))
+    return _check(s, "moe_route_backward", raise_on_error)
+
+
+def moe_backward_workspace_size(cfg: moe_config_t) -> int:
+    return int(_lib.moe_backward_workspace_size(ctypes.byref(cfg)))
+
+
+def moe_backward(cfg, x, Wr, W_gate_up, W_down, fwd_ws, dout, dx, dWr, dlogit_bias, dW_gate_up,
+                 dW_down, ws, fwd_ws_bytes=None, ws_bytes=None, stream=None, raise_on_error=True):
+    s = _lib.moe_backward(
+        ctypes.byref(cfg), _ptr(x), _ptr(Wr), _ptr(W_gate_up), _ptr(W_down), _ptr(fwd_ws),
+        _bytes(fwd_ws, fwd_ws_bytes), _ptr(dout), _ptr(dx), _ptr(dWr), _ptr(dlogit_bias),
+        _ptr(dW_gate_up), _ptr(dW_down), _ptr(ws), _bytes(ws, ws_bytes), _stream(stream))
+    return _check(s, "moe_backward", raise_on_error)
+
+
+def grad_list(grads, outs=None):
+    """The moe_grad_t array of moe_clip_grad_norm for bf16 or fp32 tensors and
+    where their clipped copies go (default: in place; None in ``outs``: that
+    tensor counts in the norm only).  It holds addresses: keep the tensors
+    alive, and build it once for buffers that stay where they are."""
+    grads = list(grads)
+    outs = grads if outs is None else list(outs)
+    if len(outs) != len(grads):
+        raise ValueError(f"{len(grads)} gradients but {len(outs)} outputs")
+    arr = (moe_grad_t * max(1, len(grads)))()
+    arr.count = len(grads)
+    for a, g, o in zip(arr, grads, outs):
+        if g.dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError(f"gradients are bf16 or fp32 tensors, not {g.dtype}")
+        if o is not None and (o.dtype != g.dtype or o.numel() != g.numel()):
+            raise ValueError("a clipped copy has its gradient's dtype and size")
+        a.grad, a.out = _ptr(g).value, None if o is None else _ptr(o).value
+        a.numel = g.numel()
+        a.dtype = MOE_BF16 if g.dtype == torch.bfloat16 else MOE_F32
+    return arr
+
+
+def moe_clip_grad_norm_workspace_size() -> int:
+    return int(_lib.moe_clip_grad_norm_workspace_size())
+
+
+def moe_clip_grad_norm(grads, max_norm, norm, ws, ws_bytes=None, n=None, stream=None,
+                       raise_on_error=True):
+    """``grads``: from grad_list (n defaults to its length)."""
+    n = grads.count if n is None else int(n)
+    s = _lib.moe_clip_grad_norm(grads, n, float(max_norm), _ptr(norm), _ptr(ws),
+                                _bytes(ws, ws_bytes), _stream(stream))
+    return _check(s, "moe_clip_grad_norm", raise_on_error)
+
+
 def moe_last_device_error(stream=None, raise_on_error=True):
     s = _lib.moe_last_device_error(_stream(stream))
     return _check(s, "moe_last_device_error", raise_on_error)
@@ -245,7 +356,10 @@ class MoELayer:
 
     The workspace holds a call's intermediates (logits, routing, permuted
     rows), so two calls in flight at once must not share one: the layer keeps
-    a separate workspace for each stream it is called on."""
+    a separate workspace for each stream it is called on.
+
+    ``backward`` runs ``moe_backward`` for the latest ``forward`` on the same
+    stream, whose intermediates it finds in that workspace."""
 
     def __init__(self, Wr, W_gate_up, W_down, k, logit_bias=None, renormalize=True,
                  scale_inputs=False):
@@ -258,6 +372,7 @@ class MoELayer:
         self.renormalize = renormalize
         self.scale_inputs = scale_inputs
         self._ws = {}  # stream handle -> workspace
+        self._bwd_ws = {}  # the same for the backward pass
 
     def config(self, T: int) -> moe_config_t:
         return config(T, self.d, self.E, self.k, self.f, self.dtype, self.renormalize,
@@ -266,12 +381,14 @@ class MoELayer:
     def workspace(self, T: int, stream=None):
         """The workspace for calls on `stream` (default: the current stream),
         grown to moe_workspace_size for T tokens when needed."""
+        return self._grown(self._ws, moe_workspace_size(self.config(T)), stream)
+
+    def _grown(self, kept, need, stream):
         key = _stream(stream).value or 0
-        need = moe_workspace_size(self.config(T))
-        ws = self._ws.get(key)
+        ws = kept.get(key)
         if ws is None or ws.numel() < need:
             ws = torch.empty(max(need, 256), dtype=torch.uint8, device=self.Wr.device)
-            self._ws[key] = ws
+            kept[key] = ws
         return ws
 
     def forward(self, x, out=None, stream=None):
@@ -284,3 +401,25 @@ class MoELayer:
         return out
 
     __call__ = forward
+
+    def backward(self, x, dout, grads=None, stream=None):
+        """Gradients of <out, dout> for the latest ``forward(x)`` on this
+        stream: a dict of "x", "Wr", "W_gate_up", "W_down" and, with a logit
+        bias, "logit_bias".  ``grads``: such a dict of buffers to write into
+        (a training loop keeps one)."""
+        if x.shape[1] != self.d or dout.shape != x.shape or dout.dtype != x.dtype:
+            raise ValueError(f"x and dout are [T, {self.d}] of one dtype, not {tuple(x.shape)} "
+                             f"{x.dtype} and {tuple(dout.shape)} {dout.dtype}")
+        T = x.shape[0]
+        cfg = self.config(T)
+        if grads is None:
+            grads = {"x": torch.empty_like(x), "Wr": torch.empty_like(self.Wr),
+                     "W_gate_up": torch.empty_like(self.W_gate_up),
+                     "W_down": torch.empty_like(self.W_down)}
+            if self.logit_bias is not None:
+                grads["logit_bias"] = torch.empty_like(self.logit_bias)
+        ws = self._grown(self._bwd_ws, moe_backward_workspace_size(cfg), stream)
+        moe_backward(cfg, x, self.Wr, self.W_gate_up, self.W_down, self.workspace(T, stream), dout,
+                     grads["x"], grads["Wr"], grads.get("logit_bias"), grads["W_gate_up"],
+                     grads["W_down"], ws, stream=stream)
+        return grads
