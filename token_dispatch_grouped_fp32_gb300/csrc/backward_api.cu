@@ -12,7 +12,9 @@ struct BwdLayout {
 
 size_t es(const Shape &s) { return s.bf16 ? 2 : 4; }
 
-size_t experts_scratch_bytes(const Shape &s) { return es(s) * (size_t)s.P() * 2 * s.f; }
+size_t experts_scratch_bytes(const Shape &s) {
+    return s.bf16 ? experts_backward_tc_scratch_bytes(s) : 4 * (size_t)s.P() * 2 * s.f;
+}
 
 BwdLayout bwd_layout(const Shape &s) {
     BwdLayout L;
@@ -30,9 +32,11 @@ BwdLayout bwd_layout(const Shape &s) {
     return L;
 }
 
-moe_status_t run_experts_backward(const Shape &s, const ExpertsBwd &a, const DevStatus &,
+moe_status_t run_experts_backward(const Shape &s, const ExpertsBwd &a, const DevStatus &ds,
                                   cudaStream_t st) {
-    return from_cuda(launch_experts_backward_f32(s, a, st), "grouped SwiGLU gradient launch");
+    return from_cuda(s.bf16 ? launch_experts_backward_tc(s, a, ds, st)
+                            : launch_experts_backward_f32(s, a, st),
+                     "grouped SwiGLU gradient launch");
 }
 
 moe_status_t check_ws(size_t have, size_t need) {

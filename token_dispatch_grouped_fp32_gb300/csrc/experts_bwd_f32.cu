@@ -178,7 +178,7 @@ cudaError_t launch_t(const Shape &s, const ExpertsBwd &a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_experts_backward_f32(const Shape &s, const ExpertsBwd &a, cudaStream_t st) {
-    return s.bf16 ? launch_t<__nv_bfloat16>(s, a, st) : launch_t<float>(s, a, st);
+    return launch_t<float>(s, a, st);
 }
 
 }  // namespace moe

@@ -1,0 +1,733 @@
+// experts_bwd_tc.cu -- gradient of the grouped SwiGLU experts for bf16
+// activations on the sm_103a tensor cores (tcgen05.mma, accumulators in
+// tensor memory, operands staged by TMA).
+//
+// For expert e and row r of its segment, five products of one persistent
+// kernel template, in this order:
+//   DH   dh[r]   = dy[r] Wd[e]^T                      fp32, to the workspace
+//   GU   (g, u)  = x[r] Wgu[e], then in the epilogue, with s = sigmoid(g),
+//        dgu[r]  = [dh u s (1 + g (1 - s)), dh g s]   bf16, to the workspace
+//   DX   dx[r]   = dgu[r] Wgu[e]^T                    bf16
+//   DWD  dWd[e]  = sum_r h[r]^T dy[r]                 bf16
+//   DWG  dWgu[e] = sum_r x[r]^T dgu[r]                bf16
+// 16 P d f floating-point operations in all, 2 of the 8 units (GU) to form
+// the gate and up products again.  g, u and dh never leave fp32: the only
+// rounding between inputs and outputs is dgu's, which is an operand of the
+// last products.
+//
+// Row products (DH, GU, DX) have the forward's tiles: 256 rows x 256 columns
+// for a CTA pair (cta_group::2), 128 x 256 for a single CTA, row tiles within
+// one expert's segment, the shape chosen by the rows per expert
+// (gemm_tiles.cuh).  The weights are read as stored: DH and DX contract over
+// their contiguous axis (K-major B), GU over the other (MN-major B; a tile's
+// 256 accumulator columns are 128 gate and the 128 matching up columns).
+//
+// Weight products contract over the rows of a segment, so both operands are
+// MN-major and the K axis is ragged.  The last K step of a segment may hold
+// rows of the next expert (any value, a NaN too): MMAs are issued for whole
+// groups of 16 rows only up to the segment's end, and where the end falls
+// inside such a group, one warp (the fixer) zeroes the group's remaining rows
+// of both operands in shared memory.  For such a stage each CTA's loads
+// complete on a barrier of its own; the fixer zeroes, orders its writes before
+// the tensor core's reads (proxy fence), and reports the stage on the full
+// barrier: an arrival, or in a pair a 16-byte bulk copy of each CTA whose
+// bytes complete the leader's barrier.  An expert with
+// no rows has zeros written by the epilogue, without an MMA.
+//
+// Roles: warp 0 TMA loads, warp 1 tensor memory and MMAs (both one thread),
+// warps 2-9 the epilogue (two warps to each 32-lane quarter, half the columns
+// each), warp 10 the fixer (weight products).  Two accumulators of 256
+// columns: one tile's epilogue overlaps the next tile's products.
+//
+// Every wait is bounded, as in the forward: one that runs out records a
+// timeout, and every role drains its copies and MMAs before the tensor memory
+// is released.
+#include <cuda.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "gemm_tiles.cuh"
+#include "kernels.h"
+#include "tc_ptx.cuh"
+
+namespace moe {
+namespace tc {
+namespace {
+
+constexpr int BM = 128, BN = 256, BK = 64, UMMA_K = 16;
+constexpr int A_BYTES = BM * BK * 2;
+constexpr int ATOM_BYTES = BK * 128;  // MN-major: 64 K-rows x 64 columns
+constexpr int TMEM_COLS = 2 * BN;
+constexpr int kEpiWarps = 8;
+constexpr int MAX_E = 1024;
+
+enum Kind { DH, GU, DX, DW };
+
+template <int KIND> constexpr int threads() { return 32 * (2 + kEpiWarps + (KIND == DW ? 1 : 0)); }
+
+template <int CTAS> struct Cfg {
+    static constexpr bool PAIR = CTAS == 2;
+    static constexpr int TILE_M = BM * CTAS;
+    static constexpr int B_COLS = BN / CTAS;  // B columns (or rows of N) held by one CTA
+    static constexpr int B_ATOMS = B_COLS / 64;
+    static constexpr int B_BYTES = B_COLS * BK * 2;
+    static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+    static constexpr int STAGES = PAIR ? 6 : 4;
+    static constexpr int OFF_A = 0;
+    static constexpr int OFF_B = STAGES * A_BYTES;
+    static constexpr int OFF_BAR = OFF_B + STAGES * B_BYTES;
+    static constexpr int NUM_BARS = 3 * STAGES + 5;  // full, empty, tail; tmem full, empty; drain
+    static constexpr int OFF_SIGNAL = (OFF_BAR + NUM_BARS * 8 + 15) / 16 * 16;
+    static constexpr int OFF_TMEM = OFF_SIGNAL + 16 * CTAS;
+    static constexpr int OFF_ABORT = OFF_TMEM + 4;
+    static constexpr int OFF_OFFS = OFF_ABORT + 4;
+    static constexpr int OFF_TILE = OFF_OFFS + 4 * (MAX_E + 1);
+    static constexpr int SMEM_BYTES = OFF_TILE + 4 * (MAX_E + 1) + 1024;
+};
+
+struct Params {
+    const int32_t *offsets;
+    int E;
+    int K;        // reduction length of a row product
+    int M;        // DW: rows of dW[e]
+    int N;        // columns of the output (GU: f, gate and up alike)
+    int n_tiles;  // column tiles
+    int m_tiles;  // DW: row tiles
+    int m_fast;   // DW: row tiles vary fastest
+    int f;        // GU: column offset of the up half
+    int a_blocks, b_blocks;  // MN-major A / B through maps of 64-column blocks
+    float *dh;               // DH writes, GU reads (see dh_block)
+    __nv_bfloat16 *out;
+    int experts, release_late, overlap_prev;  // as in the forward's launches
+    DevStatus ds;
+};
+
+struct Work {
+    int e, row0, rows;  // the rows of expert e that the tile covers (DW: its whole segment)
+    int m0, n_blk;      // DW: first row of dW; column tile
+};
+
+template <int KIND>
+__device__ __forceinline__ Work decode(int tile, const int *s_off, const int *s_tile,
+                                       const Params &p, int tile_m) {
+    Work w;
+    if constexpr (KIND == DW) {
+        const int per = p.m_tiles * p.n_tiles;
+        w.e = tile / per;
+        const int r = tile - w.e * per;
+        const int m = p.m_fast ? r % p.m_tiles : r / p.n_tiles;
+        w.n_blk = p.m_fast ? r / p.m_tiles : r % p.n_tiles;
+        w.m0 = m * tile_m;
+        w.row0 = s_off[w.e];
+        w.rows = s_off[w.e + 1] - w.row0;
+    } else {
+        const int g = tile / p.n_tiles;
+        int lo = 0, hi = p.E - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (s_tile[mid] <= g) lo = mid; else hi = mid - 1;
+        }
+        const int mt = s_tile[lo + 1] - s_tile[lo];
+        const int r = tile - s_tile[lo] * p.n_tiles;
+        w.e = lo;
+        w.n_blk = r / mt;
+        w.row0 = s_off[lo] + (r % mt) * tile_m;
+        w.rows = min(tile_m, s_off[lo + 1] - w.row0);
+        w.m0 = 0;
+    }
+    return w;
+}
+
+// dh in the workspace: groups of up to 32 rows counted from a segment's
+// start (both tile shapes are whole groups), each group's f x rows floats
+// ordered by 16-byte column quad, then row, so that a warp whose lanes hold
+// the rows writes and reads 512 contiguous bytes per instruction.  Group g of
+// `rows` rows from row r0 starts at r0 * f.
+__device__ __forceinline__ float4 *dh_quad(float *dh, int64_t r0, int f, int rows, int col, int lane) {
+    return reinterpret_cast<float4 *>(dh + r0 * f + (int64_t)col * rows) + lane;
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<uint32_t *>(&v);
+}
+
+template <int CTAS, int KIND>
+__global__ void __launch_bounds__(threads<KIND>(), 1)
+experts_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                      Params p) {
+    if (!p.release_late) pdl_release();
+    using C = Cfg<CTAS>;
+    constexpr bool PAIR = C::PAIR;
+    constexpr int STAGES = C::STAGES;
+    constexpr bool A_MN = KIND == DW, B_MN = KIND == DW || KIND == GU;
+    constexpr uint32_t IDESC = idesc_bf16_ab(C::TILE_M, BN, A_MN, B_MN);
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t raw_s = smem_u32(smem_raw);
+    const uint32_t base_s = (raw_s + 1023u) & ~1023u;
+    uint8_t *base = smem_raw + (base_s - raw_s);
+    const uint32_t bar_full = base_s + C::OFF_BAR;      // [STAGES] (a pair uses the leader's)
+    const uint32_t bar_empty = bar_full + 8 * STAGES;   // [STAGES]
+    const uint32_t bar_tail = bar_empty + 8 * STAGES;   // [STAGES] this CTA's loads of a cut stage
+    const uint32_t bar_tfull = bar_tail + 8 * STAGES;   // [2]
+    const uint32_t bar_tempty = bar_tfull + 16;         // [2] (a pair uses the leader's)
+    const uint32_t bar_drain = bar_tempty + 16;
+    volatile uint32_t *s_tmem = reinterpret_cast<volatile uint32_t *>(base + C::OFF_TMEM);
+    volatile int *s_abort = reinterpret_cast<volatile int *>(base + C::OFF_ABORT);
+    int *s_off = reinterpret_cast<int *>(base + C::OFF_OFFS);
+    int *s_tile = reinterpret_cast<int *>(base + C::OFF_TILE);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int E = p.E;
+    const uint32_t rank = PAIR ? cluster_rank() : 0u;
+    const bool leader = rank == 0;
+    const int unit = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
+    const int nunits = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
+    const uint32_t sig_full = PAIR ? map_to_rank(bar_full, 0) : bar_full;
+    const uint32_t sig_tempty = PAIR ? map_to_rank(bar_tempty, 0) : bar_tempty;
+
+    if (threadIdx.x == 0) {
+        *s_abort = 0;
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(bar_full + 8 * i, 1);
+            mbar_init(bar_empty + 8 * i, 1);
+            mbar_init(bar_tail + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar_tfull + 8 * i, 1);
+            mbar_init(bar_tempty + 8 * i, kEpiWarps * CTAS);
+        }
+        mbar_init(bar_drain, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == 1) tmem_alloc<CTAS>(base_s + C::OFF_TMEM, TMEM_COLS);
+    if (!p.overlap_prev) pdl_wait();
+    if (p.release_late) pdl_release();
+    for (int e = threadIdx.x; e <= E; e += (int)blockDim.x) s_off[e] = __ldcg(p.offsets + e);
+    __syncthreads();
+    if (KIND != DW && warp == 2) {  // row tiles of the experts before each expert
+        const int per = (E + 31) / 32;
+        const int e0 = min(E, lane * per), e1 = min(E, e0 + per);
+        int local = 0;
+        for (int e = e0; e < e1; ++e)
+            local += expert_row_tiles(s_off[e + 1] - s_off[e], C::TILE_M, p.experts);
+        int incl = local;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += v;
+        }
+        int run = incl - local;
+        for (int e = e0; e < e1; ++e) {
+            s_tile[e] = run;
+            run += expert_row_tiles(s_off[e + 1] - s_off[e], C::TILE_M, p.experts);
+        }
+        if (lane == 31) s_tile[E] = incl;
+    }
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (PAIR) cluster_sync();
+    tc_fence_after();
+
+    const uint32_t tmem_base = *s_tmem;
+    const int total = KIND == DW ? E * p.m_tiles * p.n_tiles : s_tile[E] * p.n_tiles;
+    const int nk_row = (p.K + BK - 1) / BK;
+    // K steps of a tile, and whether its last one needs the fixer
+    auto ksteps = [&](const Work &w) { return KIND == DW ? (w.rows + BK - 1) / BK : nk_row; };
+    auto cut = [&](const Work &w) { return KIND == DW && (w.rows & 15) != 0; };
+
+    if (warp == 0) {
+        // ------------------------- TMA producer -------------------------
+        if (lane == 0) {
+            int s = 0;
+            uint32_t ph = 0;
+            uint32_t issued = 0, last_par = 0;   // full barriers armed here: ever / last parity
+            uint32_t tissued = 0, tail_par = 0;  // tail barriers: ever / parity of the next phase
+            bool ok = true;
+            for (int tile = unit; tile < total && ok; tile += nunits) {
+                const Work w = decode<KIND>(tile, s_off, s_tile, p, C::TILE_M);
+                const int nk = ksteps(w);
+                for (int ks = 0; ks < nk; ++ks) {
+                    if (!wait_bounded(bar_empty + 8 * s, ph ^ 1u, p.ds, s_abort)) {
+                        ok = false;
+                        break;
+                    }
+                    const bool tail = cut(w) && ks == nk - 1;
+                    if (leader) {
+                        if (PAIR || !tail)  // (a single CTA's fixer arrives itself)
+                            mbar_arrive_expect_tx(bar_full + 8 * s,
+                                                  (tail ? 16 : C::STAGE_BYTES) * CTAS);
+                        issued |= 1u << s;
+                        last_par = (last_par & ~(1u << s)) | (ph << s);
+                    }
+                    uint32_t fb = sig_full + 8 * s;
+                    if (KIND == DW && tail) {
+                        mbar_arrive_expect_tx(bar_tail + 8 * s, C::STAGE_BYTES);
+                        tissued |= 1u << s;
+                        tail_par ^= 1u << s;
+                        fb = PAIR ? map_to_rank(bar_tail + 8 * s, rank) : bar_tail + 8 * s;
+                    }
+                    const int k0 = ks * BK;
+                    const uint32_t adst = base_s + C::OFF_A + s * A_BYTES;
+                    const uint32_t bdst = base_s + C::OFF_B + s * C::B_BYTES;
+                    if constexpr (KIND == DW) {
+                        const int kr = w.row0 + k0, mc = w.m0 + (int)rank * BM;
+                        if (p.a_blocks) {
+                            tma_load_4d<CTAS>(adst, &tmA, 0, kr, mc >> 6, 0, fb);
+                        } else {
+                            tma_load_3d<CTAS>(adst, &tmA, mc, kr, 0, fb);
+                            tma_load_3d<CTAS>(adst + ATOM_BYTES, &tmA, mc + 64, kr, 0, fb);
+                        }
+                        const int nc = w.n_blk * BN + (int)rank * C::B_COLS;
+                        if (p.b_blocks) {
+#pragma unroll
+                            for (int a = 0; a < C::B_ATOMS; a += 2)
+                                tma_load_4d<CTAS>(bdst + a * ATOM_BYTES, &tmB, 0, kr, (nc >> 6) + a, 0, fb);
+                        } else {
+#pragma unroll
+                            for (int a = 0; a < C::B_ATOMS; ++a)
+                                tma_load_3d<CTAS>(bdst + a * ATOM_BYTES, &tmB, nc + 64 * a, kr, 0, fb);
+                        }
+                    } else {
+                        tma_load_2d<CTAS>(adst, &tmA, k0, w.row0 + (int)rank * BM, fb);
+                        if constexpr (KIND == GU) {
+                            // gate columns, then the matching up columns (offset f)
+                            const int g0 = w.n_blk * (BN / 2);
+#pragma unroll
+                            for (int a = 0; a < C::B_ATOMS; a += 2) {
+                                const int nc = g0 + ((PAIR ? (int)rank : a / 2) ? p.f : 0);
+                                if (p.b_blocks) {
+                                    tma_load_4d<CTAS>(bdst + a * ATOM_BYTES, &tmB, 0, k0, nc >> 6, w.e, fb);
+                                } else {
+                                    tma_load_3d<CTAS>(bdst + a * ATOM_BYTES, &tmB, nc, k0, w.e, fb);
+                                    tma_load_3d<CTAS>(bdst + (a + 1) * ATOM_BYTES, &tmB, nc + 64, k0, w.e, fb);
+                                }
+                            }
+                        } else {
+                            tma_load_3d<CTAS>(bdst, &tmB, k0, w.n_blk * BN + (int)rank * C::B_COLS, w.e, fb);
+                        }
+                    }
+                    if (++s == STAGES) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+            // drain: every phase armed here must have received all of its bytes
+            for (int i = 0; i < STAGES; ++i) {
+                volatile int never = 0;
+                if (KIND == DW && ((tissued >> i) & 1u) &&
+                    !wait_bounded(bar_tail + 8 * i, ((tail_par >> i) & 1u) ^ 1u, p.ds, &never,
+                                  drain_limit(p.ds)))
+                    break;
+                if (((issued >> i) & 1u) &&
+                    !wait_bounded(bar_full + 8 * i, (last_par >> i) & 1u, p.ds, &never,
+                                  drain_limit(p.ds)))
+                    break;
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------- MMA issuer ---------------------------
+        if (leader && lane == 0) {
+            int s = 0;
+            uint32_t ph = 0;
+            int it = 0;
+            bool ok = true;
+            // K-major operands: rows of 128 bytes, 8-row groups 1024 B apart, a
+            // K step of 16 elements 32 bytes along the row.  MN-major: 64-column
+            // atoms 8 KB apart, 8-row K groups 1024 B apart, a K step of 16 rows
+            // 2 KB.  Stages and K steps only move the start address.
+            const uint64_t adesc0 = smem_desc_sw128(base_s + C::OFF_A, A_MN ? ATOM_BYTES : 16, 1024);
+            const uint64_t bdesc0 = smem_desc_sw128(base_s + C::OFF_B, B_MN ? ATOM_BYTES : 16, 1024);
+            constexpr uint32_t ASTEP = A_MN ? 2048 : 32, BSTEP = B_MN ? 2048 : 32;
+            if (p.ds.inject_wait_timeout) ok = wait_bounded(bar_drain, 0, p.ds, s_abort);
+            for (int tile = unit; tile < total && ok; tile += nunits, ++it) {
+                const int acc = it & 1;
+                const uint32_t aph = (uint32_t)(it >> 1) & 1u;
+                int nk = nk_row, last = BK / UMMA_K;  // MMAs of the last K step
+                if constexpr (KIND == DW) {
+                    const Work w = decode<KIND>(tile, s_off, s_tile, p, C::TILE_M);
+                    nk = ksteps(w);
+                    last = (w.rows - (nk - 1) * BK + UMMA_K - 1) / UMMA_K;
+                }
+                if (!wait_bounded(bar_tempty + 8 * acc, aph ^ 1u, p.ds, s_abort)) break;
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
+                for (int ks = 0; ks < nk; ++ks) {
+                    // a cut stage of a pair is reported from the peer CTA too
+                    if (!wait_bounded<PAIR && KIND == DW>(bar_full + 8 * s, ph, p.ds, s_abort)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t a_st = adesc0 + (uint64_t)((s * A_BYTES) >> 4);
+                    const uint64_t b_st = bdesc0 + (uint64_t)((s * C::B_BYTES) >> 4);
+                    const int n = KIND == DW && ks == nk - 1 ? last : BK / UMMA_K;
+#pragma unroll
+                    for (int kk = 0; kk < BK / UMMA_K; ++kk)
+                        if (KIND != DW || kk < n)
+                            mma_bf16<CTAS>(d_tmem, a_st + (uint64_t)((kk * ASTEP) >> 4),
+                                           b_st + (uint64_t)((kk * BSTEP) >> 4), IDESC,
+                                           (ks | kk) != 0 ? 1u : 0u);
+                    mma_commit_all<CTAS>(bar_empty + 8 * s);
+                    if (++s == STAGES) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                mma_commit_all<CTAS>(bar_tfull + 8 * acc);
+            }
+            mma_commit_local<CTAS>(bar_drain);
+            volatile int never = 0;
+            wait_bounded(bar_drain, 0, p.ds, &never, drain_limit(p.ds));
+        }
+        __syncwarp();
+    } else if (warp < 2 + kEpiWarps) {
+        // --------------------------- epilogue ----------------------------
+        const int quarter = warp & 3;          // tensor-memory lanes of this warp
+        const int half = (warp - 2) >> 2;      // its half of the columns
+        const int wrow0 = (int)rank * BM + quarter * 32;
+        int it = 0;
+        for (int tile = unit; tile < total; tile += nunits, ++it) {
+            const Work w = decode<KIND>(tile, s_off, s_tile, p, C::TILE_M);
+            const int acc = it & 1;
+            const uint32_t aph = (uint32_t)(it >> 1) & 1u;
+            if (!__all_sync(0xffffffffu, wait_bounded(bar_tfull + 8 * acc, aph, p.ds, s_abort))) break;
+            tc_fence_after();
+            const uint32_t t_row = tmem_base + (uint32_t)(acc * BN) + ((uint32_t)(quarter * 32) << 16);
+            const int have = KIND == DW ? p.M - w.m0 : w.rows;
+            const int rv = max(0, min(32, have - wrow0));  // rows of this warp
+            if constexpr (KIND == DH) {
+                const int64_t r0 = w.row0 + wrow0;
+#pragma unroll 1
+                for (int c = 0; c < BN / 2; c += 32) {
+                    uint32_t y[32];
+                    tmem_ld32(t_row + half * (BN / 2) + c, y);
+                    tmem_ld_wait();
+                    const int n0 = w.n_blk * BN + half * (BN / 2) + c;
+                    if (lane < rv)
+#pragma unroll
+                        for (int v = 0; v < 8; ++v)
+                            if (n0 + 4 * v < p.N)
+                                *dh_quad(p.dh, r0, p.N, rv, n0 + 4 * v, lane) = make_float4(
+                                    __uint_as_float(y[4 * v]), __uint_as_float(y[4 * v + 1]),
+                                    __uint_as_float(y[4 * v + 2]), __uint_as_float(y[4 * v + 3]));
+                }
+            } else if constexpr (KIND == GU) {
+                const int64_t r0 = w.row0 + wrow0;
+#pragma unroll 1
+                for (int c = 0; c < BN / 4; c += 32) {
+                    const int off = half * (BN / 4) + c, n0 = w.n_blk * (BN / 2) + off;
+                    float dh[32];
+#pragma unroll
+                    for (int v = 0; v < 8; ++v) {
+                        float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (lane < rv && n0 + 4 * v < p.N)
+                            q = __ldcg(dh_quad(p.dh, r0, p.N, rv, n0 + 4 * v, lane));
+                        dh[4 * v] = q.x;
+                        dh[4 * v + 1] = q.y;
+                        dh[4 * v + 2] = q.z;
+                        dh[4 * v + 3] = q.w;
+                    }
+                    uint32_t g[32], u[32];
+                    tmem_ld32(t_row + off, g);
+                    tmem_ld32(t_row + BN / 2 + off, u);
+                    tmem_ld_wait();
+                    uint32_t pg[16], pu[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float dg[2], du[2];
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const float gv = __uint_as_float(g[2 * i + j]), uv = __uint_as_float(u[2 * i + j]);
+                            const float s = __fdividef(1.f, 1.f + __expf(-gv));
+                            const float t = dh[2 * i + j] * s;  // dh s
+                            du[j] = t * gv;
+                            dg[j] = t * uv * fmaf(gv, 1.f - s, 1.f);
+                        }
+                        pg[i] = pack2(dg[0], dg[1]);
+                        pu[i] = pack2(du[0], du[1]);
+                    }
+                    const int64_t ld = 2 * (int64_t)p.f;
+                    store_rows_transposed<4>(pg, p.out, r0, rv, n0, p.N, ld);
+                    store_rows_transposed<4>(pu, p.out + p.f, r0, rv, n0, p.N, ld);
+                }
+            } else {
+                const bool none = KIND == DW && w.rows == 0;
+                __nv_bfloat16 *out = p.out;
+                int64_t r0 = w.row0 + wrow0;
+                if (KIND == DW) {
+                    out += (int64_t)w.e * p.M * p.N;
+                    r0 = w.m0 + wrow0;
+                }
+#pragma unroll 1
+                for (int c = 0; c < BN / 2; c += 64) {
+                    const int off = half * (BN / 2) + c;
+                    uint32_t packed[32];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t y[32];
+                        tmem_ld32(t_row + off + 32 * h, y);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            packed[16 * h + i] = none ? 0u : pack2(__uint_as_float(y[2 * i]),
+                                                                   __uint_as_float(y[2 * i + 1]));
+                    }
+                    store_rows_transposed<8>(packed, out, r0, rv, w.n_blk * BN + off, p.N, p.N);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (PAIR) mbar_arrive_cluster(sig_tempty + 8 * acc);
+                else mbar_arrive(bar_tempty + 8 * acc);
+            }
+        }
+    } else if constexpr (KIND == DW) {
+        // ---------------------------- fixer ------------------------------
+        // Zeroes rows [rem, rem rounded up to 16) of both operands in the last
+        // K step of a segment whose end cuts a group of 16 rows.  A K row is
+        // 128 bytes in each 64-column atom; the swizzle moves bytes within it.
+        int s = 0;
+        uint32_t tail_par = 0;
+        const uint32_t slot = PAIR ? map_to_rank(base_s + C::OFF_SIGNAL + 16 * rank, 0) : 0u;
+        for (int tile = unit; tile < total; tile += nunits) {
+            const Work w = decode<KIND>(tile, s_off, s_tile, p, C::TILE_M);
+            const int nk = ksteps(w);
+            s = (s + nk) % STAGES;
+            if (!cut(w)) continue;
+            const int st = (s + STAGES - 1) % STAGES;  // the tile's last stage
+            // (this warp may reach the wait long before the stage is loaded)
+            if (!__all_sync(0xffffffffu, wait_bounded(bar_tail + 8 * st, (tail_par >> st) & 1u, p.ds,
+                                                      s_abort, drain_limit(p.ds))))
+                break;
+            tail_par ^= 1u << st;
+            const int rem = w.rows - (nk - 1) * BK;
+            const int pieces = 8 * (((rem + 15) & ~15) - rem);  // 16-byte pieces per atom
+            uint8_t *a = base + C::OFF_A + st * A_BYTES + rem * 128;
+            uint8_t *b = base + C::OFF_B + st * C::B_BYTES + rem * 128;
+            for (int i = lane; i < pieces * (2 + C::B_ATOMS); i += 32) {
+                const int atom = i / pieces, o = (i - atom * pieces) * 16;
+                uint8_t *q = atom < 2 ? a + atom * ATOM_BYTES + o : b + (atom - 2) * ATOM_BYTES + o;
+                *reinterpret_cast<uint4 *>(q) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                if (PAIR)
+                    bulk_copy_to_cluster(slot, base_s + C::OFF_A + st * A_BYTES, 16, sig_full + 8 * st);
+                else
+                    mbar_arrive(bar_full + 8 * st);
+            }
+        }
+        __syncwarp();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (PAIR) cluster_sync();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc<CTAS>(tmem_base, TMEM_COLS);
+    if (p.overlap_prev) pdl_wait();
+}
+
+// ------------------------------ host side ----------------------------------
+template <int CTAS, int KIND>
+cudaLaunchConfig_t launch_config(unsigned grid, cudaStream_t st, cudaLaunchAttribute *attr) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(threads<KIND>(), 1, 1);
+    cfg.dynamicSmemBytes = Cfg<CTAS>::SMEM_BYTES;
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CTAS;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cfg;
+}
+
+template <int CTAS, int KIND> cudaError_t prepare(int *resident) {
+    cudaError_t err = cudaFuncSetAttribute(experts_bwd_tc_kernel<CTAS, KIND>,
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           Cfg<CTAS>::SMEM_BYTES);
+    if (err != cudaSuccess) return err;
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = launch_config<CTAS, KIND>(CTAS, nullptr, attr);
+    int n = 0;
+    if ((err = cudaOccupancyMaxActiveClusters(&n, experts_bwd_tc_kernel<CTAS, KIND>, &cfg)) !=
+        cudaSuccess)
+        return err;
+    *resident = std::min(*resident, n);
+    return cudaSuccess;
+}
+
+template <int CTAS> cudaError_t prepare_all(int *resident) {
+    *resident = INT32_MAX;
+    cudaError_t err;
+    if ((err = prepare<CTAS, DH>(resident)) != cudaSuccess ||
+        (err = prepare<CTAS, GU>(resident)) != cudaSuccess ||
+        (err = prepare<CTAS, DX>(resident)) != cudaSuccess ||
+        (err = prepare<CTAS, DW>(resident)) != cudaSuccess)
+        return err;
+    return *resident >= 1 ? cudaSuccess : cudaErrorInvalidConfiguration;
+}
+
+struct DeviceInfo {
+    bool ready = false;
+    int units[3] = {0, 0, 0};  // resident single CTAs [1] and pairs [2]
+};
+
+template <int CTAS, int KIND>
+cudaError_t launch_one(int units, int64_t tiles, const CUtensorMap &a, const CUtensorMap &b,
+                       const Params &p, cudaStream_t st) {
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg =
+        launch_config<CTAS, KIND>(CTAS * (unsigned)std::min<int64_t>(units, tiles), st, attr);
+    return cudaLaunchKernelEx(&cfg, experts_bwd_tc_kernel<CTAS, KIND>, a, b, p);
+}
+
+// A row product over all experts: one launch, or one per tile shape.  The
+// maps' boxes differ between the shapes (KBox: B is K-major).
+template <int KIND, typename MapB>
+cudaError_t launch_rows(const Shape &s, const DeviceInfo &d, const CUtensorMap &a, MapB map_b,
+                        Params p, cudaStream_t st) {
+    const TileMode mode = tile_mode(s);
+    CUtensorMap b;
+    cudaError_t err = cudaSuccess;
+    p.experts = kAllExperts;
+    p.release_late = p.overlap_prev = 0;
+    if (mode != kModeSingles) {
+        if (!map_b(&b, 2)) return cudaErrorInvalidValue;
+        if (mode == kModeHybrid) {
+            p.experts = kPairExperts;
+            p.release_late = 1;
+        }
+        err = launch_one<2, KIND>(d.units[2], row_tiles_bound(s, 2 * BM) * p.n_tiles, a, b, p, st);
+        if (err != cudaSuccess || mode == kModePairs) return err;
+        p.experts = kSingleExperts;
+        p.release_late = 0;
+        p.overlap_prev = 1;
+    }
+    if (!map_b(&b, 1)) return cudaErrorInvalidValue;
+    return launch_one<1, KIND>(d.units[1], row_tiles_bound(s, BM) * p.n_tiles, a, b, p, st);
+}
+
+// MN-major view of a row-major [rows][cols] matrix (weights: one per expert).
+bool mn_map(CUtensorMap *m, const void *p, int64_t E, int64_t rows, int64_t cols, int *blocks) {
+    *blocks = cols % 64 == 0;
+    return *blocks ? tensor_map_weight_blocks(m, p, E, rows, cols, 2)
+                   : tensor_map_weights(m, p, E, rows, cols);
+}
+
+// dW[e] [M][N] = sum over the segment's rows of A[r]^T B[r].
+cudaError_t launch_weights(const Shape &s, const DeviceInfo &d, const void *A, int M, const void *B,
+                           int N, void *dW, Params p, cudaStream_t st) {
+    CUtensorMap a, b;
+    if (!mn_map(&a, A, 1, s.P(), M, &p.a_blocks) || !mn_map(&b, B, 1, s.P(), N, &p.b_blocks))
+        return cudaErrorInvalidValue;
+    p.M = M;
+    p.N = N;
+    p.n_tiles = (N + BN - 1) / BN;
+    p.out = static_cast<__nv_bfloat16 *>(dW);
+    p.experts = kAllExperts;
+    p.release_late = p.overlap_prev = 0;
+    const bool pair = pair_tiles_pay(M);
+    p.m_tiles = (M + (pair ? 2 : 1) * BM - 1) / ((pair ? 2 : 1) * BM);
+    p.m_fast = p.m_tiles <= p.n_tiles;
+    const int64_t tiles = (int64_t)s.E * p.m_tiles * p.n_tiles;
+    if (tiles >= INT32_MAX) {
+        set_error_message("weight gradient tile count exceeds 2^31");
+        return cudaErrorInvalidValue;
+    }
+    return pair ? launch_one<2, DW>(d.units[2], tiles, a, b, p, st)
+                : launch_one<1, DW>(d.units[1], tiles, a, b, p, st);
+}
+
+}  // namespace
+}  // namespace tc
+
+size_t experts_backward_tc_scratch_bytes(const Shape &s) {
+    const size_t pf = (size_t)s.P() * s.f;
+    return (4 * pf + 255) / 256 * 256 + 4 * pf;  // dh (fp32), dgu (bf16, 2f columns)
+}
+
+cudaError_t launch_experts_backward_tc(const Shape &s, const ExpertsBwd &x, const DevStatus &ds,
+                                       cudaStream_t st) {
+    using namespace tc;
+    static DeviceInfo info[64];
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    DeviceInfo &d = info[dev];
+    if (!d.ready) {
+        if ((err = prepare_all<1>(&d.units[1])) != cudaSuccess ||
+            (err = prepare_all<2>(&d.units[2])) != cudaSuccess) {
+            set_error_message("the experts' gradient does not fit on device %d", dev);
+            return err;
+        }
+        d.ready = true;
+    }
+    if (!tensor_map_encoder()) {
+        set_error_message("cuTensorMapEncodeTiled is not available from the driver");
+        return cudaErrorNotSupported;
+    }
+    const int64_t P = s.P();
+    if (row_tiles_bound(s, BM) * (std::max(s.d, s.f) / (BN / 2) + 1) >= (int64_t)INT32_MAX) {
+        set_error_message("experts' gradient tile count exceeds 2^31");
+        return cudaErrorInvalidValue;
+    }
+    float *dh = static_cast<float *>(x.ws);
+    void *dgu = static_cast<uint8_t *>(x.ws) + (4 * (size_t)P * s.f + 255) / 256 * 256;
+    CUtensorMap tx, tdy, tdgu;
+    if (!tensor_map_rows(&tx, x.x_perm, P, s.d, BM) || !tensor_map_rows(&tdy, x.dy_perm, P, s.d, BM) ||
+        !tensor_map_rows(&tdgu, dgu, P, 2 * (int64_t)s.f, BM)) {
+        set_error_message("cuTensorMapEncodeTiled rejected an operand (alignment or size)");
+        return cudaErrorInvalidValue;
+    }
+    Params p = {};
+    p.offsets = x.offsets;
+    p.E = s.E;
+    p.f = s.f;
+    p.dh = dh;
+    p.ds = ds;
+    Params q = p;
+    q.K = s.d;
+    q.N = s.f;
+    q.n_tiles = (s.f + BN - 1) / BN;
+    err = launch_rows<DH>(s, d, tdy, [&](CUtensorMap *m, int ctas) {
+        return tensor_map_weights_k(m, x.Wd, s.E, s.f, s.d, BN / ctas); }, q, st);
+    if (err != cudaSuccess) return err;
+    q = p;
+    q.K = s.d;
+    q.N = s.f;
+    q.n_tiles = (s.f + BN / 2 - 1) / (BN / 2);
+    q.out = static_cast<__nv_bfloat16 *>(dgu);
+    // two-atom boxes need the up half to start on a block too
+    q.b_blocks = s.f % 64 == 0;
+    err = launch_rows<GU>(s, d, tx, [&](CUtensorMap *m, int) {
+        return q.b_blocks ? tensor_map_weight_blocks(m, x.Wgu, s.E, s.d, 2 * (int64_t)s.f, 2)
+                          : tensor_map_weights(m, x.Wgu, s.E, s.d, 2 * (int64_t)s.f); }, q, st);
+    if (err != cudaSuccess) return err;
+    q = p;
+    q.K = 2 * s.f;
+    q.N = s.d;
+    q.n_tiles = (s.d + BN - 1) / BN;
+    q.out = static_cast<__nv_bfloat16 *>(x.dx_perm);
+    err = launch_rows<DX>(s, d, tdgu, [&](CUtensorMap *m, int ctas) {
+        return tensor_map_weights_k(m, x.Wgu, s.E, s.d, 2 * (int64_t)s.f, BN / ctas); }, q, st);
+    if (err != cudaSuccess) return err;
+    if ((err = launch_weights(s, d, x.h_perm, s.f, x.dy_perm, s.d, x.dWd, p, st)) != cudaSuccess)
+        return err;
+    return launch_weights(s, d, x.x_perm, s.d, dgu, 2 * s.f, x.dWgu, p, st);
+}
+
+}  // namespace moe

@@ -76,6 +76,7 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "gemm_tiles.cuh"
 #include "kernels.h"
 #include "tc_ptx.cuh"
 
@@ -99,7 +100,6 @@ constexpr int NUM_THREADS_GATHER = NUM_THREADS + 32 * (kGatherWarps + 1);
 constexpr int kGatherRows = 128 / kGatherWarps;  // A rows per gather warp and stage
 constexpr int kGatherIters = kGatherRows / 4;    // a warp instruction copies 4 rows
 constexpr int MAX_E = 1024;
-constexpr int kPairRowsPerExpert = 512;  // average rows per expert that selects CTA pairs
 
 template <int CTAS> struct Cfg {
     static constexpr bool PAIR = CTAS == 2;
@@ -183,58 +183,6 @@ struct Params {
 // costs shuffles but fewer memory transactions; it pays when epilogues are
 // frequent relative to the main loop (short K).
 constexpr int kTransposeMaxK = 3072;
-
-// Lane l holds packed[i] = bf16 pair (columns 2i, 2i+1 of a 64-column block)
-// of row (rbase + l): eight 16-byte chunks of 8 columns, chunk c in
-// packed[4c .. 4c+3].  An 8 x 8 transpose of the chunks within each group of
-// eight lanes (three butterfly steps over lane bits 4, 2, 1) leaves lane
-// 8g + j with chunk j of rows 8g .. 8g+7 in chunk slots 0..7, so each store
-// instruction writes 128 contiguous bytes of four rows: 48 shuffles and 8
-// 16-byte stores per block.
-__device__ __forceinline__ void store_rows_transposed(uint32_t (&packed)[32], __nv_bfloat16 *out,
-                                                      int64_t rbase, int rows_valid, int col0,
-                                                      int n_out) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int s = 4; s >= 1; s >>= 1) {
-        const bool upper = (lane & s) != 0;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            if (c & s) continue;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint32_t send = upper ? packed[4 * c + q] : packed[4 * (c + s) + q];
-                const uint32_t recv = __shfl_xor_sync(0xffffffffu, send, s);
-                if (upper) packed[4 * c + q] = recv;
-                else packed[4 * (c + s) + q] = recv;
-            }
-        }
-    }
-    const int grp = lane >> 3;
-    const int col = col0 + 8 * (lane & 7);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int r = 8 * grp + i;
-        if (r < rows_valid && col + 8 <= n_out)
-            stg16(out + (rbase + r) * n_out + col,
-                  make_uint4(packed[4 * i], packed[4 * i + 1], packed[4 * i + 2], packed[4 * i + 3]));
-    }
-}
-
-// Experts split between the two tile shapes by row count: CTA-pair tiles
-// (256 rows) serve an expert when they pad its rows to no more than 1.16x
-// what 128-row single-CTA tiles would (the single tile's cost per MMA row,
-// measured, from its larger shared-memory fill per SM).  The predicate is
-// evaluated on the device from `offsets`, identically by both launches.
-constexpr int kAllExperts = 0, kPairExperts = 1, kSingleExperts = 2;
-__host__ __device__ __forceinline__ bool pair_tiles_pay(int count) {
-    const int pair_rows = (count + 255) / 256 * 256, single_rows = (count + 127) / 128 * 128;
-    return pair_rows * 100 <= single_rows * 116;
-}
-__device__ __forceinline__ int expert_row_tiles(int count, int tile_m, int experts) {
-    if (experts != kAllExperts && pair_tiles_pay(count) != (experts == kPairExperts)) return 0;
-    return (count + tile_m - 1) / tile_m;
-}
 
 struct TileInfo {
     int e, row0, rows, n_blk;  // row0/rows: the tile's slice of expert e's segment
@@ -566,7 +514,7 @@ grouped_gemm_tc_kernel(const __grid_constant__ CUtensorMap tmX,
                             }
                         }
                     }
-                    store_rows_transposed(packed, out, rbase, rows_valid, n0 + c, n_out);
+                    store_rows_transposed<8>(packed, out, rbase, rows_valid, n0 + c, n_out, n_out);
                 }
             } else if (sw) {
                 const int n0 = ti.n_blk * (BN / 2);
@@ -800,24 +748,6 @@ template <int CTAS> cudaError_t prepare(int *resident_units) {
         return err;
     *resident_units = std::min(std::min(n[0], n[1]), std::min(n[2], n[3]));
     return cudaSuccess;
-}
-
-// Upper bound of the row tiles: sum_e ceil(count_e/TM) <= P/TM + min(E, P).
-int64_t row_tiles_bound(const Shape &s, int tile_m) {
-    const int64_t P = s.P();
-    return (P + tile_m - 1) / tile_m + std::min<int64_t>(s.E, P);
-}
-
-// Tile shapes of a call.  Pairs when experts average >= 512 rows; 128-row
-// single-CTA tiles for small per-expert batches (decode); in between, each
-// expert goes to the shape that pads it less (pair_tiles_pay), in two
-// launches per product.
-enum TileMode { kModePairs, kModeHybrid, kModeSingles };
-constexpr int kHybridRowsPerExpert = 64;  // below this average: single-CTA tiles only
-TileMode tile_mode(const Shape &s) {
-    if (s.P() >= (int64_t)kPairRowsPerExpert * s.E) return kModePairs;
-    if (s.P() >= (int64_t)kHybridRowsPerExpert * s.E) return kModeHybrid;
-    return kModeSingles;
 }
 
 // The launch of one product (G1: phase 1, G2: phase 2) over the experts

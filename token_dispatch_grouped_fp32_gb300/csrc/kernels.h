@@ -138,6 +138,10 @@ struct ExpertsBwd {
     void *dx_perm, *dWgu, *dWd, *ws;
 };
 cudaError_t launch_experts_backward_f32(const Shape &s, const ExpertsBwd &a, cudaStream_t st);
+// bf16: tcgen05 tensor cores.
+size_t experts_backward_tc_scratch_bytes(const Shape &s);
+cudaError_t launch_experts_backward_tc(const Shape &s, const ExpertsBwd &a, const DevStatus &ds,
+                                       cudaStream_t st);
 
 // Operands of the router's gradient (see moe_route_backward).
 struct RouteBwd {

@@ -381,5 +381,20 @@ inline bool tensor_map_weight_blocks(CUtensorMap *m, const void *ptr, int64_t E,
                                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// E x N x K bf16 weights read along K (K contiguous): box 64 K-elements x
+// box_n rows of N x 1 expert, the K-major operand of a product over K.  Rows
+// past N read zeros, not the next expert's.
+inline bool tensor_map_weights_k(CUtensorMap *m, const void *ptr, int64_t E, int64_t N, int64_t K,
+                                 uint32_t box_n) {
+    cuuint64_t dims[3] = {(cuuint64_t)K, (cuuint64_t)N, (cuuint64_t)E};
+    cuuint64_t strides[2] = {(cuuint64_t)K * 2, (cuuint64_t)N * K * 2};
+    cuuint32_t box[3] = {64, box_n, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return tensor_map_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr),
+                                dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace tc
 }  // namespace moe
