@@ -400,43 +400,59 @@ experts_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
             const uint32_t t_row = tmem_base + (uint32_t)(acc * BN) + ((uint32_t)(quarter * 32) << 16);
             const int have = KIND == DW ? p.M - w.m0 : w.rows;
             const int rv = max(0, min(32, have - wrow0));  // rows of this warp
+            // The accumulator is handed back as soon as it is in registers.  The
+            // arrival passes on no memory contents, only that the loads from
+            // tensor memory are complete, so in a pair it is a relaxed one: a
+            // release at cluster scope would wait for the warp's global stores.
+            auto release = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (PAIR) mbar_arrive_cluster_relaxed(sig_tempty + 8 * acc);
+                    else mbar_arrive(bar_tempty + 8 * acc);
+                }
+            };
             if constexpr (KIND == DH) {
                 const int64_t r0 = w.row0 + wrow0;
-#pragma unroll 1
-                for (int c = 0; c < BN / 2; c += 32) {
-                    uint32_t y[32];
-                    tmem_ld32(t_row + half * (BN / 2) + c, y);
-                    tmem_ld_wait();
-                    const int n0 = w.n_blk * BN + half * (BN / 2) + c;
-                    if (lane < rv)
+                const int n0 = w.n_blk * BN + half * (BN / 2);
+                uint32_t y[4][32];
 #pragma unroll
-                        for (int v = 0; v < 8; ++v)
-                            if (n0 + 4 * v < p.N)
-                                *dh_quad(p.dh, r0, p.N, rv, n0 + 4 * v, lane) = make_float4(
-                                    __uint_as_float(y[4 * v]), __uint_as_float(y[4 * v + 1]),
-                                    __uint_as_float(y[4 * v + 2]), __uint_as_float(y[4 * v + 3]));
-                }
+                for (int c = 0; c < 4; ++c) tmem_ld32(t_row + half * (BN / 2) + 32 * c, y[c]);
+                tmem_ld_wait();
+                release();
+                if (lane < rv)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int v = 0; v < 8; ++v) {
+                            const int n = n0 + 32 * c + 4 * v;
+                            if (n < p.N)
+                                *dh_quad(p.dh, r0, p.N, rv, n, lane) = make_float4(
+                                    __uint_as_float(y[c][4 * v]), __uint_as_float(y[c][4 * v + 1]),
+                                    __uint_as_float(y[c][4 * v + 2]), __uint_as_float(y[c][4 * v + 3]));
+                        }
             } else if constexpr (KIND == GU) {
                 const int64_t r0 = w.row0 + wrow0;
-#pragma unroll 1
-                for (int c = 0; c < BN / 4; c += 32) {
-                    const int off = half * (BN / 4) + c, n0 = w.n_blk * (BN / 2) + off;
+                const int n0 = w.n_blk * (BN / 2) + half * (BN / 4);
+                uint32_t pg[32], pu[32];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
                     float dh[32];
 #pragma unroll
                     for (int v = 0; v < 8; ++v) {
                         float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (lane < rv && n0 + 4 * v < p.N)
-                            q = __ldcg(dh_quad(p.dh, r0, p.N, rv, n0 + 4 * v, lane));
+                        const int n = n0 + 32 * c + 4 * v;
+                        if (lane < rv && n < p.N) q = __ldcg(dh_quad(p.dh, r0, p.N, rv, n, lane));
                         dh[4 * v] = q.x;
                         dh[4 * v + 1] = q.y;
                         dh[4 * v + 2] = q.z;
                         dh[4 * v + 3] = q.w;
                     }
                     uint32_t g[32], u[32];
-                    tmem_ld32(t_row + off, g);
-                    tmem_ld32(t_row + BN / 2 + off, u);
+                    tmem_ld32(t_row + half * (BN / 4) + 32 * c, g);
+                    tmem_ld32(t_row + BN / 2 + half * (BN / 4) + 32 * c, u);
                     tmem_ld_wait();
-                    uint32_t pg[16], pu[16];
+                    if (c == 1) release();
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         float dg[2], du[2];
@@ -448,13 +464,13 @@ experts_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                             du[j] = t * gv;
                             dg[j] = t * uv * fmaf(gv, 1.f - s, 1.f);
                         }
-                        pg[i] = pack2(dg[0], dg[1]);
-                        pu[i] = pack2(du[0], du[1]);
+                        pg[16 * c + i] = pack2(dg[0], dg[1]);
+                        pu[16 * c + i] = pack2(du[0], du[1]);
                     }
-                    const int64_t ld = 2 * (int64_t)p.f;
-                    store_rows_transposed<4>(pg, p.out, r0, rv, n0, p.N, ld);
-                    store_rows_transposed<4>(pu, p.out + p.f, r0, rv, n0, p.N, ld);
                 }
+                const int64_t ld = 2 * (int64_t)p.f;
+                store_rows_transposed<8>(pg, p.out, r0, rv, n0, p.N, ld);
+                store_rows_transposed<8>(pu, p.out + p.f, r0, rv, n0, p.N, ld);
             } else {
                 const bool none = KIND == DW && w.rows == 0;
                 __nv_bfloat16 *out = p.out;
@@ -463,28 +479,22 @@ experts_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                     out += (int64_t)w.e * p.M * p.N;
                     r0 = w.m0 + wrow0;
                 }
-#pragma unroll 1
-                for (int c = 0; c < BN / 2; c += 64) {
-                    const int off = half * (BN / 2) + c;
-                    uint32_t packed[32];
+                uint32_t packed[2][32];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t y[32];
-                        tmem_ld32(t_row + off + 32 * h, y);
-                        tmem_ld_wait();
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t y[32];
+                    tmem_ld32(t_row + half * (BN / 2) + 32 * c, y);
+                    tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            packed[16 * h + i] = none ? 0u : pack2(__uint_as_float(y[2 * i]),
-                                                                   __uint_as_float(y[2 * i + 1]));
-                    }
-                    store_rows_transposed<8>(packed, out, r0, rv, w.n_blk * BN + off, p.N, p.N);
+                    for (int i = 0; i < 16; ++i)
+                        packed[c / 2][16 * (c & 1) + i] =
+                            none ? 0u : pack2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1]));
                 }
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if (PAIR) mbar_arrive_cluster(sig_tempty + 8 * acc);
-                else mbar_arrive(bar_tempty + 8 * acc);
+                release();
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    store_rows_transposed<8>(packed[c], out, r0, rv,
+                                             w.n_blk * BN + half * (BN / 2) + 64 * c, p.N, p.N);
             }
         }
     } else if constexpr (KIND == DW) {

@@ -68,6 +68,13 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
                  : "memory");
 }
+// ... without ordering this thread's memory accesses (a release at cluster
+// scope waits for its earlier global stores): for an arrival that hands over
+// nothing that this thread wrote to memory.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
+                 : "memory");
+}
 // 16-byte copy global -> this CTA's shared memory through L2 (no L1
 // allocation), asynchronous to the issuing thread; groups of them are
 // committed and waited for with the two functions after it.
