@@ -108,36 +108,70 @@ struct Work {
     int m0, n_blk;      // DW: first row of dW; column tile
 };
 
-template <int KIND>
-__device__ __forceinline__ Work decode(int tile, const int *s_off, const int *s_tile,
-                                       const Params &p, int tile_m) {
-    Work w;
-    if constexpr (KIND == DW) {
-        const int per = p.m_tiles * p.n_tiles;
-        w.e = tile / per;
-        const int r = tile - w.e * per;
-        const int m = p.m_fast ? r % p.m_tiles : r / p.n_tiles;
-        w.n_blk = p.m_fast ? r / p.m_tiles : r % p.n_tiles;
-        w.m0 = m * tile_m;
-        w.row0 = s_off[w.e];
-        w.rows = s_off[w.e + 1] - w.row0;
-    } else {
-        const int g = tile / p.n_tiles;
-        int lo = 0, hi = p.E - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (s_tile[mid] <= g) lo = mid; else hi = mid - 1;
+// A unit's walk over the tile list: tile, tile + nunits, ...  Weight products
+// step (expert, slow tile index, fast tile index) as a mixed-radix number, so
+// a tile costs no division: their tiles can be one or two K steps long, and
+// the MMA issuer's time between two tiles is then the tensor cores' too.
+template <int KIND> struct Walk {
+    int tile, total, step;
+    int e, slow, fast, de, dslow, dfast, nslow, nfast;
+    __device__ __forceinline__ Walk(const Params &p, int unit, int nunits, int total_)
+        : tile(unit), total(total_), step(nunits) {
+        if constexpr (KIND == DW) {
+            nfast = p.m_fast ? p.m_tiles : p.n_tiles;
+            nslow = p.m_fast ? p.n_tiles : p.m_tiles;
+            e = unit / (nfast * nslow);
+            slow = unit / nfast - e * nslow;
+            fast = unit % nfast;
+            de = nunits / (nfast * nslow);
+            dslow = nunits / nfast - de * nslow;
+            dfast = nunits % nfast;
         }
-        const int mt = s_tile[lo + 1] - s_tile[lo];
-        const int r = tile - s_tile[lo] * p.n_tiles;
-        w.e = lo;
-        w.n_blk = r / mt;
-        w.row0 = s_off[lo] + (r % mt) * tile_m;
-        w.rows = min(tile_m, s_off[lo + 1] - w.row0);
-        w.m0 = 0;
     }
-    return w;
-}
+    __device__ __forceinline__ bool more() const { return tile < total; }
+    __device__ __forceinline__ void next() {
+        tile += step;
+        if constexpr (KIND == DW) {
+            fast += dfast;
+            slow += dslow;
+            e += de;
+            if (fast >= nfast) {
+                fast -= nfast;
+                ++slow;
+            }
+            if (slow >= nslow) {
+                slow -= nslow;
+                ++e;
+            }
+        }
+    }
+    __device__ __forceinline__ Work at(const int *s_off, const int *s_tile, const Params &p,
+                                       int tile_m) const {
+        Work w;
+        if constexpr (KIND == DW) {
+            w.e = e;
+            w.n_blk = p.m_fast ? slow : fast;
+            w.m0 = (p.m_fast ? fast : slow) * tile_m;
+            w.row0 = s_off[e];
+            w.rows = s_off[e + 1] - w.row0;
+        } else {
+            const int g = tile / p.n_tiles;
+            int lo = 0, hi = p.E - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (s_tile[mid] <= g) lo = mid; else hi = mid - 1;
+            }
+            const int mt = s_tile[lo + 1] - s_tile[lo];
+            const int r = tile - s_tile[lo] * p.n_tiles;
+            w.e = lo;
+            w.n_blk = r / mt;
+            w.row0 = s_off[lo] + (r % mt) * tile_m;
+            w.rows = min(tile_m, s_off[lo + 1] - w.row0);
+            w.m0 = 0;
+        }
+        return w;
+    }
+};
 
 // dh in the workspace: groups of up to 32 rows counted from a segment's
 // start (both tile shapes are whole groups), each group's f x rows floats
@@ -245,8 +279,8 @@ experts_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
             uint32_t issued = 0, last_par = 0;   // full barriers armed here: ever / last parity
             uint32_t tissued = 0, tail_par = 0;  // tail barriers: ever / parity of the next phase
             bool ok = true;
-            for (int tile = unit; tile < total && ok; tile += nunits) {
-                const Work w = decode<KIND>(tile, s_off, s_tile, p, C::TILE_M);
+            for (Walk<KIND> wk(p, unit, nunits, total); wk.more() && ok; wk.next()) {
+                const Work w = wk.at(s_off, s_tile, p, C::TILE_M);
                 const int nk = ksteps(w);
                 for (int ks = 0; ks < nk; ++ks) {
                     if (!wait_bounded(bar_empty + 8 * s, ph ^ 1u, p.ds, s_abort)) {
@@ -343,12 +377,12 @@ experts_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
             const uint64_t bdesc0 = smem_desc_sw128(base_s + C::OFF_B, B_MN ? ATOM_BYTES : 16, 1024);
             constexpr uint32_t ASTEP = A_MN ? 2048 : 32, BSTEP = B_MN ? 2048 : 32;
             if (p.ds.inject_wait_timeout) ok = wait_bounded(bar_drain, 0, p.ds, s_abort);
-            for (int tile = unit; tile < total && ok; tile += nunits, ++it) {
+            for (Walk<KIND> wk(p, unit, nunits, total); wk.more() && ok; wk.next(), ++it) {
                 const int acc = it & 1;
                 const uint32_t aph = (uint32_t)(it >> 1) & 1u;
                 int nk = nk_row, last = BK / UMMA_K;  // MMAs of the last K step
                 if constexpr (KIND == DW) {
-                    const Work w = decode<KIND>(tile, s_off, s_tile, p, C::TILE_M);
+                    const Work w = wk.at(s_off, s_tile, p, C::TILE_M);
                     nk = ksteps(w);
                     last = (w.rows - (nk - 1) * BK + UMMA_K - 1) / UMMA_K;
                 }
@@ -391,8 +425,8 @@ experts_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
         const int half = (warp - 2) >> 2;      // its half of the columns
         const int wrow0 = (int)rank * BM + quarter * 32;
         int it = 0;
-        for (int tile = unit; tile < total; tile += nunits, ++it) {
-            const Work w = decode<KIND>(tile, s_off, s_tile, p, C::TILE_M);
+        for (Walk<KIND> wk(p, unit, nunits, total); wk.more(); wk.next(), ++it) {
+            const Work w = wk.at(s_off, s_tile, p, C::TILE_M);
             const int acc = it & 1;
             const uint32_t aph = (uint32_t)(it >> 1) & 1u;
             if (!__all_sync(0xffffffffu, wait_bounded(bar_tfull + 8 * acc, aph, p.ds, s_abort))) break;
@@ -505,8 +539,8 @@ experts_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
         int s = 0;
         uint32_t tail_par = 0;
         const uint32_t slot = PAIR ? map_to_rank(base_s + C::OFF_SIGNAL + 16 * rank, 0) : 0u;
-        for (int tile = unit; tile < total; tile += nunits) {
-            const Work w = decode<KIND>(tile, s_off, s_tile, p, C::TILE_M);
+        for (Walk<KIND> wk(p, unit, nunits, total); wk.more(); wk.next()) {
+            const Work w = wk.at(s_off, s_tile, p, C::TILE_M);
             const int nk = ksteps(w);
             s = (s + nk) % STAGES;
             if (!cut(w)) continue;
