@@ -66,17 +66,20 @@ enum Kind { DH, GU, DX, DW };
 
 template <int KIND> constexpr int threads() { return 32 * (2 + kEpiWarps + (KIND == DW ? 1 : 0)); }
 
-template <int CTAS> struct Cfg {
+template <int CTAS, int KIND> struct Cfg {
     static constexpr bool PAIR = CTAS == 2;
     static constexpr int TILE_M = BM * CTAS;
     static constexpr int B_COLS = BN / CTAS;  // B columns (or rows of N) held by one CTA
     static constexpr int B_ATOMS = B_COLS / 64;
     static constexpr int B_BYTES = B_COLS * BK * 2;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-    static constexpr int STAGES = PAIR ? 6 : 4;
+    // a weight product gives one stage to the epilogue's output tiles (OUT_BYTES a warp)
+    static constexpr int STAGES = (PAIR ? 6 : 4) - (KIND == DW ? 1 : 0);
+    static constexpr int OUT_BYTES = KIND == DW ? 32 * 128 : 0;
     static constexpr int OFF_A = 0;
     static constexpr int OFF_B = STAGES * A_BYTES;
-    static constexpr int OFF_BAR = OFF_B + STAGES * B_BYTES;
+    static constexpr int OFF_OUT = OFF_B + STAGES * B_BYTES;
+    static constexpr int OFF_BAR = OFF_OUT + kEpiWarps * OUT_BYTES;
     static constexpr int NUM_BARS = 3 * STAGES + 5;  // full, empty, tail; tmem full, empty; drain
     static constexpr int OFF_SIGNAL = (OFF_BAR + NUM_BARS * 8 + 15) / 16 * 16;
     static constexpr int OFF_TMEM = OFF_SIGNAL + 16 * CTAS;
@@ -182,6 +185,11 @@ __device__ __forceinline__ float4 *dh_quad(float *dh, int64_t r0, int f, int row
     return reinterpret_cast<float4 *>(dh + r0 * f + (int64_t)col * rows) + lane;
 }
 
+__device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
     __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<uint32_t *>(&v);
@@ -190,9 +198,9 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 template <int CTAS, int KIND>
 __global__ void __launch_bounds__(threads<KIND>(), 1)
 experts_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                      Params p) {
+                      const __grid_constant__ CUtensorMap tmOut, Params p) {
     if (!p.release_late) pdl_release();
-    using C = Cfg<CTAS>;
+    using C = Cfg<CTAS, KIND>;
     constexpr bool PAIR = C::PAIR;
     constexpr int STAGES = C::STAGES;
     constexpr bool A_MN = KIND == DW, B_MN = KIND == DW || KIND == GU;
@@ -507,12 +515,7 @@ experts_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                 store_rows_transposed<8>(pu, p.out + p.f, r0, rv, n0, p.N, ld);
             } else {
                 const bool none = KIND == DW && w.rows == 0;
-                __nv_bfloat16 *out = p.out;
-                int64_t r0 = w.row0 + wrow0;
-                if (KIND == DW) {
-                    out += (int64_t)w.e * p.M * p.N;
-                    r0 = w.m0 + wrow0;
-                }
+                const int n0 = w.n_blk * BN + half * (BN / 2);
                 uint32_t packed[2][32];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
@@ -525,12 +528,35 @@ experts_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                             none ? 0u : pack2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1]));
                 }
                 release();
+                if constexpr (KIND == DX) {  // a segment's rows end inside a tile: predicated stores
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    store_rows_transposed<8>(packed[c], out, r0, rv,
-                                             w.n_blk * BN + half * (BN / 2) + 64 * c, p.N, p.N);
+                    for (int c = 0; c < 2; ++c)
+                        store_rows_transposed<8>(packed[c], p.out, w.row0 + wrow0, rv, n0 + 64 * c,
+                                                 p.N, p.N);
+                } else {
+                    // a 32 x 64 block at a time through shared memory (128-byte swizzle)
+                    const uint32_t buf = base_s + C::OFF_OUT + (warp - 2) * C::OUT_BYTES;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        if (rv == 0 || n0 + 64 * c >= p.N) break;  // warp-uniform
+                        if (lane == 0) bulk_wait_read();  // the buffer's last store has read it
+                        __syncwarp();
+#pragma unroll
+                        for (int v = 0; v < 8; ++v)
+                            sts16(buf + lane * 128 + ((v ^ (lane & 7)) << 4), packed[c][4 * v],
+                                  packed[c][4 * v + 1], packed[c][4 * v + 2], packed[c][4 * v + 3]);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            tma_store_3d(&tmOut, buf, n0 + 64 * c, w.m0 + wrow0, w.e);
+                            bulk_commit();
+                        }
+                    }
+                }
             }
         }
+        if (KIND == DW && lane == 0) bulk_wait_all();  // before the shared memory is released
+        __syncwarp();
     } else if constexpr (KIND == DW) {
         // ---------------------------- fixer ------------------------------
         // Zeroes rows [rem, rem rounded up to 16) of both operands in the last
@@ -585,7 +611,7 @@ cudaLaunchConfig_t launch_config(unsigned grid, cudaStream_t st, cudaLaunchAttri
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid, 1, 1);
     cfg.blockDim = dim3(threads<KIND>(), 1, 1);
-    cfg.dynamicSmemBytes = Cfg<CTAS>::SMEM_BYTES;
+    cfg.dynamicSmemBytes = (Cfg<CTAS, KIND>::SMEM_BYTES);
     cfg.stream = st;
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = CTAS;
@@ -601,7 +627,7 @@ cudaLaunchConfig_t launch_config(unsigned grid, cudaStream_t st, cudaLaunchAttri
 template <int CTAS, int KIND> cudaError_t prepare(int *resident) {
     cudaError_t err = cudaFuncSetAttribute(experts_bwd_tc_kernel<CTAS, KIND>,
                                            cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           Cfg<CTAS>::SMEM_BYTES);
+                                           (Cfg<CTAS, KIND>::SMEM_BYTES));
     if (err != cudaSuccess) return err;
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = launch_config<CTAS, KIND>(CTAS, nullptr, attr);
@@ -631,11 +657,11 @@ struct DeviceInfo {
 
 template <int CTAS, int KIND>
 cudaError_t launch_one(int units, int64_t tiles, const CUtensorMap &a, const CUtensorMap &b,
-                       const Params &p, cudaStream_t st) {
+                       const CUtensorMap &out, const Params &p, cudaStream_t st) {
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg =
         launch_config<CTAS, KIND>(CTAS * (unsigned)std::min<int64_t>(units, tiles), st, attr);
-    return cudaLaunchKernelEx(&cfg, experts_bwd_tc_kernel<CTAS, KIND>, a, b, p);
+    return cudaLaunchKernelEx(&cfg, experts_bwd_tc_kernel<CTAS, KIND>, a, b, out, p);
 }
 
 // A row product over all experts: one launch, or one per tile shape.  The
@@ -654,14 +680,14 @@ cudaError_t launch_rows(const Shape &s, const DeviceInfo &d, const CUtensorMap &
             p.experts = kPairExperts;
             p.release_late = 1;
         }
-        err = launch_one<2, KIND>(d.units[2], row_tiles_bound(s, 2 * BM) * p.n_tiles, a, b, p, st);
+        err = launch_one<2, KIND>(d.units[2], row_tiles_bound(s, 2 * BM) * p.n_tiles, a, b, a, p, st);
         if (err != cudaSuccess || mode == kModePairs) return err;
         p.experts = kSingleExperts;
         p.release_late = 0;
         p.overlap_prev = 1;
     }
     if (!map_b(&b, 1)) return cudaErrorInvalidValue;
-    return launch_one<1, KIND>(d.units[1], row_tiles_bound(s, BM) * p.n_tiles, a, b, p, st);
+    return launch_one<1, KIND>(d.units[1], row_tiles_bound(s, BM) * p.n_tiles, a, b, a, p, st);
 }
 
 // MN-major view of a row-major [rows][cols] matrix (weights: one per expert).
@@ -674,13 +700,13 @@ bool mn_map(CUtensorMap *m, const void *p, int64_t E, int64_t rows, int64_t cols
 // dW[e] [M][N] = sum over the segment's rows of A[r]^T B[r].
 cudaError_t launch_weights(const Shape &s, const DeviceInfo &d, const void *A, int M, const void *B,
                            int N, void *dW, Params p, cudaStream_t st) {
-    CUtensorMap a, b;
-    if (!mn_map(&a, A, 1, s.P(), M, &p.a_blocks) || !mn_map(&b, B, 1, s.P(), N, &p.b_blocks))
+    CUtensorMap a, b, o;
+    if (!mn_map(&a, A, 1, s.P(), M, &p.a_blocks) || !mn_map(&b, B, 1, s.P(), N, &p.b_blocks) ||
+        !tensor_map_out(&o, dW, s.E, M, N))
         return cudaErrorInvalidValue;
     p.M = M;
     p.N = N;
     p.n_tiles = (N + BN - 1) / BN;
-    p.out = static_cast<__nv_bfloat16 *>(dW);
     p.experts = kAllExperts;
     p.release_late = p.overlap_prev = 0;
     const bool pair = pair_tiles_pay(M);
@@ -691,8 +717,8 @@ cudaError_t launch_weights(const Shape &s, const DeviceInfo &d, const void *A, i
         set_error_message("weight gradient tile count exceeds 2^31");
         return cudaErrorInvalidValue;
     }
-    return pair ? launch_one<2, DW>(d.units[2], tiles, a, b, p, st)
-                : launch_one<1, DW>(d.units[1], tiles, a, b, p, st);
+    return pair ? launch_one<2, DW>(d.units[2], tiles, a, b, o, p, st)
+                : launch_one<1, DW>(d.units[1], tiles, a, b, o, p, st);
 }
 
 }  // namespace
