@@ -1,28 +1,31 @@
-// experts_bwd_tc.cu -- gradient of the grouped SwiGLU experts for bf16
+// gemm_bwd_tc.cu -- the matrix products of the layer's gradient for bf16
 // activations on the sm_103a tensor cores (tcgen05.mma, accumulators in
-// tensor memory, operands staged by TMA).
+// tensor memory, operands staged by TMA): one persistent kernel template.
 //
-// For expert e and row r of its segment, five products of one persistent
-// kernel template, in this order:
+// Experts.  For expert e and row r of its segment, five products in order:
 //   DH   dh[r]   = dy[r] Wd[e]^T                      fp32, to the workspace
 //   GU   (g, u)  = x[r] Wgu[e], then in the epilogue, with s = sigmoid(g),
 //        dgu[r]  = [dh u s (1 + g (1 - s)), dh g s]   bf16, to the workspace
 //   DX   dx[r]   = dgu[r] Wgu[e]^T                    bf16
-//   DWD  dWd[e]  = sum_r h[r]^T dy[r]                 bf16
-//   DWG  dWgu[e] = sum_r x[r]^T dgu[r]                bf16
+//   DW   dWd[e]  = sum_r h[r]^T dy[r],  dWgu[e] = sum_r x[r]^T dgu[r]   bf16
 // 16 P d f floating-point operations in all, 2 of the 8 units (GU) to form
 // the gate and up products again.  g, u and dh never leave fp32: the only
 // rounding between inputs and outputs is dgu's, which is an operand of the
 // last products.
 //
-// Row products (DH, GU, DX) have the forward's tiles: 256 rows x 256 columns
+// Router (see route_bwd.cu, which splits the fp32 operands into bf16 terms):
+//   RX   dx[t]   = add[t] + sum_c A[t][c] B[c]        A [T][K], B [K][d]
+//   RW   part[s] = sum over the tokens of split s of x[t]^T A[t]   fp32, transposed
+//
+// Row products (DH, GU, DX, RX) have the forward's tiles: 256 rows x 256 columns
 // for a CTA pair (cta_group::2), 128 x 256 for a single CTA, row tiles within
 // one expert's segment, the shape chosen by the rows per expert
 // (gemm_tiles.cuh).  The weights are read as stored: DH and DX contract over
-// their contiguous axis (K-major B), GU over the other (MN-major B; a tile's
-// 256 accumulator columns are 128 gate and the 128 matching up columns).
+// their contiguous axis (K-major B), GU and RX over the other (MN-major B; in
+// GU a tile's 256 accumulator columns are 128 gate and the 128 matching up
+// columns).
 //
-// Weight products contract over the rows of a segment, so both operands are
+// Weight products (DW, RW) contract over the rows of a segment, so both operands are
 // MN-major and the K axis is ragged.  The last K step of a segment may hold
 // rows of the next expert (any value, a NaN too): MMAs are issued for whole
 // groups of 16 rows only up to the segment's end, and where the end falls
@@ -61,10 +64,16 @@ constexpr int ATOM_BYTES = BK * 128;  // MN-major: 64 K-rows x 64 columns
 constexpr int TMEM_COLS = 2 * BN;
 constexpr int kEpiWarps = 8;
 constexpr int MAX_E = 1024;
+// K steps of one accumulation in RW.  The tensor cores' fp32 sum drops low
+// bits at every step, so long sums lose them in proportion; sums of kChunk
+// steps are added in fp32 by the epilogue.
+constexpr int kChunk = 8;
 
-enum Kind { DH, GU, DX, DW };
+enum Kind { DH, GU, DX, DW, RX, RW };
+// Weight products: both operands MN-major, K the rows of a segment.
+template <int KIND> constexpr bool kWeights = KIND == DW || KIND == RW;
 
-template <int KIND> constexpr int threads() { return 32 * (2 + kEpiWarps + (KIND == DW ? 1 : 0)); }
+template <int KIND> constexpr int threads() { return 32 * (2 + kEpiWarps + (kWeights<KIND> ? 1 : 0)); }
 
 template <int CTAS, int KIND> struct Cfg {
     static constexpr bool PAIR = CTAS == 2;
@@ -73,9 +82,11 @@ template <int CTAS, int KIND> struct Cfg {
     static constexpr int B_ATOMS = B_COLS / 64;
     static constexpr int B_BYTES = B_COLS * BK * 2;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-    // a weight product gives one stage to the epilogue's output tiles (OUT_BYTES a warp)
-    static constexpr int STAGES = (PAIR ? 6 : 4) - (KIND == DW ? 1 : 0);
-    static constexpr int OUT_BYTES = KIND == DW ? 32 * 128 : 0;
+    // one stage goes to the epilogue's output blocks (OUT_BYTES a warp) where
+    // the output leaves by TMA stores
+    static constexpr bool STAGED = KIND == DW || KIND == RX;
+    static constexpr int STAGES = (PAIR ? 6 : 4) - (STAGED ? 1 : 0);
+    static constexpr int OUT_BYTES = STAGED ? 32 * 128 : 0;
     static constexpr int OFF_A = 0;
     static constexpr int OFF_B = STAGES * A_BYTES;
     static constexpr int OFF_OUT = OFF_B + STAGES * B_BYTES;
@@ -102,6 +113,8 @@ struct Params {
     int a_blocks, b_blocks;  // MN-major A / B through maps of 64-column blocks
     float *dh;               // DH writes, GU reads (see dh_block)
     __nv_bfloat16 *out;
+    const __nv_bfloat16 *add;  // RX: added to the product (may be out), or nullptr
+    float *part;               // RW: [segments][N][M]
     int experts, release_late, overlap_prev;  // as in the forward's launches
     DevStatus ds;
 };
@@ -120,7 +133,7 @@ template <int KIND> struct Walk {
     int e, slow, fast, de, dslow, dfast, nslow, nfast;
     __device__ __forceinline__ Walk(const Params &p, int unit, int nunits, int total_)
         : tile(unit), total(total_), step(nunits) {
-        if constexpr (KIND == DW) {
+        if constexpr (kWeights<KIND>) {
             nfast = p.m_fast ? p.m_tiles : p.n_tiles;
             nslow = p.m_fast ? p.n_tiles : p.m_tiles;
             e = unit / (nfast * nslow);
@@ -134,7 +147,7 @@ template <int KIND> struct Walk {
     __device__ __forceinline__ bool more() const { return tile < total; }
     __device__ __forceinline__ void next() {
         tile += step;
-        if constexpr (KIND == DW) {
+        if constexpr (kWeights<KIND>) {
             fast += dfast;
             slow += dslow;
             e += de;
@@ -151,7 +164,7 @@ template <int KIND> struct Walk {
     __device__ __forceinline__ Work at(const int *s_off, const int *s_tile, const Params &p,
                                        int tile_m) const {
         Work w;
-        if constexpr (KIND == DW) {
+        if constexpr (kWeights<KIND>) {
             w.e = e;
             w.n_blk = p.m_fast ? slow : fast;
             w.m0 = (p.m_fast ? fast : slow) * tile_m;
@@ -190,6 +203,15 @@ __device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uin
                  : "memory");
 }
 
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
     __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<uint32_t *>(&v);
@@ -197,13 +219,13 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 
 template <int CTAS, int KIND>
 __global__ void __launch_bounds__(threads<KIND>(), 1)
-experts_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+gemm_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                       const __grid_constant__ CUtensorMap tmOut, Params p) {
     if (!p.release_late) pdl_release();
     using C = Cfg<CTAS, KIND>;
     constexpr bool PAIR = C::PAIR;
     constexpr int STAGES = C::STAGES;
-    constexpr bool A_MN = KIND == DW, B_MN = KIND == DW || KIND == GU;
+    constexpr bool A_MN = kWeights<KIND>, B_MN = KIND != DH && KIND != DX;
     constexpr uint32_t IDESC = idesc_bf16_ab(C::TILE_M, BN, A_MN, B_MN);
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw_s = smem_u32(smem_raw);
@@ -248,7 +270,7 @@ experts_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
     if (p.release_late) pdl_release();
     for (int e = threadIdx.x; e <= E; e += (int)blockDim.x) s_off[e] = __ldcg(p.offsets + e);
     __syncthreads();
-    if (KIND != DW && warp == 2) {  // row tiles of the experts before each expert
+    if (!kWeights<KIND> && warp == 2) {  // row tiles of the experts before each expert
         const int per = (E + 31) / 32;
         const int e0 = min(E, lane * per), e1 = min(E, e0 + per);
         int local = 0;
@@ -273,11 +295,11 @@ experts_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
     tc_fence_after();
 
     const uint32_t tmem_base = *s_tmem;
-    const int total = KIND == DW ? E * p.m_tiles * p.n_tiles : s_tile[E] * p.n_tiles;
+    const int total = kWeights<KIND> ? E * p.m_tiles * p.n_tiles : s_tile[E] * p.n_tiles;
     const int nk_row = (p.K + BK - 1) / BK;
     // K steps of a tile, and whether its last one needs the fixer
-    auto ksteps = [&](const Work &w) { return KIND == DW ? (w.rows + BK - 1) / BK : nk_row; };
-    auto cut = [&](const Work &w) { return KIND == DW && (w.rows & 15) != 0; };
+    auto ksteps = [&](const Work &w) { return kWeights<KIND> ? (w.rows + BK - 1) / BK : nk_row; };
+    auto cut = [&](const Work &w) { return kWeights<KIND> && (w.rows & 15) != 0; };
 
     if (warp == 0) {
         // ------------------------- TMA producer -------------------------
@@ -304,7 +326,7 @@ experts_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                         last_par = (last_par & ~(1u << s)) | (ph << s);
                     }
                     uint32_t fb = sig_full + 8 * s;
-                    if (KIND == DW && tail) {
+                    if (kWeights<KIND> && tail) {
                         mbar_arrive_expect_tx(bar_tail + 8 * s, C::STAGE_BYTES);
                         tissued |= 1u << s;
                         tail_par ^= 1u << s;
@@ -313,7 +335,7 @@ experts_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                     const int k0 = ks * BK;
                     const uint32_t adst = base_s + C::OFF_A + s * A_BYTES;
                     const uint32_t bdst = base_s + C::OFF_B + s * C::B_BYTES;
-                    if constexpr (KIND == DW) {
+                    if constexpr (kWeights<KIND>) {
                         const int kr = w.row0 + k0, mc = w.m0 + (int)rank * BM;
                         if (p.a_blocks) {
                             tma_load_4d<CTAS>(adst, &tmA, 0, kr, mc >> 6, 0, fb);
@@ -346,6 +368,17 @@ experts_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                                     tma_load_3d<CTAS>(bdst + (a + 1) * ATOM_BYTES, &tmB, nc + 64, k0, w.e, fb);
                                 }
                             }
+                        } else if constexpr (KIND == RX) {
+                            const int nc = w.n_blk * BN + (int)rank * C::B_COLS;
+#pragma unroll
+                            for (int a = 0; a < C::B_ATOMS; a += 2) {
+                                if (p.b_blocks) {
+                                    tma_load_4d<CTAS>(bdst + a * ATOM_BYTES, &tmB, 0, k0, (nc >> 6) + a, 0, fb);
+                                } else {
+                                    tma_load_3d<CTAS>(bdst + a * ATOM_BYTES, &tmB, nc + 64 * a, k0, 0, fb);
+                                    tma_load_3d<CTAS>(bdst + (a + 1) * ATOM_BYTES, &tmB, nc + 64 * a + 64, k0, 0, fb);
+                                }
+                            }
                         } else {
                             tma_load_3d<CTAS>(bdst, &tmB, k0, w.n_blk * BN + (int)rank * C::B_COLS, w.e, fb);
                         }
@@ -359,7 +392,7 @@ experts_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
             // drain: every phase armed here must have received all of its bytes
             for (int i = 0; i < STAGES; ++i) {
                 volatile int never = 0;
-                if (KIND == DW && ((tissued >> i) & 1u) &&
+                if (kWeights<KIND> && ((tissued >> i) & 1u) &&
                     !wait_bounded(bar_tail + 8 * i, ((tail_par >> i) & 1u) ^ 1u, p.ds, &never,
                                   drain_limit(p.ds)))
                     break;
@@ -385,42 +418,50 @@ experts_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
             const uint64_t bdesc0 = smem_desc_sw128(base_s + C::OFF_B, B_MN ? ATOM_BYTES : 16, 1024);
             constexpr uint32_t ASTEP = A_MN ? 2048 : 32, BSTEP = B_MN ? 2048 : 32;
             if (p.ds.inject_wait_timeout) ok = wait_bounded(bar_drain, 0, p.ds, s_abort);
-            for (Walk<KIND> wk(p, unit, nunits, total); wk.more() && ok; wk.next(), ++it) {
-                const int acc = it & 1;
-                const uint32_t aph = (uint32_t)(it >> 1) & 1u;
+            for (Walk<KIND> wk(p, unit, nunits, total); wk.more() && ok; wk.next()) {
                 int nk = nk_row, last = BK / UMMA_K;  // MMAs of the last K step
-                if constexpr (KIND == DW) {
+                if constexpr (kWeights<KIND>) {
                     const Work w = wk.at(s_off, s_tile, p, C::TILE_M);
                     nk = ksteps(w);
                     last = (w.rows - (nk - 1) * BK + UMMA_K - 1) / UMMA_K;
                 }
-                if (!wait_bounded(bar_tempty + 8 * acc, aph ^ 1u, p.ds, s_abort)) break;
-                tc_fence_after();
-                const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
-                for (int ks = 0; ks < nk; ++ks) {
-                    // a cut stage of a pair is reported from the peer CTA too
-                    if (!wait_bounded<PAIR && KIND == DW>(bar_full + 8 * s, ph, p.ds, s_abort)) {
+                int ks = 0;
+                do {  // accumulations: one, or in RW one per kChunk steps
+                    const int acc = it & 1;
+                    const uint32_t aph = (uint32_t)(it >> 1) & 1u;
+                    ++it;
+                    if (!wait_bounded(bar_tempty + 8 * acc, aph ^ 1u, p.ds, s_abort)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint64_t a_st = adesc0 + (uint64_t)((s * A_BYTES) >> 4);
-                    const uint64_t b_st = bdesc0 + (uint64_t)((s * C::B_BYTES) >> 4);
-                    const int n = KIND == DW && ks == nk - 1 ? last : BK / UMMA_K;
+                    const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
+                    const int ks0 = ks, ks1 = KIND == RW ? min(nk, ks + kChunk) : nk;
+                    for (; ks < ks1; ++ks) {
+                        // a cut stage of a pair is reported from the peer CTA too
+                        if (!wait_bounded<PAIR && kWeights<KIND>>(bar_full + 8 * s, ph, p.ds, s_abort)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint64_t a_st = adesc0 + (uint64_t)((s * A_BYTES) >> 4);
+                        const uint64_t b_st = bdesc0 + (uint64_t)((s * C::B_BYTES) >> 4);
+                        const int n = kWeights<KIND> && ks == nk - 1 ? last : BK / UMMA_K;
 #pragma unroll
-                    for (int kk = 0; kk < BK / UMMA_K; ++kk)
-                        if (KIND != DW || kk < n)
-                            mma_bf16<CTAS>(d_tmem, a_st + (uint64_t)((kk * ASTEP) >> 4),
-                                           b_st + (uint64_t)((kk * BSTEP) >> 4), IDESC,
-                                           (ks | kk) != 0 ? 1u : 0u);
-                    mma_commit_all<CTAS>(bar_empty + 8 * s);
-                    if (++s == STAGES) {
-                        s = 0;
-                        ph ^= 1u;
+                        for (int kk = 0; kk < BK / UMMA_K; ++kk)
+                            if (!kWeights<KIND> || kk < n)
+                                mma_bf16<CTAS>(d_tmem, a_st + (uint64_t)((kk * ASTEP) >> 4),
+                                               b_st + (uint64_t)((kk * BSTEP) >> 4), IDESC,
+                                               ((ks - ks0) | kk) != 0 ? 1u : 0u);
+                        mma_commit_all<CTAS>(bar_empty + 8 * s);
+                        if (++s == STAGES) {
+                            s = 0;
+                            ph ^= 1u;
+                        }
                     }
-                }
-                if (!ok) break;
-                mma_commit_all<CTAS>(bar_tfull + 8 * acc);
+                    if (!ok) break;
+                    mma_commit_all<CTAS>(bar_tfull + 8 * acc);
+                } while (ks < nk);
             }
             mma_commit_local<CTAS>(bar_drain);
             volatile int never = 0;
@@ -433,14 +474,21 @@ experts_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
         const int half = (warp - 2) >> 2;      // its half of the columns
         const int wrow0 = (int)rank * BM + quarter * 32;
         int it = 0;
-        for (Walk<KIND> wk(p, unit, nunits, total); wk.more(); wk.next(), ++it) {
+        bool ok = true;
+        for (Walk<KIND> wk(p, unit, nunits, total); wk.more(); wk.next()) {
             const Work w = wk.at(s_off, s_tile, p, C::TILE_M);
-            const int acc = it & 1;
-            const uint32_t aph = (uint32_t)(it >> 1) & 1u;
-            if (!__all_sync(0xffffffffu, wait_bounded(bar_tfull + 8 * acc, aph, p.ds, s_abort))) break;
-            tc_fence_after();
-            const uint32_t t_row = tmem_base + (uint32_t)(acc * BN) + ((uint32_t)(quarter * 32) << 16);
-            const int have = KIND == DW ? p.M - w.m0 : w.rows;
+            uint32_t t_row = 0;
+            int acc = 0;
+            // the next accumulator, complete
+            auto ready = [&]() {
+                acc = it & 1;
+                const uint32_t aph = (uint32_t)(it >> 1) & 1u;
+                ++it;
+                ok = __all_sync(0xffffffffu, wait_bounded(bar_tfull + 8 * acc, aph, p.ds, s_abort));
+                tc_fence_after();
+                t_row = tmem_base + (uint32_t)(acc * BN) + ((uint32_t)(quarter * 32) << 16);
+            };
+            const int have = kWeights<KIND> ? p.M - w.m0 : w.rows;
             const int rv = max(0, min(32, have - wrow0));  // rows of this warp
             // The accumulator is handed back as soon as it is in registers.  The
             // arrival passes on no memory contents, only that the loads from
@@ -454,6 +502,21 @@ experts_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                     else mbar_arrive(bar_tempty + 8 * acc);
                 }
             };
+            // Outputs that end with their matrix leave 32 rows x 64 columns at a
+            // time, through shared memory (128-byte swizzle) and a TMA store.
+            const uint32_t out_buf = base_s + C::OFF_OUT + (warp - 2) * C::OUT_BYTES;
+            auto store_block = [&](int col, int row, int e) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_3d(&tmOut, out_buf, col, row, e);
+                    bulk_commit();
+                }
+            };
+            if constexpr (KIND != RW) {
+                ready();
+                if (!ok) break;
+            }
             if constexpr (KIND == DH) {
                 const int64_t r0 = w.row0 + wrow0;
                 const int n0 = w.n_blk * BN + half * (BN / 2);
@@ -513,6 +576,75 @@ experts_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                 const int64_t ld = 2 * (int64_t)p.f;
                 store_rows_transposed<8>(pg, p.out, r0, rv, n0, p.N, ld);
                 store_rows_transposed<8>(pu, p.out + p.f, r0, rv, n0, p.N, ld);
+            } else if constexpr (KIND == RW) {
+                // accumulations of kChunk steps, added here in fp32
+                const int n0 = w.n_blk * BN + half * (BN / 2);
+                float sum[128];
+#pragma unroll
+                for (int c = 0; c < 128; ++c) sum[c] = 0.f;
+                const int nk = ksteps(w);
+                for (int ks = 0; ks == 0 || ks < nk; ks += kChunk) {
+                    ready();
+                    if (!ok) break;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t y[32];
+                        tmem_ld32(t_row + half * (BN / 2) + 32 * c, y);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) sum[32 * c + i] += __uint_as_float(y[i]);
+                    }
+                    release();
+                }
+                if (!ok) break;
+                // a column of the product is 32 consecutive floats of the warp's lanes
+                float *o = p.part + ((int64_t)w.e * p.N + n0) * p.M + w.m0 + wrow0 + lane;
+                if (lane < rv)
+#pragma unroll
+                    for (int c = 0; c < 128; ++c)
+                        if (n0 + c < p.N) o[(int64_t)c * p.M] = sum[c];
+            } else if constexpr (KIND == RX) {
+                const int n0 = w.n_blk * BN + half * (BN / 2);
+                uint32_t y[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32(t_row + half * (BN / 2) + 32 * c, y[c]);
+                tmem_ld_wait();
+                release();
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int n = n0 + 64 * c;
+                    if (rv == 0 || n >= p.N) break;  // warp-uniform
+                    if (lane == 0) bulk_wait_read();  // the buffer's last store has read it
+                    __syncwarp();
+                    if (p.add) {  // the block of the other gradient, to where its lanes read it
+#pragma unroll
+                        for (int v = 0; v < 8; ++v) {
+                            const int r = 4 * v + (lane >> 3), q = lane & 7;
+                            if (r < rv && n + 8 * q < p.N)
+                                cp_async16(out_buf + r * 128 + ((q ^ (r & 7)) << 4),
+                                           p.add + ((int64_t)w.row0 + wrow0 + r) * p.N + n + 8 * q);
+                        }
+                        cp_async_wait_all();
+                        __syncwarp();
+                    }
+#pragma unroll
+                    for (int v = 0; v < 8; ++v) {
+                        const uint32_t at = out_buf + lane * 128 + ((v ^ (lane & 7)) << 4);
+                        float f[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            f[i] = __uint_as_float(y[2 * c + v / 4][8 * (v % 4) + i]);
+                        if (p.add) {
+                            float t[8];
+                            unpack16(lds16(at), t, static_cast<const __nv_bfloat16 *>(nullptr));
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) f[i] += t[i];
+                        }
+                        sts16(at, pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]),
+                              pack2(f[6], f[7]));
+                    }
+                    store_block(n, w.row0 + wrow0, 0);
+                }
             } else {
                 const bool none = KIND == DW && w.rows == 0;
                 const int n0 = w.n_blk * BN + half * (BN / 2);
@@ -534,8 +666,6 @@ experts_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                         store_rows_transposed<8>(packed[c], p.out, w.row0 + wrow0, rv, n0 + 64 * c,
                                                  p.N, p.N);
                 } else {
-                    // a 32 x 64 block at a time through shared memory (128-byte swizzle)
-                    const uint32_t buf = base_s + C::OFF_OUT + (warp - 2) * C::OUT_BYTES;
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         if (rv == 0 || n0 + 64 * c >= p.N) break;  // warp-uniform
@@ -543,21 +673,16 @@ experts_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                         __syncwarp();
 #pragma unroll
                         for (int v = 0; v < 8; ++v)
-                            sts16(buf + lane * 128 + ((v ^ (lane & 7)) << 4), packed[c][4 * v],
+                            sts16(out_buf + lane * 128 + ((v ^ (lane & 7)) << 4), packed[c][4 * v],
                                   packed[c][4 * v + 1], packed[c][4 * v + 2], packed[c][4 * v + 3]);
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) {
-                            tma_store_3d(&tmOut, buf, n0 + 64 * c, w.m0 + wrow0, w.e);
-                            bulk_commit();
-                        }
+                        store_block(n0 + 64 * c, w.m0 + wrow0, w.e);
                     }
                 }
             }
         }
-        if (KIND == DW && lane == 0) bulk_wait_all();  // before the shared memory is released
+        if (C::STAGED && lane == 0) bulk_wait_all();  // before the shared memory is released
         __syncwarp();
-    } else if constexpr (KIND == DW) {
+    } else if constexpr (kWeights<KIND>) {
         // ---------------------------- fixer ------------------------------
         // Zeroes rows [rem, rem rounded up to 16) of both operands in the last
         // K step of a segment whose end cuts a group of 16 rows.  A K row is
@@ -625,14 +750,14 @@ cudaLaunchConfig_t launch_config(unsigned grid, cudaStream_t st, cudaLaunchAttri
 }
 
 template <int CTAS, int KIND> cudaError_t prepare(int *resident) {
-    cudaError_t err = cudaFuncSetAttribute(experts_bwd_tc_kernel<CTAS, KIND>,
+    cudaError_t err = cudaFuncSetAttribute(gemm_bwd_tc_kernel<CTAS, KIND>,
                                            cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            (Cfg<CTAS, KIND>::SMEM_BYTES));
     if (err != cudaSuccess) return err;
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = launch_config<CTAS, KIND>(CTAS, nullptr, attr);
     int n = 0;
-    if ((err = cudaOccupancyMaxActiveClusters(&n, experts_bwd_tc_kernel<CTAS, KIND>, &cfg)) !=
+    if ((err = cudaOccupancyMaxActiveClusters(&n, gemm_bwd_tc_kernel<CTAS, KIND>, &cfg)) !=
         cudaSuccess)
         return err;
     *resident = std::min(*resident, n);
@@ -645,7 +770,9 @@ template <int CTAS> cudaError_t prepare_all(int *resident) {
     if ((err = prepare<CTAS, DH>(resident)) != cudaSuccess ||
         (err = prepare<CTAS, GU>(resident)) != cudaSuccess ||
         (err = prepare<CTAS, DX>(resident)) != cudaSuccess ||
-        (err = prepare<CTAS, DW>(resident)) != cudaSuccess)
+        (err = prepare<CTAS, DW>(resident)) != cudaSuccess ||
+        (err = prepare<CTAS, RX>(resident)) != cudaSuccess ||
+        (err = prepare<CTAS, RW>(resident)) != cudaSuccess)
         return err;
     return *resident >= 1 ? cudaSuccess : cudaErrorInvalidConfiguration;
 }
@@ -661,7 +788,7 @@ cudaError_t launch_one(int units, int64_t tiles, const CUtensorMap &a, const CUt
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg =
         launch_config<CTAS, KIND>(CTAS * (unsigned)std::min<int64_t>(units, tiles), st, attr);
-    return cudaLaunchKernelEx(&cfg, experts_bwd_tc_kernel<CTAS, KIND>, a, b, out, p);
+    return cudaLaunchKernelEx(&cfg, gemm_bwd_tc_kernel<CTAS, KIND>, a, b, out, p);
 }
 
 // A row product over all experts: one launch, or one per tile shape.  The
@@ -697,6 +824,16 @@ bool mn_map(CUtensorMap *m, const void *p, int64_t E, int64_t rows, int64_t cols
                    : tensor_map_weights(m, p, E, rows, cols);
 }
 
+// Tiles of a weight product's [M][N] output, and whether CTA pairs serve it.
+struct WeightTiles {
+    bool pair;
+    int m, n;
+};
+WeightTiles weight_tiles(int M, int N) {
+    const bool pair = pair_tiles_pay(M);
+    return {pair, (M + (pair ? 2 : 1) * BM - 1) / ((pair ? 2 : 1) * BM), (N + BN - 1) / BN};
+}
+
 // dW[e] [M][N] = sum over the segment's rows of A[r]^T B[r].
 cudaError_t launch_weights(const Shape &s, const DeviceInfo &d, const void *A, int M, const void *B,
                            int N, void *dW, Params p, cudaStream_t st) {
@@ -706,19 +843,49 @@ cudaError_t launch_weights(const Shape &s, const DeviceInfo &d, const void *A, i
         return cudaErrorInvalidValue;
     p.M = M;
     p.N = N;
-    p.n_tiles = (N + BN - 1) / BN;
     p.experts = kAllExperts;
     p.release_late = p.overlap_prev = 0;
-    const bool pair = pair_tiles_pay(M);
-    p.m_tiles = (M + (pair ? 2 : 1) * BM - 1) / ((pair ? 2 : 1) * BM);
+    const WeightTiles t = weight_tiles(M, N);
+    p.m_tiles = t.m;
+    p.n_tiles = t.n;
     p.m_fast = p.m_tiles <= p.n_tiles;
     const int64_t tiles = (int64_t)s.E * p.m_tiles * p.n_tiles;
     if (tiles >= INT32_MAX) {
         set_error_message("weight gradient tile count exceeds 2^31");
         return cudaErrorInvalidValue;
     }
-    return pair ? launch_one<2, DW>(d.units[2], tiles, a, b, o, p, st)
-                : launch_one<1, DW>(d.units[1], tiles, a, b, o, p, st);
+    return t.pair ? launch_one<2, DW>(d.units[2], tiles, a, b, o, p, st)
+                  : launch_one<1, DW>(d.units[1], tiles, a, b, o, p, st);
+}
+
+}  // namespace
+}  // namespace tc
+
+namespace tc {
+namespace {
+
+// The current device's resident units; also checks the tensor-map encoder.
+cudaError_t device_info(const DeviceInfo **out) {
+    static DeviceInfo info[64];
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    DeviceInfo &d = info[dev];
+    if (!d.ready) {
+        if ((err = prepare_all<1>(&d.units[1])) != cudaSuccess ||
+            (err = prepare_all<2>(&d.units[2])) != cudaSuccess) {
+            set_error_message("the gradient's matrix products do not fit on device %d", dev);
+            return err;
+        }
+        d.ready = true;
+    }
+    if (!tensor_map_encoder()) {
+        set_error_message("cuTensorMapEncodeTiled is not available from the driver");
+        return cudaErrorNotSupported;
+    }
+    *out = &d;
+    return cudaSuccess;
 }
 
 }  // namespace
@@ -732,24 +899,10 @@ size_t experts_backward_tc_scratch_bytes(const Shape &s) {
 cudaError_t launch_experts_backward_tc(const Shape &s, const ExpertsBwd &x, const DevStatus &ds,
                                        cudaStream_t st) {
     using namespace tc;
-    static DeviceInfo info[64];
-    int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
+    const DeviceInfo *info;
+    cudaError_t err = device_info(&info);
     if (err != cudaSuccess) return err;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    DeviceInfo &d = info[dev];
-    if (!d.ready) {
-        if ((err = prepare_all<1>(&d.units[1])) != cudaSuccess ||
-            (err = prepare_all<2>(&d.units[2])) != cudaSuccess) {
-            set_error_message("the experts' gradient does not fit on device %d", dev);
-            return err;
-        }
-        d.ready = true;
-    }
-    if (!tensor_map_encoder()) {
-        set_error_message("cuTensorMapEncodeTiled is not available from the driver");
-        return cudaErrorNotSupported;
-    }
+    const DeviceInfo &d = *info;
     const int64_t P = s.P();
     if (row_tiles_bound(s, BM) * (std::max(s.d, s.f) / (BN / 2) + 1) >= (int64_t)INT32_MAX) {
         set_error_message("experts' gradient tile count exceeds 2^31");
@@ -798,6 +951,71 @@ cudaError_t launch_experts_backward_tc(const Shape &s, const ExpertsBwd &x, cons
     if ((err = launch_weights(s, d, x.h_perm, s.f, x.dy_perm, s.d, x.dWd, p, st)) != cudaSuccess)
         return err;
     return launch_weights(s, d, x.x_perm, s.d, dgu, 2 * s.f, x.dWgu, p, st);
+}
+
+cudaError_t launch_route_backward_tc(const Shape &s, const RouteProducts &r, const DevStatus &ds,
+                                     cudaStream_t st) {
+    using namespace tc;
+    const DeviceInfo *info;
+    cudaError_t err = device_info(&info);
+    if (err != cudaSuccess) return err;
+    Params p = {};
+    p.ds = ds;
+    p.experts = kAllExperts;
+    CUtensorMap a, b, o;
+    // RX: the tokens are one segment
+    p.offsets = r.all;
+    p.E = 1;
+    p.K = r.K;
+    p.N = s.d;
+    p.n_tiles = (s.d + BN - 1) / BN;
+    p.add = static_cast<const __nv_bfloat16 *>(r.dx_in);
+    const bool pair = s.T > BM;
+    if (!tensor_map_rows(&a, r.dl_x, s.T, r.K, BM, r.ld) || !mn_map(&b, r.W, 1, r.K, s.d, &p.b_blocks) ||
+        !tensor_map_out(&o, r.dx, 1, s.T, s.d)) {
+        set_error_message("cuTensorMapEncodeTiled rejected an operand (alignment or size)");
+        return cudaErrorInvalidValue;
+    }
+    const int64_t row_tiles = (s.T + (pair ? 2 : 1) * BM - 1) / ((pair ? 2 : 1) * BM);
+    if (row_tiles * p.n_tiles >= INT32_MAX) {
+        set_error_message("router gradient tile count exceeds 2^31");
+        return cudaErrorInvalidValue;
+    }
+    err = pair ? launch_one<2, RX>(info->units[2], row_tiles * p.n_tiles, a, b, o, p, st)
+               : launch_one<1, RX>(info->units[1], row_tiles * p.n_tiles, a, b, o, p, st);
+    if (err != cudaSuccess) return err;
+    // RW: the splits of the token axis are the segments
+    p.offsets = r.splits;
+    p.E = r.n_splits;
+    p.M = s.d;
+    p.N = r.K;
+    p.part = r.part;
+    const WeightTiles t = weight_tiles(p.M, p.N);
+    p.m_tiles = t.m;
+    p.n_tiles = t.n;
+    p.m_fast = t.m <= t.n;
+    if (!mn_map(&a, r.x, 1, s.T, s.d, &p.a_blocks)) return cudaErrorInvalidValue;
+    p.b_blocks = 0;  // the terms' rows are wider than the columns used
+    if (!tensor_map_weights(&b, r.dl_w, 1, s.T, r.K, r.ld)) return cudaErrorInvalidValue;
+    const int64_t tiles = (int64_t)p.E * t.m * t.n;
+    return t.pair ? launch_one<2, RW>(info->units[2], tiles, a, b, a, p, st)
+                  : launch_one<1, RW>(info->units[1], tiles, a, b, a, p, st);
+}
+
+int route_backward_splits(int64_t T, int d, int cols) {
+    const tc::WeightTiles t = tc::weight_tiles(d, cols);
+    const int64_t units = t.pair ? device_sm_count() / 2 : device_sm_count();
+    int64_t best = 1, best_cost = INT64_MAX;
+    for (int64_t n = 1; n <= 32 && (n == 1 || T / n >= 128); ++n) {
+        const int64_t waves = ((int64_t)t.m * t.n * n + units - 1) / units;
+        const int64_t steps = ((T + n - 1) / n + tc::BK - 1) / tc::BK;
+        const int64_t cost = waves * (steps + 6);  // a tile's epilogue is worth about 6 steps
+        if (cost < best_cost) {
+            best = n;
+            best_cost = cost;
+        }
+    }
+    return (int)best;
 }
 
 }  // namespace moe

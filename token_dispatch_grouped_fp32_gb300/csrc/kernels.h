@@ -154,6 +154,21 @@ struct RouteBwd {
     void *dx, *ws;
 };
 size_t route_backward_scratch_bytes(const Shape &s);
+// The router gradient's products on the tensor cores (bf16 x), over operands
+// that route_bwd.cu split into bf16 terms: dx = dx_in + dl_x W with dl_x
+// [T][K] and W [K][d], and part[s] [K][d] = the sum over split s's tokens of
+// dl_w[t]^T x[t], dl_w [T][K]; rows of dl_x and dl_w are ld elements apart.
+struct RouteProducts {
+    const void *x, *dl_x, *dl_w, *W, *dx_in;
+    int K, n_splits;
+    int64_t ld;
+    const int32_t *all, *splits;  // {0, T} and the n_splits + 1 split boundaries
+    void *dx;
+    float *part;
+};
+int route_backward_splits(int64_t T, int d, int cols);
+cudaError_t launch_route_backward_tc(const Shape &s, const RouteProducts &r, const DevStatus &ds,
+                                     cudaStream_t st);
 cudaError_t launch_route_backward(const Shape &s, const RouteBwd &a, const DevStatus &ds,
                                   cudaStream_t st);
 

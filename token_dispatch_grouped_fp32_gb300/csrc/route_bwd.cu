@@ -6,6 +6,17 @@
 //   plain softmax weights: dl[e] = p_e (g_e - S), g_e = dw_j where e = idx_j
 //     and 0 elsewhere, p = softmax over all E logits.
 //   dWr = dl^T x,   dbias = sum_t dl,   dx = dx_in + dl Wr.
+//
+// bf16 x: the products run on the tensor cores (gemm_bwd_tc.cu).  dl and Wr
+// are fp32, so they are written as sums of bf16 terms: v = hi + mid + lo to
+// 2^-25 of v.  dWr takes all three terms of dl against x, which is exact in
+// bf16, each term in its own accumulator columns; dx, which is rounded to
+// bf16, takes hi Whi + mid Whi + hi Wlo, within 2^-17.  A token's terms lie as
+// [lo | hi | mid | hi], E8 (E rounded up to 8) columns each: the first three
+// blocks are dWr's operand, the last three, against [Whi; Whi; Wlo], dx's.
+// Launches: terms (with the split of Wr), dx, dWr over splits of the token
+// axis, their sum.
+// fp32 x: the same steps on the CUDA cores.
 #include "common.cuh"
 #include "kernels.h"
 #include "simt_gemm.cuh"
@@ -15,6 +26,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kMaxTokenBlocks = 152 * 8;
+constexpr int kSplitCols = 4 * kThreads;  // elements of Wr per block
 using Tl = simt::Tile<64, 64, 16, 4, 4>;
 
 template <bool MAX> __device__ __forceinline__ float warp_all(float v) {
@@ -26,51 +39,179 @@ template <bool MAX> __device__ __forceinline__ float warp_all(float v) {
     return v;
 }
 
-// One warp per token.
-__global__ void __launch_bounds__(kThreads)
-dlogits_kernel(const float *__restrict__ logits, const int32_t *__restrict__ idx,
-               const float *__restrict__ w, const float *__restrict__ dw, int64_t T, int E, int k,
-               int renorm, float *__restrict__ dl, DevStatus ds) {
+struct Terms {
+    __nv_bfloat16 hi, mid, lo;
+};
+__device__ __forceinline__ Terms split3(float v) {
+    Terms t;
+    t.hi = __float2bfloat16_rn(v);
+    const float r = v - __bfloat162float(t.hi);
+    t.mid = __float2bfloat16_rn(r);
+    t.lo = __float2bfloat16_rn(r - __bfloat162float(t.mid));
+    if (!isfinite(v)) t.mid = t.lo = __float2bfloat16_rn(0.f);  // hi alone is the value
+    return t;
+}
+
+struct TermsArgs {
+    const float *logits;
+    const int32_t *idx;
+    const float *w, *dw;
+    int64_t T;
+    int E, k, renorm;
+    float *dl, *bias_part;  // [T][E]; [token blocks][E]
+    // bf16 x only (dl4 != nullptr): the terms [T][4*E8], Wr [E][d] and its
+    // terms [3*E8][d], and the segment boundaries of the two products
+    __nv_bfloat16 *dl4, *W3;
+    const float *Wr;
+    int E8, d, token_blocks, n_splits, split;
+    int32_t *all, *splits;
+};
+
+// Blocks below token_blocks: a warp per token at a time, its row of dl in
+// shared memory (then written whole, as floats and as terms) and the warp's
+// running sum of the rows for the bias.  The blocks after: kSplitCols elements
+// of Wr each.
+__global__ void __launch_bounds__(kThreads) terms_kernel(TermsArgs a, DevStatus ds) {
     pdl_entry();
-    const int lane = threadIdx.x & 31;
-    const int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (t >= T) return;
-    int e = -1;
-    float wj = 0.f, dj = 0.f;
-    if (lane < k) {
-        e = idx[t * k + lane];
-        wj = w[t * k + lane];
-        dj = dw[t * k + lane];
-        if ((unsigned)e >= (unsigned)E) {
-            raise_error(ds, kErrBadRouting);
-            e = -1;
-            wj = dj = 0.f;
+    extern __shared__ float sh[];
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, E8 = a.E8;
+    if ((int)blockIdx.x >= a.token_blocks) {
+        const int64_t n = (int64_t)E8 * a.d, real = (int64_t)a.E * a.d;
+        const int64_t i0 = (int64_t)((int)blockIdx.x - a.token_blocks) * kSplitCols + threadIdx.x;
+#pragma unroll
+        for (int j = 0; j < kSplitCols / kThreads; ++j) {
+            const int64_t i = i0 + j * kThreads;
+            if (i >= n) break;
+            const Terms t = split3(i < real ? a.Wr[i] : 0.f);
+            a.W3[i] = t.hi;
+            a.W3[n + i] = t.hi;
+            a.W3[2 * n + i] = t.mid;
+        }
+        return;
+    }
+    if (blockIdx.x == 0 && a.dl4) {
+        for (int i = threadIdx.x; i <= a.n_splits; i += kThreads)
+            a.splits[i] = (int32_t)min(a.T, (int64_t)i * a.split);
+        if (threadIdx.x == 0) {
+            a.all[0] = 0;
+            a.all[1] = (int32_t)a.T;
         }
     }
-    const float S = warp_all<false>(wj * dj);
-    float m = 0.f, inv = 0.f;
-    if (!renorm) {
-        m = -INFINITY;
-        for (int i = lane; i < E; i += 32) m = fmaxf(m, logits[t * E + i]);
-        m = warp_all<true>(m);
-        float z = 0.f;
-        for (int i = lane; i < E; i += 32) z += expf(logits[t * E + i] - m);
-        inv = 1.f / warp_all<false>(z);
+    float *row = sh + wid * E8, *sum = sh + (kWarps + wid) * E8;
+    for (int e = lane; e < E8; e += 32) row[e] = sum[e] = 0.f;
+    __syncwarp();
+    const int64_t step = (int64_t)a.token_blocks * kWarps;
+    for (int64_t t = (int64_t)blockIdx.x * kWarps + wid; t < a.T; t += step) {
+        int e = -1;
+        float wj = 0.f, dj = 0.f;
+        if (lane < a.k) {
+            e = a.idx[t * a.k + lane];
+            wj = a.w[t * a.k + lane];
+            dj = a.dw[t * a.k + lane];
+            if ((unsigned)e >= (unsigned)a.E) {
+                raise_error(ds, kErrBadRouting);
+                e = -1;
+                wj = dj = 0.f;
+            }
+        }
+        const float S = warp_all<false>(wj * dj);
+        const float *L = a.logits + t * a.E;
+        if (!a.renorm) {
+            float m = -INFINITY;
+            for (int i = lane; i < a.E; i += 32) m = fmaxf(m, L[i]);
+            m = warp_all<true>(m);
+            float z = 0.f;
+            for (int i = lane; i < a.E; i += 32) {
+                row[i] = expf(L[i] - m);
+                z += row[i];
+            }
+            const float inv = 1.f / warp_all<false>(z);
+            for (int i = lane; i < a.E; i += 32) row[i] *= inv * (0.f - S);
+            __syncwarp();
+            if (e >= 0) row[e] = expf(L[e] - m) * inv * (dj - S);
+        } else if (e >= 0) {
+            row[e] = wj * (dj - S);
+        }
+        __syncwarp();
+        for (int i = lane; i < a.E; i += 32) {
+            a.dl[t * a.E + i] = row[i];
+            sum[i] += row[i];
+        }
+        if (a.dl4) {
+            uint4 *o = reinterpret_cast<uint4 *>(a.dl4 + t * 4 * E8);
+            for (int v = lane; v < E8 / 8; v += 32) {
+                union {
+                    __nv_bfloat16 b[8];
+                    uint4 q;
+                } hi, mid, lo;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const Terms s = split3(row[8 * v + i]);
+                    hi.b[i] = s.hi;
+                    mid.b[i] = s.mid;
+                    lo.b[i] = s.lo;
+                }
+                o[v] = lo.q;
+                o[E8 / 8 + v] = hi.q;
+                o[2 * (E8 / 8) + v] = mid.q;
+                o[3 * (E8 / 8) + v] = hi.q;
+            }
+        }
+        __syncwarp();
+        if (a.renorm && e >= 0) row[e] = 0.f;  // all zero again for the next token
+        __syncwarp();
     }
-    for (int i = lane; i < E; i += 32)
-        dl[t * E + i] = renorm ? 0.f : expf(logits[t * E + i] - m) * inv * (0.f - S);
-    __syncwarp();  // the zeros and unchosen terms above come before the chosen ones
-    if (e >= 0) {
-        const float p = renorm ? wj : expf(logits[t * E + e] - m) * inv;
-        dl[t * E + e] = p * (dj - S);
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += kThreads) {
+        float s = 0.f;
+        for (int i = 0; i < kWarps; ++i) s += sh[(kWarps + i) * E8 + e];
+        a.bias_part[(int64_t)blockIdx.x * a.E + e] = s;
     }
 }
 
-// Partial sums over the tokens of one split: part[split][e][n] with n < d
-// dWr's columns and n == d the bias (a column of ones beside x).
-template <typename TA>
+// dWr[e][c] = the sum over splits and terms of part[s][b*stride + e][c] (small
+// terms first); the blocks after those: a warp per expert sums its bias.
+__global__ void __launch_bounds__(kThreads)
+sum_kernel(const float *__restrict__ part, int splits, int terms, int stride, int E, int d,
+           float *__restrict__ dWr, const float *__restrict__ bias_part, int token_blocks,
+           int weight_blocks, float *__restrict__ dbias) {
+    pdl_entry();
+    if ((int)blockIdx.x < weight_blocks) {
+        const int64_t i = 4 * ((int64_t)blockIdx.x * kThreads + threadIdx.x);
+        if (i >= (int64_t)E * d) return;
+        const int64_t e = i / d, c = i % d;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int b = 0; b < terms; ++b) {
+            // terms lie lo, hi, mid: add lo, mid, hi
+            const int o = b == 0 ? 0 : 3 - b;
+            const float *q = part + ((int64_t)o * stride + e) * d + c;
+            const int64_t step = (int64_t)terms * stride * d;
+#pragma unroll 8
+            for (int z = 0; z < splits; ++z) {
+                const float4 v = *reinterpret_cast<const float4 *>(q + z * step);
+                acc.x += v.x;
+                acc.y += v.y;
+                acc.z += v.z;
+                acc.w += v.w;
+            }
+        }
+        *reinterpret_cast<float4 *>(dWr + i) = acc;
+        return;
+    }
+    const int e = ((int)blockIdx.x - weight_blocks) * kWarps + (threadIdx.x >> 5);
+    if (!dbias || e >= E) return;
+    const int lane = threadIdx.x & 31;
+    float s = 0.f;
+#pragma unroll 8
+    for (int b = lane; b < token_blocks; b += 32) s += bias_part[(int64_t)b * E + e];
+    s = warp_all<false>(s);
+    if (lane == 0) dbias[e] = s;
+}
+
+// ------------------------- fp32 x, on the CUDA cores ------------------------
+// part[split][e][c]: the sum over the tokens of one split.
 __global__ void __launch_bounds__(simt::kThreads)
-dwr_kernel(const float *__restrict__ dl, const TA *__restrict__ x, int64_t T, int E, int d,
+dwr_kernel(const float *__restrict__ dl, const float *__restrict__ x, int64_t T, int E, int d,
            int tokens, float *__restrict__ part) {
     pdl_entry();
     __shared__ Tl::Smem sm;
@@ -81,36 +222,19 @@ dwr_kernel(const float *__restrict__ dl, const TA *__restrict__ x, int64_t T, in
     Tl::zero(acc);
     Tl::product<false, false>(
         sm, K, [&](int m, int k) { return e0 + m < E ? dl[(t0 + k) * E + e0 + m] : 0.f; },
-        [&](int k, int n) {
-            return n0 + n < d ? Act<TA>::to_f(x[(t0 + k) * d + n0 + n]) : n0 + n == d ? 1.f : 0.f;
-        }, acc);
+        [&](int k, int n) { return n0 + n < d ? x[(t0 + k) * d + n0 + n] : 0.f; }, acc);
 #pragma unroll
     for (int i = 0; i < Tl::TM; ++i)
 #pragma unroll
         for (int j = 0; j < Tl::TN; ++j) {
             const int e = e0 + Tl::row(i), n = n0 + Tl::col(j);
-            if (e < E && n <= d)
-                part[((int64_t)blockIdx.z * E + e) * (d + 1) + n] = acc[i][j];
+            if (e < E && n < d) part[((int64_t)blockIdx.z * E + e) * d + n] = acc[i][j];
         }
 }
 
-__global__ void __launch_bounds__(kThreads)
-dwr_sum_kernel(const float *__restrict__ part, int splits, int E, int d, float *__restrict__ dWr,
-               float *__restrict__ dbias) {
-    pdl_entry();
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x, n = (int64_t)E * (d + 1);
-    if (i >= n) return;
-    float s = 0.f;
-    for (int z = 0; z < splits; ++z) s += part[z * n + i];
-    const int64_t e = i / (d + 1), c = i % (d + 1);
-    if (c < d) dWr[e * d + c] = s;
-    else if (dbias) dbias[e] = s;
-}
-
-template <typename TA>
 __global__ void __launch_bounds__(simt::kThreads)
-route_dx_kernel(const float *__restrict__ dl, const float *__restrict__ Wr, const TA *dx_in,
-                int64_t T, int E, int d, TA *dx) {
+route_dx_kernel(const float *__restrict__ dl, const float *__restrict__ Wr, const float *dx_in,
+                int64_t T, int E, int d, float *dx) {
     pdl_entry();
     __shared__ Tl::Smem sm;
     const int64_t t0 = (int64_t)blockIdx.x * Tl::BM;
@@ -127,52 +251,124 @@ route_dx_kernel(const float *__restrict__ dl, const float *__restrict__ Wr, cons
             const int64_t t = t0 + Tl::row(i);
             const int n = n0 + Tl::col(j);
             if (t >= T || n >= d) continue;
-            float v = acc[i][j];
-            if (dx_in) v += Act<TA>::to_f(dx_in[t * d + n]);
-            dx[t * d + n] = Act<TA>::from_f(v);
+            const float v = acc[i][j];
+            dx[t * d + n] = dx_in ? v + dx_in[t * d + n] : v;
         }
 }
 
+// ------------------------------- host side ---------------------------------
 struct Plan {
-    int splits, tokens;  // splits of the token axis in dWr's sum
+    int E8, terms, token_blocks;
+    int splits, tokens;  // splits of the token axis in dWr's sum, tokens each
+    size_t dl4, W3, all, split_at, bias, part, total;  // workspace offsets
 };
+
+size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+
 Plan plan(const Shape &s) {
-    const int64_t tiles = (int64_t)((s.E + 63) / 64) * ((s.d + 64) / 64);
-    int64_t want = (2 * 152 + tiles - 1) / tiles;
-    const int64_t most = (s.T + 63) / 64;
-    want = want < 1 ? 1 : want > most ? most : want;
     Plan p;
+    p.E8 = (s.E + 7) / 8 * 8;
+    p.terms = s.bf16 ? 3 : 1;
+    const int64_t blocks = (s.T + kWarps - 1) / kWarps;
+    p.token_blocks = (int)(blocks < kMaxTokenBlocks ? blocks : kMaxTokenBlocks);
+    int64_t want;
+    if (s.bf16) {
+        want = route_backward_splits(s.T, s.d, 3 * p.E8);
+    } else {
+        const int64_t tiles = (int64_t)((s.E + 63) / 64) * ((s.d + 63) / 64);
+        want = (2 * 152 + tiles - 1) / tiles;
+        const int64_t most = (s.T + 63) / 64;
+        want = want < 1 ? 1 : want > most ? most : want;
+    }
     p.tokens = (int)((s.T + want - 1) / want);
     p.splits = (int)((s.T + p.tokens - 1) / p.tokens);
+    size_t o = 0;
+    p.dl4 = o;
+    if (s.bf16) o = up256(o + 2 * (size_t)s.T * 4 * p.E8);
+    p.W3 = o;
+    if (s.bf16) o = up256(o + 2 * (size_t)3 * p.E8 * s.d);
+    p.all = o;
+    o = up256(o + 2 * sizeof(int32_t));
+    p.split_at = o;
+    o = up256(o + sizeof(int32_t) * ((size_t)p.splits + 1));
+    p.bias = o;
+    o = up256(o + sizeof(float) * (size_t)p.token_blocks * s.E);
+    p.part = o;
+    o = up256(o + sizeof(float) * (size_t)p.splits * p.terms * (s.bf16 ? p.E8 : s.E) * s.d);
+    p.total = o;
     return p;
-}
-
-template <typename TA>
-cudaError_t launch_t(const Shape &s, const RouteBwd &a, const DevStatus &ds, cudaStream_t st) {
-    const Plan p = plan(s);
-    float *part = static_cast<float *>(a.ws);
-    launch_pdl(dlogits_kernel, dim3((unsigned)((s.T + kWarps - 1) / kWarps)), dim3(kThreads), 0, st,
-               a.logits, a.idx, a.w, a.dw, s.T, s.E, s.k, s.renorm ? 1 : 0, a.dlogits, ds);
-    launch_pdl(dwr_kernel<TA>, dim3((s.d + 64) / 64, (s.E + 63) / 64, p.splits), dim3(simt::kThreads),
-               0, st, (const float *)a.dlogits, static_cast<const TA *>(a.x), s.T, s.E, s.d,
-               p.tokens, part);
-    launch_pdl(dwr_sum_kernel, dim3((unsigned)(((int64_t)s.E * (s.d + 1) + kThreads - 1) / kThreads)),
-               dim3(kThreads), 0, st, (const float *)part, p.splits, s.E, s.d, a.dWr, a.dbias);
-    launch_pdl(route_dx_kernel<TA>, dim3((unsigned)((s.T + 63) / 64), (s.d + 63) / 64),
-               dim3(simt::kThreads), 0, st, (const float *)a.dlogits, a.Wr,
-               static_cast<const TA *>(a.dx_in), s.T, s.E, s.d, static_cast<TA *>(a.dx));
-    return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t route_backward_scratch_bytes(const Shape &s) {
-    return 4 * (size_t)plan(s).splits * s.E * (s.d + 1);
-}
+size_t route_backward_scratch_bytes(const Shape &s) { return plan(s).total; }
 
 cudaError_t launch_route_backward(const Shape &s, const RouteBwd &a, const DevStatus &ds,
                                   cudaStream_t st) {
-    return s.bf16 ? launch_t<__nv_bfloat16>(s, a, ds, st) : launch_t<float>(s, a, ds, st);
+    const Plan p = plan(s);
+    uint8_t *ws = static_cast<uint8_t *>(a.ws);
+    TermsArgs t = {};
+    t.logits = a.logits;
+    t.idx = a.idx;
+    t.w = a.w;
+    t.dw = a.dw;
+    t.T = s.T;
+    t.E = s.E;
+    t.k = s.k;
+    t.renorm = s.renorm ? 1 : 0;
+    t.dl = a.dlogits;
+    t.bias_part = reinterpret_cast<float *>(ws + p.bias);
+    t.E8 = p.E8;
+    t.d = s.d;
+    t.token_blocks = p.token_blocks;
+    t.n_splits = p.splits;
+    t.split = p.tokens;
+    if (s.bf16) {
+        t.dl4 = reinterpret_cast<__nv_bfloat16 *>(ws + p.dl4);
+        t.W3 = reinterpret_cast<__nv_bfloat16 *>(ws + p.W3);
+        t.Wr = a.Wr;
+        t.all = reinterpret_cast<int32_t *>(ws + p.all);
+        t.splits = reinterpret_cast<int32_t *>(ws + p.split_at);
+    }
+    const int split_blocks =
+        s.bf16 ? (int)(((int64_t)p.E8 * s.d + kSplitCols - 1) / kSplitCols) : 0;
+    const size_t sh = sizeof(float) * 2 * kWarps * (size_t)p.E8;  // at most 64 KB
+    cudaError_t err;
+    if (sh > 48 * 1024 &&
+        (err = cudaFuncSetAttribute(terms_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)sh)) != cudaSuccess)
+        return err;
+    launch_pdl(terms_kernel, dim3(p.token_blocks + split_blocks), dim3(kThreads), sh, st, t, ds);
+    if ((err = cudaGetLastError()) != cudaSuccess) return err;
+    float *part = reinterpret_cast<float *>(ws + p.part);
+    if (s.bf16) {
+        RouteProducts r;
+        r.x = a.x;
+        r.dl_w = t.dl4;
+        r.dl_x = t.dl4 + p.E8;
+        r.W = t.W3;
+        r.dx_in = a.dx_in;
+        r.K = 3 * p.E8;
+        r.n_splits = p.splits;
+        r.ld = 4 * (int64_t)p.E8;
+        r.all = t.all;
+        r.splits = t.splits;
+        r.dx = a.dx;
+        r.part = part;
+        if ((err = launch_route_backward_tc(s, r, ds, st)) != cudaSuccess) return err;
+    } else {
+        launch_pdl(route_dx_kernel, dim3((unsigned)((s.T + 63) / 64), (s.d + 63) / 64),
+                   dim3(simt::kThreads), 0, st, (const float *)a.dlogits, a.Wr,
+                   static_cast<const float *>(a.dx_in), s.T, s.E, s.d, static_cast<float *>(a.dx));
+        launch_pdl(dwr_kernel, dim3((s.d + 63) / 64, (s.E + 63) / 64, p.splits),
+                   dim3(simt::kThreads), 0, st, (const float *)a.dlogits,
+                   static_cast<const float *>(a.x), s.T, s.E, s.d, p.tokens, part);
+    }
+    const int weight_blocks = (int)(((int64_t)s.E * s.d / 4 + kThreads - 1) / kThreads);
+    launch_pdl(sum_kernel, dim3(weight_blocks + (s.E + kWarps - 1) / kWarps), dim3(kThreads), 0, st,
+               (const float *)part, p.splits, p.terms, s.bf16 ? p.E8 : s.E, s.E, s.d, a.dWr,
+               (const float *)t.bias_part, p.token_blocks, weight_blocks, a.dbias);
+    return cudaGetLastError();
 }
 
 }  // namespace moe

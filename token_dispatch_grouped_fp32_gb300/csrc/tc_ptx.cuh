@@ -366,10 +366,11 @@ inline EncodeTiledFn tensor_map_encoder() {
 }
 
 // rows x cols bf16 matrix (cols contiguous): box 64 cols x box_rows rows, 128 B swizzle
+// (rows ld elements apart; 0: cols)
 inline bool tensor_map_rows(CUtensorMap *m, const void *ptr, int64_t rows, int64_t cols,
-                            uint32_t box_rows) {
+                            uint32_t box_rows, int64_t ld = 0) {
     cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
+    cuuint64_t strides[1] = {(cuuint64_t)(ld ? ld : cols) * 2};
     cuuint32_t box[2] = {64, box_rows};
     cuuint32_t estr[2] = {1, 1};
     return tensor_map_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr),
@@ -379,9 +380,12 @@ inline bool tensor_map_rows(CUtensorMap *m, const void *ptr, int64_t rows, int64
 }
 
 // E x K x N bf16 weights (N contiguous): box 64 cols x 64 K-rows x 1 expert
-inline bool tensor_map_weights(CUtensorMap *m, const void *ptr, int64_t E, int64_t K, int64_t N) {
+// (rows ld elements apart; 0: N)
+inline bool tensor_map_weights(CUtensorMap *m, const void *ptr, int64_t E, int64_t K, int64_t N,
+                               int64_t ld = 0) {
+    if (ld == 0) ld = N;
     cuuint64_t dims[3] = {(cuuint64_t)N, (cuuint64_t)K, (cuuint64_t)E};
-    cuuint64_t strides[2] = {(cuuint64_t)N * 2, (cuuint64_t)K * N * 2};
+    cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)K * ld * 2};
     cuuint32_t box[3] = {64, 64, 1};
     cuuint32_t estr[3] = {1, 1, 1};
     return tensor_map_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr),
