@@ -52,6 +52,10 @@ __device__ __forceinline__ Terms split3(float v) {
     return t;
 }
 
+__device__ __forceinline__ uint32_t pack(__nv_bfloat16 a, __nv_bfloat16 b) {
+    return (uint32_t)__bfloat16_as_ushort(a) | (uint32_t)__bfloat16_as_ushort(b) << 16;
+}
+
 struct TermsArgs {
     const float *logits;
     const int32_t *idx;
@@ -133,28 +137,41 @@ __global__ void __launch_bounds__(kThreads) terms_kernel(TermsArgs a, DevStatus 
             row[e] = wj * (dj - S);
         }
         __syncwarp();
-        for (int i = lane; i < a.E; i += 32) {
-            a.dl[t * a.E + i] = row[i];
-            sum[i] += row[i];
-        }
-        if (a.dl4) {
-            uint4 *o = reinterpret_cast<uint4 *>(a.dl4 + t * 4 * E8);
-            for (int v = lane; v < E8 / 8; v += 32) {
-                union {
-                    __nv_bfloat16 b[8];
-                    uint4 q;
-                } hi, mid, lo;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const Terms s = split3(row[8 * v + i]);
-                    hi.b[i] = s.hi;
-                    mid.b[i] = s.mid;
-                    lo.b[i] = s.lo;
+        // the row as floats and as terms, four columns a lane
+        const bool whole = (a.E & 3) == 0;
+        float *o = a.dl + t * a.E;
+        for (int v = lane; v < E8 / 4; v += 32) {
+            const float4 r = *reinterpret_cast<const float4 *>(row + 4 * v);
+            if (whole) {
+                if (4 * v < a.E) *reinterpret_cast<float4 *>(o + 4 * v) = r;
+            } else {
+                if (4 * v < a.E) o[4 * v] = r.x;
+                if (4 * v + 1 < a.E) o[4 * v + 1] = r.y;
+                if (4 * v + 2 < a.E) o[4 * v + 2] = r.z;
+                if (4 * v + 3 < a.E) o[4 * v + 3] = r.w;
+            }
+            uint2 hi = make_uint2(0, 0), mid = hi, lo = hi;
+            if (r.x != 0.f || r.y != 0.f || r.z != 0.f || r.w != 0.f) {  // mostly zeros when renormalised
+                float4 *acc = reinterpret_cast<float4 *>(sum + 4 * v);
+                float4 q = *acc;
+                q.x += r.x;
+                q.y += r.y;
+                q.z += r.z;
+                q.w += r.w;
+                *acc = q;
+                if (a.dl4) {
+                    const Terms x = split3(r.x), y = split3(r.y), z = split3(r.z), w = split3(r.w);
+                    hi = make_uint2(pack(x.hi, y.hi), pack(z.hi, w.hi));
+                    mid = make_uint2(pack(x.mid, y.mid), pack(z.mid, w.mid));
+                    lo = make_uint2(pack(x.lo, y.lo), pack(z.lo, w.lo));
                 }
-                o[v] = lo.q;
-                o[E8 / 8 + v] = hi.q;
-                o[2 * (E8 / 8) + v] = mid.q;
-                o[3 * (E8 / 8) + v] = hi.q;
+            }
+            if (a.dl4) {
+                uint2 *d4 = reinterpret_cast<uint2 *>(a.dl4 + t * 4 * E8) + v;
+                d4[0] = lo;
+                d4[E8 / 4] = hi;
+                d4[2 * (E8 / 4)] = mid;
+                d4[3 * (E8 / 4)] = hi;
             }
         }
         __syncwarp();
@@ -186,13 +203,20 @@ sum_kernel(const float *__restrict__ part, int splits, int terms, int stride, in
             const int o = b == 0 ? 0 : 3 - b;
             const float *q = part + ((int64_t)o * stride + e) * d + c;
             const int64_t step = (int64_t)terms * stride * d;
-#pragma unroll 8
-            for (int z = 0; z < splits; ++z) {
-                const float4 v = *reinterpret_cast<const float4 *>(q + z * step);
-                acc.x += v.x;
-                acc.y += v.y;
-                acc.z += v.z;
-                acc.w += v.w;
+            for (int z0 = 0; z0 < splits; z0 += 4) {  // four loads in flight
+                float4 v[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    v[j] = z0 + j < splits
+                               ? *reinterpret_cast<const float4 *>(q + (z0 + j) * step)
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    acc.x += v[j].x;
+                    acc.y += v[j].y;
+                    acc.z += v[j].z;
+                    acc.w += v[j].w;
+                }
             }
         }
         *reinterpret_cast<float4 *>(dWr + i) = acc;
