@@ -19,15 +19,20 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kChunk = 16384;
 constexpr int kBlocks = 152 * 6;
-constexpr int kTable = 512;  // tensors per launch
+constexpr int kTable = 512;    // tensors per launch
+constexpr int kMapped = 1024;  // chunks with a map of their own
 
 struct Table {
     const void *src[kTable];
     void *dst[kTable];
     int64_t numel[kTable];
-    int end[kTable];  // chunks of tensors 0 .. i; bit 31 of none (chunks < 2^31)
+    int end[kTable];  // chunks of tensors 0 .. i
     uint8_t bf16[kTable];
     int n;
+    // where the table's chunks are few (most tensors one chunk): the tensor
+    // of every chunk, so that a block finds its own in one load
+    int mapped;
+    uint16_t tensor_of[kMapped];
 };
 
 __device__ __forceinline__ double block_sum(double v) {
@@ -49,6 +54,7 @@ struct Chunk {
 };
 __device__ __forceinline__ Chunk find_chunk(const Table &t, int c) {
     int lo = 0, hi = t.n - 1;
+    if (t.mapped) lo = hi = t.tensor_of[c];
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
         if (t.end[mid] > c) hi = mid; else lo = mid + 1;
@@ -125,17 +131,18 @@ norm_kernel(const __grid_constant__ Table t, int add, double *__restrict__ part)
 }
 
 __global__ void __launch_bounds__(kThreads)
-scale_kernel(const __grid_constant__ Table t, const double *__restrict__ part, float max_norm,
-             float *__restrict__ norm) {
+scale_kernel(const __grid_constant__ Table t, const double *__restrict__ part, int parts,
+             float max_norm, float *__restrict__ norm) {
     pdl_entry();
     double sum = 0.0;
-    for (int i = threadIdx.x; i < kBlocks; i += kThreads) sum += part[i];
+    for (int i = threadIdx.x; i < parts; i += kThreads) sum += part[i];
     const float nrm = (float)sqrt(block_sum(sum));
     if (blockIdx.x == 0 && threadIdx.x == 0) *norm = nrm;
     float coef = max_norm / (nrm + 1e-6f);
     coef = coef > 1.f ? 1.f : coef;  // a NaN norm stays NaN
     const int chunks = t.n ? t.end[t.n - 1] : 0;
-    for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
+    // from the last chunk: what launch 1 read last is still in the L2 cache
+    for (int c = chunks - 1 - (int)blockIdx.x; c >= 0; c -= gridDim.x) {
         const Chunk k = find_chunk(t, c);
         if (t.dst[k.tensor] == nullptr) continue;
         if (t.bf16[k.tensor])
@@ -147,6 +154,8 @@ scale_kernel(const __grid_constant__ Table t, const double *__restrict__ part, f
     }
 }
 
+int chunks_of(const moe_grad_t &g) { return (int)((g.numel + kChunk - 1) / kChunk); }
+
 void fill(const moe_grad_t *g, int64_t n, Table *t) {
     int end = 0;
     for (int64_t i = 0; i < n; ++i) {
@@ -154,10 +163,13 @@ void fill(const moe_grad_t *g, int64_t n, Table *t) {
         t->dst[i] = g[i].out;
         t->numel[i] = g[i].numel;
         t->bf16[i] = g[i].dtype == MOE_BF16;
-        end += (int)((g[i].numel + kChunk - 1) / kChunk);
+        const int first = end;
+        end += chunks_of(g[i]);
         t->end[i] = end;
+        for (int c = first; c < end && c < kMapped; ++c) t->tensor_of[c] = (uint16_t)i;
     }
     t->n = (int)n;
+    t->mapped = end <= kMapped;
 }
 
 }  // namespace
@@ -169,14 +181,22 @@ cudaError_t launch_clip(const moe_grad_t *g, int64_t n, float max_norm, float *n
                         cudaStream_t st) {
     Table t;
     double *part = static_cast<double *>(ws);
+    // as many blocks as the longest launch has chunks: each writes a partial sum
+    int most = 1;
+    for (int64_t i = 0; i < n; i += kTable) {
+        int c = 0;
+        for (int64_t j = i; j < std::min<int64_t>(n, i + kTable); ++j) c += chunks_of(g[j]);
+        most = std::max(most, c);
+    }
+    const int blocks = std::min(kBlocks, most);
     for (int64_t i = 0; i == 0 || i < n; i += kTable) {
         fill(g + i, std::min<int64_t>(kTable, n - i), &t);
-        launch_pdl(norm_kernel, dim3(kBlocks), dim3(kThreads), 0, st, t, i > 0 ? 1 : 0, part);
+        launch_pdl(norm_kernel, dim3(blocks), dim3(kThreads), 0, st, t, i > 0 ? 1 : 0, part);
     }
     for (int64_t i = 0; i == 0 || i < n; i += kTable) {
-        if (n > kTable || i > 0) fill(g + i, std::min<int64_t>(kTable, n - i), &t);
-        launch_pdl(scale_kernel, dim3(kBlocks), dim3(kThreads), 0, st, t, (const double *)part, max_norm,
-                   norm);
+        if (n > kTable) fill(g + i, std::min<int64_t>(kTable, n - i), &t);
+        launch_pdl(scale_kernel, dim3(blocks), dim3(kThreads), 0, st, t, (const double *)part, blocks,
+                   max_norm, norm);
     }
     return cudaGetLastError();
 }

@@ -1,5 +1,5 @@
-// experts_bwd_f32.cu -- gradient of the grouped SwiGLU experts on the CUDA
-// cores.
+// experts_bwd_f32.cu -- gradient of the grouped SwiGLU experts for fp32
+// activations, on the CUDA cores.
 //
 // For expert e and row r of its segment, with g, u = x[r] Wgu[e] recomputed,
 // s = sigmoid(g) and dh = dy[r] Wd[e]^T:
@@ -15,9 +15,8 @@
 namespace moe {
 namespace {
 
-using Tl = simt::Tile<64, 64, 16, 4, 4>;
-
-// Warp 0: s_off = offsets, s_tile[e] = sum over e' < e of ceil(count_e' / BM).
+// s_off = offsets; s_tile[e] = sum over e' < e of ceil(count_e' / BM).
+template <int BM>
 __device__ void tile_prefix(const int32_t *__restrict__ offsets, int E, int *s_off, int *s_tile) {
     for (int e = threadIdx.x; e <= E; e += blockDim.x) s_off[e] = offsets[e];
     __syncthreads();
@@ -26,7 +25,7 @@ __device__ void tile_prefix(const int32_t *__restrict__ offsets, int E, int *s_o
         const int per = (E + 31) / 32;
         const int e0 = min(E, lane * per), e1 = min(E, e0 + per);
         int local = 0;
-        for (int e = e0; e < e1; ++e) local += (s_off[e + 1] - s_off[e] + Tl::BM - 1) / Tl::BM;
+        for (int e = e0; e < e1; ++e) local += (s_off[e + 1] - s_off[e] + BM - 1) / BM;
         int incl = local;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -36,7 +35,7 @@ __device__ void tile_prefix(const int32_t *__restrict__ offsets, int E, int *s_o
         int run = incl - local;
         for (int e = e0; e < e1; ++e) {
             s_tile[e] = run;
-            run += (s_off[e + 1] - s_off[e] + Tl::BM - 1) / Tl::BM;
+            run += (s_off[e + 1] - s_off[e] + BM - 1) / BM;
         }
         if (lane == 31) s_tile[E] = incl;
     }
@@ -46,9 +45,10 @@ __device__ void tile_prefix(const int32_t *__restrict__ offsets, int E, int *s_o
 struct RowTile {
     int e, row0, rows;
 };
+template <int BM>
 __device__ __forceinline__ bool find_tile(const int32_t *offsets, int E, int *s_dyn, RowTile *t) {
     int *s_off = s_dyn, *s_tile = s_dyn + E + 1;
-    tile_prefix(offsets, E, s_off, s_tile);
+    tile_prefix<BM>(offsets, E, s_off, s_tile);
     const int g = blockIdx.x;
     if (g >= s_tile[E]) return false;
     int lo = 0, hi = E - 1;
@@ -57,128 +57,148 @@ __device__ __forceinline__ bool find_tile(const int32_t *offsets, int E, int *s_
         if (s_tile[mid] <= g) lo = mid; else hi = mid - 1;
     }
     t->e = lo;
-    t->row0 = s_off[lo] + (g - s_tile[lo]) * Tl::BM;
-    t->rows = min(Tl::BM, s_off[lo + 1] - t->row0);
+    t->row0 = s_off[lo] + (g - s_tile[lo]) * BM;
+    t->rows = min(BM, s_off[lo + 1] - t->row0);
     return true;
 }
 
-template <typename TA>
+// Dynamic shared memory: the product's stages, then 2 (E + 1) ints.
+template <typename Tl>
 __global__ void __launch_bounds__(simt::kThreads)
-rows_kernel(const TA *__restrict__ x, const TA *__restrict__ dy, const int32_t *__restrict__ offsets,
-            int E, const TA *__restrict__ Wgu, const TA *__restrict__ Wd, int d, int f,
-            TA *__restrict__ dgu) {
+rows_kernel(const float *__restrict__ x, const float *__restrict__ dy,
+            const int32_t *__restrict__ offsets, int E, const float *__restrict__ Wgu,
+            const float *__restrict__ Wd, int d, int f, float *__restrict__ dgu) {
     pdl_entry();
-    extern __shared__ int s_dyn[];
-    __shared__ Tl::Smem sm;
+    extern __shared__ __align__(16) float smem[];
     RowTile t;
-    if (!find_tile(offsets, E, s_dyn, &t)) return;
+    if (!find_tile<Tl::BM>(offsets, E, reinterpret_cast<int *>(smem) + Tl::SMEM_BYTES / 4, &t)) return;
     const int n0 = blockIdx.y * Tl::BN;
-    const TA *xr = x + (int64_t)t.row0 * d, *yr = dy + (int64_t)t.row0 * d;
-    const TA *W = Wgu + (int64_t)t.e * d * 2 * f, *Wt = Wd + (int64_t)t.e * f * d;
+    const float *xr = x + (int64_t)t.row0 * d, *yr = dy + (int64_t)t.row0 * d;
+    const float *W = Wgu + (int64_t)t.e * d * 2 * f, *Wt = Wd + (int64_t)t.e * f * d;
     float g[Tl::TM][Tl::TN], u[Tl::TM][Tl::TN], h[Tl::TM][Tl::TN];
     Tl::zero(g);
     Tl::zero(u);
     Tl::zero(h);
-    auto la = [&](const TA *a) {
-        return [=](int m, int k) { return m < t.rows ? Act<TA>::to_f(a[(int64_t)m * d + k]) : 0.f; };
+    auto rows_of = [&](const float *a) {
+        return [=](int m, int k) { return m < t.rows ? a + (int64_t)m * d + k : nullptr; };
     };
-    Tl::product<true, false>(sm, d, la(xr), [&](int k, int n) {
-        return n0 + n < f ? Act<TA>::to_f(W[(int64_t)k * 2 * f + n0 + n]) : 0.f; }, g);
-    Tl::product<true, false>(sm, d, la(xr), [&](int k, int n) {
-        return n0 + n < f ? Act<TA>::to_f(W[(int64_t)k * 2 * f + f + n0 + n]) : 0.f; }, u);
-    Tl::product<true, true>(sm, d, la(yr), [&](int k, int n) {
-        return n0 + n < f ? Act<TA>::to_f(Wt[(int64_t)(n0 + n) * d + k]) : 0.f; }, h);
+    auto cols_of = [&](const float *b) {
+        return [=](int k, int n) { return n0 + n < f ? b + (int64_t)k * 2 * f + n0 + n : nullptr; };
+    };
+    Tl::template product<true, false, true>(smem, d, rows_of(xr), cols_of(W), g);
+    Tl::template product<true, false, true>(smem, d, rows_of(xr), cols_of(W + f), u);
+    Tl::template product<true, true, true>(smem, d, rows_of(yr), [=](int k, int n) {
+        return n0 + n < f ? Wt + (int64_t)(n0 + n) * d + k : nullptr; }, h);
 #pragma unroll
     for (int i = 0; i < Tl::TM; ++i) {
-        const int m = Tl::row(i);
+        const int m = Tl::template row<true>(i);
         if (m >= t.rows) continue;
-        TA *o = dgu + (int64_t)(t.row0 + m) * 2 * f;
+        float *o = dgu + (int64_t)(t.row0 + m) * 2 * f;
 #pragma unroll
         for (int j = 0; j < Tl::TN; ++j) {
-            const int n = n0 + Tl::col(j);
+            const int n = n0 + Tl::template col<true>(j);
             if (n >= f) continue;
             const float s = 1.f / (1.f + expf(-g[i][j]));
-            o[n] = Act<TA>::from_f(h[i][j] * u[i][j] * s * (1.f + g[i][j] * (1.f - s)));
-            o[f + n] = Act<TA>::from_f(h[i][j] * g[i][j] * s);
+            o[n] = h[i][j] * u[i][j] * s * (1.f + g[i][j] * (1.f - s));
+            o[f + n] = h[i][j] * g[i][j] * s;
         }
     }
 }
 
-template <typename TA>
+template <typename Tl>
 __global__ void __launch_bounds__(simt::kThreads)
-dx_kernel(const TA *__restrict__ dgu, const int32_t *__restrict__ offsets, int E,
-          const TA *__restrict__ Wgu, int d, int f, TA *__restrict__ dx) {
+dx_kernel(const float *__restrict__ dgu, const int32_t *__restrict__ offsets, int E,
+          const float *__restrict__ Wgu, int d, int f, float *__restrict__ dx) {
     pdl_entry();
-    extern __shared__ int s_dyn[];
-    __shared__ Tl::Smem sm;
+    extern __shared__ __align__(16) float smem[];
     RowTile t;
-    if (!find_tile(offsets, E, s_dyn, &t)) return;
+    if (!find_tile<Tl::BM>(offsets, E, reinterpret_cast<int *>(smem) + Tl::SMEM_BYTES / 4, &t)) return;
     const int n0 = blockIdx.y * Tl::BN, K = 2 * f;
-    const TA *a = dgu + (int64_t)t.row0 * K, *W = Wgu + (int64_t)t.e * d * K;
+    const float *a = dgu + (int64_t)t.row0 * K, *W = Wgu + (int64_t)t.e * d * K;
     float acc[Tl::TM][Tl::TN];
     Tl::zero(acc);
-    Tl::product<true, true>(
-        sm, K, [&](int m, int k) { return m < t.rows ? Act<TA>::to_f(a[(int64_t)m * K + k]) : 0.f; },
-        [&](int k, int n) { return n0 + n < d ? Act<TA>::to_f(W[(int64_t)(n0 + n) * K + k]) : 0.f; },
-        acc);
+    Tl::template product<true, true, true>(
+        smem, K, [=](int m, int k) { return m < t.rows ? a + (int64_t)m * K + k : nullptr; },
+        [=](int k, int n) { return n0 + n < d ? W + (int64_t)(n0 + n) * K + k : nullptr; }, acc);
 #pragma unroll
     for (int i = 0; i < Tl::TM; ++i)
 #pragma unroll
         for (int j = 0; j < Tl::TN; ++j) {
-            const int m = Tl::row(i), n = n0 + Tl::col(j);
-            if (m < t.rows && n < d) dx[(int64_t)(t.row0 + m) * d + n] = Act<TA>::from_f(acc[i][j]);
+            const int m = Tl::template row<true>(i), n = n0 + Tl::template col<true>(j);
+            if (m < t.rows && n < d) dx[(int64_t)(t.row0 + m) * d + n] = acc[i][j];
         }
 }
 
-// dW[e] [M][N] = A^T B over the rows of expert e's segment (A [P][M], B [P][N]).
-template <typename TA>
+// dW[e] [M][N] = A^T B over the rows of expert e's segment (A [P][M], B
+// [P][N]), for two such products in one launch: blocks below `first` are the
+// first one's tiles.
+struct WeightProduct {
+    const float *A, *B;
+    int M, N;
+    float *dW;
+};
+template <typename Tl>
 __global__ void __launch_bounds__(simt::kThreads)
-weights_kernel(const TA *__restrict__ A, const TA *__restrict__ B,
-               const int32_t *__restrict__ offsets, int M, int N, TA *__restrict__ dW) {
+weights_kernel(WeightProduct p0, WeightProduct p1, int first, const int32_t *__restrict__ offsets) {
     pdl_entry();
-    __shared__ Tl::Smem sm;
-    const int e = blockIdx.z, m0 = blockIdx.y * Tl::BM, n0 = blockIdx.x * Tl::BN;
+    extern __shared__ __align__(16) float smem[];
+    const bool second = (int)blockIdx.x >= first;
+    const WeightProduct &p = second ? p1 : p0;
+    const int e = blockIdx.y, b = (int)blockIdx.x - (second ? first : 0);
+    const int nt = (p.N + Tl::BN - 1) / Tl::BN;
+    const int m0 = b / nt * Tl::BM, n0 = b % nt * Tl::BN, M = p.M, N = p.N;
     const int r0 = offsets[e], rows = offsets[e + 1] - r0;
-    const TA *a = A + (int64_t)r0 * M, *b = B + (int64_t)r0 * N;
+    const float *A = p.A + (int64_t)r0 * M, *B = p.B + (int64_t)r0 * N;
     float acc[Tl::TM][Tl::TN];
     Tl::zero(acc);
-    Tl::product<false, false>(
-        sm, rows, [&](int m, int k) { return m0 + m < M ? Act<TA>::to_f(a[(int64_t)k * M + m0 + m]) : 0.f; },
-        [&](int k, int n) { return n0 + n < N ? Act<TA>::to_f(b[(int64_t)k * N + n0 + n]) : 0.f; }, acc);
-    TA *o = dW + (int64_t)e * M * N;
+    Tl::template product<false, false, false>(
+        smem, rows, [=](int m, int k) { return m0 + m < M ? A + (int64_t)k * M + m0 + m : nullptr; },
+        [=](int k, int n) { return n0 + n < N ? B + (int64_t)k * N + n0 + n : nullptr; }, acc);
+    float *o = p.dW + (int64_t)e * M * N;
 #pragma unroll
     for (int i = 0; i < Tl::TM; ++i)
 #pragma unroll
         for (int j = 0; j < Tl::TN; ++j) {
-            const int m = m0 + Tl::row(i), n = n0 + Tl::col(j);
-            if (m < M && n < N) o[(int64_t)m * N + n] = Act<TA>::from_f(acc[i][j]);
+            const int m = m0 + Tl::template row<false>(i), n = n0 + Tl::template col<false>(j);
+            if (m < M && n < N) o[(int64_t)m * N + n] = acc[i][j];
         }
 }
 
-template <typename TA>
-cudaError_t launch_t(const Shape &s, const ExpertsBwd &a, cudaStream_t st) {
-    const TA *x = static_cast<const TA *>(a.x_perm), *dy = static_cast<const TA *>(a.dy_perm);
-    const TA *Wgu = static_cast<const TA *>(a.Wgu), *Wd = static_cast<const TA *>(a.Wd);
-    TA *dgu = static_cast<TA *>(a.ws);
-    const unsigned mt = (unsigned)((s.P() + Tl::BM - 1) / Tl::BM + s.E);
-    const size_t sh = sizeof(int) * (2 * (size_t)s.E + 2);
-    auto tiles = [](int n) { return (unsigned)((n + Tl::BN - 1) / Tl::BN); };
+template <typename Tl> cudaError_t launch_t(const Shape &s, const ExpertsBwd &a, cudaStream_t st) {
+    const float *x = static_cast<const float *>(a.x_perm), *dy = static_cast<const float *>(a.dy_perm);
+    const float *Wgu = static_cast<const float *>(a.Wgu), *Wd = static_cast<const float *>(a.Wd);
+    float *dgu = static_cast<float *>(a.ws);
+    const int64_t P = s.P();
+    const unsigned mt = (unsigned)((P + Tl::BM - 1) / Tl::BM + (P < s.E ? P : s.E));
+    const size_t prefix = sizeof(int) * (2 * (size_t)s.E + 2);
+    auto tiles = [](int n, int b) { return (unsigned)((n + b - 1) / b); };
     const dim3 block(simt::kThreads);
-    launch_pdl(rows_kernel<TA>, dim3(mt, tiles(s.f)), block, sh, st, x, dy, a.offsets, s.E, Wgu, Wd,
-               s.d, s.f, dgu);
-    launch_pdl(dx_kernel<TA>, dim3(mt, tiles(s.d)), block, sh, st, (const TA *)dgu, a.offsets, s.E,
-               Wgu, s.d, s.f, static_cast<TA *>(a.dx_perm));
-    launch_pdl(weights_kernel<TA>, dim3(tiles(s.d), tiles(s.f), s.E), block, 0, st,
-               static_cast<const TA *>(a.h_perm), dy, a.offsets, s.f, s.d, static_cast<TA *>(a.dWd));
-    launch_pdl(weights_kernel<TA>, dim3(tiles(2 * s.f), tiles(s.d), s.E), block, 0, st, x,
-               (const TA *)dgu, a.offsets, s.d, 2 * s.f, static_cast<TA *>(a.dWgu));
+    cudaError_t err;
+    if ((err = simt::opt_in(rows_kernel<Tl>, Tl::SMEM_BYTES + 16 * 1024)) != cudaSuccess ||
+        (err = simt::opt_in(dx_kernel<Tl>, Tl::SMEM_BYTES + 16 * 1024)) != cudaSuccess ||
+        (err = simt::opt_in(weights_kernel<Tl>, Tl::SMEM_BYTES)) != cudaSuccess)
+        return err;
+    launch_pdl(rows_kernel<Tl>, dim3(mt, tiles(s.f, Tl::BN)), block, Tl::SMEM_BYTES + prefix, st, x, dy,
+               a.offsets, s.E, Wgu, Wd, s.d, s.f, dgu);
+    launch_pdl(dx_kernel<Tl>, dim3(mt, tiles(s.d, Tl::BN)), block, Tl::SMEM_BYTES + prefix, st,
+               (const float *)dgu, a.offsets, s.E, Wgu, s.d, s.f, static_cast<float *>(a.dx_perm));
+    const WeightProduct wd = {static_cast<const float *>(a.h_perm), dy, s.f, s.d,
+                              static_cast<float *>(a.dWd)};
+    const WeightProduct wg = {x, dgu, s.d, 2 * s.f, static_cast<float *>(a.dWgu)};
+    auto count = [&](const WeightProduct &w) { return tiles(w.M, Tl::BM) * tiles(w.N, Tl::BN); };
+    launch_pdl(weights_kernel<Tl>, dim3(count(wd) + count(wg), s.E), block, Tl::SMEM_BYTES, st, wd, wg,
+               (int)count(wd), a.offsets);
     return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_experts_backward_f32(const Shape &s, const ExpertsBwd &a, cudaStream_t st) {
-    return launch_t<float>(s, a, st);
+    using L = simt::Large;
+    const int64_t row_tiles = (s.P() + L::BM - 1) / L::BM;
+    // the row products have the fewest tiles
+    const bool large = row_tiles * ((s.d + L::BN - 1) / L::BN) >= 2 * 152;
+    return large ? launch_t<simt::Large>(s, a, st) : launch_t<simt::Small>(s, a, st);
 }
 
 }  // namespace moe

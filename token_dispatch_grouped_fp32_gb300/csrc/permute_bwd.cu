@@ -14,8 +14,13 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+// Both kernels: a group of TPT threads (a warp or the block) per token, each
+// thread holding U 16-byte vectors of the token's row, TPT apart; SG slots'
+// rows are loaded at once.  Rows of more than TPT*U vectors are walked in
+// chunks.  The token's own row is read once, whatever k, and a slot's dot
+// product is summed over each warp, then over the group's warps in order.
+constexpr int kThreads = 128;
+constexpr int kMaxK = 32;
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -23,119 +28,203 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// One warp per pair: the token's row of dout times the pair's weight, to the
-// pair's row; DOT: its dot product with the row of y_perm on the way.
-template <typename TA, bool DOT>
+// Per-warp sums of the slots' dot products.
+struct Dots {
+    float s[kThreads / 32][kMaxK];
+};
+__device__ __forceinline__ void dots_clear(Dots &d) { d.s[threadIdx.x >> 5][threadIdx.x & 31] = 0.f; }
+__device__ __forceinline__ void dots_add(Dots &d, int j, float part) {
+    part = warp_sum(part);
+    if ((threadIdx.x & 31) == 0) d.s[threadIdx.x >> 5][j] += part;
+}
+// dw[j] of the group's token, by its thread j (all threads of the group call).
+template <int TPT> __device__ __forceinline__ void dots_store(const Dots &d, int k, float *dw) {
+    if (TPT == 32) __syncwarp();
+    else __syncthreads();
+    const int j = threadIdx.x % TPT, w0 = threadIdx.x / TPT * (TPT / 32);
+    if (j >= k) return;
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < TPT / 32; ++w) s += d.s[w0 + w][j];
+    dw[j] = s;
+}
+
+// dst[pos] = w * src row of every slot; DOT: dw = <src row, y_perm[pos]>.
+template <typename TA, int TPT, int U, int SG, bool DOT>
 __global__ void __launch_bounds__(kThreads)
 scatter_rows_kernel(const TA *__restrict__ src, const TA *__restrict__ y_perm,
-                    const int32_t *__restrict__ pos, const float *__restrict__ w, int64_t P, int k,
+                    const int32_t *__restrict__ pos, const float *__restrict__ w, int64_t T, int k,
                     int d, TA *__restrict__ dst, float *__restrict__ dw) {
     pdl_entry();
     constexpr int EPV = 16 / sizeof(TA);
-    const int lane = threadIdx.x & 31;
-    const int64_t q = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (q >= P) return;
-    const int row = pos[q];
-    if (row < 0) {
-        if (DOT && lane == 0) dw[q] = 0.f;
-        return;
-    }
-    const TA *s = src + q / k * d;
-    const float wq = w ? w[q] : 1.f;
-    float dot = 0.f;
-    for (int v = lane; v < d / EPV; v += 32) {
-        float g[EPV], y[EPV];
-        unpack16(ldg16(s + (int64_t)v * EPV), g, static_cast<const TA *>(nullptr));
-        if (DOT) {
-            unpack16(ldg16(y_perm + (int64_t)row * d + (int64_t)v * EPV), y,
-                     static_cast<const TA *>(nullptr));
-#pragma unroll
-            for (int i = 0; i < EPV; ++i) dot = fmaf(g[i], y[i], dot);
-        }
-#pragma unroll
-        for (int i = 0; i < EPV; ++i) g[i] *= wq;
-        stg16(dst + (int64_t)row * d + (int64_t)v * EPV, pack16(g, static_cast<const TA *>(nullptr)));
-    }
+    __shared__ Dots dots;
+    const int64_t t = (int64_t)blockIdx.x * (kThreads / TPT) + threadIdx.x / TPT;
+    const int nvec = d / EPV;
     if (DOT) {
-        dot = warp_sum(dot);
-        if (lane == 0) dw[q] = dot;
+        dots_clear(dots);
+        __syncwarp();
     }
+    if (t >= T) return;  // whole groups; TPT = block: the block
+    for (int v0 = threadIdx.x % TPT; v0 - (int)(threadIdx.x % TPT) < nvec; v0 += TPT * U) {
+        uint4 g[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (v0 + u * TPT < nvec) g[u] = ldg16(src + t * d + (int64_t)(v0 + u * TPT) * EPV);
+        for (int j0 = 0; j0 < k; j0 += SG) {
+            int row[SG];
+            float wj[SG];
+            uint4 y[SG][U];
+#pragma unroll
+            for (int s = 0; s < SG; ++s) {
+                row[s] = j0 + s < k ? __ldg(pos + t * k + j0 + s) : -1;
+                wj[s] = w && j0 + s < k ? __ldg(w + t * k + j0 + s) : 1.f;
+            }
+            if (DOT)
+#pragma unroll
+                for (int s = 0; s < SG; ++s)
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        if (row[s] >= 0 && v0 + u * TPT < nvec)
+                            y[s][u] = ldg16(y_perm + (int64_t)row[s] * d + (int64_t)(v0 + u * TPT) * EPV);
+#pragma unroll
+            for (int s = 0; s < SG; ++s) {
+                if (row[s] < 0) continue;  // the same for the whole group
+                float part = 0.f;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (v0 + u * TPT >= nvec) continue;
+                    float a[EPV], b[EPV];
+                    unpack16(g[u], a, static_cast<const TA *>(nullptr));
+                    if (DOT) {
+                        unpack16(y[s][u], b, static_cast<const TA *>(nullptr));
+#pragma unroll
+                        for (int i = 0; i < EPV; ++i) part = fmaf(a[i], b[i], part);
+                    }
+#pragma unroll
+                    for (int i = 0; i < EPV; ++i) a[i] *= wj[s];
+                    stg16(dst + (int64_t)row[s] * d + (int64_t)(v0 + u * TPT) * EPV,
+                          pack16(a, static_cast<const TA *>(nullptr)));
+                }
+                if (DOT) dots_add(dots, j0 + s, part);
+            }
+        }
+    }
+    if (DOT) dots_store<TPT>(dots, k, dw + t * k);
 }
 
-// One warp per token: the weighted sum of its rows of dx_perm, and each
-// row's dot product with the token's row of x (the partial of slot j is
-// summed over the warp per chunk and kept by lane j).
-template <typename TA>
+// dx = the sum of w * row over a token's slots, dw = <x row, row>.
+template <typename TA, int TPT, int U, int SG>
 __global__ void __launch_bounds__(kThreads)
 gather_rows_scaled_kernel(const TA *__restrict__ dx_perm, const int32_t *__restrict__ pos,
                           const float *__restrict__ w, const TA *__restrict__ x, int64_t T, int k,
                           int d, TA *__restrict__ dx, float *__restrict__ dw) {
     pdl_entry();
     constexpr int EPV = 16 / sizeof(TA);
-    const int lane = threadIdx.x & 31;
-    const int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (t >= T) return;
-    int my_pos = -1;
-    float my_w = 0.f, my_dot = 0.f;
-    if (lane < k) {
-        my_pos = pos[t * k + lane];
-        my_w = w[t * k + lane];
-    }
+    __shared__ Dots dots;
+    const int64_t t = (int64_t)blockIdx.x * (kThreads / TPT) + threadIdx.x / TPT;
     const int nvec = d / EPV;
-    for (int v0 = 0; v0 < nvec; v0 += 32) {
-        const int v = v0 + lane;
-        float acc[EPV], xv[EPV];
+    dots_clear(dots);
+    __syncwarp();
+    if (t >= T) return;  // whole groups; TPT = block: the block
+    for (int v0 = threadIdx.x % TPT; v0 - (int)(threadIdx.x % TPT) < nvec; v0 += TPT * U) {
+        uint4 xv[U];
+        float acc[U][EPV];
 #pragma unroll
-        for (int i = 0; i < EPV; ++i) acc[i] = xv[i] = 0.f;
-        if (v < nvec)
-            unpack16(ldg16(x + t * d + (int64_t)v * EPV), xv, static_cast<const TA *>(nullptr));
-        for (int j = 0; j < k; ++j) {
-            const int row = __shfl_sync(0xffffffffu, my_pos, j);
-            const float wj = __shfl_sync(0xffffffffu, my_w, j);
-            if (row < 0) continue;  // warp-uniform
-            float part = 0.f;
-            if (v < nvec) {
-                float r[EPV];
-                unpack16(ldg16(dx_perm + (int64_t)row * d + (int64_t)v * EPV), r,
-                         static_cast<const TA *>(nullptr));
+        for (int u = 0; u < U; ++u) {
+            if (v0 + u * TPT < nvec) xv[u] = ldg16(x + t * d + (int64_t)(v0 + u * TPT) * EPV);
 #pragma unroll
-                for (int i = 0; i < EPV; ++i) {
-                    acc[i] = fmaf(wj, r[i], acc[i]);
-                    part = fmaf(xv[i], r[i], part);
-                }
-            }
-            part = warp_sum(part);
-            if (lane == j) my_dot += part;
+            for (int i = 0; i < EPV; ++i) acc[u][i] = 0.f;
         }
-        if (v < nvec)
-            stg16(dx + t * d + (int64_t)v * EPV, pack16(acc, static_cast<const TA *>(nullptr)));
+        for (int j0 = 0; j0 < k; j0 += SG) {
+            int row[SG];
+            float wj[SG];
+            uint4 r[SG][U];
+#pragma unroll
+            for (int s = 0; s < SG; ++s) {
+                row[s] = j0 + s < k ? __ldg(pos + t * k + j0 + s) : -1;
+                wj[s] = j0 + s < k ? __ldg(w + t * k + j0 + s) : 0.f;
+            }
+#pragma unroll
+            for (int s = 0; s < SG; ++s)
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (row[s] >= 0 && v0 + u * TPT < nvec)
+                        r[s][u] = ldg16(dx_perm + (int64_t)row[s] * d + (int64_t)(v0 + u * TPT) * EPV);
+#pragma unroll
+            for (int s = 0; s < SG; ++s) {
+                if (row[s] < 0) continue;  // the same for the whole group
+                float part = 0.f;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (v0 + u * TPT >= nvec) continue;
+                    float a[EPV], b[EPV];
+                    unpack16(xv[u], a, static_cast<const TA *>(nullptr));
+                    unpack16(r[s][u], b, static_cast<const TA *>(nullptr));
+#pragma unroll
+                    for (int i = 0; i < EPV; ++i) {
+                        part = fmaf(a[i], b[i], part);
+                        acc[u][i] = fmaf(wj[s], b[i], acc[u][i]);
+                    }
+                }
+                dots_add(dots, j0 + s, part);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (v0 + u * TPT < nvec)
+                stg16(dx + t * d + (int64_t)(v0 + u * TPT) * EPV,
+                      pack16(acc[u], static_cast<const TA *>(nullptr)));
     }
-    if (lane < k) dw[t * k + lane] = my_dot;
+    dots_store<TPT>(dots, k, dw + t * k);
 }
 
-template <typename TA>
-cudaError_t launch_scatter_t(const Shape &s, const void *src, const void *y_perm,
+unsigned blocks(int64_t T, int tpt) {
+    const int per = kThreads / tpt;
+    return (unsigned)((T + per - 1) / per);
+}
+
+template <typename TA, int TPT, int U, int SG>
+cudaError_t launch_scatter_v(const Shape &s, const void *src, const void *y_perm,
                              const int32_t *pos, const float *w, void *dst, float *dw,
                              cudaStream_t st) {
-    const dim3 grid((unsigned)((s.P() + kWarps - 1) / kWarps));
     const TA *x = static_cast<const TA *>(src), *y = static_cast<const TA *>(y_perm);
     TA *o = static_cast<TA *>(dst);
+    const dim3 grid(blocks(s.T, TPT));
     if (dw)
-        launch_pdl(scatter_rows_kernel<TA, true>, grid, dim3(kThreads), 0, st, x, y, pos, w, s.P(),
-                   s.k, s.d, o, dw);
+        launch_pdl(scatter_rows_kernel<TA, TPT, U, SG, true>, grid, dim3(kThreads), 0, st, x, y, pos,
+                   w, s.T, s.k, s.d, o, dw);
     else
-        launch_pdl(scatter_rows_kernel<TA, false>, grid, dim3(kThreads), 0, st, x, y, pos, w,
-                   s.P(), s.k, s.d, o, dw);
+        launch_pdl(scatter_rows_kernel<TA, TPT, U, SG, false>, grid, dim3(kThreads), 0, st, x, y, pos,
+                   w, s.T, s.k, s.d, o, dw);
     return cudaGetLastError();
 }
 
-template <typename TA>
-cudaError_t launch_gather_t(const Shape &s, const void *dx_perm, const int32_t *pos,
+template <typename TA, int TPT, int U, int SG>
+cudaError_t launch_gather_v(const Shape &s, const void *dx_perm, const int32_t *pos,
                             const float *w, const void *x, void *dx, float *dw, cudaStream_t st) {
-    launch_pdl(gather_rows_scaled_kernel<TA>, dim3((unsigned)((s.T + kWarps - 1) / kWarps)),
-               dim3(kThreads), 0, st, static_cast<const TA *>(dx_perm), pos, w,
-               static_cast<const TA *>(x), s.T, s.k, s.d, static_cast<TA *>(dx), dw);
+    launch_pdl(gather_rows_scaled_kernel<TA, TPT, U, SG>, dim3(blocks(s.T, TPT)), dim3(kThreads), 0, st,
+               static_cast<const TA *>(dx_perm), pos, w, static_cast<const TA *>(x), s.T, s.k, s.d,
+               static_cast<TA *>(dx), dw);
     return cudaGetLastError();
+}
+
+// Short rows: a warp per token; else a block, with as many vectors a thread
+// as the row needs (up to 4: then 2 slots at a time keep the registers).
+template <typename TA, typename... Args>
+cudaError_t launch_scatter_t(const Shape &s, Args... args) {
+    const int nvec = s.d / (16 / (int)sizeof(TA));
+    if (nvec <= 32) return launch_scatter_v<TA, 32, 1, 4>(s, args...);
+    if (nvec <= 128) return launch_scatter_v<TA, 128, 1, 4>(s, args...);
+    if (nvec <= 256) return launch_scatter_v<TA, 128, 2, 4>(s, args...);
+    return launch_scatter_v<TA, 128, 4, 2>(s, args...);
+}
+template <typename TA, typename... Args>
+cudaError_t launch_gather_t(const Shape &s, Args... args) {
+    const int nvec = s.d / (16 / (int)sizeof(TA));
+    if (nvec <= 32) return launch_gather_v<TA, 32, 1, 4>(s, args...);
+    if (nvec <= 128) return launch_gather_v<TA, 128, 1, 4>(s, args...);
+    if (nvec <= 256) return launch_gather_v<TA, 128, 2, 4>(s, args...);
+    return launch_gather_v<TA, 128, 4, 2>(s, args...);
 }
 
 }  // namespace

@@ -28,7 +28,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxTokenBlocks = 152 * 8;
 constexpr int kSplitCols = 4 * kThreads;  // elements of Wr per block
-using Tl = simt::Tile<64, 64, 16, 4, 4>;
+using Tl = simt::Large;
 
 template <bool MAX> __device__ __forceinline__ float warp_all(float v) {
 #pragma unroll
@@ -62,7 +62,8 @@ struct TermsArgs {
     const float *w, *dw;
     int64_t T;
     int E, k, renorm;
-    float *dl, *bias_part;  // [T][E]; [token blocks][E]
+    float *dl, *bias_part;  // [T][E]; [token blocks][E8]
+    float *dl8;  // fp32 x only: dl in rows of E8 columns
     // bf16 x only (dl4 != nullptr): the terms [T][4*E8], Wr [E][d] and its
     // terms [3*E8][d], and the segment boundaries of the two products
     __nv_bfloat16 *dl4, *W3;
@@ -150,6 +151,7 @@ __global__ void __launch_bounds__(kThreads) terms_kernel(TermsArgs a, DevStatus 
                 if (4 * v + 2 < a.E) o[4 * v + 2] = r.z;
                 if (4 * v + 3 < a.E) o[4 * v + 3] = r.w;
             }
+            if (a.dl8) *reinterpret_cast<float4 *>(a.dl8 + t * E8 + 4 * v) = r;
             uint2 hi = make_uint2(0, 0), mid = hi, lo = hi;
             if (r.x != 0.f || r.y != 0.f || r.z != 0.f || r.w != 0.f) {  // mostly zeros when renormalised
                 float4 *acc = reinterpret_cast<float4 *>(sum + 4 * v);
@@ -179,17 +181,17 @@ __global__ void __launch_bounds__(kThreads) terms_kernel(TermsArgs a, DevStatus 
         __syncwarp();
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += kThreads) {
+    for (int e = threadIdx.x; e < E8; e += kThreads) {
         float s = 0.f;
         for (int i = 0; i < kWarps; ++i) s += sh[(kWarps + i) * E8 + e];
-        a.bias_part[(int64_t)blockIdx.x * a.E + e] = s;
+        a.bias_part[(int64_t)blockIdx.x * E8 + e] = s;
     }
 }
 
 // dWr[e][c] = the sum over splits and terms of part[s][b*stride + e][c] (small
-// terms first); the blocks after those: a warp per expert sums its bias.
+// terms first); the blocks after those sum the bias.
 __global__ void __launch_bounds__(kThreads)
-sum_kernel(const float *__restrict__ part, int splits, int terms, int stride, int E, int d,
+sum_kernel(const float *__restrict__ part, int splits, int terms, int stride, int E, int E8, int d,
            float *__restrict__ dWr, const float *__restrict__ bias_part, int token_blocks,
            int weight_blocks, float *__restrict__ dbias) {
     pdl_entry();
@@ -222,58 +224,71 @@ sum_kernel(const float *__restrict__ part, int splits, int terms, int stride, in
         *reinterpret_cast<float4 *>(dWr + i) = acc;
         return;
     }
-    const int e = ((int)blockIdx.x - weight_blocks) * kWarps + (threadIdx.x >> 5);
-    if (!dbias || e >= E) return;
-    const int lane = threadIdx.x & 31;
-    float s = 0.f;
-#pragma unroll 8
-    for (int b = lane; b < token_blocks; b += 32) s += bias_part[(int64_t)b * E + e];
-    s = warp_all<false>(s);
-    if (lane == 0) dbias[e] = s;
+    // four experts a block, all threads over the token blocks
+    __shared__ float4 s_part[kThreads];
+    const int e = 4 * ((int)blockIdx.x - weight_blocks);
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 5
+    for (int b = threadIdx.x; b < token_blocks; b += kThreads) {
+        const float4 v = *reinterpret_cast<const float4 *>(bias_part + (int64_t)b * E8 + e);
+        s.x += v.x;
+        s.y += v.y;
+        s.z += v.z;
+        s.w += v.w;
+    }
+    s_part[threadIdx.x] = s;
+    __syncthreads();
+    const int c = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (c >= 4 || e + c >= E) return;
+    float t = 0.f;
+    for (int i = lane; i < kThreads; i += 32) t += reinterpret_cast<const float *>(s_part)[4 * i + c];
+    t = warp_all<false>(t);
+    if (lane == 0) dbias[e + c] = t;
 }
 
 // ------------------------- fp32 x, on the CUDA cores ------------------------
+// Over dl8, the rows of dl padded to E8 columns.
 // part[split][e][c]: the sum over the tokens of one split.
 __global__ void __launch_bounds__(simt::kThreads)
-dwr_kernel(const float *__restrict__ dl, const float *__restrict__ x, int64_t T, int E, int d,
-           int tokens, float *__restrict__ part) {
+dwr_kernel(const float *__restrict__ dl8, const float *__restrict__ x, int64_t T, int E, int E8,
+           int d, int tokens, float *__restrict__ part) {
     pdl_entry();
-    __shared__ Tl::Smem sm;
+    extern __shared__ __align__(16) float smem[];
     const int n0 = blockIdx.x * Tl::BN, e0 = blockIdx.y * Tl::BM;
     const int64_t t0 = (int64_t)blockIdx.z * tokens;
     const int K = (int)min((int64_t)tokens, T - t0);
     float acc[Tl::TM][Tl::TN];
     Tl::zero(acc);
-    Tl::product<false, false>(
-        sm, K, [&](int m, int k) { return e0 + m < E ? dl[(t0 + k) * E + e0 + m] : 0.f; },
-        [&](int k, int n) { return n0 + n < d ? x[(t0 + k) * d + n0 + n] : 0.f; }, acc);
+    Tl::product<false, false, false>(
+        smem, K, [=](int m, int k) { return e0 + m < E8 ? dl8 + (t0 + k) * E8 + e0 + m : nullptr; },
+        [=](int k, int n) { return n0 + n < d ? x + (t0 + k) * d + n0 + n : nullptr; }, acc);
 #pragma unroll
     for (int i = 0; i < Tl::TM; ++i)
 #pragma unroll
         for (int j = 0; j < Tl::TN; ++j) {
-            const int e = e0 + Tl::row(i), n = n0 + Tl::col(j);
+            const int e = e0 + Tl::row<false>(i), n = n0 + Tl::col<false>(j);
             if (e < E && n < d) part[((int64_t)blockIdx.z * E + e) * d + n] = acc[i][j];
         }
 }
 
 __global__ void __launch_bounds__(simt::kThreads)
-route_dx_kernel(const float *__restrict__ dl, const float *__restrict__ Wr, const float *dx_in,
-                int64_t T, int E, int d, float *dx) {
+route_dx_kernel(const float *__restrict__ dl8, const float *__restrict__ Wr, const float *dx_in,
+                int64_t T, int E, int E8, int d, float *dx) {
     pdl_entry();
-    __shared__ Tl::Smem sm;
+    extern __shared__ __align__(16) float smem[];
     const int64_t t0 = (int64_t)blockIdx.x * Tl::BM;
     const int n0 = blockIdx.y * Tl::BN;
     float acc[Tl::TM][Tl::TN];
     Tl::zero(acc);
-    Tl::product<true, false>(
-        sm, E, [&](int m, int k) { return t0 + m < T ? dl[(t0 + m) * E + k] : 0.f; },
-        [&](int k, int n) { return n0 + n < d ? Wr[(int64_t)k * d + n0 + n] : 0.f; }, acc);
+    Tl::product<true, false, false>(
+        smem, E8, [=](int m, int k) { return t0 + m < T ? dl8 + (t0 + m) * E8 + k : nullptr; },
+        [=](int k, int n) { return k < E && n0 + n < d ? Wr + (int64_t)k * d + n0 + n : nullptr; }, acc);
 #pragma unroll
     for (int i = 0; i < Tl::TM; ++i)
 #pragma unroll
         for (int j = 0; j < Tl::TN; ++j) {
-            const int64_t t = t0 + Tl::row(i);
-            const int n = n0 + Tl::col(j);
+            const int64_t t = t0 + Tl::row<true>(i);
+            const int n = n0 + Tl::col<false>(j);
             if (t >= T || n >= d) continue;
             const float v = acc[i][j];
             dx[t * d + n] = dx_in ? v + dx_in[t * d + n] : v;
@@ -284,7 +299,7 @@ route_dx_kernel(const float *__restrict__ dl, const float *__restrict__ Wr, cons
 struct Plan {
     int E8, terms, token_blocks;
     int splits, tokens;  // splits of the token axis in dWr's sum, tokens each
-    size_t dl4, W3, all, split_at, bias, part, total;  // workspace offsets
+    size_t dl, W3, all, split_at, bias, part, total;  // workspace offsets
 };
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -307,8 +322,8 @@ Plan plan(const Shape &s) {
     p.tokens = (int)((s.T + want - 1) / want);
     p.splits = (int)((s.T + p.tokens - 1) / p.tokens);
     size_t o = 0;
-    p.dl4 = o;
-    if (s.bf16) o = up256(o + 2 * (size_t)s.T * 4 * p.E8);
+    p.dl = o;  // bf16 x: four terms of 2 bytes; fp32 x: padded rows
+    o = up256(o + (s.bf16 ? 8 : 4) * (size_t)s.T * p.E8);
     p.W3 = o;
     if (s.bf16) o = up256(o + 2 * (size_t)3 * p.E8 * s.d);
     p.all = o;
@@ -316,7 +331,7 @@ Plan plan(const Shape &s) {
     p.split_at = o;
     o = up256(o + sizeof(int32_t) * ((size_t)p.splits + 1));
     p.bias = o;
-    o = up256(o + sizeof(float) * (size_t)p.token_blocks * s.E);
+    o = up256(o + sizeof(float) * (size_t)p.token_blocks * p.E8);
     p.part = o;
     o = up256(o + sizeof(float) * (size_t)p.splits * p.terms * (s.bf16 ? p.E8 : s.E) * s.d);
     p.total = o;
@@ -348,11 +363,13 @@ cudaError_t launch_route_backward(const Shape &s, const RouteBwd &a, const DevSt
     t.n_splits = p.splits;
     t.split = p.tokens;
     if (s.bf16) {
-        t.dl4 = reinterpret_cast<__nv_bfloat16 *>(ws + p.dl4);
+        t.dl4 = reinterpret_cast<__nv_bfloat16 *>(ws + p.dl);
         t.W3 = reinterpret_cast<__nv_bfloat16 *>(ws + p.W3);
         t.Wr = a.Wr;
         t.all = reinterpret_cast<int32_t *>(ws + p.all);
         t.splits = reinterpret_cast<int32_t *>(ws + p.split_at);
+    } else {
+        t.dl8 = reinterpret_cast<float *>(ws + p.dl);
     }
     const int split_blocks =
         s.bf16 ? (int)(((int64_t)p.E8 * s.d + kSplitCols - 1) / kSplitCols) : 0;
@@ -381,16 +398,19 @@ cudaError_t launch_route_backward(const Shape &s, const RouteBwd &a, const DevSt
         r.part = part;
         if ((err = launch_route_backward_tc(s, r, ds, st)) != cudaSuccess) return err;
     } else {
-        launch_pdl(route_dx_kernel, dim3((unsigned)((s.T + 63) / 64), (s.d + 63) / 64),
-                   dim3(simt::kThreads), 0, st, (const float *)a.dlogits, a.Wr,
-                   static_cast<const float *>(a.dx_in), s.T, s.E, s.d, static_cast<float *>(a.dx));
-        launch_pdl(dwr_kernel, dim3((s.d + 63) / 64, (s.E + 63) / 64, p.splits),
-                   dim3(simt::kThreads), 0, st, (const float *)a.dlogits,
-                   static_cast<const float *>(a.x), s.T, s.E, s.d, p.tokens, part);
+        if ((err = simt::opt_in(route_dx_kernel, Tl::SMEM_BYTES)) != cudaSuccess ||
+            (err = simt::opt_in(dwr_kernel, Tl::SMEM_BYTES)) != cudaSuccess)
+            return err;
+        launch_pdl(route_dx_kernel, dim3((unsigned)((s.T + Tl::BM - 1) / Tl::BM), (s.d + Tl::BN - 1) / Tl::BN),
+                   dim3(simt::kThreads), Tl::SMEM_BYTES, st, (const float *)t.dl8, a.Wr,
+                   static_cast<const float *>(a.dx_in), s.T, s.E, p.E8, s.d, static_cast<float *>(a.dx));
+        launch_pdl(dwr_kernel, dim3((s.d + Tl::BN - 1) / Tl::BN, (s.E + Tl::BM - 1) / Tl::BM, p.splits),
+                   dim3(simt::kThreads), Tl::SMEM_BYTES, st, (const float *)t.dl8,
+                   static_cast<const float *>(a.x), s.T, s.E, p.E8, s.d, p.tokens, part);
     }
     const int weight_blocks = (int)(((int64_t)s.E * s.d / 4 + kThreads - 1) / kThreads);
-    launch_pdl(sum_kernel, dim3(weight_blocks + (s.E + kWarps - 1) / kWarps), dim3(kThreads), 0, st,
-               (const float *)part, p.splits, p.terms, s.bf16 ? p.E8 : s.E, s.E, s.d, a.dWr,
+    launch_pdl(sum_kernel, dim3(weight_blocks + (a.dbias ? (s.E + 3) / 4 : 0)), dim3(kThreads), 0, st,
+               (const float *)part, p.splits, p.terms, s.bf16 ? p.E8 : s.E, s.E, p.E8, s.d, a.dWr,
                (const float *)t.bias_part, p.token_blocks, weight_blocks, a.dbias);
     return cudaGetLastError();
 }
