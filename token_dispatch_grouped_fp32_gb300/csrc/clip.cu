@@ -22,17 +22,21 @@ constexpr int kBlocks = 152 * 6;
 constexpr int kTable = 512;    // tensors per launch
 constexpr int kMapped = 1024;  // chunks with a map of their own
 
+// One tensor: a whole 32 bytes, so that a block finds it in one line.
+struct Entry {
+    const void *src;
+    void *dst;
+    int64_t numel;
+    int end;   // chunks of the tensors up to and with this one
+    int bf16;
+};
 struct Table {
-    const void *src[kTable];
-    void *dst[kTable];
-    int64_t numel[kTable];
-    int end[kTable];  // chunks of tensors 0 .. i
-    uint8_t bf16[kTable];
-    int n;
+    int n, chunks;
     // where the table's chunks are few (most tensors one chunk): the tensor
     // of every chunk, so that a block finds its own in one load
     int mapped;
     uint16_t tensor_of[kMapped];
+    Entry t[kTable];
 };
 
 __device__ __forceinline__ double block_sum(double v) {
@@ -48,7 +52,7 @@ __device__ __forceinline__ double block_sum(double v) {
 }
 
 struct Chunk {
-    int tensor;
+    Entry t;
     int64_t first;
     int count;
 };
@@ -57,12 +61,13 @@ __device__ __forceinline__ Chunk find_chunk(const Table &t, int c) {
     if (t.mapped) lo = hi = t.tensor_of[c];
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
-        if (t.end[mid] > c) hi = mid; else lo = mid + 1;
+        if (t.t[mid].end > c) hi = mid; else lo = mid + 1;
     }
     Chunk k;
-    k.tensor = lo;
-    k.first = (int64_t)(c - (lo ? t.end[lo - 1] : 0)) * kChunk;
-    k.count = (int)min((int64_t)kChunk, t.numel[lo] - k.first);
+    k.t = t.t[lo];
+    const int all = (int)((k.t.numel + kChunk - 1) / kChunk);
+    k.first = (int64_t)(c - (k.t.end - all)) * kChunk;
+    k.count = (int)min((int64_t)kChunk, k.t.numel - k.first);
     return k;
 }
 
@@ -103,13 +108,23 @@ __device__ __forceinline__ void chunk_scale(const TA *p, TA *o, int n, float coe
     const int head = min(n, (int)((16 - mp) & 15) / (int)sizeof(TA));
     if ((int)threadIdx.x < head) o[threadIdx.x] = Act<TA>::from_f(Act<TA>::to_f(p[threadIdx.x]) * coef);
     const int nv = (n - head) / EPV;
-#pragma unroll 4
-    for (int i = threadIdx.x; i < nv; i += kThreads) {
-        float v[EPV];
-        unpack16(*reinterpret_cast<const uint4 *>(p + head + (int64_t)i * EPV), v, static_cast<const TA *>(nullptr));
+    constexpr int U = 4;  // loads before the first store (o may be p)
+    for (int i0 = threadIdx.x; i0 < nv; i0 += U * kThreads) {
+        uint4 raw[U];
 #pragma unroll
-        for (int j = 0; j < EPV; ++j) v[j] *= coef;
-        stg16(o + head + (int64_t)i * EPV, pack16(v, static_cast<const TA *>(nullptr)));
+        for (int u = 0; u < U; ++u)
+            if (i0 + u * kThreads < nv)
+                raw[u] = *reinterpret_cast<const uint4 *>(p + head + (int64_t)(i0 + u * kThreads) * EPV);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (i0 + u * kThreads >= nv) continue;
+            float v[EPV];
+            unpack16(raw[u], v, static_cast<const TA *>(nullptr));
+#pragma unroll
+            for (int j = 0; j < EPV; ++j) v[j] *= coef;
+            stg16(o + head + (int64_t)(i0 + u * kThreads) * EPV,
+                  pack16(v, static_cast<const TA *>(nullptr)));
+        }
     }
     const int tail = head + nv * EPV + threadIdx.x;
     if (tail < n) o[tail] = Act<TA>::from_f(Act<TA>::to_f(p[tail]) * coef);
@@ -117,14 +132,13 @@ __device__ __forceinline__ void chunk_scale(const TA *p, TA *o, int n, float coe
 
 __global__ void __launch_bounds__(kThreads)
 norm_kernel(const __grid_constant__ Table t, int add, double *__restrict__ part) {
-    pdl_entry();
+    pdl_wait();
     double sum = 0.0;
-    const int chunks = t.n ? t.end[t.n - 1] : 0;
-    for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
+    for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
         const Chunk k = find_chunk(t, c);
-        sum += t.bf16[k.tensor]
-                   ? chunk_squares(static_cast<const __nv_bfloat16 *>(t.src[k.tensor]) + k.first, k.count)
-                   : chunk_squares(static_cast<const float *>(t.src[k.tensor]) + k.first, k.count);
+        sum += k.t.bf16
+                   ? chunk_squares(static_cast<const __nv_bfloat16 *>(k.t.src) + k.first, k.count)
+                   : chunk_squares(static_cast<const float *>(k.t.src) + k.first, k.count);
     }
     sum = block_sum(sum);
     if (threadIdx.x == 0) part[blockIdx.x] = add ? part[blockIdx.x] + sum : sum;
@@ -133,24 +147,22 @@ norm_kernel(const __grid_constant__ Table t, int add, double *__restrict__ part)
 __global__ void __launch_bounds__(kThreads)
 scale_kernel(const __grid_constant__ Table t, const double *__restrict__ part, int parts,
              float max_norm, float *__restrict__ norm) {
-    pdl_entry();
+    pdl_wait();
     double sum = 0.0;
     for (int i = threadIdx.x; i < parts; i += kThreads) sum += part[i];
     const float nrm = (float)sqrt(block_sum(sum));
     if (blockIdx.x == 0 && threadIdx.x == 0) *norm = nrm;
     float coef = max_norm / (nrm + 1e-6f);
     coef = coef > 1.f ? 1.f : coef;  // a NaN norm stays NaN
-    const int chunks = t.n ? t.end[t.n - 1] : 0;
-    // from the last chunk: what launch 1 read last is still in the L2 cache
-    for (int c = chunks - 1 - (int)blockIdx.x; c >= 0; c -= gridDim.x) {
+    for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
         const Chunk k = find_chunk(t, c);
-        if (t.dst[k.tensor] == nullptr) continue;
-        if (t.bf16[k.tensor])
-            chunk_scale(static_cast<const __nv_bfloat16 *>(t.src[k.tensor]) + k.first,
-                        static_cast<__nv_bfloat16 *>(t.dst[k.tensor]) + k.first, k.count, coef);
+        if (k.t.dst == nullptr) continue;
+        if (k.t.bf16)
+            chunk_scale(static_cast<const __nv_bfloat16 *>(k.t.src) + k.first,
+                        static_cast<__nv_bfloat16 *>(k.t.dst) + k.first, k.count, coef);
         else
-            chunk_scale(static_cast<const float *>(t.src[k.tensor]) + k.first,
-                        static_cast<float *>(t.dst[k.tensor]) + k.first, k.count, coef);
+            chunk_scale(static_cast<const float *>(k.t.src) + k.first,
+                        static_cast<float *>(k.t.dst) + k.first, k.count, coef);
     }
 }
 
@@ -159,16 +171,13 @@ int chunks_of(const moe_grad_t &g) { return (int)((g.numel + kChunk - 1) / kChun
 void fill(const moe_grad_t *g, int64_t n, Table *t) {
     int end = 0;
     for (int64_t i = 0; i < n; ++i) {
-        t->src[i] = g[i].grad;
-        t->dst[i] = g[i].out;
-        t->numel[i] = g[i].numel;
-        t->bf16[i] = g[i].dtype == MOE_BF16;
         const int first = end;
         end += chunks_of(g[i]);
-        t->end[i] = end;
+        t->t[i] = {g[i].grad, g[i].out, g[i].numel, end, g[i].dtype == MOE_BF16};
         for (int c = first; c < end && c < kMapped; ++c) t->tensor_of[c] = (uint16_t)i;
     }
     t->n = (int)n;
+    t->chunks = end;
     t->mapped = end <= kMapped;
 }
 

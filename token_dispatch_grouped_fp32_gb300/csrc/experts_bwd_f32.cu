@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(simt::kThreads)
 rows_kernel(const float *__restrict__ x, const float *__restrict__ dy,
             const int32_t *__restrict__ offsets, int E, const float *__restrict__ Wgu,
             const float *__restrict__ Wd, int d, int f, float *__restrict__ dgu) {
-    pdl_entry();
+    pdl_wait();
     extern __shared__ __align__(16) float smem[];
     RowTile t;
     if (!find_tile<Tl::BM>(offsets, E, reinterpret_cast<int *>(smem) + Tl::SMEM_BYTES / 4, &t)) return;
@@ -109,7 +109,7 @@ template <typename Tl>
 __global__ void __launch_bounds__(simt::kThreads)
 dx_kernel(const float *__restrict__ dgu, const int32_t *__restrict__ offsets, int E,
           const float *__restrict__ Wgu, int d, int f, float *__restrict__ dx) {
-    pdl_entry();
+    pdl_wait();
     extern __shared__ __align__(16) float smem[];
     RowTile t;
     if (!find_tile<Tl::BM>(offsets, E, reinterpret_cast<int *>(smem) + Tl::SMEM_BYTES / 4, &t)) return;
@@ -140,7 +140,7 @@ struct WeightProduct {
 template <typename Tl>
 __global__ void __launch_bounds__(simt::kThreads)
 weights_kernel(WeightProduct p0, WeightProduct p1, int first, const int32_t *__restrict__ offsets) {
-    pdl_entry();
+    pdl_wait();
     extern __shared__ __align__(16) float smem[];
     const bool second = (int)blockIdx.x >= first;
     const WeightProduct &p = second ? p1 : p0;
@@ -174,9 +174,9 @@ template <typename Tl> cudaError_t launch_t(const Shape &s, const ExpertsBwd &a,
     auto tiles = [](int n, int b) { return (unsigned)((n + b - 1) / b); };
     const dim3 block(simt::kThreads);
     cudaError_t err;
-    if ((err = simt::opt_in(rows_kernel<Tl>, Tl::SMEM_BYTES + 16 * 1024)) != cudaSuccess ||
-        (err = simt::opt_in(dx_kernel<Tl>, Tl::SMEM_BYTES + 16 * 1024)) != cudaSuccess ||
-        (err = simt::opt_in(weights_kernel<Tl>, Tl::SMEM_BYTES)) != cudaSuccess)
+    if ((err = simt::opt_in<rows_kernel<Tl>>(Tl::SMEM_BYTES + 16 * 1024)) != cudaSuccess ||
+        (err = simt::opt_in<dx_kernel<Tl>>(Tl::SMEM_BYTES + 16 * 1024)) != cudaSuccess ||
+        (err = simt::opt_in<weights_kernel<Tl>>(Tl::SMEM_BYTES)) != cudaSuccess)
         return err;
     launch_pdl(rows_kernel<Tl>, dim3(mt, tiles(s.f, Tl::BN)), block, Tl::SMEM_BYTES + prefix, st, x, dy,
                a.offsets, s.E, Wgu, Wd, s.d, s.f, dgu);

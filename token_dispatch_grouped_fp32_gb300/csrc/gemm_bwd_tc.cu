@@ -221,7 +221,6 @@ template <int CTAS, int KIND>
 __global__ void __launch_bounds__(threads<KIND>(), 1)
 gemm_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                       const __grid_constant__ CUtensorMap tmOut, Params p) {
-    if (!p.release_late) pdl_release();
     using C = Cfg<CTAS, KIND>;
     constexpr bool PAIR = C::PAIR;
     constexpr int STAGES = C::STAGES;

@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kThreads)
 scatter_rows_kernel(const TA *__restrict__ src, const TA *__restrict__ y_perm,
                     const int32_t *__restrict__ pos, const float *__restrict__ w, int64_t T, int k,
                     int d, TA *__restrict__ dst, float *__restrict__ dw) {
-    pdl_entry();
+    pdl_wait();
     constexpr int EPV = 16 / sizeof(TA);
     __shared__ Dots dots;
     const int64_t t = (int64_t)blockIdx.x * (kThreads / TPT) + threadIdx.x / TPT;
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kThreads)
 gather_rows_scaled_kernel(const TA *__restrict__ dx_perm, const int32_t *__restrict__ pos,
                           const float *__restrict__ w, const TA *__restrict__ x, int64_t T, int k,
                           int d, TA *__restrict__ dx, float *__restrict__ dw) {
-    pdl_entry();
+    pdl_wait();
     constexpr int EPV = 16 / sizeof(TA);
     __shared__ Dots dots;
     const int64_t t = (int64_t)blockIdx.x * (kThreads / TPT) + threadIdx.x / TPT;

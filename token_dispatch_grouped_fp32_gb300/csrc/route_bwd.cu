@@ -77,7 +77,7 @@ struct TermsArgs {
 // running sum of the rows for the bias.  The blocks after: kSplitCols elements
 // of Wr each.
 __global__ void __launch_bounds__(kThreads) terms_kernel(TermsArgs a, DevStatus ds) {
-    pdl_entry();
+    pdl_wait();
     extern __shared__ float sh[];
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, E8 = a.E8;
     if ((int)blockIdx.x >= a.token_blocks) {
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kThreads)
 sum_kernel(const float *__restrict__ part, int splits, int terms, int stride, int E, int E8, int d,
            float *__restrict__ dWr, const float *__restrict__ bias_part, int token_blocks,
            int weight_blocks, float *__restrict__ dbias) {
-    pdl_entry();
+    pdl_wait();
     if ((int)blockIdx.x < weight_blocks) {
         const int64_t i = 4 * ((int64_t)blockIdx.x * kThreads + threadIdx.x);
         if (i >= (int64_t)E * d) return;
@@ -252,7 +252,7 @@ sum_kernel(const float *__restrict__ part, int splits, int terms, int stride, in
 __global__ void __launch_bounds__(simt::kThreads)
 dwr_kernel(const float *__restrict__ dl8, const float *__restrict__ x, int64_t T, int E, int E8,
            int d, int tokens, float *__restrict__ part) {
-    pdl_entry();
+    pdl_wait();
     extern __shared__ __align__(16) float smem[];
     const int n0 = blockIdx.x * Tl::BN, e0 = blockIdx.y * Tl::BM;
     const int64_t t0 = (int64_t)blockIdx.z * tokens;
@@ -274,7 +274,7 @@ dwr_kernel(const float *__restrict__ dl8, const float *__restrict__ x, int64_t T
 __global__ void __launch_bounds__(simt::kThreads)
 route_dx_kernel(const float *__restrict__ dl8, const float *__restrict__ Wr, const float *dx_in,
                 int64_t T, int E, int E8, int d, float *dx) {
-    pdl_entry();
+    pdl_wait();
     extern __shared__ __align__(16) float smem[];
     const int64_t t0 = (int64_t)blockIdx.x * Tl::BM;
     const int n0 = blockIdx.y * Tl::BN;
@@ -375,10 +375,7 @@ cudaError_t launch_route_backward(const Shape &s, const RouteBwd &a, const DevSt
         s.bf16 ? (int)(((int64_t)p.E8 * s.d + kSplitCols - 1) / kSplitCols) : 0;
     const size_t sh = sizeof(float) * 2 * kWarps * (size_t)p.E8;  // at most 64 KB
     cudaError_t err;
-    if (sh > 48 * 1024 &&
-        (err = cudaFuncSetAttribute(terms_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)sh)) != cudaSuccess)
-        return err;
+    if (sh > 48 * 1024 && (err = simt::opt_in<terms_kernel>(64 * 1024)) != cudaSuccess) return err;
     launch_pdl(terms_kernel, dim3(p.token_blocks + split_blocks), dim3(kThreads), sh, st, t, ds);
     if ((err = cudaGetLastError()) != cudaSuccess) return err;
     float *part = reinterpret_cast<float *>(ws + p.part);
@@ -398,8 +395,8 @@ cudaError_t launch_route_backward(const Shape &s, const RouteBwd &a, const DevSt
         r.part = part;
         if ((err = launch_route_backward_tc(s, r, ds, st)) != cudaSuccess) return err;
     } else {
-        if ((err = simt::opt_in(route_dx_kernel, Tl::SMEM_BYTES)) != cudaSuccess ||
-            (err = simt::opt_in(dwr_kernel, Tl::SMEM_BYTES)) != cudaSuccess)
+        if ((err = simt::opt_in<route_dx_kernel>(Tl::SMEM_BYTES)) != cudaSuccess ||
+            (err = simt::opt_in<dwr_kernel>(Tl::SMEM_BYTES)) != cudaSuccess)
             return err;
         launch_pdl(route_dx_kernel, dim3((unsigned)((s.T + Tl::BM - 1) / Tl::BM), (s.d + Tl::BN - 1) / Tl::BN),
                    dim3(simt::kThreads), Tl::SMEM_BYTES, st, (const float *)t.dl8, a.Wr,

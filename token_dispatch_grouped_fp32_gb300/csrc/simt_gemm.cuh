@@ -5,6 +5,8 @@
 // matrix; such elements are zeros.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 #include "tc_ptx.cuh"
 
@@ -90,7 +92,7 @@ template <int BM_, int BN_> struct Tile {
             __syncthreads();  // this stage has landed; the one before it has been read
             load(step + kStages - 1);
             const float *a_s = sa + step % kStages * A_FLOATS, *b_s = sb + step % kStages * B_FLOATS;
-#pragma unroll 2
+#pragma unroll(TM <= 2 ? BK / 4 : 2)  // small tiles: all of the step's loads ahead
             for (int kk = 0; kk < BK; kk += 4) {
                 float a[TM][4], b[TN][4];
                 if constexpr (A_K) {
@@ -131,10 +133,19 @@ template <int BM_, int BN_> struct Tile {
 using Large = Tile<64, 64>;
 using Small = Tile<32, 32>;
 
-// Dynamic shared memory of a kernel over the tile Tl, past the first `extra`
-// bytes (each kernel's own); opts the kernel in once per device.
-template <typename K> inline cudaError_t opt_in(K kernel, size_t bytes) {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+// Raises a kernel's dynamic shared memory limit, once per kernel and device.
+template <auto K> inline cudaError_t opt_in(size_t bytes) {
+    static std::atomic<bool> done[64];
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+    if ((err = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes)) !=
+        cudaSuccess)
+        return err;
+    done[dev].store(true, std::memory_order_relaxed);
+    return cudaSuccess;
 }
 
 }  // namespace simt
