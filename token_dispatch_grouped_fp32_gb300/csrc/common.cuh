@@ -81,6 +81,18 @@ __device__ __forceinline__ void stg16(void *p, const uint4 &v) {
     *reinterpret_cast<uint4 *>(p) = v;
 }
 
+// Two fp32 fused multiply-adds in one instruction (each rounded as fmaf).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\t"
+        "mov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
 // Programmatic dependent launch.  Every kernel of the layer starts with
 // pdl_entry(): it lets the next kernel in the stream be scheduled (once all
 // of this grid's blocks have started, so a dependent never takes SMs from
