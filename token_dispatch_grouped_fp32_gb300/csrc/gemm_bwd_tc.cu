@@ -15,7 +15,7 @@
 //
 // Router (see route_bwd.cu, which splits the fp32 operands into bf16 terms):
 //   RX   dx[t]   = add[t] + sum_c A[t][c] B[c]        A [T][K], B [K][d]
-//   RW   part[s] = sum over the tokens of split s of x[t]^T A[t]   fp32, transposed
+//   RW   part[s] = sum over the tokens of split s of A[t]^T x[t]   fp32
 //
 // Row products (DH, GU, DX, RX) have the forward's tiles: 256 rows x 256 columns
 // for a CTA pair (cta_group::2), 128 x 256 for a single CTA, row tiles within
@@ -25,8 +25,8 @@
 // GU a tile's 256 accumulator columns are 128 gate and the 128 matching up
 // columns).
 //
-// Weight products (DW, RW) contract over the rows of a segment, so both operands are
-// MN-major and the K axis is ragged.  The last K step of a segment may hold
+// Weight products (DW, RW) contract over the rows of a segment, so both
+// operands are MN-major and the K axis is ragged.  The last K step of a segment may hold
 // rows of the next expert (any value, a NaN too): MMAs are issued for whole
 // groups of 16 rows only up to the segment's end, and where the end falls
 // inside such a group, one warp (the fixer) zeroes the group's remaining rows
@@ -34,8 +34,19 @@
 // complete on a barrier of its own; the fixer zeroes, orders its writes before
 // the tensor core's reads (proxy fence), and reports the stage on the full
 // barrier: an arrival, or in a pair a 16-byte bulk copy of each CTA whose
-// bytes complete the leader's barrier.  An expert with
-// no rows has zeros written by the epilogue, without an MMA.
+// bytes complete the leader's barrier.  An expert with no rows has zeros
+// written by the epilogue, without an MMA.
+//
+// What bounds a pair's tile is shared memory: a K step fills 32 KB per CTA and
+// the MMAs read 32 KB of it in 512 cycles, all of its 128 bytes a cycle.  Four
+// experts of 1024 rows, d = 4096, f = 7168: DX 94 % of the tensor pipe (1654
+// TFLOP/s over its last, partial round too), DH and GU 84 to 86 % (1720, 1696),
+// DW 75 % (1650): its tiles of 16 K steps pass their 64 KB of output per CTA
+// through shared memory as well, 9.2 K cycles at 128 bytes, 10.9 K measured.
+// With few rows an expert the bound is memory: the weights read by DH, GU and
+// DX, the gradients that DW writes (24 experts of 100 rows, d = f = 2880: dWgu
+// 143 us, 5.5 TB/s).  The Mixtral shape (T = 4096) takes 5.2 to 5.5 ms in all,
+// 1410 to 1480 TFLOP/s under the power cap, the gpt-oss one (T = 8192) 4.1 to 4.6.
 //
 // Roles: warp 0 TMA loads, warp 1 tensor memory and MMAs (both one thread),
 // warps 2-9 the epilogue (two warps to each 32-lane quarter, half the columns
@@ -65,8 +76,9 @@ constexpr int TMEM_COLS = 2 * BN;
 constexpr int kEpiWarps = 8;
 constexpr int MAX_E = 1024;
 // K steps of one accumulation in RW.  The tensor cores' fp32 sum drops low
-// bits at every step, so long sums lose them in proportion; sums of kChunk
-// steps are added in fp32 by the epilogue.
+// bits at every step, so long sums lose them in proportion (4096 tokens: dWr
+// more than 1e-6 off); sums of kChunk steps are added in fp32 by the epilogue
+// (3e-7 to 6e-7 off, and no slower).
 constexpr int kChunk = 8;
 
 enum Kind { DH, GU, DX, DW, RX, RW };
@@ -82,8 +94,10 @@ template <int CTAS, int KIND> struct Cfg {
     static constexpr int B_ATOMS = B_COLS / 64;
     static constexpr int B_BYTES = B_COLS * BK * 2;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-    // one stage goes to the epilogue's output blocks (OUT_BYTES a warp) where
-    // the output leaves by TMA stores
+    // One stage goes to the epilogue's output blocks (OUT_BYTES a warp) where
+    // the output leaves by TMA stores: tiles with few K steps, whose time is
+    // their epilogue (24 experts of 100 rows: dWgu 163 -> 143 us against
+    // transposing shuffles; 32 bytes a lane from registers 231).
     static constexpr bool STAGED = KIND == DW || KIND == RX;
     static constexpr int STAGES = (PAIR ? 6 : 4) - (STAGED ? 1 : 0);
     static constexpr int OUT_BYTES = STAGED ? 32 * 128 : 0;
@@ -104,14 +118,14 @@ struct Params {
     const int32_t *offsets;
     int E;
     int K;        // reduction length of a row product
-    int M;        // DW: rows of dW[e]
+    int M;        // weight products: rows of an output
     int N;        // columns of the output (GU: f, gate and up alike)
     int n_tiles;  // column tiles
-    int m_tiles;  // DW: row tiles
-    int m_fast;   // DW: row tiles vary fastest
+    int m_tiles;  // weight products: row tiles
+    int m_fast;   // weight products: row tiles vary fastest
     int f;        // GU: column offset of the up half
     int a_blocks, b_blocks;  // MN-major A / B through maps of 64-column blocks
-    float *dh;               // DH writes, GU reads (see dh_block)
+    float *dh;               // DH writes, GU reads (see dh_quad)
     __nv_bfloat16 *out;
     const __nv_bfloat16 *add;  // RX: added to the product (may be out), or nullptr
     float *part;               // RW: [segments][N][M]
@@ -129,8 +143,8 @@ struct Params {
 };
 
 struct Work {
-    int e, row0, rows;  // the rows of expert e that the tile covers (DW: its whole segment)
-    int m0, n_blk;      // DW: first row of dW; column tile
+    int e, row0, rows;  // the rows of segment e that the tile covers (weight products: all)
+    int m0, n_blk;      // weight products: first row of the output; column tile
 };
 
 // A unit's walk over the tile list: tile, tile + nunits, ...  Weight products
@@ -501,7 +515,8 @@ gemm_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
             // The accumulator is handed back as soon as it is in registers.  The
             // arrival passes on no memory contents, only that the loads from
             // tensor memory are complete, so in a pair it is a relaxed one: a
-            // release at cluster scope would wait for the warp's global stores.
+            // release at cluster scope would wait for the warp's global stores
+            // (Qwen3 shape, T = 2048, Zipf: 803 us, relaxed 671).
             auto release = [&]() {
                 tc_fence_before();
                 __syncwarp();
