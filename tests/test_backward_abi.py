@@ -171,3 +171,28 @@ def test_grad_list(moe):
 
 def test_struct_layouts_match(moe):
     assert ctypes.sizeof(moe.moe_grad_t) == 32
+
+
+def test_layer_backward_refuses_what_it_cannot_use(moe):
+    """Before any launch: no forward on the stream, other sizes or types, and
+    gradient buffers of another shape."""
+    d, E, k, f = 64, 8, 2, 128
+    bf = torch.bfloat16
+    lay = moe.MoELayer(torch.zeros(E, d), torch.zeros(E, d, 2 * f, dtype=bf), torch.zeros(E, f, d, dtype=bf), k)
+    x = torch.zeros(16, d, dtype=bf)
+    with pytest.raises(RuntimeError, match="latest forward"):
+        lay.backward(x, x, stream=0)
+    lay._tokens[0] = 16
+    with pytest.raises(RuntimeError, match="latest forward"):
+        lay.backward(x[:8], x[:8], stream=0)
+    for bad in (x.float(), x[:, :32], x[:8]):
+        with pytest.raises(ValueError):
+            lay.backward(x, bad, stream=0)
+    with pytest.raises(ValueError):
+        lay.backward(x.float(), x.float(), stream=0)
+    good = {"x": torch.empty_like(x), "Wr": torch.empty_like(lay.Wr),
+            "W_gate_up": torch.empty_like(lay.W_gate_up), "W_down": torch.empty_like(lay.W_down)}
+    for n, t in good.items():
+        for bad in (None, t[:1], t.double()):
+            with pytest.raises(ValueError, match=n):
+                lay.backward(x, x, grads={**good, n: bad}, stream=0)

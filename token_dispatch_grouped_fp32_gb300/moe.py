@@ -379,6 +379,7 @@ class MoELayer:
         self.scale_inputs = scale_inputs
         self._ws = {}  # stream handle -> workspace
         self._bwd_ws = {}  # the same for the backward pass
+        self._tokens = {}  # stream handle -> tokens of its latest forward
 
     def config(self, T: int) -> moe_config_t:
         return config(T, self.d, self.E, self.k, self.f, self.dtype, self.renormalize,
@@ -404,6 +405,7 @@ class MoELayer:
         cfg = self.config(T)
         moe_forward(cfg, x, self.Wr, self.logit_bias, self.W_gate_up, self.W_down, out,
                     self.workspace(T, stream), stream=stream)
+        self._tokens[_stream(stream)] = T
         return out
 
     __call__ = forward
@@ -413,17 +415,26 @@ class MoELayer:
         stream: a dict of "x", "Wr", "W_gate_up", "W_down" and, with a logit
         bias, "logit_bias".  ``grads``: such a dict of buffers to write into
         (a training loop keeps one)."""
-        if x.shape[1] != self.d or dout.shape != x.shape or dout.dtype != x.dtype:
-            raise ValueError(f"x and dout are [T, {self.d}] of one dtype, not {tuple(x.shape)} "
+        if x.shape[1] != self.d or x.dtype != self.dtype or dout.shape != x.shape \
+                or dout.dtype != x.dtype:
+            raise ValueError(f"x and dout are [T, {self.d}] {self.dtype}, not {tuple(x.shape)} "
                              f"{x.dtype} and {tuple(dout.shape)} {dout.dtype}")
         T = x.shape[0]
+        if T and self._tokens.get(_stream(stream)) != T:
+            raise RuntimeError(f"backward of {T} tokens, but the latest forward on this stream had "
+                               f"{self._tokens.get(_stream(stream))}")
         cfg = self.config(T)
+        like = {"x": x, "Wr": self.Wr, "W_gate_up": self.W_gate_up, "W_down": self.W_down}
+        if self.logit_bias is not None:
+            like["logit_bias"] = self.logit_bias
         if grads is None:
-            grads = {"x": torch.empty_like(x), "Wr": torch.empty_like(self.Wr),
-                     "W_gate_up": torch.empty_like(self.W_gate_up),
-                     "W_down": torch.empty_like(self.W_down)}
-            if self.logit_bias is not None:
-                grads["logit_bias"] = torch.empty_like(self.logit_bias)
+            grads = {n: torch.empty_like(t) for n, t in like.items()}
+        for n, t in like.items():
+            g = grads.get(n)
+            if g is None and n == "logit_bias":
+                continue
+            if g is None or g.shape != t.shape or g.dtype != t.dtype:
+                raise ValueError(f"the gradient of {n} is {tuple(t.shape)} {t.dtype}")
         ws = self._grown(self._bwd_ws, moe_backward_workspace_size(cfg), stream)
         moe_backward(cfg, x, self.Wr, self.W_gate_up, self.W_down, self.workspace(T, stream), dout,
                      grads["x"], grads["Wr"], grads.get("logit_bias"), grads["W_gate_up"],
