@@ -191,9 +191,12 @@ __global__ void __launch_bounds__(kThreads) terms_kernel(TermsArgs a, DevStatus 
     }
 }
 
-// dWr[e][c] = the sum over splits and terms of part[s][b*stride + e][c]: a
-// block takes 128 columns' worth of elements, its warps a range of the partial
-// sums each.  The blocks after those sum the bias.
+// dWr[e][c] = the sum over splits and terms of part[s][b*stride + e][c]: SHARE
+// warps take 128 elements, a range of the partial sums each.  1 or 8: 12
+// partial sums (the Qwen3 router) take 5.5 us with 1 and 7.4 with 8, while one
+// warp alone would wait for 114 (the Mixtral router, 5.6 us with 8) in 29 rounds.
+// The blocks after those sum the bias.
+template <int SHARE>
 __global__ void __launch_bounds__(kThreads)
 sum_kernel(const float *__restrict__ part, int splits, int terms, int stride, int E, int E8, int d,
            float *__restrict__ dWr, const float *__restrict__ bias_part, int token_blocks,
@@ -202,14 +205,15 @@ sum_kernel(const float *__restrict__ part, int splits, int terms, int stride, in
     __shared__ float4 s_part[kThreads];
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     if ((int)blockIdx.x < weight_blocks) {
-        const int64_t i = 4 * ((int64_t)blockIdx.x * 32 + lane);
+        const int64_t group = (int64_t)blockIdx.x * (kWarps / SHARE) + wid / SHARE;
+        const int64_t i = 4 * (group * 32 + lane);
         const bool have = i < (int64_t)E * d;
-        const int n = splits * terms, per = (n + kWarps - 1) / kWarps;
-        const int z1 = min(n, (wid + 1) * per);
+        const int n = splits * terms, per = (n + SHARE - 1) / SHARE, mine = wid % SHARE;
+        const int z1 = min(n, (mine + 1) * per);
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         if (have) {
             const int64_t e = i / d, c = i % d;
-            for (int z0 = wid * per; z0 < z1; z0 += 4) {  // four loads in flight
+            for (int z0 = mine * per; z0 < z1; z0 += 4) {  // four loads in flight
                 float4 v[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -229,10 +233,9 @@ sum_kernel(const float *__restrict__ part, int splits, int terms, int stride, in
         }
         s_part[threadIdx.x] = acc;
         __syncthreads();
-        if (wid > 0 || !have) return;
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) {
-            const float4 v = s_part[32 * w + lane];
+        if (mine > 0 || !have) return;
+        for (int w = 1; w < SHARE; ++w) {
+            const float4 v = s_part[32 * (wid + w) + lane];
             acc.x += v.x;
             acc.y += v.y;
             acc.z += v.z;
@@ -612,8 +615,11 @@ cudaError_t launch_route_backward(const Shape &s, const RouteBwd &a, const DevSt
     cudaError_t err = p.few ? launch_few(s, a, p, part, bias_part, ds, st)
                             : launch_products(s, a, p, part, bias_part, ds, st);
     if (err != cudaSuccess) return err;
-    const int weight_blocks = (int)(((int64_t)s.E * s.d / 4 + 31) / 32);
-    launch_pdl(sum_kernel, dim3(weight_blocks + (a.dbias ? (s.E + 3) / 4 : 0)), dim3(kThreads), 0, st,
+    const int share = p.splits * p.terms > 32 ? kWarps : 1;
+    const int columns = 32 * kWarps / share;  // float4 columns of a block
+    const int weight_blocks = (int)(((int64_t)s.E * s.d / 4 + columns - 1) / columns);
+    auto sum = share == 1 ? sum_kernel<1> : sum_kernel<kWarps>;
+    launch_pdl(sum, dim3(weight_blocks + (a.dbias ? (s.E + 3) / 4 : 0)), dim3(kThreads), 0, st,
                (const float *)part, p.splits, p.terms, p.terms > 1 ? p.E8 : s.E, s.E, p.E8, s.d, a.dWr,
                (const float *)bias_part, p.token_blocks, weight_blocks, a.dbias);
     return cudaGetLastError();
