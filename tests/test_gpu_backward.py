@@ -369,6 +369,10 @@ LAYERS = [  # T, d, E, k, f, dtype, renorm, scale, bias
     (200, 128, 4, 4, 192, torch.bfloat16, True, True, False),      # k == E, weights on the inputs
     (300, 192, 8, 2, 128, torch.bfloat16, True, True, False),      # gathered, weights on the inputs
     (1, 64, 4, 2, 64, torch.bfloat16, True, False, False),
+    (250, 200, 8, 2, 136, torch.bfloat16, True, True, True),       # weights on the inputs, copied rows
+    (1500, 128, 8, 2, 192, torch.bfloat16, True, False, False),    # both tile shapes
+    (3000, 128, 4, 2, 192, torch.bfloat16, False, False, True),    # CTA pairs
+    (700, 128, 40, 8, 64, torch.bfloat16, True, False, True),      # single CTAs, E > 8
 ]
 
 

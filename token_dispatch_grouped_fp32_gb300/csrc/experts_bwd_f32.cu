@@ -4,16 +4,16 @@
 // For expert e and row r of its segment, with g, u = x[r] Wgu[e] recomputed,
 // s = sigmoid(g) and dh = dy[r] Wd[e]^T:
 //   dg = dh u s (1 + g (1 - s)),   du = dh g s          (rows_kernel -> dgu)
-//   dx[r] = [dg du] Wgu[e]^T                            (dx_kernel)
-//   dWd[e] = h^T dy,  dWgu[e] = x^T [dg du]             (weights_kernel)
+//   dx[r] = [dg du] Wgu[e]^T,
+//   dWd[e] = h^T dy,  dWgu[e] = x^T [dg du]             (dx_weights_kernel)
 // over the rows of the segment; an expert with no rows gets zero weight
 // gradients.  Every sum is fp32 in a fixed order.
 //
-// Three launches over the tile of simt_gemm.cuh.  T = 64, d = 128, f = 256, E =
-// 8: 24 us, latency (tiles of 32 x 32; 64 x 64 without the pipeline took 45 to
-// 100).  T = 1024, k = E = 8, d = f = 512 (34 GFLOP): 923 us, 37 TFLOP/s, bound by
-// the multiply-adds and the shared-memory loads beside them (128 x 64 tiles
-// 957, 128 x 128 1491).
+// Two launches over the tile of simt_gemm.cuh.  T = 64, d = 128, f = 256, E =
+// 8: 22.4 us, latency (tiles of 32 x 32; 64 x 64 without the pipeline 45 to 100;
+// dx and the weights in launches of their own 24).  T = 1024, k = E = 8, d = f =
+// 512 (34 GFLOP): 914 us, 38 TFLOP/s, bound by the multiply-adds and the
+// shared-memory loads beside them (128 x 64 tiles 957, 128 x 128 1491).
 #include "common.cuh"
 #include "kernels.h"
 #include "simt_gemm.cuh"
@@ -52,10 +52,9 @@ struct RowTile {
     int e, row0, rows;
 };
 template <int BM>
-__device__ __forceinline__ bool find_tile(const int32_t *offsets, int E, int *s_dyn, RowTile *t) {
+__device__ __forceinline__ bool find_tile(const int32_t *offsets, int E, int *s_dyn, int g, RowTile *t) {
     int *s_off = s_dyn, *s_tile = s_dyn + E + 1;
     tile_prefix<BM>(offsets, E, s_off, s_tile);
-    const int g = blockIdx.x;
     if (g >= s_tile[E]) return false;
     int lo = 0, hi = E - 1;
     while (lo < hi) {
@@ -77,7 +76,8 @@ rows_kernel(const float *__restrict__ x, const float *__restrict__ dy,
     pdl_wait();
     extern __shared__ __align__(16) float smem[];
     RowTile t;
-    if (!find_tile<Tl::BM>(offsets, E, reinterpret_cast<int *>(smem) + Tl::SMEM_BYTES / 4, &t)) return;
+    if (!find_tile<Tl::BM>(offsets, E, reinterpret_cast<int *>(smem) + Tl::SMEM_BYTES / 4, blockIdx.x, &t))
+        return;
     const int n0 = blockIdx.y * Tl::BN;
     const float *xr = x + (int64_t)t.row0 * d, *yr = dy + (int64_t)t.row0 * d;
     const float *W = Wgu + (int64_t)t.e * d * 2 * f, *Wt = Wd + (int64_t)t.e * f * d;
@@ -111,52 +111,53 @@ rows_kernel(const float *__restrict__ x, const float *__restrict__ dy,
     }
 }
 
-template <typename Tl>
-__global__ void __launch_bounds__(simt::kThreads)
-dx_kernel(const float *__restrict__ dgu, const int32_t *__restrict__ offsets, int E,
-          const float *__restrict__ Wgu, int d, int f, float *__restrict__ dx) {
-    pdl_wait();
-    extern __shared__ __align__(16) float smem[];
-    RowTile t;
-    if (!find_tile<Tl::BM>(offsets, E, reinterpret_cast<int *>(smem) + Tl::SMEM_BYTES / 4, &t)) return;
-    const int n0 = blockIdx.y * Tl::BN, K = 2 * f;
-    const float *a = dgu + (int64_t)t.row0 * K, *W = Wgu + (int64_t)t.e * d * K;
-    float acc[Tl::TM][Tl::TN];
-    Tl::zero(acc);
-    Tl::template product<true, true, true>(
-        smem, K, [=](int m, int k) { return m < t.rows ? a + (int64_t)m * K + k : nullptr; },
-        [=](int k, int n) { return n0 + n < d ? W + (int64_t)(n0 + n) * K + k : nullptr; }, acc);
-#pragma unroll
-    for (int i = 0; i < Tl::TM; ++i)
-#pragma unroll
-        for (int j = 0; j < Tl::TN; ++j) {
-            const int m = Tl::template row<true>(i), n = n0 + Tl::template col<true>(j);
-            if (m < t.rows && n < d) dx[(int64_t)(t.row0 + m) * d + n] = acc[i][j];
-        }
-}
-
-// dW[e] [M][N] = A^T B over the rows of expert e's segment (A [P][M], B
-// [P][N]), for two such products in one launch: blocks below `first` are the
-// first one's tiles.
+// dW[e] [M][N] = A^T B over the rows of expert e's segment (A [P][M], B [P][N]).
 struct WeightProduct {
     const float *A, *B;
-    int M, N;
+    int M, N, tiles;  // tiles of one expert's dW
     float *dW;
 };
+
+// dx and both weight gradients, none of which reads another's output, in one
+// launch: blocks below dx_blocks are dx's tiles (column tiles fastest), whose
+// chain over 2f is the longest, then every expert's tiles of wd and wg.
 template <typename Tl>
 __global__ void __launch_bounds__(simt::kThreads)
-weights_kernel(WeightProduct p0, WeightProduct p1, int first, const int32_t *__restrict__ offsets) {
+dx_weights_kernel(const float *__restrict__ dgu, const int32_t *__restrict__ offsets, int E,
+                  const float *__restrict__ Wgu, int d, int f, float *__restrict__ dx, int dx_blocks,
+                  WeightProduct wd, WeightProduct wg) {
     pdl_wait();
     extern __shared__ __align__(16) float smem[];
-    const bool second = (int)blockIdx.x >= first;
-    const WeightProduct &p = second ? p1 : p0;
-    const int e = blockIdx.y, b = (int)blockIdx.x - (second ? first : 0);
-    const int nt = (p.N + Tl::BN - 1) / Tl::BN;
-    const int m0 = b / nt * Tl::BM, n0 = b % nt * Tl::BN, M = p.M, N = p.N;
-    const int r0 = offsets[e], rows = offsets[e + 1] - r0;
-    const float *A = p.A + (int64_t)r0 * M, *B = p.B + (int64_t)r0 * N;
     float acc[Tl::TM][Tl::TN];
     Tl::zero(acc);
+    if ((int)blockIdx.x < dx_blocks) {
+        const int nt = (d + Tl::BN - 1) / Tl::BN;
+        RowTile t;
+        if (!find_tile<Tl::BM>(offsets, E, reinterpret_cast<int *>(smem) + Tl::SMEM_BYTES / 4,
+                               (int)blockIdx.x / nt, &t))
+            return;
+        const int n0 = (int)blockIdx.x % nt * Tl::BN, K = 2 * f;
+        const float *a = dgu + (int64_t)t.row0 * K, *W = Wgu + (int64_t)t.e * d * K;
+        Tl::template product<true, true, true>(
+            smem, K, [=](int m, int k) { return m < t.rows ? a + (int64_t)m * K + k : nullptr; },
+            [=](int k, int n) { return n0 + n < d ? W + (int64_t)(n0 + n) * K + k : nullptr; }, acc);
+#pragma unroll
+        for (int i = 0; i < Tl::TM; ++i)
+#pragma unroll
+            for (int j = 0; j < Tl::TN; ++j) {
+                const int m = Tl::template row<true>(i), n = n0 + Tl::template col<true>(j);
+                if (m < t.rows && n < d) dx[(int64_t)(t.row0 + m) * d + n] = acc[i][j];
+            }
+        return;
+    }
+    const int per = wd.tiles + wg.tiles, b = (int)blockIdx.x - dx_blocks;
+    const int e = b / per, g = b % per;
+    const WeightProduct &p = g < wd.tiles ? wd : wg;
+    const int tile = g < wd.tiles ? g : g - wd.tiles;
+    const int nt = (p.N + Tl::BN - 1) / Tl::BN;
+    const int m0 = tile / nt * Tl::BM, n0 = tile % nt * Tl::BN, M = p.M, N = p.N;
+    const int r0 = offsets[e], rows = offsets[e + 1] - r0;
+    const float *A = p.A + (int64_t)r0 * M, *B = p.B + (int64_t)r0 * N;
     Tl::template product<false, false, false>(
         smem, rows, [=](int m, int k) { return m0 + m < M ? A + (int64_t)k * M + m0 + m : nullptr; },
         [=](int k, int n) { return n0 + n < N ? B + (int64_t)k * N + n0 + n : nullptr; }, acc);
@@ -181,19 +182,24 @@ template <typename Tl> cudaError_t launch_t(const Shape &s, const ExpertsBwd &a,
     const dim3 block(simt::kThreads);
     cudaError_t err;
     if ((err = simt::opt_in<rows_kernel<Tl>>(Tl::SMEM_BYTES + 16 * 1024)) != cudaSuccess ||
-        (err = simt::opt_in<dx_kernel<Tl>>(Tl::SMEM_BYTES + 16 * 1024)) != cudaSuccess ||
-        (err = simt::opt_in<weights_kernel<Tl>>(Tl::SMEM_BYTES)) != cudaSuccess)
+        (err = simt::opt_in<dx_weights_kernel<Tl>>(Tl::SMEM_BYTES + 16 * 1024)) != cudaSuccess)
         return err;
     launch_pdl(rows_kernel<Tl>, dim3(mt, tiles(s.f, Tl::BN)), block, Tl::SMEM_BYTES + prefix, st, x, dy,
                a.offsets, s.E, Wgu, Wd, s.d, s.f, dgu);
-    launch_pdl(dx_kernel<Tl>, dim3(mt, tiles(s.d, Tl::BN)), block, Tl::SMEM_BYTES + prefix, st,
-               (const float *)dgu, a.offsets, s.E, Wgu, s.d, s.f, static_cast<float *>(a.dx_perm));
-    const WeightProduct wd = {static_cast<const float *>(a.h_perm), dy, s.f, s.d,
-                              static_cast<float *>(a.dWd)};
-    const WeightProduct wg = {x, dgu, s.d, 2 * s.f, static_cast<float *>(a.dWgu)};
-    auto count = [&](const WeightProduct &w) { return tiles(w.M, Tl::BM) * tiles(w.N, Tl::BN); };
-    launch_pdl(weights_kernel<Tl>, dim3(count(wd) + count(wg), s.E), block, Tl::SMEM_BYTES, st, wd, wg,
-               (int)count(wd), a.offsets);
+    auto product = [&](const float *A, int M, const float *B, int N, void *dW) {
+        return WeightProduct{A, B, M, N, (int)(tiles(M, Tl::BM) * tiles(N, Tl::BN)), static_cast<float *>(dW)};
+    };
+    const WeightProduct wd = product(static_cast<const float *>(a.h_perm), s.f, dy, s.d, a.dWd);
+    const WeightProduct wg = product(x, s.d, dgu, 2 * s.f, a.dWgu);
+    const int64_t dx_blocks = (int64_t)mt * tiles(s.d, Tl::BN);
+    const int64_t blocks = dx_blocks + (int64_t)s.E * (wd.tiles + wg.tiles);
+    if (blocks > INT32_MAX) {
+        set_error_message("experts' gradient tile count exceeds 2^31");
+        return cudaErrorInvalidValue;
+    }
+    launch_pdl(dx_weights_kernel<Tl>, dim3((unsigned)blocks), block, Tl::SMEM_BYTES + prefix, st,
+               (const float *)dgu, a.offsets, s.E, Wgu, s.d, s.f, static_cast<float *>(a.dx_perm),
+               (int)dx_blocks, wd, wg);
     return cudaGetLastError();
 }
 
