@@ -130,6 +130,10 @@ cudaError_t launch_dispatch_backward(const Shape &s, const void *dx_perm, const 
                                      const float *w, const void *x, void *dx, float *dw,
                                      cudaStream_t st);
 
+// fp32: out[t] = add[t] (if given; may be out) + sum_j w[t*k+j] rows[idx[t*k+j]].
+cudaError_t launch_gather_sum_f32(const Shape &s, const float *rows, const int32_t *idx,
+                                  const float *w, const float *add, float *out, cudaStream_t st);
+
 // Operands of the grouped SwiGLU's gradient (see moe_grouped_swiglu_backward).
 struct ExpertsBwd {
     const void *x_perm;

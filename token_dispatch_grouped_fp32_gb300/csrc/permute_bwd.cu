@@ -116,26 +116,30 @@ scatter_rows_kernel(const TA *__restrict__ src, const TA *__restrict__ y_perm,
     if (DOT) dots_store<TPT>(dots, k, dw + t * k);
 }
 
-// dx = the sum of w * row over a token's slots, dw = <x row, row>.
-template <typename TA, int TPT, int U, int SG>
+// dx = the sum of w * row over a token's slots; DOT: dw = <x row, row>, else x
+// (if given) is added to dx.
+template <typename TA, int TPT, int U, int SG, bool DOT>
 __global__ void __launch_bounds__(kThreads)
 gather_rows_scaled_kernel(const TA *__restrict__ dx_perm, const int32_t *__restrict__ pos,
-                          const float *__restrict__ w, const TA *__restrict__ x, int64_t T, int k,
-                          int d, TA *__restrict__ dx, float *__restrict__ dw) {
+                          const float *__restrict__ w, const TA *x, int64_t T, int k, int d, TA *dx,
+                          float *__restrict__ dw) {
     pdl_wait();
     constexpr int EPV = 16 / sizeof(TA);
     __shared__ Dots dots;
     const int64_t t = (int64_t)blockIdx.x * (kThreads / TPT) + threadIdx.x / TPT;
     const int nvec = d / EPV;
-    dots_clear(dots);
-    __syncwarp();
+    if (DOT) {
+        dots_clear(dots);
+        __syncwarp();
+    }
     if (t >= T) return;  // whole groups; TPT = block: the block
     for (int v0 = threadIdx.x % TPT; v0 - (int)(threadIdx.x % TPT) < nvec; v0 += TPT * U) {
         uint4 xv[U];
         float acc[U][EPV];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (v0 + u * TPT < nvec) xv[u] = ldg16(x + t * d + (int64_t)(v0 + u * TPT) * EPV);
+            if ((DOT || x) && v0 + u * TPT < nvec)
+                xv[u] = *reinterpret_cast<const uint4 *>(x + t * d + (int64_t)(v0 + u * TPT) * EPV);
 #pragma unroll
             for (int i = 0; i < EPV; ++i) acc[u][i] = 0.f;
         }
@@ -162,24 +166,32 @@ gather_rows_scaled_kernel(const TA *__restrict__ dx_perm, const int32_t *__restr
                 for (int u = 0; u < U; ++u) {
                     if (v0 + u * TPT >= nvec) continue;
                     float a[EPV], b[EPV];
-                    unpack16(xv[u], a, static_cast<const TA *>(nullptr));
                     unpack16(r[s][u], b, static_cast<const TA *>(nullptr));
+                    if (DOT) {
+                        unpack16(xv[u], a, static_cast<const TA *>(nullptr));
 #pragma unroll
-                    for (int i = 0; i < EPV; ++i) {
-                        part = fmaf(a[i], b[i], part);
-                        acc[u][i] = fmaf(wj[s], b[i], acc[u][i]);
+                        for (int i = 0; i < EPV; ++i) part = fmaf(a[i], b[i], part);
                     }
+#pragma unroll
+                    for (int i = 0; i < EPV; ++i) acc[u][i] = fmaf(wj[s], b[i], acc[u][i]);
                 }
-                dots_add(dots, j0 + s, part);
+                if (DOT) dots_add(dots, j0 + s, part);
             }
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (v0 + u * TPT < nvec)
-                stg16(dx + t * d + (int64_t)(v0 + u * TPT) * EPV,
-                      pack16(acc[u], static_cast<const TA *>(nullptr)));
+        for (int u = 0; u < U; ++u) {
+            if (v0 + u * TPT >= nvec) continue;
+            if (!DOT && x) {
+                float a[EPV];
+                unpack16(xv[u], a, static_cast<const TA *>(nullptr));
+#pragma unroll
+                for (int i = 0; i < EPV; ++i) acc[u][i] += a[i];
+            }
+            stg16(dx + t * d + (int64_t)(v0 + u * TPT) * EPV,
+                  pack16(acc[u], static_cast<const TA *>(nullptr)));
+        }
     }
-    dots_store<TPT>(dots, k, dw + t * k);
+    if (DOT) dots_store<TPT>(dots, k, dw + t * k);
 }
 
 unsigned blocks(int64_t T, int tpt) {
@@ -206,9 +218,15 @@ cudaError_t launch_scatter_v(const Shape &s, const void *src, const void *y_perm
 template <typename TA, int TPT, int U, int SG>
 cudaError_t launch_gather_v(const Shape &s, const void *dx_perm, const int32_t *pos,
                             const float *w, const void *x, void *dx, float *dw, cudaStream_t st) {
-    launch_pdl(gather_rows_scaled_kernel<TA, TPT, U, SG>, dim3(blocks(s.T, TPT)), dim3(kThreads), 0, st,
-               static_cast<const TA *>(dx_perm), pos, w, static_cast<const TA *>(x), s.T, s.k, s.d,
-               static_cast<TA *>(dx), dw);
+    const dim3 grid(blocks(s.T, TPT));
+    const TA *r = static_cast<const TA *>(dx_perm), *xs = static_cast<const TA *>(x);
+    TA *o = static_cast<TA *>(dx);
+    if (dw)
+        launch_pdl(gather_rows_scaled_kernel<TA, TPT, U, SG, true>, grid, dim3(kThreads), 0, st, r, pos,
+                   w, xs, s.T, s.k, s.d, o, dw);
+    else
+        launch_pdl(gather_rows_scaled_kernel<TA, TPT, U, SG, false>, grid, dim3(kThreads), 0, st, r, pos,
+                   w, xs, s.T, s.k, s.d, o, dw);
     return cudaGetLastError();
 }
 
@@ -246,6 +264,12 @@ cudaError_t launch_dispatch_backward(const Shape &s, const void *dx_perm, const 
     if (!w) return launch_combine(s, dx_perm, pos, nullptr, dx, st);
     return s.bf16 ? launch_gather_t<__nv_bfloat16>(s, dx_perm, pos, w, x, dx, dw, st)
                   : launch_gather_t<float>(s, dx_perm, pos, w, x, dx, dw, st);
+}
+
+cudaError_t launch_gather_sum_f32(const Shape &s, const float *rows, const int32_t *idx,
+                                  const float *w, const float *add, float *out, cudaStream_t st) {
+    return launch_gather_t<float>(s, (const void *)rows, idx, w, (const void *)add, (void *)out,
+                                  (float *)nullptr, st);
 }
 
 }  // namespace moe

@@ -18,7 +18,9 @@
 // axis, their sum.  T = 16384, d = 2048, E = 128, k = 8: 70 us, of them about 20 in
 // dx's and 33 in dWr's products (bound by shared memory, see gemm_bwd_tc.cu),
 // where fp32 products on the CUDA cores took 860.
-// fp32 x: the same steps on the CUDA cores (T = 8192, d = 4096, E = 128: 475 us).
+// fp32 x: the same steps on the CUDA cores; renormalised with many experts, dx
+// is the sum of the chosen experts' rows of Wr (T = 8192, d = 4096, k = 8, E =
+// 128: 309 us; with the product over all E 472).
 // At most 8 experts: one pass on the CUDA cores for both types (below).
 #include "common.cuh"
 #include "kernels.h"
@@ -67,6 +69,10 @@ struct TermsArgs {
     int E, k, renorm;
     float *dl, *bias_part;  // [T][E]; [token blocks][E8]
     float *dl8;  // fp32 x only: dl in rows of E8 columns
+    // fp32 x, dx from the chosen rows of Wr: their dl [T][k], and the ids with
+    // -1 for one outside [0, E)
+    float *dlk;
+    int32_t *rows;
     // bf16 x only (dl4 != nullptr): the terms [T][4*E8], Wr [E][d] and its
     // terms [3*E8][d], and the segment boundaries of the two products
     __nv_bfloat16 *dl4, *W3;
@@ -137,8 +143,12 @@ __global__ void __launch_bounds__(kThreads) terms_kernel(TermsArgs a, DevStatus 
             for (int i = lane; i < a.E; i += 32) row[i] *= inv * (0.f - S);
             __syncwarp();
             if (e >= 0) row[e] = expf(L[e] - m) * inv * (dj - S);
-        } else if (e >= 0) {
-            row[e] = wj * (dj - S);
+        } else {
+            if (e >= 0) row[e] = wj * (dj - S);
+            if (a.dlk && lane < a.k) {
+                a.dlk[t * a.k + lane] = wj * (dj - S);
+                a.rows[t * a.k + lane] = e;
+            }
         }
         __syncwarp();
         // the row as floats and as terms, four columns a lane
@@ -471,12 +481,18 @@ route_dx_kernel(const float *__restrict__ dl8, const float *__restrict__ Wr, con
 }
 
 // ------------------------------- host side ---------------------------------
+// fp32 x, renormalised: dx takes k rows of Wr a token instead of all E where
+// that is the lesser: a gathered element costs L2 traffic, about 9 times a
+// multiply-add of the dense product (T = 8192, d = 4096, gathered against dense:
+// E = 128, k = 8 309 us to 472, E = 72 307 to 421, E = 18, k = 2 185 to 227).
+bool gathers_rows(const Shape &s) { return !s.bf16 && s.renorm && s.E >= 9 * s.k; }
+
 struct Plan {
     bool few;  // few_experts_kernel
     int few_cols;  // columns of one of its blocks
     int E8, terms, token_blocks;
     int splits, tokens;  // splits of the token axis in dWr's sum, tokens each
-    size_t dl, W3, all, split_at, bias, part, total;  // workspace offsets
+    size_t dl, dlk, rows, W3, all, split_at, bias, part, total;  // workspace offsets
 };
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -510,6 +526,10 @@ Plan plan(const Shape &s) {
     size_t o = 0;
     p.dl = o;  // bf16 x: four terms of 2 bytes; fp32 x: padded rows
     if (!p.few) o = up256(o + (s.bf16 ? 8 : 4) * (size_t)s.T * p.E8);
+    p.dlk = o;
+    if (!p.few && gathers_rows(s)) o = up256(o + 4 * (size_t)s.P());
+    p.rows = o;
+    if (!p.few && gathers_rows(s)) o = up256(o + 4 * (size_t)s.P());
     p.W3 = o;
     if (s.bf16 && !p.few) o = up256(o + 2 * (size_t)3 * p.E8 * s.d);
     p.all = o;
@@ -565,6 +585,10 @@ cudaError_t launch_products(const Shape &s, const RouteBwd &a, const Plan &p, fl
         t.splits = reinterpret_cast<int32_t *>(ws + p.split_at);
     } else {
         t.dl8 = reinterpret_cast<float *>(ws + p.dl);
+        if (gathers_rows(s)) {
+            t.dlk = reinterpret_cast<float *>(ws + p.dlk);
+            t.rows = reinterpret_cast<int32_t *>(ws + p.rows);
+        }
     }
     const int split_blocks =
         s.bf16 ? (int)(((int64_t)p.E8 * s.d + kSplitCols - 1) / kSplitCols) : 0;
@@ -592,9 +616,17 @@ cudaError_t launch_products(const Shape &s, const RouteBwd &a, const Plan &p, fl
         if ((err = simt::opt_in<route_dx_kernel>(Tl::SMEM_BYTES)) != cudaSuccess ||
             (err = simt::opt_in<dwr_kernel>(Tl::SMEM_BYTES)) != cudaSuccess)
             return err;
-        launch_pdl(route_dx_kernel, dim3((unsigned)((s.T + Tl::BM - 1) / Tl::BM), (s.d + Tl::BN - 1) / Tl::BN),
-                   dim3(simt::kThreads), Tl::SMEM_BYTES, st, (const float *)t.dl8, a.Wr,
-                   static_cast<const float *>(a.dx_in), s.T, s.E, p.E8, s.d, static_cast<float *>(a.dx));
+        if (gathers_rows(s)) {
+            if ((err = launch_gather_sum_f32(s, a.Wr, t.rows, t.dlk, static_cast<const float *>(a.dx_in),
+                                             static_cast<float *>(a.dx), st)) != cudaSuccess)
+                return err;
+        } else {
+            launch_pdl(route_dx_kernel,
+                       dim3((unsigned)((s.T + Tl::BM - 1) / Tl::BM), (s.d + Tl::BN - 1) / Tl::BN),
+                       dim3(simt::kThreads), Tl::SMEM_BYTES, st, (const float *)t.dl8, a.Wr,
+                       static_cast<const float *>(a.dx_in), s.T, s.E, p.E8, s.d,
+                       static_cast<float *>(a.dx));
+        }
         launch_pdl(dwr_kernel, dim3((s.d + Tl::BN - 1) / Tl::BN, (s.E + Tl::BM - 1) / Tl::BM, p.splits),
                    dim3(simt::kThreads), Tl::SMEM_BYTES, st, (const float *)t.dl8,
                    static_cast<const float *>(a.x), s.T, s.E, p.E8, s.d, p.tokens, part);
