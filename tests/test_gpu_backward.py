@@ -230,6 +230,15 @@ def test_experts_backward_larger(moe, counts, d, f):
     check_experts(moe, counts, d, f, torch.bfloat16, seed=6)
 
 
+@pytest.mark.parametrize("counts,d,f", [
+    ([5] * 60 + [0, 9, 1, 40], 96, 360),     # short segments, many columns
+    ([70, 3, 0, 150, 90, 33, 64, 190], 200, 488),
+    ([1030, 970], 1200, 1000),               # the largest tiles, all cut
+    ([600, 1], 200, 200), ([130, 470, 600], 200, 200), ([5000], 64, 64), ([4990], 200, 200)])
+def test_experts_backward_f32_tiles(moe, counts, d, f):
+    check_experts(moe, counts, d, f, torch.float32, seed=7)
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_experts_backward_keeps_segments_apart(moe, dtype):
     """NaN and infinite rows of one expert reach that expert's gradients only."""
@@ -303,6 +312,13 @@ def test_route_backward(moe, T, d, E, k, renorm, dtype):
     total = want + dx_in.double()
     tol = tol + (UB if dtype == torch.bfloat16 else U32) * total.abs()
     assert ((acc.double() - total).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("T,d,E,k", [(1500, 1096, 9, 2), (1400, 1040, 24, 6), (1300, 1032, 40, 8),
+                                     (700, 2064, 72, 15), (200, 4808, 500, 2), (4100, 136, 33, 1)])
+def test_route_backward_f32_tiles(moe, T, d, E, k, renorm):
+    test_route_backward(moe, T, d, E, k, renorm, torch.float32)
 
 
 def test_route_backward_without_bias_output(moe):

@@ -10,10 +10,11 @@
 // gradients.  Every sum is fp32 in a fixed order.
 //
 // Two launches over the tile of simt_gemm.cuh.  T = 64, d = 128, f = 256, E =
-// 8: 22.4 us, latency (tiles of 32 x 32; 64 x 64 without the pipeline 45 to 100;
-// dx and the weights in launches of their own 24).  T = 1024, k = E = 8, d = f =
-// 512 (34 GFLOP): 914 us, 38 TFLOP/s, bound by the multiply-adds and the
-// shared-memory loads beside them (128 x 64 tiles 957, 128 x 128 1491).
+// 8: 14.1 us, latency (one tile shape of 32 x 32 for all products 22.4; dx and
+// the weights in launches of their own 24).  T = 1024, k = E = 8, d = f = 512 (34
+// GFLOP): 838 us, 41 TFLOP/s, bound by the multiply-adds and the instructions
+// beside them (64 x 64 tiles of 4 x 4 micro tiles, g and u apart, unpacked: 914).
+// T = 512, d = f = 488, E = 32, k = 4, routed unevenly: 304 us (508).
 #include "common.cuh"
 #include "kernels.h"
 #include "simt_gemm.cuh"
@@ -67,46 +68,61 @@ __device__ __forceinline__ bool find_tile(const int32_t *offsets, int E, int *s_
     return true;
 }
 
-// Dynamic shared memory: the product's stages, then 2 (E + 1) ints.
+// Dynamic shared memory of a kernel with products of two tile shapes: the larger
+// one's stages; then 2 (E + 1) ints of tile_prefix.
+template <typename A, typename B>
+constexpr int kSmem = A::SMEM_BYTES > B::SMEM_BYTES ? A::SMEM_BYTES : B::SMEM_BYTES;
+
+// g and u are one product over twice the columns, so that x's fragments are read
+// once for both: a thread holds g in its first TN accumulators of a row, u of the
+// same columns in the others.
+template <typename Tl> using Wide = simt::Tile<Tl::BM, 2 * Tl::BN, Tl::TM, 2 * Tl::TN, Tl::VN>;
+
 template <typename Tl>
-__global__ void __launch_bounds__(simt::kThreads)
+__global__ void __launch_bounds__(Tl::THREADS)
 rows_kernel(const float *__restrict__ x, const float *__restrict__ dy,
             const int32_t *__restrict__ offsets, int E, const float *__restrict__ Wgu,
             const float *__restrict__ Wd, int d, int f, float *__restrict__ dgu) {
+    using GU = Wide<Tl>;
+    static_assert(Tl::TN == Tl::VN, "a run of g is followed by u's");
     pdl_wait();
     extern __shared__ __align__(16) float smem[];
     RowTile t;
-    if (!find_tile<Tl::BM>(offsets, E, reinterpret_cast<int *>(smem) + Tl::SMEM_BYTES / 4, blockIdx.x, &t))
+    if (!find_tile<Tl::BM>(offsets, E, reinterpret_cast<int *>(smem) + kSmem<Tl, GU> / 4, blockIdx.x, &t))
         return;
     const int n0 = blockIdx.y * Tl::BN;
     const float *xr = x + (int64_t)t.row0 * d, *yr = dy + (int64_t)t.row0 * d;
     const float *W = Wgu + (int64_t)t.e * d * 2 * f, *Wt = Wd + (int64_t)t.e * f * d;
-    float g[Tl::TM][Tl::TN], u[Tl::TM][Tl::TN], h[Tl::TM][Tl::TN];
-    Tl::zero(g);
-    Tl::zero(u);
+    float gu[Tl::TM][2 * Tl::TN], h[Tl::TM][Tl::TN];  // g, then u
+    GU::zero(gu);
     Tl::zero(h);
     auto rows_of = [&](const float *a) {
         return [=](int m, int k) { return m < t.rows ? a + (int64_t)m * d + k : nullptr; };
     };
-    auto cols_of = [&](const float *b) {
-        return [=](int k, int n) { return n0 + n < f ? b + (int64_t)k * 2 * f + n0 + n : nullptr; };
-    };
-    Tl::template product<true, false, true>(smem, d, rows_of(xr), cols_of(W), g);
-    Tl::template product<true, false, true>(smem, d, rows_of(xr), cols_of(W + f), u);
-    Tl::template product<true, true, true>(smem, d, rows_of(yr), [=](int k, int n) {
+    GU::template product<true, false>(smem, d, rows_of(xr), [=](int k, int n) {
+        const int half = n < Tl::BN ? 0 : 1, c = n0 + n - half * Tl::BN;
+        return c < f ? W + (int64_t)k * 2 * f + half * f + c : nullptr; }, gu);
+    Tl::template product<true, true>(smem, d, rows_of(yr), [=](int k, int n) {
         return n0 + n < f ? Wt + (int64_t)(n0 + n) * d + k : nullptr; }, h);
 #pragma unroll
     for (int i = 0; i < Tl::TM; ++i) {
-        const int m = Tl::template row<true>(i);
+        const int m = Tl::row(i);
         if (m >= t.rows) continue;
         float *o = dgu + (int64_t)(t.row0 + m) * 2 * f;
 #pragma unroll
-        for (int j = 0; j < Tl::TN; ++j) {
-            const int n = n0 + Tl::template col<true>(j);
+        for (int j = 0; j < Tl::TN; j += Tl::VN) {
+            const int n = n0 + Tl::col(j);
             if (n >= f) continue;
-            const float s = 1.f / (1.f + expf(-g[i][j]));
-            o[n] = h[i][j] * u[i][j] * s * (1.f + g[i][j] * (1.f - s));
-            o[f + n] = h[i][j] * g[i][j] * s;
+            float dg[Tl::VN], du[Tl::VN];
+#pragma unroll
+            for (int l = 0; l < Tl::VN; ++l) {
+                const float g = gu[i][j + l], u = gu[i][Tl::TN + j + l], dh = h[i][j + l];
+                const float s = 1.f / (1.f + expf(-g));
+                dg[l] = dh * u * s * (1.f + g * (1.f - s));
+                du[l] = dh * g * s;
+            }
+            Tl::store(o + n, dg);
+            Tl::store(o + f + n, du);
         }
     }
 }
@@ -121,96 +137,153 @@ struct WeightProduct {
 // dx and both weight gradients, none of which reads another's output, in one
 // launch: blocks below dx_blocks are dx's tiles (column tiles fastest), whose
 // chain over 2f is the longest, then every expert's tiles of wd and wg.
-template <typename Tl>
-__global__ void __launch_bounds__(simt::kThreads)
+template <typename X, typename W>
+__global__ void __launch_bounds__(W::THREADS)
 dx_weights_kernel(const float *__restrict__ dgu, const int32_t *__restrict__ offsets, int E,
                   const float *__restrict__ Wgu, int d, int f, float *__restrict__ dx, int dx_blocks,
                   WeightProduct wd, WeightProduct wg) {
     pdl_wait();
     extern __shared__ __align__(16) float smem[];
-    float acc[Tl::TM][Tl::TN];
-    Tl::zero(acc);
+    static_assert(X::THREADS == W::THREADS, "one block size");
     if ((int)blockIdx.x < dx_blocks) {
-        const int nt = (d + Tl::BN - 1) / Tl::BN;
+        const int nt = (d + X::BN - 1) / X::BN;
         RowTile t;
-        if (!find_tile<Tl::BM>(offsets, E, reinterpret_cast<int *>(smem) + Tl::SMEM_BYTES / 4,
+        if (!find_tile<X::BM>(offsets, E, reinterpret_cast<int *>(smem) + kSmem<X, W> / 4,
                                (int)blockIdx.x / nt, &t))
             return;
-        const int n0 = (int)blockIdx.x % nt * Tl::BN, K = 2 * f;
-        const float *a = dgu + (int64_t)t.row0 * K, *W = Wgu + (int64_t)t.e * d * K;
-        Tl::template product<true, true, true>(
+        float acc[X::TM][X::TN];
+        X::zero(acc);
+        const int n0 = (int)blockIdx.x % nt * X::BN, K = 2 * f;
+        const float *a = dgu + (int64_t)t.row0 * K, *w = Wgu + (int64_t)t.e * d * K;
+        X::template product<true, true>(
             smem, K, [=](int m, int k) { return m < t.rows ? a + (int64_t)m * K + k : nullptr; },
-            [=](int k, int n) { return n0 + n < d ? W + (int64_t)(n0 + n) * K + k : nullptr; }, acc);
-#pragma unroll
-        for (int i = 0; i < Tl::TM; ++i)
-#pragma unroll
-            for (int j = 0; j < Tl::TN; ++j) {
-                const int m = Tl::template row<true>(i), n = n0 + Tl::template col<true>(j);
-                if (m < t.rows && n < d) dx[(int64_t)(t.row0 + m) * d + n] = acc[i][j];
-            }
+            [=](int k, int n) { return n0 + n < d ? w + (int64_t)(n0 + n) * K + k : nullptr; }, acc);
+        X::each_run(acc, [&](int m, int c, const float *v) {
+            if (m < t.rows && n0 + c < d) X::store(dx + (int64_t)(t.row0 + m) * d + n0 + c, v);
+        });
         return;
     }
     const int per = wd.tiles + wg.tiles, b = (int)blockIdx.x - dx_blocks;
     const int e = b / per, g = b % per;
     const WeightProduct &p = g < wd.tiles ? wd : wg;
     const int tile = g < wd.tiles ? g : g - wd.tiles;
-    const int nt = (p.N + Tl::BN - 1) / Tl::BN;
-    const int m0 = tile / nt * Tl::BM, n0 = tile % nt * Tl::BN, M = p.M, N = p.N;
+    const int nt = (p.N + W::BN - 1) / W::BN;
+    const int m0 = tile / nt * W::BM, n0 = tile % nt * W::BN, M = p.M, N = p.N;
     const int r0 = offsets[e], rows = offsets[e + 1] - r0;
     const float *A = p.A + (int64_t)r0 * M, *B = p.B + (int64_t)r0 * N;
-    Tl::template product<false, false, false>(
+    float acc[W::TM][W::TN];
+    W::zero(acc);
+    W::template product<false, false>(
         smem, rows, [=](int m, int k) { return m0 + m < M ? A + (int64_t)k * M + m0 + m : nullptr; },
         [=](int k, int n) { return n0 + n < N ? B + (int64_t)k * N + n0 + n : nullptr; }, acc);
     float *o = p.dW + (int64_t)e * M * N;
-#pragma unroll
-    for (int i = 0; i < Tl::TM; ++i)
-#pragma unroll
-        for (int j = 0; j < Tl::TN; ++j) {
-            const int m = m0 + Tl::template row<false>(i), n = n0 + Tl::template col<false>(j);
-            if (m < M && n < N) o[(int64_t)m * N + n] = acc[i][j];
-        }
+    W::each_run(acc, [&](int m, int c, const float *v) {
+        if (m0 + m < M && n0 + c < N) W::store(o + (int64_t)(m0 + m) * N + n0 + c, v);
+    });
 }
 
-template <typename Tl> cudaError_t launch_t(const Shape &s, const ExpertsBwd &a, cudaStream_t st) {
-    const float *x = static_cast<const float *>(a.x_perm), *dy = static_cast<const float *>(a.dy_perm);
-    const float *Wgu = static_cast<const float *>(a.Wgu), *Wd = static_cast<const float *>(a.Wd);
-    float *dgu = static_cast<float *>(a.ws);
-    const int64_t P = s.P();
-    const unsigned mt = (unsigned)((P + Tl::BM - 1) / Tl::BM + (P < s.E ? P : s.E));
-    const size_t prefix = sizeof(int) * (2 * (size_t)s.E + 2);
-    auto tiles = [](int n, int b) { return (unsigned)((n + b - 1) / b); };
-    const dim3 block(simt::kThreads);
-    cudaError_t err;
-    if ((err = simt::opt_in<rows_kernel<Tl>>(Tl::SMEM_BYTES + 16 * 1024)) != cudaSuccess ||
-        (err = simt::opt_in<dx_weights_kernel<Tl>>(Tl::SMEM_BYTES + 16 * 1024)) != cudaSuccess)
-        return err;
-    launch_pdl(rows_kernel<Tl>, dim3(mt, tiles(s.f, Tl::BN)), block, Tl::SMEM_BYTES + prefix, st, x, dy,
-               a.offsets, s.E, Wgu, Wd, s.d, s.f, dgu);
-    auto product = [&](const float *A, int M, const float *B, int N, void *dW) {
-        return WeightProduct{A, B, M, N, (int)(tiles(M, Tl::BM) * tiles(N, Tl::BN)), static_cast<float *>(dW)};
+unsigned tiles(int n, int b) { return (unsigned)((n + b - 1) / b); }
+// Row tiles at most: a partial one for each expert with rows.
+unsigned row_tiles_most(const Shape &s, int b) {
+    return (unsigned)((s.P() + b - 1) / b + (s.P() < s.E ? s.P() : s.E));
+}
+constexpr int kPrefixMax = 16 * 1024;
+size_t prefix_bytes(const Shape &s) { return sizeof(int) * (2 * (size_t)s.E + 2); }
+
+// 128 threads each.  Rows of the segment x columns:
+using Tiny = simt::Tile<16, 32, 2, 2>;    // the most blocks, six stages: short chains of latency
+using Short = simt::Tile<16, 64, 2, 4>;
+using Mid = simt::Tile<32, 64, 4, 4>;
+using Tall = simt::Tile<64, 64, 8, 4>;    // the largest whose g, u and dh fit a thread
+using Large = simt::Tile<64, 128, 8, 8>;
+
+template <typename R> cudaError_t launch_rows(const Shape &s, const ExpertsBwd &a, cudaStream_t st) {
+    constexpr int smem = kSmem<R, Wide<R>>;
+    cudaError_t err = simt::opt_in<rows_kernel<R>>(smem + kPrefixMax);
+    if (err != cudaSuccess) return err;
+    launch_pdl(rows_kernel<R>, dim3(row_tiles_most(s, R::BM), tiles(s.f, R::BN)), dim3(R::THREADS),
+               smem + prefix_bytes(s), st, static_cast<const float *>(a.x_perm),
+               static_cast<const float *>(a.dy_perm), a.offsets, s.E,
+               static_cast<const float *>(a.Wgu), static_cast<const float *>(a.Wd), s.d, s.f,
+               static_cast<float *>(a.ws));
+    return cudaGetLastError();
+}
+
+template <typename X, typename W>
+cudaError_t launch_dx_weights(const Shape &s, const ExpertsBwd &a, cudaStream_t st) {
+    constexpr int smem = kSmem<X, W>;
+    cudaError_t err = simt::opt_in<dx_weights_kernel<X, W>>(smem + kPrefixMax);
+    if (err != cudaSuccess) return err;
+    const float *dgu = static_cast<const float *>(a.ws);
+    auto product = [&](const void *A, int M, const void *B, int N, void *dW) {
+        return WeightProduct{static_cast<const float *>(A), static_cast<const float *>(B), M, N,
+                             (int)(tiles(M, W::BM) * tiles(N, W::BN)), static_cast<float *>(dW)};
     };
-    const WeightProduct wd = product(static_cast<const float *>(a.h_perm), s.f, dy, s.d, a.dWd);
-    const WeightProduct wg = product(x, s.d, dgu, 2 * s.f, a.dWgu);
-    const int64_t dx_blocks = (int64_t)mt * tiles(s.d, Tl::BN);
+    const WeightProduct wd = product(a.h_perm, s.f, a.dy_perm, s.d, a.dWd);
+    const WeightProduct wg = product(a.x_perm, s.d, dgu, 2 * s.f, a.dWgu);
+    const int64_t dx_blocks = (int64_t)row_tiles_most(s, X::BM) * tiles(s.d, X::BN);
     const int64_t blocks = dx_blocks + (int64_t)s.E * (wd.tiles + wg.tiles);
     if (blocks > INT32_MAX) {
         set_error_message("experts' gradient tile count exceeds 2^31");
         return cudaErrorInvalidValue;
     }
-    launch_pdl(dx_weights_kernel<Tl>, dim3((unsigned)blocks), block, Tl::SMEM_BYTES + prefix, st,
-               (const float *)dgu, a.offsets, s.E, Wgu, s.d, s.f, static_cast<float *>(a.dx_perm),
-               (int)dx_blocks, wd, wg);
+    launch_pdl(dx_weights_kernel<X, W>, dim3((unsigned)blocks), dim3(W::THREADS), smem + prefix_bytes(s), st,
+               dgu, a.offsets, s.E, static_cast<const float *>(a.Wgu), s.d, s.f,
+               static_cast<float *>(a.dx_perm), (int)dx_blocks, wd, wg);
     return cudaGetLastError();
+}
+
+// Tiles of a product over the rows of all segments: each expert's last one is
+// half full on average.
+int64_t row_tiles(const Shape &s, int bm, int columns) {
+    const int64_t experts = s.P() < s.E ? s.P() : s.E;
+    return (s.P() / bm + (experts + 1) / 2) * columns;
 }
 
 }  // namespace
 
+// The tiles, by what runs out first.  Few blocks, or segments shorter than a
+// tile: smaller tiles; else the larger micro tile, which reads less shared
+// memory per multiply-add.  Measured (us), rows an expert r:
+//   rows_kernel, Tiny / Short / Mid / Tall
+//     T = 64, d = 128, f = 256, E = 8, k = 2               7.0 / 9.5 / 13.4 / 19
+//     T = 64, d = f = 512, E = 128, k = 8 (r = 4)          147 / 126 / 193 / 326
+//     T = 1024, d = 256, f = 512, E = 8, k = 2 (r = 256)   73 / 64 / 60 / 76
+//     T = 1024, d = f = 512, E = 128, k = 8 (r = 64)       606 / 527 / 452 / 466
+//     T = 1024, d = f = 512, E = k = 8 (r = 1024)          530 / 458 / 373 / 329
+//   dx in Tiny / Mid / Large tiles, the weight gradients' Large, same shapes
+//     8.3 / 18 / 48,  189 / 227 / 336,  94 / 85 / 105,  741 / 656 / 666,  686 / 567 / 508
+//   weight gradients in Tiny / Mid / Large tiles, dx's Tiny
+//     T = 64, d = 128, f = 256, E = 8, k = 2               11.0 / 11.0 / 8.3
+//     T = 300, d = f = 128, E = 4, k = 2 (r = 150)         9.6 / 7.9 / 13.9
+//     T = 200, d = f = 512, E = 4, k = 2 (r = 100)         59.5 / 45.1 / 41.4
 cudaError_t launch_experts_backward_f32(const Shape &s, const ExpertsBwd &a, cudaStream_t st) {
-    using L = simt::Large;
-    const int64_t row_tiles = (s.P() + L::BM - 1) / L::BM;
-    // the row products have the fewest tiles
-    const bool large = row_tiles * ((s.d + L::BN - 1) / L::BN) >= 2 * 152;
-    return large ? launch_t<simt::Large>(s, a, st) : launch_t<simt::Small>(s, a, st);
+    constexpr int kSms = 152;
+    const int64_t r = s.P() / s.E;
+    cudaError_t err;
+    if (r < 16 || row_tiles(s, Mid::BM, tiles(s.f, Mid::BN)) < kSms)
+        err = row_tiles(s, Tiny::BM, tiles(s.f, Tiny::BN)) < 2 * kSms ? launch_rows<Tiny>(s, a, st)
+                                                                     : launch_rows<Short>(s, a, st);
+    else
+        err = r >= 256 && row_tiles(s, Tall::BM, tiles(s.f, Tall::BN)) >= 3 * kSms
+                  ? launch_rows<Tall>(s, a, st)
+                  : launch_rows<Mid>(s, a, st);
+    if (err != cudaSuccess) return err;
+    auto weight_tiles = [&](int bm, int bn) {
+        return (int64_t)s.E * (tiles(s.f, bm) * tiles(s.d, bn) + tiles(s.d, bm) * tiles(2 * s.f, bn));
+    };
+    // a weight gradient's chain is as long as its segment
+    const bool w_large = r <= 64 || weight_tiles(Large::BM, Large::BN) >= kSms;
+    const bool w_mid = weight_tiles(Mid::BM, Mid::BN) >= kSms;
+    if (r < 16 || row_tiles(s, Mid::BM, tiles(s.d, Mid::BN)) < kSms)
+        return w_large ? launch_dx_weights<Tiny, Large>(s, a, st)
+               : w_mid ? launch_dx_weights<Tiny, Mid>(s, a, st)
+                       : launch_dx_weights<Tiny, Tiny>(s, a, st);
+    if (!w_large)
+        return w_mid ? launch_dx_weights<Mid, Mid>(s, a, st) : launch_dx_weights<Mid, Tiny>(s, a, st);
+    return r >= 256 && row_tiles(s, Large::BM, tiles(s.d, Large::BN)) >= 2 * kSms
+               ? launch_dx_weights<Large, Large>(s, a, st)
+               : launch_dx_weights<Mid, Large>(s, a, st);
 }
 
 }  // namespace moe

@@ -18,9 +18,10 @@
 // axis, their sum.  T = 16384, d = 2048, E = 128, k = 8: 70 us, of them about 20 in
 // dx's and 33 in dWr's products (bound by shared memory, see gemm_bwd_tc.cu),
 // where fp32 products on the CUDA cores took 860.
-// fp32 x: the same steps on the CUDA cores; renormalised with many experts, dx
-// is the sum of the chosen experts' rows of Wr (T = 8192, d = 4096, k = 8, E =
-// 128: 309 us; with the product over all E 472).
+// fp32 x: the same steps on the CUDA cores, bound by the multiply-adds (T = 8192,
+// d = 4096, k = 8, E = 64 without renormalisation: 187 us, dx 97 and dWr 84);
+// renormalised with many experts, dx is the sum of the chosen experts' rows of
+// Wr (145 us; E = 128 222, with the product over all E 348).
 // At most 8 experts: one pass on the CUDA cores for both types (below).
 #include "common.cuh"
 #include "kernels.h"
@@ -33,7 +34,6 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxTokenBlocks = 152 * 8;
 constexpr int kSplitCols = 4 * kThreads;  // elements of Wr per block
-using Tl = simt::Large;
 
 template <bool MAX> __device__ __forceinline__ float warp_all(float v) {
 #pragma unroll
@@ -434,7 +434,8 @@ few_experts_kernel(FewArgs a, DevStatus ds) {
 // ------------------------- fp32 x, on the CUDA cores ------------------------
 // Over dl8, the rows of dl padded to E8 columns.
 // part[split][e][c]: the sum over the tokens of one split.
-__global__ void __launch_bounds__(simt::kThreads)
+template <typename Tl>
+__global__ void __launch_bounds__(Tl::THREADS)
 dwr_kernel(const float *__restrict__ dl8, const float *__restrict__ x, int64_t T, int E, int E8,
            int d, int tokens, float *__restrict__ part) {
     pdl_wait();
@@ -444,19 +445,17 @@ dwr_kernel(const float *__restrict__ dl8, const float *__restrict__ x, int64_t T
     const int K = (int)min((int64_t)tokens, T - t0);
     float acc[Tl::TM][Tl::TN];
     Tl::zero(acc);
-    Tl::product<false, false, false>(
+    Tl::product<false, false>(
         smem, K, [=](int m, int k) { return e0 + m < E8 ? dl8 + (t0 + k) * E8 + e0 + m : nullptr; },
         [=](int k, int n) { return n0 + n < d ? x + (t0 + k) * d + n0 + n : nullptr; }, acc);
-#pragma unroll
-    for (int i = 0; i < Tl::TM; ++i)
-#pragma unroll
-        for (int j = 0; j < Tl::TN; ++j) {
-            const int e = e0 + Tl::row<false>(i), n = n0 + Tl::col<false>(j);
-            if (e < E && n < d) part[((int64_t)blockIdx.z * E + e) * d + n] = acc[i][j];
-        }
+    Tl::each_run(acc, [&](int m, int c, const float *v) {
+        const int e = e0 + m, n = n0 + c;
+        if (e < E && n < d) Tl::store(part + ((int64_t)blockIdx.z * E + e) * d + n, v);
+    });
 }
 
-__global__ void __launch_bounds__(simt::kThreads)
+template <typename Tl>
+__global__ void __launch_bounds__(Tl::THREADS)
 route_dx_kernel(const float *__restrict__ dl8, const float *__restrict__ Wr, const float *dx_in,
                 int64_t T, int E, int E8, int d, float *dx) {
     pdl_wait();
@@ -465,27 +464,58 @@ route_dx_kernel(const float *__restrict__ dl8, const float *__restrict__ Wr, con
     const int n0 = blockIdx.y * Tl::BN;
     float acc[Tl::TM][Tl::TN];
     Tl::zero(acc);
-    Tl::product<true, false, false>(
+    Tl::product<true, false>(
         smem, E8, [=](int m, int k) { return t0 + m < T ? dl8 + (t0 + m) * E8 + k : nullptr; },
         [=](int k, int n) { return k < E && n0 + n < d ? Wr + (int64_t)k * d + n0 + n : nullptr; }, acc);
-#pragma unroll
-    for (int i = 0; i < Tl::TM; ++i)
-#pragma unroll
-        for (int j = 0; j < Tl::TN; ++j) {
-            const int64_t t = t0 + Tl::row<true>(i);
-            const int n = n0 + Tl::col<false>(j);
-            if (t >= T || n >= d) continue;
-            const float v = acc[i][j];
-            dx[t * d + n] = dx_in ? v + dx_in[t * d + n] : v;
+    Tl::each_run(acc, [&](int m, int c, const float *v) {
+        const int64_t t = t0 + m;
+        const int n = n0 + c;
+        if (t >= T || n >= d) return;
+        float4 o = make_float4(v[0], v[1], v[2], v[3]);
+        if (dx_in) {
+            const float4 in = *reinterpret_cast<const float4 *>(dx_in + t * d + n);
+            o = make_float4(o.x + in.x, o.y + in.y, o.z + in.z, o.w + in.w);
         }
+        *reinterpret_cast<float4 *>(dx + t * d + n) = o;
+    });
 }
 
 // ------------------------------- host side ---------------------------------
 // fp32 x, renormalised: dx takes k rows of Wr a token instead of all E where
-// that is the lesser: a gathered element costs L2 traffic, about 9 times a
-// multiply-add of the dense product (T = 8192, d = 4096, gathered against dense:
-// E = 128, k = 8 309 us to 472, E = 72 307 to 421, E = 18, k = 2 185 to 227).
-bool gathers_rows(const Shape &s) { return !s.bf16 && s.renorm && s.E >= 9 * s.k; }
+// that is the lesser (T = 8192, d = 4096, whole gradient, product over all E
+// against gathered: k = 8, E = 64 187 us to 145, E = 48 169 to 146, E = 32 112 to 115;
+// k = 4, E = 24 104 to 98, E = 16 78 to 77).
+bool gathers_rows(const Shape &s) { return !s.bf16 && s.renorm && s.E >= 5 * s.k; }
+
+// dx's tiles: tokens x columns (T = 8192, d = 4096, E = 64: large 97 us, small 107;
+// T = 512, d = 1024: 6.8 and 4.7, too few blocks).
+using DxLarge = simt::Tile<64, 128, 8, 8>;
+using DxSmall = simt::Tile<64, 64, 4, 4>;
+template <typename Tl> int64_t dx_tiles(const Shape &s) {
+    return (s.T + Tl::BM - 1) / Tl::BM * ((s.d + Tl::BN - 1) / Tl::BN);
+}
+
+// dWr's tiles: experts x columns, by the experts there are (T = 8192, d = 4096:
+// E = 16 35 us, 32 53, 64 82, 128 157; tiles of 64 experts take 82 at any E <= 64).
+using Dwr16 = simt::Tile<16, 256, 4, 4>;
+using Dwr32 = simt::Tile<32, 128, 8, 4>;
+using Dwr64 = simt::Tile<64, 128, 8, 4>;
+enum DwrTile { kDwr16, kDwr32, kDwr64 };
+DwrTile dwr_tile(const Shape &s) { return s.E <= 16 ? kDwr16 : s.E <= 32 ? kDwr32 : kDwr64; }
+// Splits of the token axis that fill the SMs' slots for blocks: one block more
+// than the slots costs a second round (T = 8192, d = 4096, E = 64 in 64 x 64 tiles:
+// 7 splits, 448 blocks, 106 us; 5 splits, three blocks on some SMs and two on the
+// others, 149).  With more tiles than slots, the number whose rounds are fullest.
+template <typename Tl> int64_t dwr_splits(const Shape &s) {
+    const int64_t slots = 152 * (227 * 1024 / (Tl::SMEM_BYTES + 1024));
+    const int64_t t = (int64_t)((s.E + Tl::BM - 1) / Tl::BM) * ((s.d + Tl::BN - 1) / Tl::BN);
+    int64_t best = slots / t < 1 ? 1 : slots / t;
+    const int64_t least = best;
+    for (int64_t n = least + 1; n <= least + 4; ++n)  // 5 % for the larger sum of parts
+        if ((t * n + slots - 1) / slots * best * 105 < (t * best + slots - 1) / slots * n * 100)
+            best = n;
+    return best;
+}
 
 struct Plan {
     bool few;  // few_experts_kernel
@@ -515,8 +545,10 @@ Plan plan(const Shape &s) {
     } else if (s.bf16) {
         want = route_backward_splits(s.T, s.d, 3 * p.E8);
     } else {
-        const int64_t tiles = (int64_t)((s.E + 63) / 64) * ((s.d + 63) / 64);
-        want = (2 * 152 + tiles - 1) / tiles;
+        const DwrTile tile = dwr_tile(s);
+        want = tile == kDwr64 ? dwr_splits<Dwr64>(s)
+               : tile == kDwr32 ? dwr_splits<Dwr32>(s)
+                                : dwr_splits<Dwr16>(s);
         const int64_t most = (s.T + 63) / 64;
         want = want < 1 ? 1 : want > most ? most : want;
     }
@@ -556,6 +588,28 @@ cudaError_t launch_few(const Shape &s, const RouteBwd &a, const Plan &p, float *
     if (err != cudaSuccess) return err;
     return s.bf16 ? launch_pdl(few_experts_kernel<__nv_bfloat16>, grid, block, ring, st, f, ds)
                   : launch_pdl(few_experts_kernel<float>, grid, block, ring, st, f, ds);
+}
+
+template <typename Tl>
+cudaError_t launch_dx(const Shape &s, const RouteBwd &a, const Plan &p, const float *dl8, cudaStream_t st) {
+    cudaError_t err = simt::opt_in<route_dx_kernel<Tl>>(Tl::SMEM_BYTES);
+    if (err != cudaSuccess) return err;
+    launch_pdl(route_dx_kernel<Tl>,
+               dim3((unsigned)((s.T + Tl::BM - 1) / Tl::BM), (s.d + Tl::BN - 1) / Tl::BN),
+               dim3(Tl::THREADS), Tl::SMEM_BYTES, st, dl8, a.Wr,
+               static_cast<const float *>(a.dx_in), s.T, s.E, p.E8, s.d, static_cast<float *>(a.dx));
+    return cudaGetLastError();
+}
+
+template <typename Tl>
+cudaError_t launch_dwr(const Shape &s, const RouteBwd &a, const Plan &p, const float *dl8, float *part,
+                       cudaStream_t st) {
+    cudaError_t err = simt::opt_in<dwr_kernel<Tl>>(Tl::SMEM_BYTES);
+    if (err != cudaSuccess) return err;
+    launch_pdl(dwr_kernel<Tl>, dim3((s.d + Tl::BN - 1) / Tl::BN, (s.E + Tl::BM - 1) / Tl::BM, p.splits),
+               dim3(Tl::THREADS), Tl::SMEM_BYTES, st, dl8,
+               static_cast<const float *>(a.x), s.T, s.E, p.E8, s.d, p.tokens, part);
+    return cudaGetLastError();
 }
 
 cudaError_t launch_products(const Shape &s, const RouteBwd &a, const Plan &p, float *part,
@@ -613,23 +667,20 @@ cudaError_t launch_products(const Shape &s, const RouteBwd &a, const Plan &p, fl
         r.part = part;
         if ((err = launch_route_backward_tc(s, r, ds, st)) != cudaSuccess) return err;
     } else {
-        if ((err = simt::opt_in<route_dx_kernel>(Tl::SMEM_BYTES)) != cudaSuccess ||
-            (err = simt::opt_in<dwr_kernel>(Tl::SMEM_BYTES)) != cudaSuccess)
-            return err;
         if (gathers_rows(s)) {
             if ((err = launch_gather_sum_f32(s, a.Wr, t.rows, t.dlk, static_cast<const float *>(a.dx_in),
                                              static_cast<float *>(a.dx), st)) != cudaSuccess)
                 return err;
         } else {
-            launch_pdl(route_dx_kernel,
-                       dim3((unsigned)((s.T + Tl::BM - 1) / Tl::BM), (s.d + Tl::BN - 1) / Tl::BN),
-                       dim3(simt::kThreads), Tl::SMEM_BYTES, st, (const float *)t.dl8, a.Wr,
-                       static_cast<const float *>(a.dx_in), s.T, s.E, p.E8, s.d,
-                       static_cast<float *>(a.dx));
+            err = dx_tiles<DxLarge>(s) >= 152 ? launch_dx<DxLarge>(s, a, p, t.dl8, st)
+                                              : launch_dx<DxSmall>(s, a, p, t.dl8, st);
+            if (err != cudaSuccess) return err;
         }
-        launch_pdl(dwr_kernel, dim3((s.d + Tl::BN - 1) / Tl::BN, (s.E + Tl::BM - 1) / Tl::BM, p.splits),
-                   dim3(simt::kThreads), Tl::SMEM_BYTES, st, (const float *)t.dl8,
-                   static_cast<const float *>(a.x), s.T, s.E, p.E8, s.d, p.tokens, part);
+        const DwrTile tile = dwr_tile(s);
+        err = tile == kDwr64 ? launch_dwr<Dwr64>(s, a, p, t.dl8, part, st)
+              : tile == kDwr32 ? launch_dwr<Dwr32>(s, a, p, t.dl8, part, st)
+                               : launch_dwr<Dwr16>(s, a, p, t.dl8, part, st);
+        if (err != cudaSuccess) return err;
     }
     return cudaGetLastError();
 }

@@ -13,36 +13,49 @@
 namespace moe {
 namespace simt {
 
-constexpr int kThreads = 256;
-constexpr int BK = 32;      // k per stage
-constexpr int kStages = 3;  // stages in flight (cp.async)
+constexpr int BK = 32;  // k per stage
 
 __device__ __forceinline__ void copy16_or_zero(float *dst, const float *src) {
     if (src) tc::cp_async16(tc::smem_u32(dst), src);
     else *reinterpret_cast<float4 *>(dst) = make_float4(0.f, 0.f, 0.f, 0.f);
 }
+template <int V> __device__ __forceinline__ void lds(float *v, const float *s) {
+    if constexpr (V == 4) *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(s);
+    else *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(s);
+}
 
-// BM x BN tile of 256 threads, TM x TN elements each.  A k-contiguous operand
-// is staged as [rows][BK], the other kind as [BK][columns], both in rows of
-// 16 bytes more, so that a thread's four elements along the contiguous axis
-// are one shared-memory load and a warp's loads fall into different banks.
-template <int BM_, int BN_> struct Tile {
-    static constexpr int BM = BM_, BN = BN_, TM = BM / 16, TN = BN / 16;
-    static constexpr int RG = 16, CG = 16;
-    static constexpr int A_FLOATS = BM * BK + 4 * (BM > BK ? BM : BK);
-    static constexpr int B_FLOATS = BN * BK + 4 * (BN > BK ? BN : BK);
-    static constexpr int SMEM_BYTES = kStages * (A_FLOATS + B_FLOATS) * (int)sizeof(float);
+// BM x BN tile, TM x TN elements a thread, in runs of V (four, or two where a
+// thread has only two) that lie next to each other: every read of shared memory
+// is a vector.  A k-contiguous operand is staged as [rows][BK], 16-byte chunk c of
+// row r at c ^ (r / V % 8), so that threads reading the same k of neighbouring
+// runs meet different banks; the other kind as [BK][columns].
+template <int BM_, int BN_, int TM_, int TN_, int VN_ = (TN_ < 4 ? TN_ : 4)> struct Tile {
+    static constexpr int BM = BM_, BN = BN_, TM = TM_, TN = TN_;
+    static constexpr int RG = BM / TM, CG = BN / TN, THREADS = RG * CG;
+    static constexpr int VM = TM < 4 ? TM : 4, VN = VN_;
+    static constexpr int STAGES = BM * BN <= 16 * 32 ? 6 : 3;  // in flight (cp.async)
+    static constexpr int A_FLOATS = BM * BK, B_FLOATS = BN * BK;
+    static constexpr int SMEM_BYTES = STAGES * (A_FLOATS + B_FLOATS) * (int)sizeof(float);
 
-    // Element (i, j) of this thread.  A_K: A is k-contiguous.  Columns are
-    // strided where an operand of the tile's products is a k-contiguous B,
-    // else consecutive.
-    template <bool A_K> static __device__ __forceinline__ int row(int i) {
-        const int ty = (int)threadIdx.x / CG;
-        return A_K ? ty + i * RG : ty * TM + i;
+    static_assert(TM % VM == 0 && TN % VN == 0 && VN % 2 == 0 && VN <= 4 && BM % 4 == 0 && BN % 4 == 0, "");
+
+    // Element (i, j) of this thread.
+    static __device__ __forceinline__ int row(int i) {
+        return i / VM * (RG * VM) + (int)threadIdx.x / CG * VM + i % VM;
     }
-    template <bool STRIDED> static __device__ __forceinline__ int col(int j) {
-        const int tx = (int)threadIdx.x % CG;
-        return STRIDED ? tx + j * CG : tx * TN + j;
+    static __device__ __forceinline__ int col(int j) {
+        return j / VN * (CG * VN) + (int)threadIdx.x % CG * VN + j % VN;
+    }
+    // f(row, col, run) for each run of VN elements.
+    template <typename F> static __device__ __forceinline__ void each_run(const float (&acc)[TM][TN], F f) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; j += VN) f(row(i), col(j), &acc[i][j]);
+    }
+    static __device__ __forceinline__ void store(float *dst, const float *v) {
+        if constexpr (VN == 4) *reinterpret_cast<float4 *>(dst) = make_float4(v[0], v[1], v[2], v[3]);
+        else *reinterpret_cast<float2 *>(dst) = make_float2(v[0], v[1]);
     }
     static __device__ __forceinline__ void zero(float (&acc)[TM][TN]) {
 #pragma unroll
@@ -51,87 +64,84 @@ template <int BM_, int BN_> struct Tile {
             for (int j = 0; j < TN; ++j) acc[i][j] = 0.f;
     }
 
+    // Stages rows k0 .. k0 + BK - 1 of k of an operand with N rows or columns.
+    template <bool KC, int N, int V, typename L>
+    static __device__ __forceinline__ void stage(float *dst, int k0, int K, L at) {
+        constexpr int C = (KC ? BK : N) / 4, ALL = N * BK / 4;  // chunks of a row, and in all
+#pragma unroll
+        for (int r = 0; r < (ALL + THREADS - 1) / THREADS; ++r) {
+            const int i = (int)threadIdx.x + r * THREADS;
+            if (ALL % THREADS && i >= ALL) break;
+            const int o = i / C, c = i % C;
+            const int m = KC ? o : 4 * c, k = k0 + (KC ? 4 * c : o);
+            copy16_or_zero(dst + (KC ? o * BK + 4 * (c ^ (o / V % 8)) : 4 * i), k < K ? at(m, k) : nullptr);
+        }
+    }
+    // v[i][q]: element at(i) of the operand, k = kk + q, q < 4.
+    template <bool KC, int N, int T, int V, typename AT>
+    static __device__ __forceinline__ void fragment(const float *src, int kk, float (&v)[T][4], AT at) {
+        if constexpr (KC) {
+#pragma unroll
+            for (int i = 0; i < T; ++i) lds<4>(v[i], src + at(i) * BK + 4 * (kk / 4 ^ (at(i) / V % 8)));
+        } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int i = 0; i < T; i += V) {
+                    float w[V];
+                    lds<V>(w, src + (kk + q) * N + at(i));
+#pragma unroll
+                    for (int l = 0; l < V; ++l) v[i + l][q] = w[l];
+                }
+        }
+    }
+
     // la(m, k) / lb(k, n): address of four consecutive elements (along k for
     // a k-contiguous operand, else along m / n), or nullptr.  K: any; a
     // k-contiguous operand has K a multiple of 4.
-    template <bool A_K, bool B_K, bool STRIDED, typename LA, typename LB>
+    template <bool A_K, bool B_K, typename LA, typename LB>
     static __device__ __forceinline__ void product(float *smem, int K, LA la, LB lb,
                                                    float (&acc)[TM][TN]) {
-        static_assert(!B_K || STRIDED, "a k-contiguous B needs strided columns");
-        constexpr int LDA = (A_K ? BK : BM) + 4, LDB = (B_K ? BK : BN) + 4;
-        float *sa = smem, *sb = smem + kStages * A_FLOATS;
+        float *sa = smem, *sb = smem + STAGES * A_FLOATS;
         const int steps = (K + BK - 1) / BK;
         auto load = [&](int step) {
             if (step < steps) {
-                const int k0 = step * BK, s = step % kStages;
-                constexpr int CA = (A_K ? BK : BM) / 4, CB = (B_K ? BK : BN) / 4;  // chunks a row
-#pragma unroll
-                for (int r = 0; r < (BM * BK / 4 + kThreads - 1) / kThreads; ++r) {
-                    const int i = (int)threadIdx.x + r * kThreads;
-                    if (BM * BK / 4 % kThreads && i >= BM * BK / 4) break;
-                    const int o = i / CA, c = i % CA * 4;
-                    const int m = A_K ? o : c, k = k0 + (A_K ? c : o);
-                    copy16_or_zero(sa + s * A_FLOATS + o * LDA + c, k < K ? la(m, k) : nullptr);
-                }
-#pragma unroll
-                for (int r = 0; r < (BN * BK / 4 + kThreads - 1) / kThreads; ++r) {
-                    const int i = (int)threadIdx.x + r * kThreads;
-                    if (BN * BK / 4 % kThreads && i >= BN * BK / 4) break;
-                    const int o = i / CB, c = i % CB * 4;
-                    const int n = B_K ? o : c, k = k0 + (B_K ? c : o);
-                    copy16_or_zero(sb + s * B_FLOATS + o * LDB + c, k < K ? lb(k, n) : nullptr);
-                }
+                const int k0 = step * BK, s = step % STAGES;
+                stage<A_K, BM, VM>(sa + s * A_FLOATS, k0, K, la);
+                stage<B_K, BN, VN>(sb + s * B_FLOATS, k0, K, [&](int n, int k) { return lb(k, n); });
             }
             tc::cp_async_commit();  // an empty group past the end keeps the count
         };
         __syncthreads();  // an earlier product's reads are done
 #pragma unroll
-        for (int s = 0; s < kStages - 1; ++s) load(s);
+        for (int s = 0; s < STAGES - 1; ++s) load(s);
         for (int step = 0; step < steps; ++step) {
-            tc::cp_async_wait_group<kStages - 2>();
+            tc::cp_async_wait_group<STAGES - 2>();
             __syncthreads();  // this stage has landed; the one before it has been read
-            load(step + kStages - 1);
-            const float *a_s = sa + step % kStages * A_FLOATS, *b_s = sb + step % kStages * B_FLOATS;
+            load(step + STAGES - 1);
+            const float *a_s = sa + step % STAGES * A_FLOATS, *b_s = sb + step % STAGES * B_FLOATS;
 #pragma unroll(TM <= 2 ? BK / 4 : 2)  // small tiles: all of the step's loads ahead
-            for (int kk = 0; kk < BK; kk += 4) {
+            for (int kk = 0; kk < (TM <= 2 ? BK : min(BK, K - step * BK)); kk += 4) {
                 float a[TM][4], b[TN][4];
-                if constexpr (A_K) {
+                fragment<A_K, BM, TM, VM>(a_s, kk, a, [](int i) { return row(i); });
+                fragment<B_K, BN, TN, VN>(b_s, kk, b, [](int j) { return col(j); });
 #pragma unroll
-                    for (int i = 0; i < TM; ++i)
-                        *reinterpret_cast<float4 *>(a[i]) =
-                            *reinterpret_cast<const float4 *>(a_s + row<A_K>(i) * LDA + kk);
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-#pragma unroll
-                        for (int i = 0; i < TM; ++i) a[i][q] = a_s[(kk + q) * LDA + row<A_K>(i)];
-                }
-                if constexpr (B_K) {
-#pragma unroll
-                    for (int j = 0; j < TN; ++j)
-                        *reinterpret_cast<float4 *>(b[j]) =
-                            *reinterpret_cast<const float4 *>(b_s + col<STRIDED>(j) * LDB + kk);
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-#pragma unroll
-                        for (int j = 0; j < TN; ++j) b[j][q] = b_s[(kk + q) * LDB + col<STRIDED>(j)];
-                }
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
+                for (int q = 0; q < 4; ++q)  // packed: 5 to 12 % faster than scalar multiply-adds
 #pragma unroll
                     for (int i = 0; i < TM; ++i)
 #pragma unroll
-                        for (int j = 0; j < TN; ++j) acc[i][j] = fmaf(a[i][q], b[j][q], acc[i][j]);
+                        for (int j = 0; j < TN; j += 2) {
+                            const float2 r =
+                                fma2(make_float2(a[i][q], a[i][q]), make_float2(b[j][q], b[j + 1][q]),
+                                     make_float2(acc[i][j], acc[i][j + 1]));
+                            acc[i][j] = r.x;
+                            acc[i][j + 1] = r.y;
+                        }
             }
         }
         tc::cp_async_wait_group<0>();
     }
 };
-
-// Tiles: 64 x 64, or 32 x 32 where the larger would leave SMs without a block.
-using Large = Tile<64, 64>;
-using Small = Tile<32, 32>;
 
 // Raises a kernel's dynamic shared memory limit, once per kernel and device.
 template <auto K> inline cudaError_t opt_in(size_t bytes) {
