@@ -239,6 +239,14 @@ def test_experts_backward_f32_tiles(moe, counts, d, f):
     check_experts(moe, counts, d, f, torch.float32, seed=7)
 
 
+@pytest.mark.parametrize("counts,d,f", [
+    ([1], 1096, 72), ([3, 0, 130], 2056, 40), ([1, 2], 64, 1032), ([5] * 6, 4104, 136),
+    ([257, 0, 1], 1544, 520), ([0, 128, 129], 640, 2056), ([16] * 8, 2048, 768)])
+def test_experts_backward_few_tiles(moe, counts, d, f):
+    """Row products whose K axis is split among the CTAs of a cluster."""
+    check_experts(moe, counts, d, f, torch.bfloat16, seed=8)
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_experts_backward_keeps_segments_apart(moe, dtype):
     """NaN and infinite rows of one expert reach that expert's gradients only."""

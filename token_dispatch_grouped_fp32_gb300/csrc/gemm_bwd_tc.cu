@@ -25,6 +25,11 @@
 // GU a tile's 256 accumulator columns are 128 gate and the 128 matching up
 // columns).
 //
+// Batches whose row products have fewer tiles than SMs take two launches for them
+// (SPLIT): GU, which forms dh as well in a third of its accumulator columns, and
+// DX, each tile's K axis divided among the CTAs of a cluster, which add up one
+// another's accumulators through distributed shared memory in a fixed order.
+//
 // Weight products (DW, RW) contract over the rows of a segment, so both
 // operands are MN-major and the K axis is ragged.  The last K step of a segment may hold
 // rows of the next expert (any value, a NaN too): MMAs are issued for whole
@@ -221,6 +226,28 @@ __device__ __forceinline__ float4 *dh_quad(float *dh, int64_t r0, int f, int row
     return reinterpret_cast<float4 *>(dh + r0 * f + (int64_t)col * rows) + lane;
 }
 
+// 32 columns of lane's row, zeros outside the rows and columns there are.
+__device__ __forceinline__ void load_dh(const Params &p, int64_t r0, int rows, int col, int lane,
+                                        float (&dh)[32]) {
+#pragma unroll
+    for (int v = 0; v < 8; ++v) {
+        float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int n = col + 4 * v;
+        if (lane < rows && n < p.N) q = __ldcg(dh_quad(p.dh, r0, p.N, rows, n, lane));
+        dh[4 * v] = q.x;
+        dh[4 * v + 1] = q.y;
+        dh[4 * v + 2] = q.z;
+        dh[4 * v + 3] = q.w;
+    }
+}
+
+__device__ __forceinline__ void gate_gradient(float g, float u, float dh, float &dg, float &du) {
+    const float s = __fdividef(1.f, 1.f + __expf(-g));
+    const float t = dh * s;
+    du = t * g;
+    dg = t * u * fmaf(g, 1.f - s, 1.f);
+}
+
 __device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
                  : "memory");
@@ -240,10 +267,26 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return *reinterpret_cast<uint32_t *>(&v);
 }
 
-template <int CTAS, int KIND>
+// Sum over the CTAs of a cluster of 32 columns, from column col0, of this lane's
+// row of their accumulators (each at `dump`, [BN columns][BM rows]), in the order
+// of the CTAs.
+__device__ __forceinline__ void sum_cluster(uint32_t dump, int ctas, int col0, int row, float (&v)[32]) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = 0.f;
+    for (int c = 0; c < ctas; ++c) {
+        const uint32_t at = map_to_rank(dump, c) + 4 * (col0 * BM + row);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] += ld_cluster(at + 4 * BM * i);
+    }
+}
+
+// SPLIT (GU, DX): a cluster of single CTAs serves one tile, each CTA a part of K;
+// the launch has a cluster for every tile there can be.
+template <int CTAS, int KIND, bool SPLIT>
 __global__ void __launch_bounds__(threads<KIND>(), 1)
 gemm_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                      const __grid_constant__ CUtensorMap tmOut, Params p) {
+                   const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmB2,
+                   Params p) {
     using C = Cfg<CTAS, KIND>;
     constexpr bool PAIR = C::PAIR;
     constexpr int STAGES = C::STAGES;
@@ -265,10 +308,18 @@ gemm_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
     int *s_tile = reinterpret_cast<int *>(base + C::OFF_TILE);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int E = p.E;
-    const uint32_t rank = PAIR ? cluster_rank() : 0u;
+    const uint32_t rank = PAIR ? cluster_rank() : 0u;  // of the tile's rows
     const bool leader = rank == 0;
-    const int unit = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
-    const int nunits = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
+    // GU forms dh too: 128 columns of dy Wd^T beside the gate and up ones,
+    // from K steps of their own after the others (A through tmOut, B tmB2).
+    constexpr bool WITH_DH = SPLIT && KIND == GU;
+    constexpr int DUMP_COLS = BN + (WITH_DH ? BN / 2 : 0);
+    static_assert(!SPLIT || (!PAIR && (KIND == GU || KIND == DX) && C::OFF_BAR >= 4 * BM * DUMP_COLS &&
+                             DUMP_COLS <= TMEM_COLS),
+                  "the accumulators of a split product take the stages' place");
+    const int parts = SPLIT ? (int)cluster_size() : 1, part = SPLIT ? (int)cluster_rank() : 0;
+    const int unit = (int)blockIdx.x / (SPLIT ? parts : CTAS);
+    const int nunits = (int)gridDim.x / (SPLIT ? parts : CTAS);
     const uint32_t sig_full = PAIR ? map_to_rank(bar_full, 0) : bar_full;
     const uint32_t sig_tempty = PAIR ? map_to_rank(bar_tempty, 0) : bar_tempty;
 
@@ -318,8 +369,11 @@ gemm_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
 
     const uint32_t tmem_base = *s_tmem;
     const int total = kWeights<KIND> ? E * p.m_tiles * p.n_tiles : s_tile[E] * p.n_tiles;
-    const int nk_row = (p.K + BK - 1) / BK;
-    // K steps of a tile, and whether its last one needs the fixer
+    // K steps of a row product's tile that are this CTA's
+    const int nk_all = (p.K + BK - 1) / BK;
+    const int ks_row = nk_all * part / parts, nk_row = nk_all * (part + 1) / parts;
+    const int nk_dh = WITH_DH ? nk_row - ks_row : 0;  // ... and as many again of dh
+    // Past-the-end K step of a tile, and whether its last one needs the fixer
     auto ksteps = [&](const Work &w) { return kWeights<KIND> ? (w.rows + BK - 1) / BK : nk_row; };
     auto cut = [&](const Work &w) { return kWeights<KIND> && (w.rows & 15) != 0; };
 
@@ -333,8 +387,8 @@ gemm_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
             bool ok = true;
             for (Walk<KIND> wk(p, unit, nunits, total); wk.more() && ok; wk.next()) {
                 const Work w = wk.at(s_off, s_tile, p, C::TILE_M);
-                const int nk = ksteps(w);
-                for (int ks = 0; ks < nk; ++ks) {
+                const int nk = ksteps(w) + nk_dh;
+                for (int ks = ks_row; ks < nk; ++ks) {
                     if (!wait_bounded(bar_empty + 8 * s, ph ^ 1u, p.ds, s_abort)) {
                         ok = false;
                         break;
@@ -343,7 +397,9 @@ gemm_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                     if (leader) {
                         if (PAIR || !tail)  // (a single CTA's fixer arrives itself)
                             mbar_arrive_expect_tx(bar_full + 8 * s,
-                                                  (tail ? 16 : C::STAGE_BYTES) * CTAS);
+                                                  (tail ? 16
+                                                   : WITH_DH && ks >= nk_row ? A_BYTES + C::B_BYTES / 2
+                                                                             : C::STAGE_BYTES) * CTAS);
                         issued |= 1u << s;
                         last_par = (last_par & ~(1u << s)) | (ph << s);
                     }
@@ -375,6 +431,10 @@ gemm_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                             for (int a = 0; a < C::B_ATOMS; ++a)
                                 tma_load_3d<CTAS>(bdst + a * ATOM_BYTES, &tmB, nc + 64 * a, kr, 0, fb);
                         }
+                    } else if (WITH_DH && ks >= nk_row) {
+                        const int kd = (ks - nk_dh) * BK;
+                        tma_load_2d<CTAS>(adst, &tmOut, kd, w.row0, fb);
+                        tma_load_3d<CTAS>(bdst, &tmB2, kd, w.n_blk * (BN / 2), w.e, fb);
                     } else {
                         tma_load_2d<CTAS>(adst, &tmA, k0, w.row0 + (int)rank * BM, fb);
                         if constexpr (KIND == GU) {
@@ -438,6 +498,8 @@ gemm_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
             // 2 KB.  Stages and K steps only move the start address.
             const uint64_t adesc0 = smem_desc_sw128(base_s + C::OFF_A, A_MN ? ATOM_BYTES : 16, 1024);
             const uint64_t bdesc0 = smem_desc_sw128(base_s + C::OFF_B, B_MN ? ATOM_BYTES : 16, 1024);
+            const uint64_t bdesc_dh = smem_desc_sw128(base_s + C::OFF_B, 16, 1024);
+            constexpr uint32_t IDESC_DH = idesc_bf16_ab(C::TILE_M, BN / 2, false, false);
             constexpr uint32_t ASTEP = A_MN ? 2048 : 32, BSTEP = B_MN ? 2048 : 32;
             if (p.ds.inject_wait_timeout) ok = wait_bounded(bar_drain, 0, p.ds, s_abort);
             for (Walk<KIND> wk(p, unit, nunits, total); wk.more() && ok; wk.next()) {
@@ -447,7 +509,7 @@ gemm_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                     nk = ksteps(w);
                     last = (w.rows - (nk - 1) * BK + UMMA_K - 1) / UMMA_K;
                 }
-                int ks = 0;
+                int ks = ks_row;
                 do {  // accumulations: one, or in RW one per kChunk steps
                     const int acc = it & 1;
                     const uint32_t aph = (uint32_t)(it >> 1) & 1u;
@@ -458,7 +520,7 @@ gemm_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                     }
                     tc_fence_after();
                     const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
-                    const int ks0 = ks, ks1 = KIND == RW ? min(nk, ks + kChunk) : nk;
+                    const int ks0 = ks, ks1 = KIND == RW ? min(nk, ks + kChunk) : nk + nk_dh;
                     for (; ks < ks1; ++ks) {
                         // a cut stage of a pair is reported from the peer CTA too
                         if (!wait_bounded<PAIR && kWeights<KIND>>(bar_full + 8 * s, ph, p.ds, s_abort)) {
@@ -469,6 +531,14 @@ gemm_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                         const uint64_t a_st = adesc0 + (uint64_t)((s * A_BYTES) >> 4);
                         const uint64_t b_st = bdesc0 + (uint64_t)((s * C::B_BYTES) >> 4);
                         const int n = kWeights<KIND> && ks == nk - 1 ? last : BK / UMMA_K;
+                        if (WITH_DH && ks >= nk_row) {
+                            const uint64_t b_dh = bdesc_dh + (uint64_t)((s * C::B_BYTES) >> 4);
+#pragma unroll
+                            for (int kk = 0; kk < BK / UMMA_K; ++kk)
+                                mma_bf16<CTAS>(d_tmem + BN, a_st + (uint64_t)((kk * ASTEP) >> 4),
+                                               b_dh + (uint64_t)((kk * 32) >> 4), IDESC_DH,
+                                               ((ks - nk_row) | kk) != 0 ? 1u : 0u);
+                        } else
 #pragma unroll
                         for (int kk = 0; kk < BK / UMMA_K; ++kk)
                             if (!kWeights<KIND> || kk < n)
@@ -540,7 +610,18 @@ gemm_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                 ready();
                 if (!ok) break;
             }
-            if constexpr (KIND == DH) {
+            if constexpr (SPLIT) {  // the accumulator to shared memory, for the cluster
+                if (rv > 0)
+#pragma unroll
+                    for (int c = half * (DUMP_COLS / 2); c < (half + 1) * (DUMP_COLS / 2); c += 32) {
+                        uint32_t y[32];
+                        tmem_ld32(t_row + c, y);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            reinterpret_cast<uint32_t *>(base)[(c + i) * BM + wrow0 + lane] = y[i];
+                    }
+            } else if constexpr (KIND == DH) {
                 const int64_t r0 = w.row0 + wrow0;
                 const int n0 = w.n_blk * BN + half * (BN / 2);
                 uint32_t y[4][32];
@@ -566,16 +647,7 @@ gemm_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     float dh[32];
-#pragma unroll
-                    for (int v = 0; v < 8; ++v) {
-                        float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
-                        const int n = n0 + 32 * c + 4 * v;
-                        if (lane < rv && n < p.N) q = __ldcg(dh_quad(p.dh, r0, p.N, rv, n, lane));
-                        dh[4 * v] = q.x;
-                        dh[4 * v + 1] = q.y;
-                        dh[4 * v + 2] = q.z;
-                        dh[4 * v + 3] = q.w;
-                    }
+                    load_dh(p, r0, rv, n0 + 32 * c, lane, dh);
                     uint32_t g[32], u[32];
                     tmem_ld32(t_row + half * (BN / 4) + 32 * c, g);
                     tmem_ld32(t_row + BN / 2 + half * (BN / 4) + 32 * c, u);
@@ -585,13 +657,9 @@ gemm_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                     for (int i = 0; i < 16; ++i) {
                         float dg[2], du[2];
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const float gv = __uint_as_float(g[2 * i + j]), uv = __uint_as_float(u[2 * i + j]);
-                            const float s = __fdividef(1.f, 1.f + __expf(-gv));
-                            const float t = dh[2 * i + j] * s;  // dh s
-                            du[j] = t * gv;
-                            dg[j] = t * uv * fmaf(gv, 1.f - s, 1.f);
-                        }
+                        for (int j = 0; j < 2; ++j)
+                            gate_gradient(__uint_as_float(g[2 * i + j]), __uint_as_float(u[2 * i + j]),
+                                          dh[2 * i + j], dg[j], du[j]);
                         pg[16 * c + i] = pack2(dg[0], dg[1]);
                         pu[16 * c + i] = pack2(du[0], du[1]);
                     }
@@ -745,9 +813,55 @@ gemm_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
         __syncwarp();
     }
 
+    if constexpr (SPLIT) {
+        // Every CTA's accumulators lie in its shared memory now, in the stages' place
+        // (a cluster has one tile at most, so no more loads come).  Each adds up and
+        // stores 32-column blocks of the tile: block b (GU: b of the gate columns, of
+        // the up and of the dh ones) is CTA b mod parts' task.
+        cluster_sync();
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        const Walk<KIND> wk(p, unit, nunits, total);
+        if (warp >= 2 && wk.more() && *s_abort == 0) {
+            const Work w = wk.at(s_off, s_tile, p, C::TILE_M);
+            const int rv = max(0, min(32, w.rows - quarter * 32)), row = quarter * 32 + lane;
+            const int64_t r0 = w.row0 + quarter * 32;
+            constexpr int BLOCKS = BN / 32 / (KIND == GU ? 2 : 1);
+            for (int b = half * (BLOCKS / 2); b < (half + 1) * (BLOCKS / 2); ++b) {
+                const int n = (w.n_blk * BLOCKS + b) * 32;
+                if (b % parts != part || rv == 0 || n >= p.N) continue;  // warp-uniform
+                float y[32];
+                sum_cluster(base_s, parts, 32 * b, row, y);
+                if constexpr (KIND == GU) {
+                    float u[32], dh[32];
+                    sum_cluster(base_s, parts, BN / 2 + 32 * b, row, u);
+                    sum_cluster(base_s, parts, BN + 32 * b, row, dh);
+                    uint32_t pg[16], pu[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float dg[2], du[2];
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            gate_gradient(y[2 * i + j], u[2 * i + j], dh[2 * i + j], dg[j], du[j]);
+                        pg[i] = pack2(dg[0], dg[1]);
+                        pu[i] = pack2(du[0], du[1]);
+                    }
+                    const int64_t ld = 2 * (int64_t)p.f;
+                    store_rows_transposed<4>(pg, p.out, r0, rv, n, p.N, ld);
+                    store_rows_transposed<4>(pu, p.out + p.f, r0, rv, n, p.N, ld);
+                } else {
+                    uint32_t packed[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) packed[i] = pack2(y[2 * i], y[2 * i + 1]);
+                    store_rows_transposed<4>(packed, p.out, r0, rv, n, p.N, p.N);
+                }
+            }
+        }
+        __syncwarp();
+    }
+
     tc_fence_before();
     __syncthreads();
-    if constexpr (PAIR) cluster_sync();
+    if constexpr (PAIR || SPLIT) cluster_sync();  // (SPLIT: the others have read this CTA's memory)
     tc_fence_after();
     if (warp == 1) tmem_dealloc<CTAS>(tmem_base, TMEM_COLS);
     if (p.overlap_prev) pdl_wait();
@@ -755,14 +869,14 @@ gemm_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
 
 // ------------------------------ host side ----------------------------------
 template <int CTAS, int KIND>
-cudaLaunchConfig_t launch_config(unsigned grid, cudaStream_t st, cudaLaunchAttribute *attr) {
+cudaLaunchConfig_t launch_config(unsigned grid, int cluster, cudaStream_t st, cudaLaunchAttribute *attr) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid, 1, 1);
     cfg.blockDim = dim3(threads<KIND>(), 1, 1);
     cfg.dynamicSmemBytes = (Cfg<CTAS, KIND>::SMEM_BYTES);
     cfg.stream = st;
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = CTAS;
+    attr[0].val.clusterDim.x = (unsigned)cluster;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -773,14 +887,14 @@ cudaLaunchConfig_t launch_config(unsigned grid, cudaStream_t st, cudaLaunchAttri
 }
 
 template <int CTAS, int KIND> cudaError_t prepare(int *resident) {
-    cudaError_t err = cudaFuncSetAttribute(gemm_bwd_tc_kernel<CTAS, KIND>,
+    cudaError_t err = cudaFuncSetAttribute(gemm_bwd_tc_kernel<CTAS, KIND, false>,
                                            cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            (Cfg<CTAS, KIND>::SMEM_BYTES));
     if (err != cudaSuccess) return err;
     cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = launch_config<CTAS, KIND>(CTAS, nullptr, attr);
+    cudaLaunchConfig_t cfg = launch_config<CTAS, KIND>(CTAS, CTAS, nullptr, attr);
     int n = 0;
-    if ((err = cudaOccupancyMaxActiveClusters(&n, gemm_bwd_tc_kernel<CTAS, KIND>, &cfg)) !=
+    if ((err = cudaOccupancyMaxActiveClusters(&n, gemm_bwd_tc_kernel<CTAS, KIND, false>, &cfg)) !=
         cudaSuccess)
         return err;
     *resident = std::min(*resident, n);
@@ -810,8 +924,35 @@ cudaError_t launch_one(int units, int64_t tiles, const CUtensorMap &a, const CUt
                        const CUtensorMap &out, const Params &p, cudaStream_t st) {
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg =
-        launch_config<CTAS, KIND>(CTAS * (unsigned)std::min<int64_t>(units, tiles), st, attr);
-    return cudaLaunchKernelEx(&cfg, gemm_bwd_tc_kernel<CTAS, KIND>, a, b, out, p);
+        launch_config<CTAS, KIND>(CTAS * (unsigned)std::min<int64_t>(units, tiles), CTAS, st, attr);
+    return cudaLaunchKernelEx(&cfg, gemm_bwd_tc_kernel<CTAS, KIND, false>, a, b, out, b, p);
+}
+
+// Row products with so few tiles that SMs would idle: each tile on a cluster of up
+// to eight CTAs, with at least eight K steps each (shorter parts cost more in the
+// sum than they save: T = 1024, E = 1, d = f = 256 45 us to 48), and dh in GU's launch.
+// Five launches took (d = 2048, f = 768, E = 8, k = 2) at T = 1 67 us, now 45 with the
+// weight products beside them; T = 64 77 and 62; T = 24, d = 2880, f = 168, E = 3 63 and 31;
+// T = 178, d = 256, f = 2712 74 and 36.
+template <int KIND> cudaError_t prepare_split() {
+    return cudaFuncSetAttribute(gemm_bwd_tc_kernel<1, KIND, true>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (Cfg<1, KIND>::SMEM_BYTES));
+}
+// CTAs a tile, or 0 (fewer than `least`, or the tiles more than one round).
+int split_parts(const Shape &s, const DeviceInfo &d, int n_tiles, int K, int least) {
+    const int64_t steps = (K + BK - 1) / BK, tiles = row_tiles_bound(s, BM) * n_tiles;
+    const int64_t parts = std::min<int64_t>({8, d.units[1] / tiles, std::max<int64_t>(1, steps / 8)});
+    return parts >= least ? (int)parts : 0;
+}
+template <int KIND>
+cudaError_t launch_split(const Shape &s, int parts, const CUtensorMap &a, const CUtensorMap &b,
+                         const CUtensorMap &a2, const CUtensorMap &b2, Params p, cudaStream_t st) {
+    p.experts = kAllExperts;
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = launch_config<1, KIND>(
+        (unsigned)(parts * row_tiles_bound(s, BM) * p.n_tiles), parts, st, attr);
+    return cudaLaunchKernelEx(&cfg, gemm_bwd_tc_kernel<1, KIND, true>, a, b, a2, b2, p);
 }
 
 // A row product over all experts: one launch, or one per tile shape.  The
@@ -823,7 +964,7 @@ cudaError_t launch_rows(const Shape &s, const DeviceInfo &d, const CUtensorMap &
     CUtensorMap b;
     cudaError_t err = cudaSuccess;
     p.experts = kAllExperts;
-    p.release_late = p.overlap_prev = 0;
+    const int late = p.release_late;
     if (mode != kModeSingles) {
         if (!map_b(&b, 2)) return cudaErrorInvalidValue;
         if (mode == kModeHybrid) {
@@ -833,7 +974,7 @@ cudaError_t launch_rows(const Shape &s, const DeviceInfo &d, const CUtensorMap &
         err = launch_one<2, KIND>(d.units[2], row_tiles_bound(s, 2 * BM) * p.n_tiles, a, b, a, p, st);
         if (err != cudaSuccess || mode == kModePairs) return err;
         p.experts = kSingleExperts;
-        p.release_late = 0;
+        p.release_late = late;
         p.overlap_prev = 1;
     }
     if (!map_b(&b, 1)) return cudaErrorInvalidValue;
@@ -859,7 +1000,7 @@ WeightTiles weight_tiles(int M, int N) {
 
 // dW[e] [M][N] = sum over the segment's rows of A[r]^T B[r].
 cudaError_t launch_weights(const Shape &s, const DeviceInfo &d, const void *A, int M, const void *B,
-                           int N, void *dW, Params p, cudaStream_t st) {
+                           int N, void *dW, bool overlap, Params p, cudaStream_t st) {
     CUtensorMap a, b, o;
     if (!mn_map(&a, A, 1, s.P(), M, &p.a_blocks) || !mn_map(&b, B, 1, s.P(), N, &p.b_blocks) ||
         !tensor_map_out(&o, dW, s.E, M, N))
@@ -867,10 +1008,8 @@ cudaError_t launch_weights(const Shape &s, const DeviceInfo &d, const void *A, i
     p.M = M;
     p.N = N;
     p.experts = kAllExperts;
-    // DX and the two weight products do not depend on one another, but each
-    // waits: overlapping their launches measured 1 % slower on the gpt-oss
-    // shape and 1.5 % on the Mixtral one (1 % faster on the short Zipf batch)
-    p.release_late = p.overlap_prev = 0;
+    p.release_late = 0;
+    p.overlap_prev = overlap;
     const WeightTiles t = weight_tiles(M, N);
     p.m_tiles = t.m;
     p.n_tiles = t.n;
@@ -900,7 +1039,8 @@ cudaError_t device_info(const DeviceInfo **out) {
     DeviceInfo &d = info[dev];
     if (!d.ready) {
         if ((err = prepare_all<1>(&d.units[1])) != cudaSuccess ||
-            (err = prepare_all<2>(&d.units[2])) != cudaSuccess) {
+            (err = prepare_all<2>(&d.units[2])) != cudaSuccess ||
+            (err = prepare_split<GU>()) != cudaSuccess || (err = prepare_split<DX>()) != cudaSuccess) {
             set_error_message("the gradient's matrix products do not fit on device %d", dev);
             return err;
         }
@@ -951,32 +1091,57 @@ cudaError_t launch_experts_backward_tc(const Shape &s, const ExpertsBwd &x, cons
     Params q = p;
     q.K = s.d;
     q.N = s.f;
-    q.n_tiles = (s.f + BN - 1) / BN;
-    err = launch_rows<DH>(s, d, tdy, [&](CUtensorMap *m, int ctas) {
-        return tensor_map_weights_k(m, x.Wd, s.E, s.f, s.d, BN / ctas); }, q, st);
+    auto map_wd = [&](CUtensorMap *m, int rows) {
+        return tensor_map_weights_k(m, x.Wd, s.E, s.f, s.d, rows); };
+    auto map_gu = [&](CUtensorMap *m, int) {
+        // two-atom boxes need the up half to start on a block too
+        return s.f % 64 == 0 ? tensor_map_weight_blocks(m, x.Wgu, s.E, s.d, 2 * (int64_t)s.f, 2)
+                             : tensor_map_weights(m, x.Wgu, s.E, s.d, 2 * (int64_t)s.f); };
+    Params g = q;
+    g.n_tiles = (s.f + BN / 2 - 1) / (BN / 2);
+    g.out = static_cast<__nv_bfloat16 *>(dgu);
+    g.b_blocks = s.f % 64 == 0;
+    const int parts = split_parts(s, d, g.n_tiles, g.K, 1);
+    // dWd's product reads neither dh nor dgu, dWgu's no dx: while the weights fit in
+    // L2 each starts beside the product before it, where SMs are free (T = 64, d = 128,
+    // f = 256, E = 8: 29 us to 19; T = 4096, k = 2, d = 2048, f = 768, E = 8: 184 to 174).
+    // With more weights their writes meet the other's reads in HBM: T = 20, k = 2, d = f =
+    // 4096, E = 4 222 to 241, the gpt-oss shape +2 %.
+    const bool overlap = (int64_t)s.E * s.d * s.f * 6 <= (int64_t)128 << 20;
+    auto weights_d = [&] {
+        return launch_weights(s, d, x.h_perm, s.f, x.dy_perm, s.d, x.dWd, overlap, p, st); };
+    g.release_late = overlap;
+    if (parts) {
+        CUtensorMap b, b2;
+        if (!map_gu(&b, 1) || !map_wd(&b2, BN / 2)) return cudaErrorInvalidValue;
+        err = launch_split<GU>(s, parts, tx, b, tdy, b2, g, st);
+    } else {
+        q.n_tiles = (s.f + BN - 1) / BN;
+        err = launch_rows<DH>(
+            s, d, tdy, [&](CUtensorMap *m, int ctas) { return map_wd(m, BN / ctas); }, q, st);
+        if (err != cudaSuccess) return err;
+        err = launch_rows<GU>(s, d, tx, map_gu, g, st);
+    }
     if (err != cudaSuccess) return err;
-    q = p;
-    q.K = s.d;
-    q.N = s.f;
-    q.n_tiles = (s.f + BN / 2 - 1) / (BN / 2);
-    q.out = static_cast<__nv_bfloat16 *>(dgu);
-    // two-atom boxes need the up half to start on a block too
-    q.b_blocks = s.f % 64 == 0;
-    err = launch_rows<GU>(s, d, tx, [&](CUtensorMap *m, int) {
-        return q.b_blocks ? tensor_map_weight_blocks(m, x.Wgu, s.E, s.d, 2 * (int64_t)s.f, 2)
-                          : tensor_map_weights(m, x.Wgu, s.E, s.d, 2 * (int64_t)s.f); }, q, st);
-    if (err != cudaSuccess) return err;
+    if (overlap && (err = weights_d()) != cudaSuccess) return err;
     q = p;
     q.K = 2 * s.f;
     q.N = s.d;
     q.n_tiles = (s.d + BN - 1) / BN;
     q.out = static_cast<__nv_bfloat16 *>(x.dx_perm);
-    err = launch_rows<DX>(s, d, tdgu, [&](CUtensorMap *m, int ctas) {
-        return tensor_map_weights_k(m, x.Wgu, s.E, s.d, 2 * (int64_t)s.f, BN / ctas); }, q, st);
+    auto map_dx = [&](CUtensorMap *m, int ctas) {
+        return tensor_map_weights_k(m, x.Wgu, s.E, s.d, 2 * (int64_t)s.f, BN / ctas); };
+    q.release_late = overlap;
+    if (const int parts = split_parts(s, d, q.n_tiles, q.K, 2)) {
+        CUtensorMap b;
+        if (!map_dx(&b, 1)) return cudaErrorInvalidValue;
+        err = launch_split<DX>(s, parts, tdgu, b, tdgu, b, q, st);
+    } else {
+        err = launch_rows<DX>(s, d, tdgu, map_dx, q, st);
+    }
     if (err != cudaSuccess) return err;
-    if ((err = launch_weights(s, d, x.h_perm, s.f, x.dy_perm, s.d, x.dWd, p, st)) != cudaSuccess)
-        return err;
-    return launch_weights(s, d, x.x_perm, s.d, dgu, 2 * s.f, x.dWgu, p, st);
+    if (!overlap && (err = weights_d()) != cudaSuccess) return err;
+    return launch_weights(s, d, x.x_perm, s.d, dgu, 2 * s.f, x.dWgu, overlap, p, st);
 }
 
 cudaError_t launch_route_backward_tc(const Shape &s, const RouteProducts &r, const DevStatus &ds,
