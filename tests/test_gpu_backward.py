@@ -329,6 +329,14 @@ def test_route_backward_f32_tiles(moe, T, d, E, k, renorm):
     test_route_backward(moe, T, d, E, k, renorm, torch.float32)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("T,d,E,k", [(1, 2048, 128, 8), (16, 1032, 26, 7), (256, 264, 100, 4), (100, 7168, 9, 2),
+                                     (128, 72, 512, 8), (31, 8, 17, 1)])
+def test_route_backward_short_batches(moe, T, d, E, k, renorm, dtype):
+    test_route_backward(moe, T, d, E, k, renorm, dtype)
+
+
 def test_route_backward_without_bias_output(moe):
     T, d, E, k = 40, 64, 16, 2
     g = gen(3)

@@ -22,7 +22,8 @@
 // d = 4096, k = 8, E = 64 without renormalisation: 187 us, dx 97 and dWr 84);
 // renormalised with many experts, dx is the sum of the chosen experts' rows of
 // Wr (145 us; E = 128 222, with the product over all E 348).
-// At most 8 experts: one pass on the CUDA cores for both types (below).
+// At most 8 experts: one pass on the CUDA cores for both types (below).  Short
+// batches: all sums in one launch after the terms (small_batch).
 #include "common.cuh"
 #include "kernels.h"
 #include "simt_gemm.cuh"
@@ -34,6 +35,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxTokenBlocks = 152 * 8;
 constexpr int kSplitCols = 4 * kThreads;  // elements of Wr per block
+constexpr int kCopyCols = 8 * kThreads;   // elements of x per block
 
 template <bool MAX> __device__ __forceinline__ float warp_all(float v) {
 #pragma unroll
@@ -79,16 +81,28 @@ struct TermsArgs {
     const float *Wr;
     int E8, d, token_blocks, n_splits, split;
     int32_t *all, *splits;
+    // small batches, bf16 x: its copy in fp32, T * d elements
+    const __nv_bfloat16 *x;
+    float *x32;
 };
 
 // Blocks below token_blocks: a warp per token at a time, its row of dl in
 // shared memory (then written whole, as floats and as terms) and the warp's
 // running sum of the rows for the bias.  The blocks after: kSplitCols elements
-// of Wr each.
+// of Wr, or kCopyCols of x, each.
 __global__ void __launch_bounds__(kThreads) terms_kernel(TermsArgs a, DevStatus ds) {
     pdl_wait();
     extern __shared__ float sh[];
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, E8 = a.E8;
+    if ((int)blockIdx.x >= a.token_blocks && a.x32) {
+        const int64_t i = (int64_t)((int)blockIdx.x - a.token_blocks) * kCopyCols + 8 * threadIdx.x;
+        if (i >= a.T * a.d) return;
+        float v[8];
+        unpack16(ldg16(a.x + i), v, static_cast<const __nv_bfloat16 *>(nullptr));
+        *reinterpret_cast<float4 *>(a.x32 + i) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4 *>(a.x32 + i + 4) = make_float4(v[4], v[5], v[6], v[7]);
+        return;
+    }
     if ((int)blockIdx.x >= a.token_blocks) {
         const int64_t n = (int64_t)E8 * a.d, real = (int64_t)a.E * a.d;
         const int64_t i0 = (int64_t)((int)blockIdx.x - a.token_blocks) * kSplitCols + threadIdx.x;
@@ -432,39 +446,43 @@ few_experts_kernel(FewArgs a, DevStatus ds) {
 }
 
 // ------------------------- fp32 x, on the CUDA cores ------------------------
-// Over dl8, the rows of dl padded to E8 columns.
-// part[split][e][c]: the sum over the tokens of one split.
+// Tiles of the two products over dl8, the rows of dl padded to E8 columns.
+// out[e][n] = the sum over the K tokens from dl8 and x on: experts e0 .., columns n0 ..
 template <typename Tl>
-__global__ void __launch_bounds__(Tl::THREADS)
-dwr_kernel(const float *__restrict__ dl8, const float *__restrict__ x, int64_t T, int E, int E8,
-           int d, int tokens, float *__restrict__ part) {
-    pdl_wait();
-    extern __shared__ __align__(16) float smem[];
-    const int n0 = blockIdx.x * Tl::BN, e0 = blockIdx.y * Tl::BM;
-    const int64_t t0 = (int64_t)blockIdx.z * tokens;
-    const int K = (int)min((int64_t)tokens, T - t0);
+__device__ __forceinline__ void dwr_block(float *smem, const float *dl8, const float *x, int K, int E,
+                                          int E8, int d, float *out, int e0, int n0) {
     float acc[Tl::TM][Tl::TN];
     Tl::zero(acc);
-    Tl::product<false, false>(
-        smem, K, [=](int m, int k) { return e0 + m < E8 ? dl8 + (t0 + k) * E8 + e0 + m : nullptr; },
-        [=](int k, int n) { return n0 + n < d ? x + (t0 + k) * d + n0 + n : nullptr; }, acc);
+    Tl::template product<false, false>(
+        smem, K,
+        [=](int m, int k) { return e0 + m < E8 ? dl8 + (int64_t)k * E8 + e0 + m : nullptr; },
+        [=](int k, int n) { return n0 + n < d ? x + (int64_t)k * d + n0 + n : nullptr; }, acc);
     Tl::each_run(acc, [&](int m, int c, const float *v) {
-        const int e = e0 + m, n = n0 + c;
-        if (e < E && n < d) Tl::store(part + ((int64_t)blockIdx.z * E + e) * d + n, v);
+        if (e0 + m < E && n0 + c < d) Tl::store(out + (int64_t)(e0 + m) * d + n0 + c, v);
     });
 }
 
-template <typename Tl>
-__global__ void __launch_bounds__(Tl::THREADS)
-route_dx_kernel(const float *__restrict__ dl8, const float *__restrict__ Wr, const float *dx_in,
-                int64_t T, int E, int E8, int d, float *dx) {
-    pdl_wait();
-    extern __shared__ __align__(16) float smem[];
-    const int64_t t0 = (int64_t)blockIdx.x * Tl::BM;
-    const int n0 = blockIdx.y * Tl::BN;
+__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
+    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u),
+                       __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
+}
+__device__ __forceinline__ void store4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 v) {
+    *reinterpret_cast<uint2 *>(p) =
+        make_uint2(pack(__float2bfloat16_rn(v.x), __float2bfloat16_rn(v.y)),
+                   pack(__float2bfloat16_rn(v.z), __float2bfloat16_rn(v.w)));
+}
+
+// dx of tokens t0 .., columns n0 ..
+template <typename Tl, typename TA>
+__device__ __forceinline__ void dx_block(float *smem, const float *dl8, const float *Wr,
+                                         const TA *dx_in, int64_t T, int E, int E8, int d, TA *dx,
+                                         int64_t t0, int n0) {
     float acc[Tl::TM][Tl::TN];
     Tl::zero(acc);
-    Tl::product<true, false>(
+    Tl::template product<true, false>(
         smem, E8, [=](int m, int k) { return t0 + m < T ? dl8 + (t0 + m) * E8 + k : nullptr; },
         [=](int k, int n) { return k < E && n0 + n < d ? Wr + (int64_t)k * d + n0 + n : nullptr; }, acc);
     Tl::each_run(acc, [&](int m, int c, const float *v) {
@@ -473,11 +491,68 @@ route_dx_kernel(const float *__restrict__ dl8, const float *__restrict__ Wr, con
         if (t >= T || n >= d) return;
         float4 o = make_float4(v[0], v[1], v[2], v[3]);
         if (dx_in) {
-            const float4 in = *reinterpret_cast<const float4 *>(dx_in + t * d + n);
+            const float4 in = load4(dx_in + t * d + n);
             o = make_float4(o.x + in.x, o.y + in.y, o.z + in.z, o.w + in.w);
         }
-        *reinterpret_cast<float4 *>(dx + t * d + n) = o;
+        store4(dx + t * d + n, o);
     });
+}
+
+// part[split][e][c]: the sum over the tokens of one split.
+template <typename Tl>
+__global__ void __launch_bounds__(Tl::THREADS)
+dwr_kernel(const float *__restrict__ dl8, const float *__restrict__ x, int64_t T, int E, int E8,
+           int d, int tokens, float *__restrict__ part) {
+    pdl_wait();
+    extern __shared__ __align__(16) float smem[];
+    const int64_t t0 = (int64_t)blockIdx.z * tokens;
+    dwr_block<Tl>(smem, dl8 + t0 * E8, x + t0 * d, (int)min((int64_t)tokens, T - t0), E, E8, d,
+                  part + (int64_t)blockIdx.z * E * d, blockIdx.y * Tl::BM, blockIdx.x * Tl::BN);
+}
+
+template <typename Tl>
+__global__ void __launch_bounds__(Tl::THREADS)
+route_dx_kernel(const float *__restrict__ dl8, const float *__restrict__ Wr, const float *dx_in,
+                int64_t T, int E, int E8, int d, float *dx) {
+    pdl_wait();
+    extern __shared__ __align__(16) float smem[];
+    dx_block<Tl>(smem, dl8, Wr, dx_in, T, E, E8, d, dx, (int64_t)blockIdx.x * Tl::BM, blockIdx.y * Tl::BN);
+}
+
+// Small batches of both types: all three sums in one launch, dWr over all
+// tokens in one go.
+using SmallTile = simt::Tile<32, 64, 4, 4>;
+struct SmallArgs {
+    const float *dl8, *x, *Wr, *bias_part;
+    const void *dx_in;
+    int64_t T;
+    int E, E8, d, token_blocks, dx_blocks, dwr_blocks;
+    void *dx;
+    float *dWr, *dbias;
+};
+template <typename TA>
+__global__ void __launch_bounds__(SmallTile::THREADS) small_products_kernel(SmallArgs a) {
+    pdl_wait();
+    using Tl = SmallTile;
+    extern __shared__ __align__(16) float smem[];
+    const int nt = (a.d + Tl::BN - 1) / Tl::BN;
+    int b = blockIdx.x;
+    if (b < a.dx_blocks) {
+        dx_block<Tl>(smem, a.dl8, a.Wr, static_cast<const TA *>(a.dx_in), a.T, a.E, a.E8, a.d,
+                     static_cast<TA *>(a.dx), (int64_t)(b / nt) * Tl::BM, b % nt * Tl::BN);
+        return;
+    }
+    b -= a.dx_blocks;
+    if (b < a.dwr_blocks) {
+        dwr_block<Tl>(smem, a.dl8, a.x, (int)a.T, a.E, a.E8, a.d, a.dWr, b / nt * Tl::BM, b % nt * Tl::BN);
+        return;
+    }
+    const int e = (b - a.dwr_blocks) * Tl::THREADS + threadIdx.x;
+    if (e >= a.E) return;
+    float s = 0.f;
+#pragma unroll 8
+    for (int i = 0; i < a.token_blocks; ++i) s += a.bias_part[(int64_t)i * a.E8 + e];
+    a.dbias[e] = s;
 }
 
 // ------------------------------- host side ---------------------------------
@@ -486,6 +561,15 @@ route_dx_kernel(const float *__restrict__ dl8, const float *__restrict__ Wr, con
 // against gathered: k = 8, E = 64 187 us to 145, E = 48 169 to 146, E = 32 112 to 115;
 // k = 4, E = 24 104 to 98, E = 16 78 to 77).
 bool gathers_rows(const Shape &s) { return !s.bf16 && s.renorm && s.E >= 5 * s.k; }
+
+// Short batches: two launches, terms and small_products_kernel, instead of four, on
+// the CUDA cores for both types (bf16, us: T = 16, d = 7168, E = 26 15.5 to 5.8; T = 1,
+// d = 7168, E = 256 28 to 14; T = 256, d = 4096, E = 128 24 to 21.5, but T = 512, d = 1024,
+// E = 64 17.7 to 20.6, where one block adds over all tokens; fp32, four launches on the
+// CUDA cores: T = 64, d = 2048, E = 128 11.3 to 9.1, T = 256, d = 4096, E = 32 11.1 to 12.3).
+bool small_batch(const Shape &s) {
+    return s.E > kFewMaxE && s.T <= (s.bf16 ? 256 : 128) && s.T * s.E * s.d <= (int64_t)1 << 27;
+}
 
 // dx's tiles: tokens x columns (T = 8192, d = 4096, E = 64: large 97 us, small 107;
 // T = 512, d = 1024: 6.8 and 4.7, too few blocks).
@@ -518,11 +602,12 @@ template <typename Tl> int64_t dwr_splits(const Shape &s) {
 }
 
 struct Plan {
-    bool few;  // few_experts_kernel
+    bool few;    // few_experts_kernel
+    bool small;  // small_products_kernel
     int few_cols;  // columns of one of its blocks
     int E8, terms, token_blocks;
     int splits, tokens;  // splits of the token axis in dWr's sum, tokens each
-    size_t dl, dlk, rows, W3, all, split_at, bias, part, total;  // workspace offsets
+    size_t dl, x32, dlk, rows, W3, all, split_at, bias, part, total;  // workspace offsets
 };
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -532,7 +617,9 @@ Plan plan(const Shape &s) {
     p.E8 = (s.E + 7) / 8 * 8;
     p.few = s.E <= kFewMaxE;
     p.few_cols = kFewThreads * (s.bf16 ? 8 : 4);
-    p.terms = s.bf16 && !p.few ? 3 : 1;
+    p.small = small_batch(s);
+    const bool tensor = s.bf16 && !p.few && !p.small, cores = !s.bf16 && !p.few && !p.small;
+    p.terms = tensor ? 3 : 1;
     const int64_t blocks = (s.T + kWarps - 1) / kWarps;
     p.token_blocks = (int)(blocks < kMaxTokenBlocks ? blocks : kMaxTokenBlocks);
     int64_t want;
@@ -542,6 +629,8 @@ Plan plan(const Shape &s) {
         const int64_t most = (s.T + 7) / 8;
         want = want < 1 ? 1 : want > most ? most : want;
         want = want < least ? least : want;
+    } else if (p.small) {
+        want = 1;
     } else if (s.bf16) {
         want = route_backward_splits(s.T, s.d, 3 * p.E8);
     } else {
@@ -556,14 +645,16 @@ Plan plan(const Shape &s) {
     p.splits = (int)((s.T + p.tokens - 1) / p.tokens);
     if (p.few) p.token_blocks = p.splits;
     size_t o = 0;
-    p.dl = o;  // bf16 x: four terms of 2 bytes; fp32 x: padded rows
-    if (!p.few) o = up256(o + (s.bf16 ? 8 : 4) * (size_t)s.T * p.E8);
+    p.dl = o;  // four terms of 2 bytes, or padded rows
+    if (!p.few) o = up256(o + (tensor ? 8 : 4) * (size_t)s.T * p.E8);
+    p.x32 = o;
+    if (p.small && s.bf16) o = up256(o + 4 * (size_t)s.T * s.d);
     p.dlk = o;
-    if (!p.few && gathers_rows(s)) o = up256(o + 4 * (size_t)s.P());
+    if (cores && gathers_rows(s)) o = up256(o + 4 * (size_t)s.P());
     p.rows = o;
-    if (!p.few && gathers_rows(s)) o = up256(o + 4 * (size_t)s.P());
+    if (cores && gathers_rows(s)) o = up256(o + 4 * (size_t)s.P());
     p.W3 = o;
-    if (s.bf16 && !p.few) o = up256(o + 2 * (size_t)3 * p.E8 * s.d);
+    if (tensor) o = up256(o + 2 * (size_t)3 * p.E8 * s.d);
     p.all = o;
     o = up256(o + 2 * sizeof(int32_t));
     p.split_at = o;
@@ -571,7 +662,8 @@ Plan plan(const Shape &s) {
     p.bias = o;
     o = up256(o + sizeof(float) * (size_t)p.token_blocks * p.E8);
     p.part = o;
-    o = up256(o + sizeof(float) * (size_t)p.splits * p.terms * (p.terms > 1 ? p.E8 : s.E) * s.d);
+    if (!p.small)
+        o = up256(o + sizeof(float) * (size_t)p.splits * p.terms * (p.terms > 1 ? p.E8 : s.E) * s.d);
     p.total = o;
     return p;
 }
@@ -631,7 +723,13 @@ cudaError_t launch_products(const Shape &s, const RouteBwd &a, const Plan &p, fl
     t.token_blocks = p.token_blocks;
     t.n_splits = p.splits;
     t.split = p.tokens;
-    if (s.bf16) {
+    if (p.small) {
+        t.dl8 = reinterpret_cast<float *>(ws + p.dl);
+        if (s.bf16) {
+            t.x = static_cast<const __nv_bfloat16 *>(a.x);
+            t.x32 = reinterpret_cast<float *>(ws + p.x32);
+        }
+    } else if (s.bf16) {
         t.dl4 = reinterpret_cast<__nv_bfloat16 *>(ws + p.dl);
         t.W3 = reinterpret_cast<__nv_bfloat16 *>(ws + p.W3);
         t.Wr = a.Wr;
@@ -644,13 +742,27 @@ cudaError_t launch_products(const Shape &s, const RouteBwd &a, const Plan &p, fl
             t.rows = reinterpret_cast<int32_t *>(ws + p.rows);
         }
     }
-    const int split_blocks =
-        s.bf16 ? (int)(((int64_t)p.E8 * s.d + kSplitCols - 1) / kSplitCols) : 0;
+    const int more_blocks = !s.bf16  ? 0
+                            : p.small ? (int)((s.T * s.d + kCopyCols - 1) / kCopyCols)
+                                      : (int)(((int64_t)p.E8 * s.d + kSplitCols - 1) / kSplitCols);
     const size_t sh = sizeof(float) * 2 * kWarps * (size_t)p.E8;  // at most 64 KB
     cudaError_t err;
     if (sh > 48 * 1024 && (err = simt::opt_in<terms_kernel>(64 * 1024)) != cudaSuccess) return err;
-    launch_pdl(terms_kernel, dim3(p.token_blocks + split_blocks), dim3(kThreads), sh, st, t, ds);
+    launch_pdl(terms_kernel, dim3(p.token_blocks + more_blocks), dim3(kThreads), sh, st, t, ds);
     if ((err = cudaGetLastError()) != cudaSuccess) return err;
+    if (p.small) {
+        using Tl = SmallTile;
+        const int nt = (s.d + Tl::BN - 1) / Tl::BN;
+        SmallArgs q = {t.dl8, s.bf16 ? t.x32 : static_cast<const float *>(a.x), a.Wr, bias_part, a.dx_in,
+                       s.T, s.E, p.E8, s.d, p.token_blocks, (int)((s.T + Tl::BM - 1) / Tl::BM) * nt,
+                       (s.E + Tl::BM - 1) / Tl::BM * nt, a.dx, a.dWr, a.dbias};
+        const int bias_blocks = a.dbias ? (s.E + Tl::THREADS - 1) / Tl::THREADS : 0;
+        const dim3 grid(q.dx_blocks + q.dwr_blocks + bias_blocks);
+        static_assert(Tl::SMEM_BYTES <= 48 * 1024, "no opt-in");
+        launch_pdl(s.bf16 ? small_products_kernel<__nv_bfloat16> : small_products_kernel<float>, grid,
+                   dim3(Tl::THREADS), Tl::SMEM_BYTES, st, q);
+        return cudaGetLastError();
+    }
     if (s.bf16) {
         RouteProducts r;
         r.x = a.x;
@@ -697,7 +809,7 @@ cudaError_t launch_route_backward(const Shape &s, const RouteBwd &a, const DevSt
     float *bias_part = reinterpret_cast<float *>(ws + p.bias);
     cudaError_t err = p.few ? launch_few(s, a, p, part, bias_part, ds, st)
                             : launch_products(s, a, p, part, bias_part, ds, st);
-    if (err != cudaSuccess) return err;
+    if (err != cudaSuccess || p.small) return err;
     const int share = p.splits * p.terms > 32 ? kWarps : 1;
     const int columns = 32 * kWarps / share;  // float4 columns of a block
     const int weight_blocks = (int)(((int64_t)s.E * s.d / 4 + columns - 1) / columns);
