@@ -642,6 +642,7 @@ Plan plan(const Shape &s) {
         want = want < 1 ? 1 : want > most ? most : want;
     }
     p.tokens = (int)((s.T + want - 1) / want);
+    if (tensor) p.tokens = (p.tokens + 63) / 64 * 64;  // whole K steps but for the last split's
     p.splits = (int)((s.T + p.tokens - 1) / p.tokens);
     if (p.few) p.token_blocks = p.splits;
     size_t o = 0;
