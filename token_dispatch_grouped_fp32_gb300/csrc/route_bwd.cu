@@ -498,16 +498,19 @@ __device__ __forceinline__ void dx_block(float *smem, const float *dl8, const fl
     });
 }
 
-// part[split][e][c]: the sum over the tokens of one split.
+// part[split][e][c]: the sum over the tokens of one split.  beside_dx: started
+// once route_dx_kernel's blocks run, whose output it does not read; it waits for that
+// launch at its end, so that the next one follows both.
 template <typename Tl>
 __global__ void __launch_bounds__(Tl::THREADS)
 dwr_kernel(const float *__restrict__ dl8, const float *__restrict__ x, int64_t T, int E, int E8,
-           int d, int tokens, float *__restrict__ part) {
-    pdl_wait();
+           int d, int tokens, int beside_dx, float *__restrict__ part) {
+    if (!beside_dx) pdl_wait();
     extern __shared__ __align__(16) float smem[];
     const int64_t t0 = (int64_t)blockIdx.z * tokens;
     dwr_block<Tl>(smem, dl8 + t0 * E8, x + t0 * d, (int)min((int64_t)tokens, T - t0), E, E8, d,
                   part + (int64_t)blockIdx.z * E * d, blockIdx.y * Tl::BM, blockIdx.x * Tl::BN);
+    if (beside_dx) pdl_wait();
 }
 
 template <typename Tl>
@@ -515,6 +518,7 @@ __global__ void __launch_bounds__(Tl::THREADS)
 route_dx_kernel(const float *__restrict__ dl8, const float *__restrict__ Wr, const float *dx_in,
                 int64_t T, int E, int E8, int d, float *dx) {
     pdl_wait();
+    pdl_release();
     extern __shared__ __align__(16) float smem[];
     dx_block<Tl>(smem, dl8, Wr, dx_in, T, E, E8, d, dx, (int64_t)blockIdx.x * Tl::BM, blockIdx.y * Tl::BN);
 }
@@ -701,7 +705,8 @@ cudaError_t launch_dwr(const Shape &s, const RouteBwd &a, const Plan &p, const f
     if (err != cudaSuccess) return err;
     launch_pdl(dwr_kernel<Tl>, dim3((s.d + Tl::BN - 1) / Tl::BN, (s.E + Tl::BM - 1) / Tl::BM, p.splits),
                dim3(Tl::THREADS), Tl::SMEM_BYTES, st, dl8,
-               static_cast<const float *>(a.x), s.T, s.E, p.E8, s.d, p.tokens, part);
+               static_cast<const float *>(a.x), s.T, s.E, p.E8, s.d, p.tokens, gathers_rows(s) ? 0 : 1,
+               part);
     return cudaGetLastError();
 }
 
