@@ -12,9 +12,9 @@
 // Two launches over the tile of simt_gemm.cuh.  T = 64, d = 128, f = 256, E =
 // 8: 14.1 us, latency (one tile shape of 32 x 32 for all products 22.4; dx and
 // the weights in launches of their own 24).  T = 1024, k = E = 8, d = f = 512 (34
-// GFLOP): 838 us, 41 TFLOP/s, bound by the multiply-adds and the instructions
+// GFLOP): 821 us, 42 TFLOP/s, bound by the multiply-adds and the instructions
 // beside them (64 x 64 tiles of 4 x 4 micro tiles, g and u apart, unpacked: 914).
-// T = 512, d = f = 488, E = 32, k = 4, routed unevenly: 304 us (508).
+// T = 512, d = f = 488, E = 32, k = 4, routed unevenly: 298 us (508).
 #include "common.cuh"
 #include "kernels.h"
 #include "simt_gemm.cuh"
@@ -138,7 +138,7 @@ struct WeightProduct {
 // launch: blocks below dx_blocks are dx's tiles (column tiles fastest), whose
 // chain over 2f is the longest, then every expert's tiles of wd and wg.
 template <typename X, typename W>
-__global__ void __launch_bounds__(W::THREADS)
+__global__ void __launch_bounds__(W::THREADS, W::MIN_BLOCKS)
 dx_weights_kernel(const float *__restrict__ dgu, const int32_t *__restrict__ offsets, int E,
                   const float *__restrict__ Wgu, int d, int f, float *__restrict__ dx, int dx_blocks,
                   WeightProduct wd, WeightProduct wg) {

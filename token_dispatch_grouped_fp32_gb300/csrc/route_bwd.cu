@@ -19,9 +19,9 @@
 // dx's and 33 in dWr's products (bound by shared memory, see gemm_bwd_tc.cu),
 // where fp32 products on the CUDA cores took 860.
 // fp32 x: the same steps on the CUDA cores, bound by the multiply-adds (T = 8192,
-// d = 4096, k = 8, E = 64 without renormalisation: 187 us, dx 97 and dWr 84);
+// d = 4096, k = 8, E = 64 without renormalisation: 172 us, dx 88 and dWr 82);
 // renormalised with many experts, dx is the sum of the chosen experts' rows of
-// Wr (145 us; E = 128 222, with the product over all E 348).
+// Wr (143 us; E = 128 220, with the product over all E 320).
 // At most 8 experts: one pass on the CUDA cores for both types (below).  Short
 // batches: all sums in one launch after the terms (small_batch).
 #include "common.cuh"
@@ -514,7 +514,7 @@ dwr_kernel(const float *__restrict__ dl8, const float *__restrict__ x, int64_t T
 }
 
 template <typename Tl>
-__global__ void __launch_bounds__(Tl::THREADS)
+__global__ void __launch_bounds__(Tl::THREADS, Tl::MIN_BLOCKS)
 route_dx_kernel(const float *__restrict__ dl8, const float *__restrict__ Wr, const float *dx_in,
                 int64_t T, int E, int E8, int d, float *dx) {
     pdl_wait();
@@ -562,8 +562,8 @@ __global__ void __launch_bounds__(SmallTile::THREADS) small_products_kernel(Smal
 // ------------------------------- host side ---------------------------------
 // fp32 x, renormalised: dx takes k rows of Wr a token instead of all E where
 // that is the lesser (T = 8192, d = 4096, whole gradient, product over all E
-// against gathered: k = 8, E = 64 187 us to 145, E = 48 169 to 146, E = 32 112 to 115;
-// k = 4, E = 24 104 to 98, E = 16 78 to 77).
+// against gathered: k = 8, E = 64 172 us to 143, E = 48 157 to 143, E = 32 108 to 115;
+// k = 4, E = 24 104 to 99, E = 16 73 to 77).
 bool gathers_rows(const Shape &s) { return !s.bf16 && s.renorm && s.E >= 5 * s.k; }
 
 // Short batches: two launches, terms and small_products_kernel, instead of four, on
@@ -575,7 +575,7 @@ bool small_batch(const Shape &s) {
     return s.E > kFewMaxE && s.T <= (s.bf16 ? 256 : 128) && s.T * s.E * s.d <= (int64_t)1 << 27;
 }
 
-// dx's tiles: tokens x columns (T = 8192, d = 4096, E = 64: large 97 us, small 107;
+// dx's tiles: tokens x columns (T = 8192, d = 4096, E = 64: large 88 us, small 107;
 // T = 512, d = 1024: 6.8 and 4.7, too few blocks).
 using DxLarge = simt::Tile<64, 128, 8, 8>;
 using DxSmall = simt::Tile<64, 64, 4, 4>;

@@ -29,11 +29,16 @@ template <int V> __device__ __forceinline__ void lds(float *v, const float *s) {
 // is a vector.  A k-contiguous operand is staged as [rows][BK], 16-byte chunk c of
 // row r at c ^ (r / V % 8), so that threads reading the same k of neighbouring
 // runs meet different banks; the other kind as [BK][columns].
+//
+// Stages in flight (cp.async): six for the smallest tiles, and two where micro tiles of
+// 8 x 8 leave room for more blocks by that, with the registers of four a block of 128
+// threads (router's fp32 products, T = 8192, d = 4096, E = 128: 341 us to 320).
 template <int BM_, int BN_, int TM_, int TN_, int VN_ = (TN_ < 4 ? TN_ : 4)> struct Tile {
     static constexpr int BM = BM_, BN = BN_, TM = TM_, TN = TN_;
     static constexpr int RG = BM / TM, CG = BN / TN, THREADS = RG * CG;
     static constexpr int VM = TM < 4 ? TM : 4, VN = VN_;
-    static constexpr int STAGES = BM * BN <= 16 * 32 ? 6 : 3;  // in flight (cp.async)
+    static constexpr int STAGES = BM * BN <= 16 * 32 ? 6 : TM * TN == 64 ? 2 : 3;
+    static constexpr int MIN_BLOCKS = STAGES == 2 ? 4 : 1;
     static constexpr int A_FLOATS = BM * BK, B_FLOATS = BN * BK;
     static constexpr int SMEM_BYTES = STAGES * (A_FLOATS + B_FLOATS) * (int)sizeof(float);
 
@@ -143,7 +148,10 @@ template <int BM_, int BN_, int TM_, int TN_, int VN_ = (TN_ < 4 ? TN_ : 4)> str
     }
 };
 
-// Raises a kernel's dynamic shared memory limit, once per kernel and device.
+// Raises a kernel's dynamic shared memory limit, once per kernel and device, and asks for
+// all of an SM's shared memory: blocks of two kernels share an SM only under one division
+// between shared memory and L1 (dWr's blocks beside dx's: T = 16384, d = 128, E = 40 32 us,
+// so 28).
 template <auto K> inline cudaError_t opt_in(size_t bytes) {
     static std::atomic<bool> done[64];
     int dev = 0;
@@ -152,7 +160,9 @@ template <auto K> inline cudaError_t opt_in(size_t bytes) {
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
     if ((err = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes)) !=
-        cudaSuccess)
+            cudaSuccess ||
+        (err = cudaFuncSetAttribute(K, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                    cudaSharedmemCarveoutMaxShared)) != cudaSuccess)
         return err;
     done[dev].store(true, std::memory_order_relaxed);
     return cudaSuccess;
