@@ -354,6 +354,14 @@ def moe_last_device_error(stream=None, raise_on_error=True):
     return _check(s, "moe_last_device_error", raise_on_error)
 
 
+def _version(x):
+    """torch's count of the in-place writes to x, or None where there is none or
+    it says nothing: inference tensors, and a stream that is being captured."""
+    if x.is_inference() or (x.is_cuda and torch.cuda.is_current_stream_capturing()):
+        return None
+    return x._version
+
+
 class MoELayer:
     """Weights of one MoE layer plus reusable workspaces; ``forward`` runs
     ``moe_forward`` on the given (default: current) stream.  Weights: Wr [E, d]
@@ -365,7 +373,13 @@ class MoELayer:
     a separate workspace for each stream it is called on.
 
     ``backward`` runs ``moe_backward`` for the latest ``forward`` on the same
-    stream, whose intermediates it finds in that workspace."""
+    stream, whose intermediates it finds in that workspace.  It refuses when
+    they are not there: after a ``forward`` that failed, when the workspace has
+    been replaced by a larger one, when the layer's sizes or modes have changed,
+    and for an ``x`` that is not the memory the forward read or has been written
+    to since (by torch's count of in-place writes, which views of one tensor
+    share; not looked at where the forward was captured in a graph, whose
+    replays read ``x`` afresh)."""
 
     def __init__(self, Wr, W_gate_up, W_down, k, logit_bias=None, renormalize=True,
                  scale_inputs=False):
@@ -380,6 +394,7 @@ class MoELayer:
         self._ws = {}  # stream handle -> workspace
         self._bwd_ws = {}  # the same for the backward pass
         self._tokens = {}  # stream handle -> tokens of its latest forward
+        self._forwards = {}  # ... and its workspace, sizes and x
 
     def config(self, T: int) -> moe_config_t:
         return config(T, self.d, self.E, self.k, self.f, self.dtype, self.renormalize,
@@ -387,8 +402,17 @@ class MoELayer:
 
     def workspace(self, T: int, stream=None):
         """The workspace for calls on `stream` (default: the current stream),
-        grown to moe_workspace_size for T tokens when needed."""
-        return self._grown(self._ws, moe_workspace_size(self.config(T)), stream)
+        grown to moe_workspace_size for T tokens when needed.  A workspace that
+        grows is a new one: the latest forward's intermediates are gone."""
+        kept = self._ws.get(_stream(stream))
+        ws = self._grown(self._ws, moe_workspace_size(self.config(T)), stream)
+        if ws is not kept:
+            self._forget(stream)
+        return ws
+
+    def _forget(self, stream):
+        self._tokens.pop(_stream(stream), None)
+        self._forwards.pop(_stream(stream), None)
 
     def _grown(self, kept, need, stream):
         key = _stream(stream)
@@ -403,9 +427,13 @@ class MoELayer:
         if out is None:
             out = torch.empty_like(x)
         cfg = self.config(T)
-        moe_forward(cfg, x, self.Wr, self.logit_bias, self.W_gate_up, self.W_down, out,
-                    self.workspace(T, stream), stream=stream)
+        ws = self.workspace(T, stream)
+        self._forget(stream)  # until all of its kernels are launched
+        moe_forward(cfg, x, self.Wr, self.logit_bias, self.W_gate_up, self.W_down, out, ws,
+                    stream=stream)
         self._tokens[_stream(stream)] = T
+        if _ptr(out) != _ptr(x):
+            self._forwards[_stream(stream)] = (ws, bytes(cfg), x.data_ptr(), _version(x))
         return out
 
     __call__ = forward
@@ -435,8 +463,13 @@ class MoELayer:
                 continue
             if g is None or g.shape != t.shape or g.dtype != t.dtype:
                 raise ValueError(f"the gradient of {n} is {tuple(t.shape)} {t.dtype}")
+        fwd_ws, ran, at, version = self._forwards.get(_stream(stream), (None,) * 4)
+        written = version is not None and _version(x) not in (None, version)
+        if T and (ran != bytes(cfg) or at != x.data_ptr() or written):
+            raise RuntimeError("x is not what the latest forward on this stream read, has been "
+                               "written to since, or the layer has changed since")
         ws = self._grown(self._bwd_ws, moe_backward_workspace_size(cfg), stream)
-        moe_backward(cfg, x, self.Wr, self.W_gate_up, self.W_down, self.workspace(T, stream), dout,
-                     grads["x"], grads["Wr"], grads.get("logit_bias"), grads["W_gate_up"],
-                     grads["W_down"], ws, stream=stream)
+        moe_backward(cfg, x, self.Wr, self.W_gate_up, self.W_down, fwd_ws, dout, grads["x"],
+                     grads["Wr"], grads.get("logit_bias"), grads["W_gate_up"], grads["W_down"], ws,
+                     stream=stream)
         return grads
