@@ -11,6 +11,7 @@ workspace per stream (allocated with torch) and calls ``moe_forward``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -362,6 +363,18 @@ def _version(x):
     return x._version
 
 
+def _allocating_on(side):
+    return contextlib.nullcontext() if side is None else torch.cuda.stream(side)
+
+
+def _record(side, tensors):
+    """Keeps the tensors' memory from its pool until `side` is done with it."""
+    if side is not None:
+        for t in tensors:
+            if isinstance(t, torch.Tensor):
+                t.record_stream(side)
+
+
 class MoELayer:
     """Weights of one MoE layer plus reusable workspaces; ``forward`` runs
     ``moe_forward`` on the given (default: current) stream.  Weights: Wr [E, d]
@@ -370,7 +383,11 @@ class MoELayer:
 
     The workspace holds a call's intermediates (logits, routing, permuted
     rows), so two calls in flight at once must not share one: the layer keeps
-    a separate workspace for each stream it is called on.
+    a separate workspace for each stream it is called on.  A call with a
+    ``stream`` that is not the current one allocates from that stream's pool,
+    and neither what it returns nor the tensors given to it go back to a pool
+    before both streams are done with them; ordering the two streams is the
+    caller's part.
 
     ``backward`` runs ``moe_backward`` for the latest ``forward`` on the same
     stream, whose intermediates it finds in that workspace.  It refuses when
@@ -418,14 +435,28 @@ class MoELayer:
         key = _stream(stream)
         ws = kept.get(key)
         if ws is None or ws.numel() < need:
-            ws = torch.empty(max(need, 256), dtype=torch.uint8, device=self.Wr.device)
+            with _allocating_on(self._other(stream)):
+                ws = torch.empty(max(need, 256), dtype=torch.uint8, device=self.Wr.device)
             kept[key] = ws
         return ws
 
+    def _other(self, stream):
+        """`stream` as a torch stream, or None where it is the current one."""
+        if stream is None or not self.Wr.is_cuda or _stream(stream) == _stream(None):
+            return None
+        if isinstance(stream, torch.cuda.Stream):
+            return stream
+        return torch.cuda.ExternalStream(int(stream)) if stream else torch.cuda.default_stream()
+
     def forward(self, x, out=None, stream=None):
         T = x.shape[0]
+        side, given = self._other(stream), (x, out)
         if out is None:
-            out = torch.empty_like(x)
+            with _allocating_on(side):
+                out = torch.empty_like(x)
+            if side is not None:
+                _record(torch.cuda.current_stream(), (out,))
+        _record(side, given)
         cfg = self.config(T)
         ws = self.workspace(T, stream)
         self._forget(stream)  # until all of its kernels are launched
@@ -455,8 +486,10 @@ class MoELayer:
         like = {"x": x, "Wr": self.Wr, "W_gate_up": self.W_gate_up, "W_down": self.W_down}
         if self.logit_bias is not None:
             like["logit_bias"] = self.logit_bias
-        if grads is None:
-            grads = {n: torch.empty_like(t) for n, t in like.items()}
+        side, made = self._other(stream), grads is None
+        if made:
+            with _allocating_on(side):
+                grads = {n: torch.empty_like(t) for n, t in like.items()}
         for n, t in like.items():
             g = grads.get(n)
             if g is None and n == "logit_bias":
@@ -468,6 +501,9 @@ class MoELayer:
         if T and (ran != bytes(cfg) or at != x.data_ptr() or written):
             raise RuntimeError("x is not what the latest forward on this stream read, has been "
                                "written to since, or the layer has changed since")
+        _record(side, (x, dout))
+        if side is not None:
+            _record(torch.cuda.current_stream() if made else side, grads.values())
         ws = self._grown(self._bwd_ws, moe_backward_workspace_size(cfg), stream)
         moe_backward(cfg, x, self.Wr, self.W_gate_up, self.W_down, fwd_ws, dout, grads["x"],
                      grads["Wr"], grads.get("logit_bias"), grads["W_gate_up"], grads["W_down"], ws,
