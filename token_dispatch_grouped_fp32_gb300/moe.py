@@ -387,7 +387,8 @@ class MoELayer:
     ``stream`` that is not the current one allocates from that stream's pool,
     and neither what it returns nor the tensors given to it go back to a pool
     before both streams are done with them; ordering the two streams is the
-    caller's part.
+    caller's part.  A workspace that a graph was captured with stays allocated as
+    long as the layer, also when a longer batch gets a new one.
 
     ``backward`` runs ``moe_backward`` for the latest ``forward`` on the same
     stream, whose intermediates it finds in that workspace.  It refuses when
@@ -412,6 +413,7 @@ class MoELayer:
         self._bwd_ws = {}  # the same for the backward pass
         self._tokens = {}  # stream handle -> tokens of its latest forward
         self._forwards = {}  # ... and its workspace, sizes and x
+        self._captured = {}  # workspaces in captured graphs: kept with the layer
 
     def config(self, T: int) -> moe_config_t:
         return config(T, self.d, self.E, self.k, self.f, self.dtype, self.renormalize,
@@ -438,6 +440,8 @@ class MoELayer:
             with _allocating_on(self._other(stream)):
                 ws = torch.empty(max(need, 256), dtype=torch.uint8, device=self.Wr.device)
             kept[key] = ws
+        if ws.is_cuda and torch.cuda.is_current_stream_capturing():
+            self._captured[ws.data_ptr()] = ws
         return ws
 
     def _other(self, stream):
