@@ -461,10 +461,13 @@ size_t moe_clip_grad_norm_workspace_size(void);
  * layer's gradients and its optimizer):
  *   norm = sqrt(sum over all tensors and elements of g^2)
  *   out  = g * min(1, max_norm / (norm + 1e-6)),  rounded once
- * Squares are summed in fp32 within 16384 elements and in fp64 across, in a
- * fixed order; the norm never leaves the device.  A NaN or infinite gradient
- * gives a NaN or infinite norm, and the scale follows the formula (an
- * infinite norm scales finite gradients to 0): a caller that wants to skip
+ * A thread sums 64 of 16384 elements' squares in fp32, scaled by a power of two
+ * where they would leave its range; beyond that sums are fp64, in a fixed
+ * order.  So the norm is within a few fp32 roundings for any finite
+ * gradients, as long as it is a finite float itself.  It never leaves the device.
+ * A NaN or infinite gradient gives a NaN or infinite norm, finite gradients
+ * whose norm is past 3.4e38 an infinite one, and the scale follows the formula
+ * (an infinite norm scales finite gradients to 0): a caller that wants to skip
  * such a step reads `norm`.
  * grads: HOST array of n >= 0 entries, read before the call returns; `norm`:
  * one float on the device, written (0 for no elements).  max_norm >= 0.

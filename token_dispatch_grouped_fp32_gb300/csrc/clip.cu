@@ -2,8 +2,9 @@
 // copies:  N = sqrt(sum of all squares),  out = g * min(1, max_norm / (N + 1e-6)).
 //
 // Launch 1 (norm_kernel): the tensors are cut into chunks of kChunk elements;
-// block b sums the squares of chunks b, b + grid, ... (fp32 inside a chunk,
-// doubles across chunks) and writes one double.  Launch 2 (scale_kernel):
+// block b sums the squares of chunks b, b + grid, ... (a thread's 64 of a chunk
+// in fp32, with their scale adjusted where they leave its range; doubles beyond)
+// and writes one double.  Launch 2 (scale_kernel):
 // every block adds the partial sums of launch 1 in the same order, so each
 // has the same norm and no block waits for another, and scales its chunks.
 // The tensors' addresses and sizes travel as kernel parameters: no copy to
@@ -77,42 +78,80 @@ __device__ __forceinline__ Chunk find_chunk(const Table &t, int c) {
     return k;
 }
 
-template <typename TA> __device__ __forceinline__ float chunk_squares(const TA *p, int n) {
+// This thread's share of the sum of (scale g)^2 over a chunk; any: the bits set in
+// its elements, but for their signs.
+template <typename TA, bool SCALED>
+__device__ __forceinline__ float thread_squares(const TA *p, int n, float scale, uint32_t *any) {
     constexpr int EPV = 16 / sizeof(TA);
     const int head = min(n, (int)((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / (int)sizeof(TA));
     float s = 0.f;
-    if ((int)threadIdx.x < head) {
-        const float v = Act<TA>::to_f(p[threadIdx.x]);
-        s = v * v;
-    }
+    uint32_t bits = 0;
+    auto one = [&](TA g) {
+        const float v = SCALED ? scale * Act<TA>::to_f(g) : Act<TA>::to_f(g);
+        bits |= __float_as_uint(v) & 0x7fffffffu;
+        s = fmaf(v, v, s);
+    };
+    if ((int)threadIdx.x < head) one(p[threadIdx.x]);
     const int nv = (n - head) / EPV;
     const TA *q = p + head;
 #pragma unroll 4
     for (int i = threadIdx.x; i < nv; i += kThreads) {
+        const uint4 raw = ldg16(q + (int64_t)i * EPV);
         float v[EPV];
-        unpack16(ldg16(q + (int64_t)i * EPV), v, static_cast<const TA *>(nullptr));
+        unpack16(raw, v, static_cast<const TA *>(nullptr));
+        if (!SCALED)
+            bits |= (raw.x | raw.y | raw.z | raw.w) & (sizeof(TA) == 2 ? 0x7fff7fffu : 0x7fffffffu);
 #pragma unroll
-        for (int j = 0; j < EPV; ++j) s = fmaf(v[j], v[j], s);
+        for (int j = 0; j < EPV; ++j) {
+            if (SCALED) v[j] *= scale;
+            s = fmaf(v[j], v[j], s);
+        }
     }
     const int tail = head + nv * EPV + threadIdx.x;
-    if (tail < n) {
-        const float v = Act<TA>::to_f(p[tail]);
-        s = fmaf(v, v, s);
-    }
+    if (tail < n) one(p[tail]);
+    *any = bits;
     return s;
 }
 
+// ... without a scale, and where that sum left fp32's range, again with a power of
+// two that is taken out afterwards.  A sum that overflowed: all terms are within
+// 2^96 then, and what underflows is below 2^-110 of it.  A sum below 2^-100 that
+// is not of zeros alone: every element is below 2^-50, and the smallest
+// subnormal's square becomes 2^-98.  From 2^-100 up, what a square lost by
+// underflow is below 2^-43 of the sum.  The zeros of an expert without rows stay
+// on the first pass.
+template <typename TA> __device__ __forceinline__ double chunk_squares(const TA *p, int n) {
+    uint32_t any, unused;
+    const float s = thread_squares<TA, false>(p, n, 1.f, &any);
+    if (any == 0 || (s >= 0x1p-100f && s < INFINITY)) return s;
+    const bool small = s < 0x1p-100f;  // else an overflow, an infinity or a NaN
+    return (double)thread_squares<TA, true>(p, n, small ? 0x1p100f : 0x1p-80f, &unused) *
+           (small ? 0x1p-200 : 0x1p160);
+}
+
+// The scale as a product of two factors, the second 1 or, where the scale itself
+// would be subnormal (a norm near fp32's end), a power of two.
+struct Scale {
+    float a, b;
+    __device__ __forceinline__ float operator()(float g) const { return g * a * b; }
+};
+__device__ __forceinline__ Scale scale_for(float max_norm, float nrm) {
+    const float c = max_norm / (nrm + 1e-6f);
+    if (c < 0x1p-100f) return {max_norm * 0x1p100f / (nrm + 1e-6f), 0x1p-100f};
+    return {c > 1.f ? 1.f : c, 1.f};  // a NaN norm stays NaN
+}
+
 template <typename TA>
-__device__ __forceinline__ void chunk_scale(const TA *p, TA *o, int n, float coef) {
+__device__ __forceinline__ void chunk_scale(const TA *p, TA *o, int n, const Scale &scale) {
     constexpr int EPV = 16 / sizeof(TA);
     const unsigned mp = reinterpret_cast<uintptr_t>(p) & 15, mo = reinterpret_cast<uintptr_t>(o) & 15;
     if (mp != mo) {  // no common 16-byte boundary
         for (int i = threadIdx.x; i < n; i += kThreads)
-            o[i] = Act<TA>::from_f(Act<TA>::to_f(p[i]) * coef);
+            o[i] = Act<TA>::from_f(scale(Act<TA>::to_f(p[i])));
         return;
     }
     const int head = min(n, (int)((16 - mp) & 15) / (int)sizeof(TA));
-    if ((int)threadIdx.x < head) o[threadIdx.x] = Act<TA>::from_f(Act<TA>::to_f(p[threadIdx.x]) * coef);
+    if ((int)threadIdx.x < head) o[threadIdx.x] = Act<TA>::from_f(scale(Act<TA>::to_f(p[threadIdx.x])));
     const int nv = (n - head) / EPV;
     constexpr int U = 4;  // loads before the first store (o may be p)
     for (int i0 = threadIdx.x; i0 < nv; i0 += U * kThreads) {
@@ -127,13 +166,13 @@ __device__ __forceinline__ void chunk_scale(const TA *p, TA *o, int n, float coe
             float v[EPV];
             unpack16(raw[u], v, static_cast<const TA *>(nullptr));
 #pragma unroll
-            for (int j = 0; j < EPV; ++j) v[j] *= coef;
+            for (int j = 0; j < EPV; ++j) v[j] = scale(v[j]);
             stg16(o + head + (int64_t)(i0 + u * kThreads) * EPV,
                   pack16(v, static_cast<const TA *>(nullptr)));
         }
     }
     const int tail = head + nv * EPV + threadIdx.x;
-    if (tail < n) o[tail] = Act<TA>::from_f(Act<TA>::to_f(p[tail]) * coef);
+    if (tail < n) o[tail] = Act<TA>::from_f(scale(Act<TA>::to_f(p[tail])));
 }
 
 __global__ void __launch_bounds__(kThreads)
@@ -158,8 +197,7 @@ scale_kernel(const __grid_constant__ Table t, const double *__restrict__ part, i
     for (int i = threadIdx.x; i < parts; i += kThreads) sum += part[i];
     const float nrm = (float)sqrt(block_sum(sum));
     if (blockIdx.x == 0 && threadIdx.x == 0) *norm = nrm;
-    float coef = max_norm / (nrm + 1e-6f);
-    coef = coef > 1.f ? 1.f : coef;  // a NaN norm stays NaN
+    const Scale scale = scale_for(max_norm, nrm);
     // from the last chunk: what launch 1 read last is still in the L2 cache
     // (the Mixtral-shaped layer's gradients: 1350 us forward, 1277 us backward)
     for (int c = t.chunks - 1 - (int)blockIdx.x; c >= 0; c -= gridDim.x) {
@@ -167,10 +205,10 @@ scale_kernel(const __grid_constant__ Table t, const double *__restrict__ part, i
         if (k.t.dst == nullptr) continue;
         if (k.t.bf16)
             chunk_scale(static_cast<const __nv_bfloat16 *>(k.t.src) + k.first,
-                        static_cast<__nv_bfloat16 *>(k.t.dst) + k.first, k.count, coef);
+                        static_cast<__nv_bfloat16 *>(k.t.dst) + k.first, k.count, scale);
         else
             chunk_scale(static_cast<const float *>(k.t.src) + k.first,
-                        static_cast<float *>(k.t.dst) + k.first, k.count, coef);
+                        static_cast<float *>(k.t.dst) + k.first, k.count, scale);
     }
 }
 
