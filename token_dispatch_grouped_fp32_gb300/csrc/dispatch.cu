@@ -30,6 +30,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "once.h"
 #include "tc_ptx.cuh"
 
 namespace moe {
@@ -544,21 +545,17 @@ template <typename TA>
 cudaError_t launch_token_rows(const void *x, const int32_t *hist, const Shape &s,
                               const DispatchGrid &g, int32_t *pos, int32_t *src_token,
                               void *x_perm, unsigned blocks, size_t smem, cudaStream_t st) {
-    static bool attr_set[64] = {};
-    int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
+    static OncePerDevice once;
+    cudaError_t err = once([](int) {
+        cudaError_t e = cudaFuncSetAttribute(place_token_rows_kernel<TA>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             kTokWarps * kStageRowMax);
+        if (e != cudaSuccess) return e;
+        return cudaFuncSetAttribute(place_token_rows_kernel<TA>,
+                                    cudaFuncAttributePreferredSharedMemoryCarveout,
+                                    (int)cudaSharedmemCarveoutMaxShared);
+    });
     if (err != cudaSuccess) return err;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!attr_set[dev]) {
-        if ((err = cudaFuncSetAttribute(place_token_rows_kernel<TA>,
-                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        kTokWarps * kStageRowMax)) != cudaSuccess ||
-            (err = cudaFuncSetAttribute(place_token_rows_kernel<TA>,
-                                        cudaFuncAttributePreferredSharedMemoryCarveout,
-                                        (int)cudaSharedmemCarveoutMaxShared)) != cudaSuccess)
-            return err;
-        attr_set[dev] = true;
-    }
     launch_pdl(place_token_rows_kernel<TA>, dim3(blocks), dim3(32 * kTokWarps), smem, st,
                static_cast<const TA *>(x), hist, s.T, s.k, s.d, g.chunk, g.blocks, pos, src_token,
                static_cast<TA *>(x_perm));
@@ -575,28 +572,20 @@ cudaError_t launch_dispatch_one(const Shape &s, const int32_t *idx, const void *
                                 int32_t *src_token, void *x_perm, const DevStatus &ds,
                                 cudaStream_t st, bool in_forward, bool *launched) {
     *launched = false;
-    static bool attr_set[64] = {};
-    static int sms[64] = {};
+    static OncePerDevice once;
     const int64_t row_bytes = (int64_t)s.d * (int64_t)sizeof(TA);
     if (!dispatch_fits_one_launch(s)) return cudaSuccess;
-    int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
+    cudaError_t err = once([](int) {
+        cudaError_t e = cudaFuncSetAttribute(dispatch_one_launch_kernel<TA, true>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             kOneStageBytes);
+        if (e != cudaSuccess) return e;
+        return cudaFuncSetAttribute(dispatch_one_launch_kernel<TA, false>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, kOneStageBytes);
+    });
     if (err != cudaSuccess) return err;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!attr_set[dev]) {
-        if ((err = cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev)) !=
-                cudaSuccess ||
-            (err = cudaFuncSetAttribute(dispatch_one_launch_kernel<TA, true>,
-                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        kOneStageBytes)) != cudaSuccess ||
-            (err = cudaFuncSetAttribute(dispatch_one_launch_kernel<TA, false>,
-                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        kOneStageBytes)) != cudaSuccess)
-            return err;
-        attr_set[dev] = true;
-    }
     const int64_t P = s.P();
-    const int64_t blocks = std::min<int64_t>(sms[dev], s.T);
+    const int64_t blocks = std::min<int64_t>(device_sm_count(), s.T);
     const int64_t tok = (s.T + blocks - 1) / blocks;  // most tokens a block owns
     const int nw = (int)std::min<int64_t>(std::min<int64_t>(kOneMaxWarps, tok),
                                           kOneStageBytes / row_bytes);
@@ -669,21 +658,17 @@ cudaError_t launch_dispatch(const Shape &s, const int32_t *idx, const void *x, i
                             int32_t *offsets, int32_t *pos, int32_t *src_token, void *x_perm,
                             int32_t *hist, const DevStatus &ds, cudaStream_t st,
                             const float *scale, bool in_forward, float *row_scale) {
-    static bool attr_set[64] = {};
-    int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
+    static OncePerDevice once;
+    cudaError_t err = once([](int) {  // E = 1024: 32 warps x 1024 counts = 128 KB
+        cudaError_t e = cudaFuncSetAttribute(rank_kernel<kRankThreads>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             kRankWarps * 1024 * (int)sizeof(int));
+        if (e != cudaSuccess) return e;
+        return cudaFuncSetAttribute(rank_kernel<kSmallRankThreads>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    kScanStageMax * (int)sizeof(int));
+    });
     if (err != cudaSuccess) return err;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!attr_set[dev]) {  // E = 1024: 32 warps x 1024 counts = 128 KB
-        if ((err = cudaFuncSetAttribute(rank_kernel<kRankThreads>,
-                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        kRankWarps * 1024 * (int)sizeof(int))) != cudaSuccess ||
-            (err = cudaFuncSetAttribute(rank_kernel<kSmallRankThreads>,
-                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        kScanStageMax * (int)sizeof(int))) != cudaSuccess)
-            return err;
-        attr_set[dev] = true;
-    }
     const int64_t P = s.P();
     if (scale == nullptr && x_perm != nullptr) {
         bool one = false;

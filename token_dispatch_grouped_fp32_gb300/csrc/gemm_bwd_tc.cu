@@ -68,6 +68,7 @@
 #include "common.cuh"
 #include "gemm_tiles.cuh"
 #include "kernels.h"
+#include "once.h"
 #include "tc_ptx.cuh"
 
 namespace moe {
@@ -915,8 +916,7 @@ template <int CTAS> cudaError_t prepare_all(int *resident) {
 }
 
 struct DeviceInfo {
-    bool ready = false;
-    int units[3] = {0, 0, 0};  // resident single CTAs [1] and pairs [2]
+    std::atomic<int> units[3];  // resident single CTAs [1] and pairs [2]
 };
 
 template <int CTAS, int KIND>
@@ -1031,26 +1031,28 @@ namespace {
 
 // The current device's resident units; also checks the tensor-map encoder.
 cudaError_t device_info(const DeviceInfo **out) {
-    static DeviceInfo info[64];
+    static DeviceInfo info[OncePerDevice::kDevices];
+    static OncePerDevice once;
     int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
-    if (err != cudaSuccess) return err;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    DeviceInfo &d = info[dev];
-    if (!d.ready) {
-        if ((err = prepare_all<1>(&d.units[1])) != cudaSuccess ||
-            (err = prepare_all<2>(&d.units[2])) != cudaSuccess ||
-            (err = prepare_split<GU>()) != cudaSuccess || (err = prepare_split<DX>()) != cudaSuccess) {
-            set_error_message("the gradient's matrix products do not fit on device %d", dev);
-            return err;
+    cudaError_t err = once([&](int device) {
+        int singles = 0, pairs = 0;
+        cudaError_t e;
+        if ((e = prepare_all<1>(&singles)) != cudaSuccess ||
+            (e = prepare_all<2>(&pairs)) != cudaSuccess ||
+            (e = prepare_split<GU>()) != cudaSuccess || (e = prepare_split<DX>()) != cudaSuccess) {
+            set_error_message("the gradient's matrix products do not fit on device %d", device);
+            return e;
         }
-        d.ready = true;
-    }
+        info[device].units[1] = singles;
+        info[device].units[2] = pairs;
+        return cudaSuccess;
+    });
+    if (err != cudaSuccess || (err = cudaGetDevice(&dev)) != cudaSuccess) return err;
     if (!tensor_map_encoder()) {
         set_error_message("cuTensorMapEncodeTiled is not available from the driver");
         return cudaErrorNotSupported;
     }
-    *out = &d;
+    *out = &info[dev];
     return cudaSuccess;
 }
 

@@ -78,6 +78,7 @@
 #include "common.cuh"
 #include "gemm_tiles.cuh"
 #include "kernels.h"
+#include "once.h"
 #include "tc_ptx.cuh"
 
 namespace moe {
@@ -675,9 +676,8 @@ grouped_gemm_tc_kernel(const __grid_constant__ CUtensorMap tmX,
 
 // ------------------------------ host side ----------------------------------
 struct DeviceInfo {
-    bool ready = false;
-    int sms = 0;    // single CTAs that fit at once (one per SM)
-    int pairs = 0;  // CTA pairs that fit at once
+    std::atomic<int> sms;    // single CTAs that fit at once (one per SM)
+    std::atomic<int> pairs;  // CTA pairs that fit at once
 };
 
 template <int CTAS>
@@ -812,23 +812,22 @@ cudaError_t launch_grouped_swiglu_tc(const Shape &s, const void *x_perm, const i
                                      const DevStatus &ds, cudaStream_t st, bool a_local,
                                      const int32_t *src_token, const float *row_scale) {
     using namespace tc;
-    static DeviceInfo info[64];
+    static DeviceInfo info[OncePerDevice::kDevices];
+    static OncePerDevice once;
     int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
-    if (err != cudaSuccess) return err;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!info[dev].ready) {
+    cudaError_t err = once([&](int device) {
         int a = 0, c = 0;
-        if ((err = prepare<1>(&a)) != cudaSuccess || (err = prepare<2>(&c)) != cudaSuccess)
-            return err;
-        info[dev].sms = a;
-        info[dev].pairs = c;
-        if (info[dev].sms < 1 || info[dev].pairs < 1) {
-            set_error_message("the grouped GEMM does not fit on device %d", dev);
+        cudaError_t e;
+        if ((e = prepare<1>(&a)) != cudaSuccess || (e = prepare<2>(&c)) != cudaSuccess) return e;
+        if (a < 1 || c < 1) {
+            set_error_message("the grouped GEMM does not fit on device %d", device);
             return cudaErrorInvalidConfiguration;
         }
-        info[dev].ready = true;
-    }
+        info[device].sms = a;
+        info[device].pairs = c;
+        return cudaSuccess;
+    });
+    if (err != cudaSuccess || (err = cudaGetDevice(&dev)) != cudaSuccess) return err;
     if (!tensor_map_encoder()) {
         set_error_message("cuTensorMapEncodeTiled is not available from the driver");
         return cudaErrorNotSupported;

@@ -60,10 +60,12 @@ namespace {
 
 constexpr int kMaxDevices = 64;
 
+// Threads whose first calls meet may each fill it in, with the same values; one
+// that finds `checked` (acquire) has seen the others.
 struct DevState {
-    bool checked = false;
-    bool supported = false;
-    unsigned *err_word = nullptr;
+    std::atomic<bool> checked;
+    std::atomic<bool> supported;
+    std::atomic<unsigned *> err_word;
 };
 DevState g_dev[kMaxDevices];
 
@@ -83,12 +85,12 @@ moe_status_t device_status(DevStatus *out) {
         return MOE_ERR_UNSUPPORTED;
     }
     DevState &s = g_dev[dev];
-    if (!s.checked) {
+    if (!s.checked.load(std::memory_order_acquire)) {
         int major = 0, minor = 0;
         cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
         cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
-        s.supported = (major == 10 && minor == 3);
-        if (s.supported) {
+        const bool supported = major == 10 && minor == 3;
+        if (supported) {
             void *p = nullptr;
             e = cudaGetSymbolAddress(&p, g_device_error_word);
             if (e != cudaSuccess) {
@@ -100,7 +102,8 @@ moe_status_t device_status(DevStatus *out) {
             set_error_message("device %d is sm_%d%d; libmoe is built for sm_103a only", dev, major,
                               minor);
         }
-        s.checked = true;
+        s.supported = supported;
+        s.checked.store(true, std::memory_order_release);
     }
     if (!s.supported) return MOE_ERR_UNSUPPORTED;
     out->err = s.err_word;

@@ -37,6 +37,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "once.h"
 #include "tc_ptx.cuh"
 
 namespace moe {
@@ -318,18 +319,12 @@ size_t router_tc_scratch_bytes(const Shape &s) {
 template <int CTAS>
 cudaError_t launch_router_kernel(dim3 grid, size_t smem, cudaStream_t st, const CUtensorMap &mx,
                                  const CUtensorMap &mw, const RouterParams &p) {
-    static bool attr_set[64] = {};
-    int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
+    static OncePerDevice once;
+    cudaError_t err = once([](int) {
+        return cudaFuncSetAttribute(router_logits_tc_kernel<CTAS>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, R_SMEM_MAX);
+    });
     if (err != cudaSuccess) return err;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!attr_set[dev]) {
-        if ((err = cudaFuncSetAttribute(router_logits_tc_kernel<CTAS>,
-                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        R_SMEM_MAX)) != cudaSuccess)
-            return err;
-        attr_set[dev] = true;
-    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(R_THREADS, 1, 1);

@@ -5,9 +5,8 @@
 // matrix; such elements are zeros.
 #pragma once
 
-#include <atomic>
-
 #include "common.cuh"
+#include "once.h"
 #include "tc_ptx.cuh"
 
 namespace moe {
@@ -153,19 +152,14 @@ template <int BM_, int BN_, int TM_, int TN_, int VN_ = (TN_ < 4 ? TN_ : 4)> str
 // between shared memory and L1 (dWr's blocks beside dx's: T = 16384, d = 128, E = 40 32 us,
 // so 28).
 template <auto K> inline cudaError_t opt_in(size_t bytes) {
-    static std::atomic<bool> done[64];
-    int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
-    if (err != cudaSuccess) return err;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
-    if ((err = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes)) !=
-            cudaSuccess ||
-        (err = cudaFuncSetAttribute(K, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                    cudaSharedmemCarveoutMaxShared)) != cudaSuccess)
-        return err;
-    done[dev].store(true, std::memory_order_relaxed);
-    return cudaSuccess;
+    static OncePerDevice once;
+    return once([&](int) {
+        cudaError_t err =
+            cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        if (err != cudaSuccess) return err;
+        return cudaFuncSetAttribute(K, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                    cudaSharedmemCarveoutMaxShared);
+    });
 }
 
 }  // namespace simt
