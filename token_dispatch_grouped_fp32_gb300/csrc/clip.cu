@@ -11,8 +11,8 @@
 // the device, and the calls can be captured in a graph.
 //
 // Bound by HBM where the set exceeds L2: three passes over its bytes (1.41 G
-// elements of a Mixtral-shaped layer, 8.46 GB: 1270 us, 0.98 of the copy rate).
-// 300 tensors of up to 20,000 elements: 10.2 us, two launches and their chains
+// elements of a Mixtral-shaped layer, 8.46 GB: 1266 us, 0.98 of the copy rate).
+// 300 tensors of up to 20,000 elements: 10.3 us, two launches and their chains
 // of table, data and norm (25.7 with 912 blocks whatever the chunks, and the
 // table in separate arrays).
 #include <algorithm>
@@ -130,10 +130,11 @@ template <typename TA> __device__ __forceinline__ double chunk_squares(const TA 
 }
 
 // The scale as a product of two factors, the second 1 or, where the scale itself
-// would be subnormal (a norm near fp32's end), a power of two.
+// would be subnormal (a norm near fp32's end), a power of two.  Two factors take
+// the simple loop: in the vector loop the second one cost the whole Mixtral-shaped
+// set 6 % (1266 us to 1346), whatever its value.
 struct Scale {
     float a, b;
-    __device__ __forceinline__ float operator()(float g) const { return g * a * b; }
 };
 __device__ __forceinline__ Scale scale_for(float max_norm, float nrm) {
     const float c = max_norm / (nrm + 1e-6f);
@@ -145,13 +146,14 @@ template <typename TA>
 __device__ __forceinline__ void chunk_scale(const TA *p, TA *o, int n, const Scale &scale) {
     constexpr int EPV = 16 / sizeof(TA);
     const unsigned mp = reinterpret_cast<uintptr_t>(p) & 15, mo = reinterpret_cast<uintptr_t>(o) & 15;
-    if (mp != mo) {  // no common 16-byte boundary
+    if (mp != mo || scale.b != 1.f) {  // no common 16-byte boundary, or two factors
         for (int i = threadIdx.x; i < n; i += kThreads)
-            o[i] = Act<TA>::from_f(scale(Act<TA>::to_f(p[i])));
+            o[i] = Act<TA>::from_f(Act<TA>::to_f(p[i]) * scale.a * scale.b);
         return;
     }
+    const float coef = scale.a;
     const int head = min(n, (int)((16 - mp) & 15) / (int)sizeof(TA));
-    if ((int)threadIdx.x < head) o[threadIdx.x] = Act<TA>::from_f(scale(Act<TA>::to_f(p[threadIdx.x])));
+    if ((int)threadIdx.x < head) o[threadIdx.x] = Act<TA>::from_f(Act<TA>::to_f(p[threadIdx.x]) * coef);
     const int nv = (n - head) / EPV;
     constexpr int U = 4;  // loads before the first store (o may be p)
     for (int i0 = threadIdx.x; i0 < nv; i0 += U * kThreads) {
@@ -166,13 +168,13 @@ __device__ __forceinline__ void chunk_scale(const TA *p, TA *o, int n, const Sca
             float v[EPV];
             unpack16(raw[u], v, static_cast<const TA *>(nullptr));
 #pragma unroll
-            for (int j = 0; j < EPV; ++j) v[j] = scale(v[j]);
+            for (int j = 0; j < EPV; ++j) v[j] *= coef;
             stg16(o + head + (int64_t)(i0 + u * kThreads) * EPV,
                   pack16(v, static_cast<const TA *>(nullptr)));
         }
     }
     const int tail = head + nv * EPV + threadIdx.x;
-    if (tail < n) o[tail] = Act<TA>::from_f(scale(Act<TA>::to_f(p[tail])));
+    if (tail < n) o[tail] = Act<TA>::from_f(Act<TA>::to_f(p[tail]) * coef);
 }
 
 __global__ void __launch_bounds__(kThreads)
