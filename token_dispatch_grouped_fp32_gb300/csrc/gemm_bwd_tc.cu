@@ -144,6 +144,12 @@ struct Params {
     //    completion still implies the previous launch's.
     // Else a launch waits at its start and the next one starts at its end: the
     // blocks of a launch resident before their time took slots from this one.
+    // Neither order can leave launches waiting for one another, on one stream or
+    // several.  A launch starts only when every block of the one before it has
+    // started (each has released it or ended), and waits for nothing but that
+    // launch; started blocks keep their SMs, and wait inside only for their own
+    // cluster, which starts as a whole.  So, from the first launch on, each one
+    // that others wait for runs to its end, whatever waits on the other SMs.
     int release_late, overlap_prev;
     DevStatus ds;
 };
