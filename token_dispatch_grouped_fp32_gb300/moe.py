@@ -356,11 +356,8 @@ def moe_last_device_error(stream=None, raise_on_error=True):
 
 
 def _version(x):
-    """torch's count of the in-place writes to x, or None where there is none or
-    it says nothing: inference tensors, and a stream that is being captured."""
-    if x.is_inference() or (x.is_cuda and torch.cuda.is_current_stream_capturing()):
-        return None
-    return x._version
+    """torch's count of the in-place writes to x (inference tensors have none)."""
+    return None if x.is_inference() else x._version
 
 
 def _allocating_on(side):
@@ -423,52 +420,62 @@ class MoELayer:
         """The workspace for calls on `stream` (default: the current stream),
         grown to moe_workspace_size for T tokens when needed.  A workspace that
         grows is a new one: the latest forward's intermediates are gone."""
-        kept = self._ws.get(_stream(stream))
-        ws = self._grown(self._ws, moe_workspace_size(self.config(T)), stream)
-        if ws is not kept:
-            self._forget(stream)
+        ws = self._forward_ws(self.config(T), stream, _stream(stream))
+        self._capturing(ws)
         return ws
 
-    def _forget(self, stream):
-        self._tokens.pop(_stream(stream), None)
-        self._forwards.pop(_stream(stream), None)
+    def _forward_ws(self, cfg, stream, key):
+        kept = self._ws.get(key)
+        ws = self._grown(self._ws, moe_workspace_size(cfg), stream, key)
+        if ws is not kept:
+            self._forget(key)
+        return ws
 
-    def _grown(self, kept, need, stream):
-        key = _stream(stream)
+    def _forget(self, key):
+        self._tokens.pop(key, None)
+        self._forwards.pop(key, None)
+
+    def _grown(self, kept, need, stream, key):
         ws = kept.get(key)
         if ws is None or ws.numel() < need:
-            with _allocating_on(self._other(stream)):
+            with _allocating_on(self._other(stream, key)):
                 ws = torch.empty(max(need, 256), dtype=torch.uint8, device=self.Wr.device)
             kept[key] = ws
-        if ws.is_cuda and torch.cuda.is_current_stream_capturing():
-            self._captured[ws.data_ptr()] = ws
         return ws
 
-    def _other(self, stream):
-        """`stream` as a torch stream, or None where it is the current one."""
-        if stream is None or not self.Wr.is_cuda or _stream(stream) == _stream(None):
+    def _capturing(self, *workspaces):
+        """Whether a graph is being captured: it will hold these addresses."""
+        if not (workspaces[0].is_cuda and torch.cuda.is_current_stream_capturing()):
+            return False
+        for ws in workspaces:
+            self._captured[ws.data_ptr()] = ws
+        return True
+
+    def _other(self, stream, key):
+        """`stream` (of handle key) for torch, or None where it is the current one."""
+        if stream is None or not self.Wr.is_cuda or key == _stream(None):
             return None
         if isinstance(stream, torch.cuda.Stream):
             return stream
-        return torch.cuda.ExternalStream(int(stream)) if stream else torch.cuda.default_stream()
+        return torch.cuda.ExternalStream(key) if key else torch.cuda.default_stream()
 
     def forward(self, x, out=None, stream=None):
-        T = x.shape[0]
-        side, given = self._other(stream), (x, out)
+        key, cfg = _stream(stream), self.config(x.shape[0])
+        side, given = self._other(stream, key), (x, out)
         if out is None:
             with _allocating_on(side):
                 out = torch.empty_like(x)
             if side is not None:
                 _record(torch.cuda.current_stream(), (out,))
         _record(side, given)
-        cfg = self.config(T)
-        ws = self.workspace(T, stream)
-        self._forget(stream)  # until all of its kernels are launched
+        ws = self._forward_ws(cfg, stream, key)
+        self._forget(key)  # until all of its kernels are launched
         moe_forward(cfg, x, self.Wr, self.logit_bias, self.W_gate_up, self.W_down, out, ws,
-                    stream=stream)
-        self._tokens[_stream(stream)] = T
-        if _ptr(out) != _ptr(x):
-            self._forwards[_stream(stream)] = (ws, bytes(cfg), x.data_ptr(), _version(x))
+                    stream=key)
+        self._tokens[key] = cfg.T
+        version = None if self._capturing(ws) else _version(x)
+        if _ptr(out) != x.data_ptr():
+            self._forwards[key] = (ws, bytes(cfg), x.data_ptr(), version)
         return out
 
     __call__ = forward
@@ -482,15 +489,15 @@ class MoELayer:
                 or dout.dtype != x.dtype:
             raise ValueError(f"x and dout are [T, {self.d}] {self.dtype}, not {tuple(x.shape)} "
                              f"{x.dtype} and {tuple(dout.shape)} {dout.dtype}")
-        T = x.shape[0]
-        if T and self._tokens.get(_stream(stream)) != T:
+        key, T = _stream(stream), x.shape[0]
+        if T and self._tokens.get(key) != T:
             raise RuntimeError(f"backward of {T} tokens, but the latest forward on this stream had "
-                               f"{self._tokens.get(_stream(stream))}")
+                               f"{self._tokens.get(key)}")
         cfg = self.config(T)
         like = {"x": x, "Wr": self.Wr, "W_gate_up": self.W_gate_up, "W_down": self.W_down}
         if self.logit_bias is not None:
             like["logit_bias"] = self.logit_bias
-        side, made = self._other(stream), grads is None
+        side, made = self._other(stream, key), grads is None
         if made:
             with _allocating_on(side):
                 grads = {n: torch.empty_like(t) for n, t in like.items()}
@@ -500,7 +507,7 @@ class MoELayer:
                 continue
             if g is None or g.shape != t.shape or g.dtype != t.dtype:
                 raise ValueError(f"the gradient of {n} is {tuple(t.shape)} {t.dtype}")
-        fwd_ws, ran, at, version = self._forwards.get(_stream(stream), (None,) * 4)
+        fwd_ws, ran, at, version = self._forwards.get(key, (None,) * 4)
         written = version is not None and _version(x) not in (None, version)
         if T and (ran != bytes(cfg) or at != x.data_ptr() or written):
             raise RuntimeError("x is not what the latest forward on this stream read, has been "
@@ -508,8 +515,9 @@ class MoELayer:
         _record(side, (x, dout))
         if side is not None:
             _record(torch.cuda.current_stream() if made else side, grads.values())
-        ws = self._grown(self._bwd_ws, moe_backward_workspace_size(cfg), stream)
+        ws = self._grown(self._bwd_ws, moe_backward_workspace_size(cfg), stream, key)
+        self._capturing(ws, *(() if fwd_ws is None else (fwd_ws,)))
         moe_backward(cfg, x, self.Wr, self.W_gate_up, self.W_down, fwd_ws, dout, grads["x"],
                      grads["Wr"], grads.get("logit_bias"), grads["W_gate_up"], grads["W_down"], ws,
-                     stream=stream)
+                     stream=key)
         return grads
