@@ -489,6 +489,9 @@ class MoELayer:
                 or dout.dtype != x.dtype:
             raise ValueError(f"x and dout are [T, {self.d}] {self.dtype}, not {tuple(x.shape)} "
                              f"{x.dtype} and {tuple(dout.shape)} {dout.dtype}")
+        if x.device != self.Wr.device or dout.device != x.device:
+            raise ValueError(f"x is on device {x.device} and dout on {dout.device}, the layer on "
+                             f"{self.Wr.device}")
         key, T = _stream(stream), x.shape[0]
         if T and self._tokens.get(key) != T:
             raise RuntimeError(f"backward of {T} tokens, but the latest forward on this stream had "
@@ -501,12 +504,14 @@ class MoELayer:
         if made:
             with _allocating_on(side):
                 grads = {n: torch.empty_like(t) for n, t in like.items()}
-        for n, t in like.items():
+        shapes = {n: (t.shape, t.dtype) for n, t in like.items()}
+        shapes["logit_bias"] = (self.Wr.shape[:1], torch.float32)  # written if given
+        for n, (shape, dtype) in shapes.items():
             g = grads.get(n)
             if g is None and n == "logit_bias":
                 continue
-            if g is None or g.shape != t.shape or g.dtype != t.dtype:
-                raise ValueError(f"the gradient of {n} is {tuple(t.shape)} {t.dtype}")
+            if g is None or g.shape != shape or g.dtype != dtype or g.device != x.device:
+                raise ValueError(f"the gradient of {n} is {tuple(shape)} {dtype} on {x.device}")
         fwd_ws, ran, at, version = self._forwards.get(key, (None,) * 4)
         written = version is not None and _version(x) not in (None, version)
         if T and (ran != bytes(cfg) or at != x.data_ptr() or written):
