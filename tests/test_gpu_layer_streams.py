@@ -77,3 +77,36 @@ def test_growing_batches_equal_the_serial_ones(moe):
         assert torch.equal(out, wout)
         for n in wgrads:
             assert torch.equal(grads[n], wgrads[n]), n
+
+
+def test_a_graph_after_a_longer_batch(moe):
+    """The graph's workspaces are replaced for later calls, not taken from it."""
+    lay, randn = make(moe)
+    x, dout, out = randn(300, 256), randn(300, 256), torch.empty(300, 256, device="cuda", dtype=BF)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        lay(x, out)
+        got = lay.backward(x, dout)  # workspaces from before the capture, as a warm-up leaves them
+    side.synchronize()
+    want = {"out": out.clone(), **{n: t.clone() for n, t in got.items()}}
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        lay(x, out)
+        lay.backward(x, dout, got)
+    x2, dout2 = randn(2500, 256), randn(2500, 256)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        lay(x2)
+        lay.backward(x2, dout2)
+        for n in (1 << 20, 1 << 22, 1 << 24):  # what a freed workspace's block would go to
+            torch.full((n,), float("nan"), device="cuda")
+    side.synchronize()
+    out.zero_()
+    for t in got.values():
+        t.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert moe.moe_last_device_error() == moe.MOE_OK
+    for n, t in {"out": out, **got}.items():
+        assert torch.equal(t, want[n]), n
