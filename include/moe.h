@@ -1,7 +1,8 @@
 /*
  * moe.h -- C ABI of libmoe: one mixture-of-experts layer on one GPU: its
  * forward pass (router -> token dispatch -> grouped SwiGLU experts ->
- * combine), its backward pass, and the clipping of gradients by their norm.
+ * combine), its backward pass, the clipping of gradients by their norm, and
+ * what a training step does next: AdamW and the update of a balance bias.
  *
  * Sources, by page title and section:
  *   [EP]       Transformers docs, "Expert parallelism" (intro): a router sends
@@ -66,7 +67,11 @@ typedef enum {
     MOE_ERR_BAD_ROUTING = -6     /* a kernel met an expert id outside [0, E) (device error word) */
 } moe_status_t;
 
-typedef enum { MOE_F32 = 0, MOE_BF16 = 1 } moe_dtype_t;
+typedef enum {
+    MOE_F32 = 0,
+    MOE_BF16 = 1,
+    MOE_E4M3 = 2 /* states of moe_adamw_step only */
+} moe_dtype_t;
 
 typedef struct {
     int64_t T;           /* tokens in the batch (>= 0) */
@@ -476,6 +481,213 @@ size_t moe_clip_grad_norm_workspace_size(void);
  */
 moe_status_t moe_clip_grad_norm(const moe_grad_t *grads, int64_t n, float max_norm, float *norm,
                                 void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------- routing by other scores -------------------------
+ *
+ * The router of a layer that is balanced by a bias instead of a loss, and whose
+ * experts come in groups (no counterpart on the pages).  With L a token's
+ * logits (including logit_bias) and b the balance bias:
+ *   s_e = exp(L_e) / sum_i exp(L_i)     (MOE_SCORE_SOFTMAX)
+ *       = 1 / (1 + exp(-L_e))           (MOE_SCORE_SIGMOID)
+ *   q_e = s_e + b_e
+ *   the E experts form `groups` groups of E / groups consecutive ones; the
+ *     topk_groups groups with the largest u_g stay, u_g = the largest q of the
+ *     group (MOE_GROUP_MAX) or the sum of its two largest (MOE_GROUP_TOP2; a
+ *     group of one expert: its q); equal u go to the lower group;
+ *   topk_idx[t][j]: the j-th largest q among the experts that stay; equal q go
+ *     to the lower id;
+ *   topk_w[t][j] = weight_scale * s_e / (cfg->renormalize ? sum of s over the
+ *     chosen k : 1),  e = topk_idx[t][j].
+ * The bias moves the choice and not the weights, and has no gradient:
+ * moe_update_balance_bias trains it.  Without a bias the experts are ordered by
+ * their logits (the order of s as real numbers).  With one, and for sums of two, q
+ * and u are compared as 64-bit values, however near they are in fp32.
+ * Edges: a NaN q or u ranks below every number (a NaN logit makes all of a
+ * softmax row NaN).  A logit of -inf has a score of 0, and still a q of b_e: to
+ * exclude an expert from every choice give it a bias of -inf.  A row of -inf alone
+ * has scores of 0.  Where all chosen scores are 0 their renormalised weights are
+ * 0; scores that fp32 cannot hold keep their shares.  A logit of +inf is not
+ * supported with softmax scores.
+ * Limits: 1 <= groups <= 32, E a multiple of groups, 1 <= topk_groups <=
+ * groups, k <= topk_groups * E / groups, weight_scale > 0 and finite.
+ */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_t;
+typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } moe_group_score_t;
+
+typedef struct {
+    int32_t score;       /* moe_score_t */
+    int32_t groups;      /* 1: no groups */
+    int32_t topk_groups;
+    int32_t group_score; /* moe_group_score_t */
+    float weight_scale;  /* factor on the routing weights */
+    int32_t reserved;    /* 0 */
+} moe_router_t;
+
+/*
+ * moe_route with the scores of `router`.  balance_bias [E] fp32 or NULL; the
+ * other arguments, and the workspace, are moe_route's.
+ */
+moe_status_t moe_route_scored(const moe_config_t *cfg, const moe_router_t *router, const void *x,
+                              const float *Wr, const float *logit_bias, const float *balance_bias,
+                              float *logits, int32_t *topk_idx, float *topk_w, void *ws,
+                              size_t ws_bytes, void *stream);
+
+/* The same selection and weights on a GIVEN fp32 logit buffer [T][E] (read
+ * only); cfg's d, f and act_dtype are checked but not used. */
+moe_status_t moe_route_scored_from_logits(const moe_config_t *cfg, const moe_router_t *router,
+                                          const float *logits, const float *balance_bias,
+                                          int32_t *topk_idx, float *topk_w, void *stream);
+
+/*
+ * Gradient of the weights above with respect to the logits, with
+ * S = sum_j topk_w[t][j] dtopk_w[t][j], c = weight_scale, w and d for
+ * topk_w[t][j] and dtopk_w[t][j], e = topk_idx[t][j]:
+ *   softmax, renormalize: dlogits[t][e] = w (d - S / c), 0 elsewhere;
+ *   softmax:              dlogits[t][i] = s_i (c g_i - S), g_e = d, 0 elsewhere;
+ *   sigmoid, renormalize: dlogits[t][e] = w (d - S / c) (1 - s_e), 0 elsewhere;
+ *   sigmoid:              dlogits[t][e] = w d (1 - s_e), 0 elsewhere.
+ * The choice itself has no gradient, and groups play no part.  logits, topk_idx
+ * (a token's ids distinct) and topk_w as the route wrote them (logits may be
+ * NULL for softmax with renormalize).  An id outside [0, E) sets
+ * MOE_ERR_BAD_ROUTING in the device error word and contributes nothing.
+ * dlogits [T][E] written.
+ */
+moe_status_t moe_route_scored_from_logits_backward(const moe_config_t *cfg,
+                                                   const moe_router_t *router,
+                                                   const float *logits, const int32_t *topk_idx,
+                                                   const float *topk_w, const float *dtopk_w,
+                                                   float *dlogits, void *stream);
+
+/* Bytes of workspace moe_route_scored_backward needs. */
+size_t moe_route_scored_backward_workspace_size(const moe_config_t *cfg,
+                                                const moe_router_t *router);
+
+/* moe_route_backward with these dlogits: the same arguments, sums and edges. */
+moe_status_t moe_route_scored_backward(const moe_config_t *cfg, const moe_router_t *router,
+                                       const void *x, const float *Wr, const float *logits,
+                                       const int32_t *topk_idx, const float *topk_w,
+                                       const float *dtopk_w, const void *dx_in, float *dlogits,
+                                       float *dWr, float *dlogit_bias, void *dx, void *ws,
+                                       size_t ws_bytes, void *stream);
+
+/*
+ * The whole layer and its gradient with such a router: moe_forward and
+ * moe_backward but for the routing (the same workspace layout and size for the
+ * forward pass; one launch more than moe_forward_kernel_launches says where
+ * E <= 32 and the logits are formed on the CUDA cores).
+ */
+moe_status_t moe_forward_scored(const moe_config_t *cfg, const moe_router_t *router, const void *x,
+                                const float *Wr, const float *logit_bias,
+                                const float *balance_bias, const void *W_gate_up,
+                                const void *W_down, void *out, void *ws, size_t ws_bytes,
+                                void *stream);
+
+/* Bytes of workspace moe_backward_scored needs (0 when T == 0). */
+size_t moe_backward_scored_workspace_size(const moe_config_t *cfg, const moe_router_t *router);
+
+moe_status_t moe_backward_scored(const moe_config_t *cfg, const moe_router_t *router,
+                                 const void *x, const float *Wr, const void *W_gate_up,
+                                 const void *W_down, const void *fwd_ws, size_t fwd_ws_bytes,
+                                 const void *dout, void *dx, float *dWr, float *dlogit_bias,
+                                 void *dW_gate_up, void *dW_down, void *ws, size_t ws_bytes,
+                                 void *stream);
+
+/*
+ * One step of the balance bias of `layers` layers: with n the pairs that each
+ * expert of a layer received (moe_dispatch's counts, or their sums over several
+ * batches),
+ *   balance_bias[l][e] += rate * sign(sum_i n[l][i] - E n[l][e])
+ *   imbalance[l]        = E max_e n[l][e] / sum_e n[l][e]   (0 without pairs)
+ * An expert whose load is the mean keeps its bias; counts are compared as
+ * whole numbers.
+ * counts [layers][E] int32 >= 0, balance_bias [layers][E] fp32 (updated),
+ * imbalance [layers] fp32 (written) or NULL: element-aligned pointers.
+ * layers >= 0 (0 launches nothing), 1 <= E <= 1024, rate finite.
+ */
+moe_status_t moe_update_balance_bias(const int32_t *counts, int64_t layers, int32_t E, float rate,
+                                     float *balance_bias, float *imbalance, void *stream);
+
+/* --------------------------------- AdamW -----------------------------------
+ *
+ * One AdamW step over many parameter tensors at once, in place (no counterpart
+ * on the pages: the step after moe_clip_grad_norm).  With g a gradient, t the
+ * step's number, counted from 1:
+ *   g' = g * min(1, max_norm / (norm + 1e-6))      (norm given; else g' = g)
+ *   m  = beta1 m + (1 - beta1) g',  v = beta2 v + (1 - beta2) g'^2
+ *   p  = p (1 - lr weight_decay)
+ *        - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * in fp32, from the new m and v before they are rounded to their storage.  With
+ * moe_clip_grad_norm's `norm` (its out = NULL) the clipped gradients are never
+ * written.
+ *
+ * Storage.  A parameter is fp32 or bf16, and so is its gradient.  A bf16
+ * parameter may have an fp32 master copy: then the master is stepped and the
+ * parameter is its rounding.  Without one, `stochastic` rounds the new bf16
+ * value to one of its two neighbours, with the probabilities that keep it right
+ * on average (rounding to the nearest loses every update below 2^-9 of the
+ * value); 0 rounds to the nearest.
+ * States are fp32 (m and v), or 8 bits (MOE_E4M3): m and r = sqrt(v) in blocks
+ * of 256 consecutive elements, each an e4m3 value times the block's scale, a
+ * power of two 2^(e - 7) with 2^e <= the block's largest magnitude < 2^(e + 1)
+ * (at least 2^-126).  They are rounded stochastically: a state's change of a few
+ * percent of itself, or less, is far below a step of e4m3, and would be lost
+ * whole by rounding to the nearest.  An r above 0 is stored as at least the
+ * smallest code, so that no later step divides by eps alone.  (Zeros in all bytes
+ * and scales are valid initial states of either kind.)
+ * A block with a NaN or an infinity keeps NaN and the format's largest value
+ * for those elements.
+ *
+ * Random numbers: 32 bits of every element, a function of `seed` (a caller takes
+ * another each step), the number of its block of 256 elements counted over the
+ * whole list, and its place in the block.  So a step repeats bit for bit.
+ */
+typedef struct {
+    void *param;       /* updated */
+    const void *grad;
+    void *exp_avg;     /* m; updated */
+    void *exp_avg_sq;  /* v (fp32 states) or r = sqrt(v) (8-bit states); updated */
+    float *exp_avg_scale;     /* 8-bit states: [ceil(numel / 256)], updated; else NULL */
+    float *exp_avg_sq_scale;  /* the same */
+    float *master;     /* bf16 parameters: fp32 copy, updated, or NULL; fp32: NULL */
+    int64_t numel;     /* >= 0 */
+    int32_t param_dtype, grad_dtype; /* MOE_F32 or MOE_BF16 */
+    int32_t state_dtype;             /* MOE_F32 or MOE_E4M3 */
+    float weight_decay;
+} moe_adamw_tensor_t;
+
+typedef struct {
+    double lr, beta1, beta2, eps;  /* lr, eps >= 0; 0 <= beta < 1 */
+    int64_t step;                  /* >= 1 */
+    uint64_t seed;
+    float max_norm;                /* >= 0; read when `norm` is given */
+    int32_t stochastic;            /* bf16 parameters without a master copy */
+    int32_t skip_nonfinite;        /* 1: a NaN or infinite `norm` leaves everything as it was */
+    int32_t reserved;              /* 0 */
+} moe_adamw_hyper_t;
+
+/* What changes from step to step, for a call that is captured in a graph. */
+typedef struct {
+    float lr;
+    float step_size;    /* lr / (1 - beta1^t) */
+    float inv_sqrt_bc2; /* 1 / sqrt(1 - beta2^t) */
+    uint32_t seed_lo, seed_hi;
+    uint32_t reserved[3];
+} moe_adamw_scalars_t;
+
+/* Fills *out from hyper's lr, betas, step and seed (on the host). */
+moe_status_t moe_adamw_scalars(const moe_adamw_hyper_t *hyper, moe_adamw_scalars_t *out);
+
+/*
+ * tensors: HOST array of n >= 0 entries, read before the call returns; pointers
+ * element-aligned (the fastest path wants 16 bytes), tensors that do not
+ * overlap.  norm: one float on the device or NULL.  scalars: NULL, or 16-byte
+ * aligned device memory that the kernels read lr, step and seed from instead of
+ * `hyper`: a captured graph is replayed after a copy of new moe_adamw_scalars.
+ * No workspace.
+ */
+moe_status_t moe_adamw_step(const moe_adamw_tensor_t *tensors, int64_t n,
+                            const moe_adamw_hyper_t *hyper, const float *norm,
+                            const moe_adamw_scalars_t *scalars, void *stream);
 
 /*
  * Synchronises `stream`, then reads and clears the current device's error

@@ -17,6 +17,12 @@ moe_status_t device_status(DevStatus *out);
 bool aligned16(const void *p);
 // Sizes and types of `cfg`, checked, as a Shape.
 moe_status_t check_cfg(const moe_config_t *cfg, Shape *s);
+// The scores of `router` for a checked config.
+moe_status_t check_router(const moe_router_t *router, const Shape &s, Router *r);
+// ... as the gradient of the routing weights uses them; r == nullptr: moe_route's.
+ScoreGrad score_grad(const Shape &s, const Router *r);
+// A pointer that may be NULL: 16-byte aligned.
+moe_status_t check_optional(const void *p, const char *name);
 // Every pointer given and 16-byte aligned.
 moe_status_t check_ptrs(std::initializer_list<const void *> ptrs);
 moe_status_t from_cuda(cudaError_t e, const char *what);

@@ -16,7 +16,7 @@ size_t experts_scratch_bytes(const Shape &s) {
     return s.bf16 ? experts_backward_tc_scratch_bytes(s) : 4 * (size_t)s.P() * 2 * s.f;
 }
 
-BwdLayout bwd_layout(const Shape &s) {
+BwdLayout bwd_layout(const Shape &s, const Shape &route) {
     BwdLayout L;
     const size_t P = (size_t)s.P();
     size_t o = 0;
@@ -27,7 +27,7 @@ BwdLayout bwd_layout(const Shape &s) {
     L.dw = o; o = up256(o + 4 * P);
     L.dlogits = o; o = up256(o + 4 * (size_t)s.T * s.E);
     L.experts = o; o = up256(o + experts_scratch_bytes(s));
-    L.route = o; o = up256(o + route_backward_scratch_bytes(s));
+    L.route = o; o = up256(o + route_backward_scratch_bytes(route));
     L.total = o;
     return L;
 }
@@ -43,6 +43,13 @@ moe_status_t check_ws(size_t have, size_t need) {
     if (have >= need) return MOE_OK;
     set_error_message("workspace %zu bytes < %zu needed", have, need);
     return MOE_ERR_WORKSPACE;
+}
+
+// The shape as the router's gradient takes it: `renorm` for every case in which
+// only the chosen logits have a gradient.
+Shape grad_shape(Shape s, const ScoreGrad &f) {
+    s.renorm = !f.dense;
+    return s;
 }
 
 // Weight gradients of an empty batch.
@@ -134,20 +141,18 @@ size_t moe_route_backward_workspace_size(const moe_config_t *cfg) {
     return route_backward_scratch_bytes(s);
 }
 
-moe_status_t moe_route_backward(const moe_config_t *cfg, const void *x, const float *Wr,
-                                const float *logits, const int32_t *topk_idx, const float *topk_w,
-                                const float *dtopk_w, const void *dx_in, float *dlogits, float *dWr,
-                                float *dlogit_bias, void *dx, void *ws, size_t ws_bytes,
-                                void *stream) {
-    set_error_message("");
-    Shape s;
-    moe_status_t st = check_cfg(cfg, &s);
-    if (st != MOE_OK) return st;
+namespace {
+
+// moe_route_backward and moe_route_scored_backward.
+moe_status_t route_backward_call(const Shape &s, const ScoreGrad &f, const void *x, const float *Wr,
+                                 const float *logits, const int32_t *topk_idx, const float *topk_w,
+                                 const float *dtopk_w, const void *dx_in, float *dlogits,
+                                 float *dWr, float *dlogit_bias, void *dx, void *ws,
+                                 size_t ws_bytes, void *stream) {
+    const Shape g = grad_shape(s, f);
+    moe_status_t st;
     if ((st = check_ptrs({dWr})) != MOE_OK) return st;
-    if (dlogit_bias && !aligned16(dlogit_bias)) {
-        set_error_message("dlogit_bias is not 16-byte aligned");
-        return MOE_ERR_INVALID_ARG;
-    }
+    if ((st = check_optional(dlogit_bias, "dlogit_bias")) != MOE_OK) return st;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     DevStatus ds;
     if (s.T == 0) {
@@ -157,37 +162,81 @@ moe_status_t moe_route_backward(const moe_config_t *cfg, const void *x, const fl
         return clear(dlogit_bias, 4 * (size_t)s.E, cs);
     }
     if ((st = check_ptrs({x, Wr, topk_idx, topk_w, dtopk_w, dlogits, dx, ws})) != MOE_OK) return st;
-    if (!s.renorm && (st = check_ptrs({logits})) != MOE_OK) return st;
-    if (dx_in && !aligned16(dx_in)) {
-        set_error_message("dx_in is not 16-byte aligned");
-        return MOE_ERR_INVALID_ARG;
-    }
-    if ((st = check_ws(ws_bytes, route_backward_scratch_bytes(s))) != MOE_OK) return st;
+    if ((f.dense || f.sigmoid) && (st = check_ptrs({logits})) != MOE_OK) return st;
+    if ((st = check_optional(dx_in, "dx_in")) != MOE_OK) return st;
+    if ((st = check_ws(ws_bytes, route_backward_scratch_bytes(g))) != MOE_OK) return st;
     if ((st = device_status(&ds)) != MOE_OK) return st;
-    return from_cuda(launch_route_backward(s, {x, Wr, logits, topk_idx, topk_w, dtopk_w, dx_in,
-                                               dlogits, dWr, dlogit_bias, dx, ws}, ds, cs),
+    return from_cuda(launch_route_backward(g, {x, Wr, logits, topk_idx, topk_w, dtopk_w, dx_in,
+                                               dlogits, dWr, dlogit_bias, dx, ws, f}, ds, cs),
                      "router gradient launch");
+}
+
+}  // namespace
+
+moe_status_t moe_route_backward(const moe_config_t *cfg, const void *x, const float *Wr,
+                                const float *logits, const int32_t *topk_idx, const float *topk_w,
+                                const float *dtopk_w, const void *dx_in, float *dlogits, float *dWr,
+                                float *dlogit_bias, void *dx, void *ws, size_t ws_bytes,
+                                void *stream) {
+    set_error_message("");
+    Shape s;
+    moe_status_t st = check_cfg(cfg, &s);
+    if (st != MOE_OK) return st;
+    return route_backward_call(s, score_grad(s, nullptr), x, Wr, logits, topk_idx, topk_w, dtopk_w,
+                               dx_in, dlogits, dWr, dlogit_bias, dx, ws, ws_bytes, stream);
+}
+
+size_t moe_route_scored_backward_workspace_size(const moe_config_t *cfg,
+                                                const moe_router_t *router) {
+    Shape s;
+    Router r;
+    if (check_cfg(cfg, &s) != MOE_OK || check_router(router, s, &r) != MOE_OK || s.T == 0) return 0;
+    return route_backward_scratch_bytes(grad_shape(s, score_grad(s, &r)));
+}
+
+moe_status_t moe_route_scored_backward(const moe_config_t *cfg, const moe_router_t *router,
+                                       const void *x, const float *Wr, const float *logits,
+                                       const int32_t *topk_idx, const float *topk_w,
+                                       const float *dtopk_w, const void *dx_in, float *dlogits,
+                                       float *dWr, float *dlogit_bias, void *dx, void *ws,
+                                       size_t ws_bytes, void *stream) {
+    set_error_message("");
+    Shape s;
+    Router r;
+    moe_status_t st = check_cfg(cfg, &s);
+    if (st != MOE_OK || (st = check_router(router, s, &r)) != MOE_OK) return st;
+    return route_backward_call(s, score_grad(s, &r), x, Wr, logits, topk_idx, topk_w, dtopk_w, dx_in,
+                               dlogits, dWr, dlogit_bias, dx, ws, ws_bytes, stream);
 }
 
 size_t moe_backward_workspace_size(const moe_config_t *cfg) {
     Shape s;
     if (check_cfg(cfg, &s) != MOE_OK || s.T == 0) return 0;
-    return bwd_layout(s).total;
+    return bwd_layout(s, grad_shape(s, score_grad(s, nullptr))).total;
 }
 
-moe_status_t moe_backward(const moe_config_t *cfg, const void *x, const float *Wr,
-                          const void *W_gate_up, const void *W_down, const void *fwd_ws,
-                          size_t fwd_ws_bytes, const void *dout, void *dx, float *dWr,
-                          float *dlogit_bias, void *dW_gate_up, void *dW_down, void *ws,
-                          size_t ws_bytes, void *stream) {
-    set_error_message("");
+size_t moe_backward_scored_workspace_size(const moe_config_t *cfg, const moe_router_t *router) {
     Shape s;
-    moe_status_t st = check_cfg(cfg, &s);
-    if (st != MOE_OK) return st;
+    Router r;
+    if (check_cfg(cfg, &s) != MOE_OK || check_router(router, s, &r) != MOE_OK || s.T == 0) return 0;
+    return bwd_layout(s, grad_shape(s, score_grad(s, &r))).total;
+}
+
+namespace {
+
+// moe_backward and moe_backward_scored.
+moe_status_t backward_call(const moe_config_t *cfg, const Shape &s, const ScoreGrad &f,
+                           const void *x, const float *Wr, const void *W_gate_up,
+                           const void *W_down, const void *fwd_ws, size_t fwd_ws_bytes,
+                           const void *dout, void *dx, float *dWr, float *dlogit_bias,
+                           void *dW_gate_up, void *dW_down, void *ws, size_t ws_bytes,
+                           void *stream) {
+    const Shape g = grad_shape(s, f);
+    moe_status_t st;
     if (s.T == 0) {  // clears the weight gradients
-        if ((st = moe_route_backward(cfg, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr,
-                                     nullptr, nullptr, dWr, dlogit_bias, nullptr, nullptr, 0,
-                                     stream)) != MOE_OK)
+        if ((st = route_backward_call(s, f, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr,
+                                      nullptr, nullptr, dWr, dlogit_bias, nullptr, nullptr, 0,
+                                      stream)) != MOE_OK)
             return st;
         return moe_grouped_swiglu_backward(cfg, nullptr, nullptr, nullptr, nullptr, nullptr,
                                            nullptr, nullptr, dW_gate_up, dW_down, nullptr, 0,
@@ -196,12 +245,9 @@ moe_status_t moe_backward(const moe_config_t *cfg, const void *x, const float *W
     if ((st = check_ptrs({x, Wr, W_gate_up, W_down, fwd_ws, dout, dx, dWr, dW_gate_up, dW_down,
                           ws})) != MOE_OK)
         return st;
-    if (dlogit_bias && !aligned16(dlogit_bias)) {
-        set_error_message("dlogit_bias is not 16-byte aligned");
-        return MOE_ERR_INVALID_ARG;
-    }
+    if ((st = check_optional(dlogit_bias, "dlogit_bias")) != MOE_OK) return st;
     const WsLayout F = ws_layout(s);
-    const BwdLayout L = bwd_layout(s);
+    const BwdLayout L = bwd_layout(s, g);
     if (fwd_ws_bytes < F.total) {
         set_error_message("forward workspace %zu bytes < %zu needed", fwd_ws_bytes, F.total);
         return MOE_ERR_WORKSPACE;
@@ -242,11 +288,42 @@ moe_status_t moe_backward(const moe_config_t *cfg, const void *x, const float *W
                                                  scale ? x : nullptr, dx, scale ? dw : nullptr, cs),
                         "dispatch gradient launch")) != MOE_OK)
         return st;
-    return from_cuda(launch_route_backward(s, {x, Wr, at<float>(fwd_ws, F.logits),
+    return from_cuda(launch_route_backward(g, {x, Wr, at<float>(fwd_ws, F.logits),
                                                at<int32_t>(fwd_ws, F.idx), w, dw, dx,
                                                at<float>(ws, L.dlogits), dWr, dlogit_bias, dx,
-                                               at<uint8_t>(ws, L.route)}, ds, cs),
+                                               at<uint8_t>(ws, L.route), f}, ds, cs),
                      "router gradient launch");
+}
+
+}  // namespace
+
+moe_status_t moe_backward(const moe_config_t *cfg, const void *x, const float *Wr,
+                          const void *W_gate_up, const void *W_down, const void *fwd_ws,
+                          size_t fwd_ws_bytes, const void *dout, void *dx, float *dWr,
+                          float *dlogit_bias, void *dW_gate_up, void *dW_down, void *ws,
+                          size_t ws_bytes, void *stream) {
+    set_error_message("");
+    Shape s;
+    moe_status_t st = check_cfg(cfg, &s);
+    if (st != MOE_OK) return st;
+    return backward_call(cfg, s, score_grad(s, nullptr), x, Wr, W_gate_up, W_down, fwd_ws,
+                         fwd_ws_bytes, dout, dx, dWr, dlogit_bias, dW_gate_up, dW_down, ws, ws_bytes,
+                         stream);
+}
+
+moe_status_t moe_backward_scored(const moe_config_t *cfg, const moe_router_t *router,
+                                 const void *x, const float *Wr, const void *W_gate_up,
+                                 const void *W_down, const void *fwd_ws, size_t fwd_ws_bytes,
+                                 const void *dout, void *dx, float *dWr, float *dlogit_bias,
+                                 void *dW_gate_up, void *dW_down, void *ws, size_t ws_bytes,
+                                 void *stream) {
+    set_error_message("");
+    Shape s;
+    Router r;
+    moe_status_t st = check_cfg(cfg, &s);
+    if (st != MOE_OK || (st = check_router(router, s, &r)) != MOE_OK) return st;
+    return backward_call(cfg, s, score_grad(s, &r), x, Wr, W_gate_up, W_down, fwd_ws, fwd_ws_bytes,
+                         dout, dx, dWr, dlogit_bias, dW_gate_up, dW_down, ws, ws_bytes, stream);
 }
 
 size_t moe_clip_grad_norm_workspace_size(void) { return clip_scratch_bytes(); }

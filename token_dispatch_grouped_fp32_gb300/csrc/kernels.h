@@ -147,6 +147,20 @@ size_t experts_backward_tc_scratch_bytes(const Shape &s);
 cudaError_t launch_experts_backward_tc(const Shape &s, const ExpertsBwd &a, const DevStatus &ds,
                                        cudaStream_t st);
 
+// How the routing weights' gradient becomes the logits' (route_scored.cu has the
+// formulas): the chosen logits alone, or (dense: softmax scores that are not
+// renormalised) every logit's.
+struct ScoreGrad {
+    int sigmoid, dense;
+    float scale;  // the factor on the weights
+    float share;  // of the weighted sum S that a chosen logit loses: 1/scale if renormalised, or 0
+    // dl of a chosen logit L (read for sigmoid scores only), with weight w and dLoss/dw d
+    __device__ __forceinline__ float chosen(float w, float d, float S, float L) const {
+        const float t = w * (share != 0.f ? d - S * share : d);
+        return sigmoid ? t * (1.f / (1.f + expf(L))) : t;
+    }
+};
+
 // Operands of the router's gradient (see moe_route_backward).
 struct RouteBwd {
     const void *x;
@@ -156,6 +170,7 @@ struct RouteBwd {
     const void *dx_in;
     float *dlogits, *dWr, *dbias;
     void *dx, *ws;
+    ScoreGrad f;
 };
 size_t route_backward_scratch_bytes(const Shape &s);
 // The router gradient's products on the tensor cores (bf16 x), over operands
@@ -175,6 +190,30 @@ cudaError_t launch_route_backward_tc(const Shape &s, const RouteProducts &r, con
                                      cudaStream_t st);
 cudaError_t launch_route_backward(const Shape &s, const RouteBwd &a, const DevStatus &ds,
                                   cudaStream_t st);
+
+// ------------------------- scored routing (route_scored.cu) -------------------------
+struct Router {
+    bool sigmoid, top2;
+    int G, Gk;
+    float scale;
+};
+// Selection and weights by r's scores, on given logits (nparts == 0) or on the
+// sum of nparts partial buffers plus logit_bias, which is written to `logits`.
+// bias: the balance bias, or null.  zero_word: as for launch_topk.
+cudaError_t launch_select(const Shape &s, const Router &r, float *logits, const float *partial,
+                          int nparts, const float *logit_bias, const float *bias, int32_t *idx,
+                          float *w, cudaStream_t st, unsigned *zero_word = nullptr);
+cudaError_t launch_logits_grad(const Shape &s, const ScoreGrad &f, const float *logits,
+                               const int32_t *idx, const float *w, const float *dw, float *dlogits,
+                               const DevStatus &ds, cudaStream_t st);
+cudaError_t launch_balance(const int32_t *counts, int64_t layers, int E, float rate, float *bias,
+                           float *imbalance, cudaStream_t st);
+
+// ------------------------------ AdamW (adamw.cu) ------------------------------
+int64_t adamw_chunk();  // elements per unit of work (the limit is 2^30 units)
+cudaError_t launch_adamw(const moe_adamw_tensor_t *t, int64_t n, const moe_adamw_scalars_t &sc,
+                         const moe_adamw_scalars_t *dev, const moe_adamw_hyper_t &h,
+                         const float *norm, cudaStream_t st);
 
 // Global norm of n gradient tensors and their clipped copies.
 size_t clip_scratch_bytes();

@@ -5,6 +5,7 @@
 #include <string.h>
 
 #include <atomic>
+#include <cmath>
 
 #include "api.h"
 
@@ -151,6 +152,51 @@ moe_status_t check_cfg(const moe_config_t *cfg, Shape *s) {
     return MOE_OK;
 }
 
+moe_status_t check_router(const moe_router_t *router, const Shape &s, Router *r) {
+    if (!router) {
+        set_error_message("router is NULL");
+        return MOE_ERR_INVALID_ARG;
+    }
+    if ((router->score != MOE_SCORE_SOFTMAX && router->score != MOE_SCORE_SIGMOID) ||
+        (router->group_score != MOE_GROUP_MAX && router->group_score != MOE_GROUP_TOP2)) {
+        set_error_message("unknown score %d or group_score %d", router->score, router->group_score);
+        return MOE_ERR_UNSUPPORTED;
+    }
+    const int G = router->groups, Gk = router->topk_groups;
+    if (G < 1 || Gk < 1 || Gk > G || G > s.E || s.E % G != 0) {
+        set_error_message("bad groups: %d of %d for E=%d", Gk, G, s.E);
+        return MOE_ERR_INVALID_ARG;
+    }
+    if (G > 32) {
+        set_error_message("unsupported groups=%d (at most 32)", G);
+        return MOE_ERR_UNSUPPORTED;
+    }
+    if (s.k > Gk * (s.E / G)) {
+        set_error_message("k=%d exceeds the %d experts of %d groups", s.k, Gk * (s.E / G), Gk);
+        return MOE_ERR_INVALID_ARG;
+    }
+    if (!(router->weight_scale > 0.f) || !(router->weight_scale < INFINITY)) {
+        set_error_message("weight_scale %g is not a positive finite number",
+                          (double)router->weight_scale);
+        return MOE_ERR_INVALID_ARG;
+    }
+    *r = {router->score == MOE_SCORE_SIGMOID, router->group_score == MOE_GROUP_TOP2, G, Gk,
+          router->weight_scale};
+    return MOE_OK;
+}
+
+ScoreGrad score_grad(const Shape &s, const Router *r) {
+    const float c = r ? r->scale : 1.f;
+    const bool sigmoid = r && r->sigmoid;
+    return {sigmoid, !sigmoid && !s.renorm, c, s.renorm ? 1.f / c : 0.f};
+}
+
+moe_status_t check_optional(const void *p, const char *name) {
+    if (aligned16(p)) return MOE_OK;
+    set_error_message("%s is not 16-byte aligned", name);
+    return MOE_ERR_INVALID_ARG;
+}
+
 moe_status_t check_ptrs(std::initializer_list<const void *> ptrs) {
     int i = 0;
     for (const void *p : ptrs) {
@@ -232,9 +278,15 @@ namespace {
 // top-k kernel) when the shape allows, else the SIMT logits kernel.
 // zero_word (optional): cleared by the route's last launch (the dispatch's
 // ticket, when moe_forward runs the dispatch next).
+// scores: selection and weights by other scores than softmax and top-k alone.
+struct Scores {
+    Router router;
+    const float *bias;  // the balance bias, or null
+};
 moe_status_t run_route(const Shape &s, const void *x, const float *Wr, const float *bias,
                        float *logits, int32_t *idx, float *w, void *route_ws,
-                       const DevStatus &ds, cudaStream_t st, unsigned *zero_word = nullptr) {
+                       const DevStatus &ds, cudaStream_t st, unsigned *zero_word = nullptr,
+                       const Scores *scores = nullptr) {
     if (router_tc_eligible(s)) {
         float *partial = nullptr;
         int splits = 0;
@@ -242,16 +294,24 @@ moe_status_t run_route(const Shape &s, const void *x, const float *Wr, const flo
             launch_router_logits_tc(s, x, Wr, route_ws, &partial, &splits, ds, st),
             "router logits launch");
         if (r != MOE_OK) return r;
+        if (scores)
+            return from_cuda(launch_select(s, scores->router, logits, partial, splits, bias,
+                                           scores->bias, idx, w, st, zero_word),
+                             "selection launch");
         return from_cuda(
             launch_topk_partials(s, partial, splits, bias, logits, idx, w, st, zero_word),
             "top-k launch");
     }
-    if (router_selects_in_logits(s))  // one launch: logits, selection and weights
+    if (!scores && router_selects_in_logits(s))  // one launch: logits, selection and weights
         return from_cuda(launch_router_logits(s, x, Wr, bias, logits, st, idx, w, zero_word),
                          "router launch");
     moe_status_t r = from_cuda(launch_router_logits(s, x, Wr, bias, logits, st),
                                "router logits launch");
     if (r != MOE_OK) return r;
+    if (scores)
+        return from_cuda(launch_select(s, scores->router, logits, nullptr, 0, nullptr, scores->bias,
+                                       idx, w, st, zero_word),
+                         "selection launch");
     return from_cuda(launch_topk(s, logits, idx, w, st, zero_word), "top-k launch");
 }
 
@@ -367,19 +427,16 @@ void moe_debug_inject_wait_timeout(int enable) {
     g_inject_wait_timeout.store(enable ? 1 : 0, std::memory_order_relaxed);
 }
 
-moe_status_t moe_route(const moe_config_t *cfg, const void *x, const float *Wr,
-                       const float *logit_bias, float *logits, int32_t *topk_idx, float *topk_w,
-                       void *ws, size_t ws_bytes, void *stream) {
-    g_msg[0] = 0;
-    Shape s;
-    moe_status_t st = check_cfg(cfg, &s);
-    if (st != MOE_OK) return st;
-    if (s.T == 0) return MOE_OK;  // empty batch: nothing to check or launch
+namespace {
+
+// moe_route and moe_route_scored.
+moe_status_t route_call(const Shape &s, const Scores *scores, const void *x, const float *Wr,
+                        const float *logit_bias, float *logits, int32_t *topk_idx, float *topk_w,
+                        void *ws, size_t ws_bytes, void *stream) {
+    moe_status_t st;
     if ((st = check_ptrs({x, Wr, logits, topk_idx, topk_w})) != MOE_OK) return st;
-    if (logit_bias && !aligned16(logit_bias)) {
-        set_error_message("logit_bias is not 16-byte aligned");
-        return MOE_ERR_INVALID_ARG;
-    }
+    if ((st = check_optional(logit_bias, "logit_bias")) != MOE_OK) return st;
+    if (scores && (st = check_optional(scores->bias, "balance_bias")) != MOE_OK) return st;
     const size_t need = router_tc_scratch_bytes(s);
     if (need > 0) {
         if ((st = check_ptrs({ws})) != MOE_OK) return st;
@@ -391,7 +448,33 @@ moe_status_t moe_route(const moe_config_t *cfg, const void *x, const float *Wr,
     DevStatus ds;
     if ((st = device_status(&ds)) != MOE_OK) return st;
     return run_route(s, x, Wr, logit_bias, logits, topk_idx, topk_w, ws, ds,
-                     static_cast<cudaStream_t>(stream));
+                     static_cast<cudaStream_t>(stream), nullptr, scores);
+}
+
+}  // namespace
+
+moe_status_t moe_route(const moe_config_t *cfg, const void *x, const float *Wr,
+                       const float *logit_bias, float *logits, int32_t *topk_idx, float *topk_w,
+                       void *ws, size_t ws_bytes, void *stream) {
+    g_msg[0] = 0;
+    Shape s;
+    moe_status_t st = check_cfg(cfg, &s);
+    if (st != MOE_OK) return st;
+    if (s.T == 0) return MOE_OK;  // empty batch: nothing to check or launch
+    return route_call(s, nullptr, x, Wr, logit_bias, logits, topk_idx, topk_w, ws, ws_bytes, stream);
+}
+
+moe_status_t moe_route_scored(const moe_config_t *cfg, const moe_router_t *router, const void *x,
+                              const float *Wr, const float *logit_bias, const float *balance_bias,
+                              float *logits, int32_t *topk_idx, float *topk_w, void *ws,
+                              size_t ws_bytes, void *stream) {
+    g_msg[0] = 0;
+    Shape s;
+    Scores scores = {{}, balance_bias};
+    moe_status_t st = check_cfg(cfg, &s);
+    if (st != MOE_OK || (st = check_router(router, s, &scores.router)) != MOE_OK) return st;
+    if (s.T == 0) return MOE_OK;  // empty batch: nothing more to check or launch
+    return route_call(s, &scores, x, Wr, logit_bias, logits, topk_idx, topk_w, ws, ws_bytes, stream);
 }
 
 moe_status_t moe_route_from_logits(const moe_config_t *cfg, const float *logits, int32_t *topk_idx,
@@ -406,6 +489,47 @@ moe_status_t moe_route_from_logits(const moe_config_t *cfg, const float *logits,
     if ((st = device_status(&ds)) != MOE_OK) return st;
     return from_cuda(launch_topk(s, logits, topk_idx, topk_w, static_cast<cudaStream_t>(stream)),
                      "top-k launch");
+}
+
+moe_status_t moe_route_scored_from_logits(const moe_config_t *cfg, const moe_router_t *router,
+                                          const float *logits, const float *balance_bias,
+                                          int32_t *topk_idx, float *topk_w, void *stream) {
+    g_msg[0] = 0;
+    Shape s;
+    Router r;
+    moe_status_t st = check_cfg(cfg, &s);
+    if (st != MOE_OK || (st = check_router(router, s, &r)) != MOE_OK) return st;
+    if (s.T == 0) return MOE_OK;  // empty batch: nothing more to check or launch
+    if ((st = check_ptrs({logits, topk_idx, topk_w})) != MOE_OK) return st;
+    if ((st = check_optional(balance_bias, "balance_bias")) != MOE_OK) return st;
+    DevStatus ds;
+    if ((st = device_status(&ds)) != MOE_OK) return st;
+    // nparts == 0: the kernel only reads `logits`
+    return from_cuda(launch_select(s, r, const_cast<float *>(logits), nullptr, 0, nullptr,
+                                   balance_bias, topk_idx, topk_w,
+                                   static_cast<cudaStream_t>(stream)),
+                     "selection launch");
+}
+
+moe_status_t moe_route_scored_from_logits_backward(const moe_config_t *cfg,
+                                                   const moe_router_t *router,
+                                                   const float *logits, const int32_t *topk_idx,
+                                                   const float *topk_w, const float *dtopk_w,
+                                                   float *dlogits, void *stream) {
+    g_msg[0] = 0;
+    Shape s;
+    Router r;
+    moe_status_t st = check_cfg(cfg, &s);
+    if (st != MOE_OK || (st = check_router(router, s, &r)) != MOE_OK) return st;
+    if (s.T == 0) return MOE_OK;  // empty batch: nothing more to check or launch
+    if ((st = check_ptrs({topk_idx, topk_w, dtopk_w, dlogits})) != MOE_OK) return st;
+    const ScoreGrad f = score_grad(s, &r);
+    if ((f.dense || f.sigmoid) && (st = check_ptrs({logits})) != MOE_OK) return st;
+    DevStatus ds;
+    if ((st = device_status(&ds)) != MOE_OK) return st;
+    return from_cuda(launch_logits_grad(s, f, logits, topk_idx, topk_w, dtopk_w, dlogits, ds,
+                                        static_cast<cudaStream_t>(stream)),
+                     "logits' gradient launch");
 }
 
 moe_status_t moe_dispatch(const moe_config_t *cfg, const int32_t *topk_idx, const float *topk_w,
@@ -465,19 +589,16 @@ moe_status_t moe_combine(const moe_config_t *cfg, const void *y_perm, const int3
                      "combine launch");
 }
 
-moe_status_t moe_forward(const moe_config_t *cfg, const void *x, const float *Wr,
-                         const float *logit_bias, const void *W_gate_up, const void *W_down,
-                         void *out, void *ws, size_t ws_bytes, void *stream) {
-    g_msg[0] = 0;
-    Shape s;
-    moe_status_t st = check_cfg(cfg, &s);
-    if (st != MOE_OK) return st;
-    if (s.T == 0) return MOE_OK;  // empty batch: nothing to check or launch
+namespace {
+
+// moe_forward and moe_forward_scored.
+moe_status_t forward_call(const Shape &s, const Scores *scores, const void *x, const float *Wr,
+                          const float *logit_bias, const void *W_gate_up, const void *W_down,
+                          void *out, void *ws, size_t ws_bytes, void *stream) {
+    moe_status_t st;
     if ((st = check_ptrs({x, Wr, W_gate_up, W_down, out, ws})) != MOE_OK) return st;
-    if (logit_bias && !aligned16(logit_bias)) {
-        set_error_message("logit_bias is not 16-byte aligned");
-        return MOE_ERR_INVALID_ARG;
-    }
+    if ((st = check_optional(logit_bias, "logit_bias")) != MOE_OK) return st;
+    if (scores && (st = check_optional(scores->bias, "balance_bias")) != MOE_OK) return st;
     const WsLayout L = ws_layout(s);
     if (ws_bytes < L.total) {
         set_error_message("workspace %zu bytes < %zu needed", ws_bytes, L.total);
@@ -500,7 +621,7 @@ moe_status_t moe_forward(const moe_config_t *cfg, const void *x, const float *Wr
     float *row_scale = rows_scaled_in_gemm(s) ? at<float>(ws, L.row_scale) : nullptr;
     // the route's last launch clears the dispatch's ticket counter
     if ((st = run_route(s, x, Wr, logit_bias, logits, idx, w, at<uint8_t>(ws, L.route), ds, cs,
-                        all_experts ? nullptr : dispatch_ticket(s, hist))) != MOE_OK)
+                        all_experts ? nullptr : dispatch_ticket(s, hist), scores)) != MOE_OK)
         return st;
     if (all_experts)
         st = from_cuda(launch_dispatch_all_experts(s, idx, counts, offsets, pos, src, ds, cs,
@@ -518,6 +639,33 @@ moe_status_t moe_forward(const moe_config_t *cfg, const void *x, const float *Wr
         return st;
     return from_cuda(launch_combine(s, y_perm, pos, s.scale_inputs ? nullptr : w, out, cs),
                      "combine launch");
+}
+
+}  // namespace
+
+moe_status_t moe_forward(const moe_config_t *cfg, const void *x, const float *Wr,
+                         const float *logit_bias, const void *W_gate_up, const void *W_down,
+                         void *out, void *ws, size_t ws_bytes, void *stream) {
+    g_msg[0] = 0;
+    Shape s;
+    moe_status_t st = check_cfg(cfg, &s);
+    if (st != MOE_OK) return st;
+    if (s.T == 0) return MOE_OK;  // empty batch: nothing to check or launch
+    return forward_call(s, nullptr, x, Wr, logit_bias, W_gate_up, W_down, out, ws, ws_bytes, stream);
+}
+
+moe_status_t moe_forward_scored(const moe_config_t *cfg, const moe_router_t *router, const void *x,
+                                const float *Wr, const float *logit_bias,
+                                const float *balance_bias, const void *W_gate_up,
+                                const void *W_down, void *out, void *ws, size_t ws_bytes,
+                                void *stream) {
+    g_msg[0] = 0;
+    Shape s;
+    Scores scores = {{}, balance_bias};
+    moe_status_t st = check_cfg(cfg, &s);
+    if (st != MOE_OK || (st = check_router(router, s, &scores.router)) != MOE_OK) return st;
+    if (s.T == 0) return MOE_OK;  // empty batch: nothing more to check or launch
+    return forward_call(s, &scores, x, Wr, logit_bias, W_gate_up, W_down, out, ws, ws_bytes, stream);
 }
 
 moe_status_t moe_forward_host(const moe_config_t *cfg, const void *x_host, const float *Wr,

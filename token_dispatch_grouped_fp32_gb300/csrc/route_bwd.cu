@@ -1,6 +1,8 @@
 // route_bwd.cu -- gradient of the router.
 //
-// With dw the gradient of the chosen experts' weights, S = sum_i w_i dw_i:
+// With dw the gradient of the chosen experts' weights, S = sum_i w_i dw_i (other
+// scores than moe_route's by ScoreGrad; "renormalised" below is every case in
+// which only the chosen logits have a gradient):
 //   renormalised weights are a softmax over the chosen logits alone, so
 //     dl[idx_j] = w_j (dw_j - S), every other logit's gradient is zero;
 //   plain softmax weights: dl[e] = p_e (g_e - S), g_e = dw_j where e = idx_j
@@ -69,6 +71,7 @@ struct TermsArgs {
     const float *w, *dw;
     int64_t T;
     int E, k, renorm;
+    ScoreGrad f;
     float *dl, *bias_part;  // [T][E]; [token blocks][E8]
     float *dl8;  // fp32 x only: dl in rows of E8 columns
     // fp32 x, dx from the chosen rows of Wr: their dl [T][k], and the ids with
@@ -156,11 +159,12 @@ __global__ void __launch_bounds__(kThreads) terms_kernel(TermsArgs a, DevStatus 
             const float inv = 1.f / warp_all<false>(z);
             for (int i = lane; i < a.E; i += 32) row[i] *= inv * (0.f - S);
             __syncwarp();
-            if (e >= 0) row[e] = expf(L[e] - m) * inv * (dj - S);
+            if (e >= 0) row[e] = expf(L[e] - m) * inv * (a.f.scale * dj - S);
         } else {
-            if (e >= 0) row[e] = wj * (dj - S);
+            const float v = a.f.chosen(wj, dj, S, a.f.sigmoid && e >= 0 ? L[e] : 0.f);
+            if (e >= 0) row[e] = v;
             if (a.dlk && lane < a.k) {
-                a.dlk[t * a.k + lane] = wj * (dj - S);
+                a.dlk[t * a.k + lane] = v;
                 a.rows[t * a.k + lane] = e;
             }
         }
@@ -309,6 +313,7 @@ struct FewArgs {
     const float *w, *dw;
     int64_t T;
     int E, E8, k, d, renorm, tokens;
+    ScoreGrad f;
     float *dl, *part, *bias_part;
     void *dx;
 };
@@ -370,8 +375,10 @@ few_experts_kernel(FewArgs a, DevStatus ds) {
         for (int j = 0; j < k; ++j) {
             const int e = a.idx[t * k + j];
             if ((unsigned)e >= (unsigned)E) continue;
-            const float d = a.dw[t * k + j] - S;
-            s_dl[i][e] = (a.renorm ? a.w[t * k + j] : expf(a.logits[t * E + e] - m) * inv) * d;
+            const float d = a.dw[t * k + j];
+            s_dl[i][e] = a.renorm ? a.f.chosen(a.w[t * k + j], d, S,
+                                               a.f.sigmoid ? a.logits[t * E + e] : 0.f)
+                                  : expf(a.logits[t * E + e] - m) * inv * (a.f.scale * d - S);
         }
     }
     __syncthreads();
@@ -677,7 +684,7 @@ cudaError_t launch_few(const Shape &s, const RouteBwd &a, const Plan &p, float *
                        float *bias_part, const DevStatus &ds, cudaStream_t st) {
     FewArgs f = {a.x,  a.dx_in,       a.Wr,       a.logits, a.idx, a.w,       a.dw,
                  s.T,  s.E,           p.E8,       s.k,      s.d,   s.renorm ? 1 : 0,
-                 p.tokens, a.dlogits, part,       bias_part, a.dx};
+                 p.tokens, a.f, a.dlogits, part, bias_part, a.dx};
     const dim3 grid(p.splits, (s.d + p.few_cols - 1) / p.few_cols), block(kFewThreads);
     const size_t ring = (size_t)kFewRing * kFewThreads * 16 * (a.dx_in ? 2 : 1);
     cudaError_t err = s.bf16 ? simt::opt_in<few_experts_kernel<__nv_bfloat16>>(64 * 1024)
@@ -722,6 +729,7 @@ cudaError_t launch_products(const Shape &s, const RouteBwd &a, const Plan &p, fl
     t.E = s.E;
     t.k = s.k;
     t.renorm = s.renorm ? 1 : 0;
+    t.f = a.f;
     t.dl = a.dlogits;
     t.bias_part = bias_part;
     t.E8 = p.E8;

@@ -7,7 +7,8 @@ is missing this module raises at import time instead of falling back to
 anything else.
 
 ``MoELayer`` is a small convenience holder: it keeps the weights and one
-workspace per stream (allocated with torch) and calls ``moe_forward``.
+workspace per stream (allocated with torch) and calls ``moe_forward``;
+``AdamW`` holds an optimizer's states and calls ``moe_adamw_step``.
 """
 from __future__ import annotations
 
@@ -29,6 +30,12 @@ MOE_ERR_DEVICE_TIMEOUT = -5
 MOE_ERR_BAD_ROUTING = -6
 MOE_F32 = 0
 MOE_BF16 = 1
+MOE_E4M3 = 2
+MOE_SCORE_SOFTMAX = 0
+MOE_SCORE_SIGMOID = 1
+MOE_GROUP_MAX = 0
+MOE_GROUP_TOP2 = 1
+ADAMW_BLOCK = 256  # elements under one scale of an 8-bit state
 
 
 class MoEError(RuntimeError):
@@ -58,6 +65,32 @@ class moe_grad_t(ctypes.Structure):
                 ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class moe_router_t(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("topk_groups", ctypes.c_int32), ("group_score", ctypes.c_int32),
+                ("weight_scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class moe_adamw_tensor_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("param", "grad", "exp_avg", "exp_avg_sq",
+                                               "exp_avg_scale", "exp_avg_sq_scale", "master")] + \
+        [("numel", ctypes.c_int64), ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
+         ("state_dtype", ctypes.c_int32), ("weight_decay", ctypes.c_float)]
+
+
+class moe_adamw_hyper_t(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("step", ctypes.c_int64), ("seed", ctypes.c_uint64),
+                ("max_norm", ctypes.c_float), ("stochastic", ctypes.c_int32),
+                ("skip_nonfinite", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class moe_adamw_scalars_t(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_float), ("step_size", ctypes.c_float),
+                ("inv_sqrt_bc2", ctypes.c_float), ("seed_lo", ctypes.c_uint32),
+                ("seed_hi", ctypes.c_uint32), ("reserved", ctypes.c_uint32 * 3)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -65,7 +98,7 @@ def _load():
             "(nvcc, sm_103a). There is no fallback path.")
     lib = ctypes.CDLL(LIB_PATH)
     vp, sz, st = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
-    cfgp = ctypes.POINTER(moe_config_t)
+    cfgp, rtp = ctypes.POINTER(moe_config_t), ctypes.POINTER(moe_router_t)
     sig = {
         "moe_status_string": ([st], ctypes.c_char_p),
         "moe_last_error_message": ([], ctypes.c_char_p),
@@ -91,6 +124,20 @@ def _load():
         "moe_clip_grad_norm_workspace_size": ([], sz),
         "moe_clip_grad_norm": ([ctypes.POINTER(moe_grad_t), ctypes.c_int64, ctypes.c_float, vp, vp,
                                 sz, vp], st),
+        "moe_route_scored": ([cfgp, rtp] + [vp] * 8 + [sz, vp], st),
+        "moe_route_scored_from_logits": ([cfgp, rtp] + [vp] * 5, st),
+        "moe_route_scored_from_logits_backward": ([cfgp, rtp] + [vp] * 6, st),
+        "moe_route_scored_backward_workspace_size": ([cfgp, rtp], sz),
+        "moe_route_scored_backward": ([cfgp, rtp] + [vp] * 12 + [sz, vp], st),
+        "moe_forward_scored": ([cfgp, rtp] + [vp] * 8 + [sz, vp], st),
+        "moe_backward_scored_workspace_size": ([cfgp, rtp], sz),
+        "moe_backward_scored": ([cfgp, rtp] + [vp] * 5 + [sz] + [vp] * 7 + [sz, vp], st),
+        "moe_update_balance_bias": ([vp, ctypes.c_int64, ctypes.c_int32, ctypes.c_float] + [vp] * 3,
+                                    st),
+        "moe_adamw_scalars": ([ctypes.POINTER(moe_adamw_hyper_t),
+                               ctypes.POINTER(moe_adamw_scalars_t)], st),
+        "moe_adamw_step": ([ctypes.POINTER(moe_adamw_tensor_t), ctypes.c_int64,
+                            ctypes.POINTER(moe_adamw_hyper_t), vp, vp, vp], st),
         "moe_last_device_error": ([vp], st),
         "moe_set_wait_limit_ns": ([ctypes.c_uint64], None),
         "moe_wait_limit_ns": ([], ctypes.c_uint64),
@@ -350,6 +397,160 @@ def moe_clip_grad_norm(grads, max_norm, norm, ws, ws_bytes=None, n=None, stream=
     return _check(s, "moe_clip_grad_norm", raise_on_error)
 
 
+def router(score="softmax", groups: int = 1, topk_groups: int | None = None, group_score="max",
+           weight_scale: float = 1.0) -> moe_router_t:
+    """Scores "softmax" or "sigmoid"; the best ``topk_groups`` (default: all) of
+    ``groups`` groups of experts by their "max" or the sum of their "top2"."""
+    score = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}.get(score, score)
+    group_score = {"max": MOE_GROUP_MAX, "top2": MOE_GROUP_TOP2}.get(group_score, group_score)
+    return moe_router_t(int(score), int(groups), int(groups if topk_groups is None else topk_groups),
+                        int(group_score), float(weight_scale), 0)
+
+
+def moe_route_scored(cfg, router, x, Wr, logit_bias, balance_bias, logits, topk_idx, topk_w, ws=None,
+                     ws_bytes=None, stream=None, raise_on_error=True):
+    s = _lib.moe_route_scored(
+        ctypes.byref(cfg), ctypes.byref(router), _ptr(x), _ptr(Wr), _ptr(logit_bias),
+        _ptr(balance_bias), _ptr(logits), _ptr(topk_idx), _ptr(topk_w), _ptr(ws),
+        _bytes(ws, ws_bytes), _stream(stream))
+    return _check(s, "moe_route_scored", raise_on_error)
+
+
+def moe_route_scored_from_logits(cfg, router, logits, balance_bias, topk_idx, topk_w, stream=None,
+                                 raise_on_error=True):
+    s = _lib.moe_route_scored_from_logits(ctypes.byref(cfg), ctypes.byref(router), _ptr(logits),
+                                          _ptr(balance_bias), _ptr(topk_idx), _ptr(topk_w),
+                                          _stream(stream))
+    return _check(s, "moe_route_scored_from_logits", raise_on_error)
+
+
+def moe_route_scored_from_logits_backward(cfg, router, logits, topk_idx, topk_w, dtopk_w, dlogits,
+                                          stream=None, raise_on_error=True):
+    s = _lib.moe_route_scored_from_logits_backward(
+        ctypes.byref(cfg), ctypes.byref(router), _ptr(logits), _ptr(topk_idx), _ptr(topk_w),
+        _ptr(dtopk_w), _ptr(dlogits), _stream(stream))
+    return _check(s, "moe_route_scored_from_logits_backward", raise_on_error)
+
+
+def moe_route_scored_backward_workspace_size(cfg: moe_config_t, router: moe_router_t) -> int:
+    return int(_lib.moe_route_scored_backward_workspace_size(ctypes.byref(cfg),
+                                                             ctypes.byref(router)))
+
+
+def moe_route_scored_backward(cfg, router, x, Wr, logits, topk_idx, topk_w, dtopk_w, dx_in, dlogits,
+                              dWr, dlogit_bias, dx, ws, ws_bytes=None, stream=None,
+                              raise_on_error=True):
+    s = _lib.moe_route_scored_backward(
+        ctypes.byref(cfg), ctypes.byref(router), _ptr(x), _ptr(Wr), _ptr(logits), _ptr(topk_idx),
+        _ptr(topk_w), _ptr(dtopk_w), _ptr(dx_in), _ptr(dlogits), _ptr(dWr), _ptr(dlogit_bias),
+        _ptr(dx), _ptr(ws), _bytes(ws, ws_bytes), _stream(stream))
+    return _check(s, "moe_route_scored_backward", raise_on_error)
+
+
+def moe_forward_scored(cfg, router, x, Wr, logit_bias, balance_bias, W_gate_up, W_down, out, ws,
+                       ws_bytes=None, stream=None, raise_on_error=True):
+    s = _lib.moe_forward_scored(
+        ctypes.byref(cfg), ctypes.byref(router), _ptr(x), _ptr(Wr), _ptr(logit_bias),
+        _ptr(balance_bias), _ptr(W_gate_up), _ptr(W_down), _ptr(out), _ptr(ws),
+        _bytes(ws, ws_bytes), _stream(stream))
+    return _check(s, "moe_forward_scored", raise_on_error)
+
+
+def moe_backward_scored_workspace_size(cfg: moe_config_t, router: moe_router_t) -> int:
+    return int(_lib.moe_backward_scored_workspace_size(ctypes.byref(cfg), ctypes.byref(router)))
+
+
+def moe_backward_scored(cfg, router, x, Wr, W_gate_up, W_down, fwd_ws, dout, dx, dWr, dlogit_bias,
+                        dW_gate_up, dW_down, ws, fwd_ws_bytes=None, ws_bytes=None, stream=None,
+                        raise_on_error=True):
+    s = _lib.moe_backward_scored(
+        ctypes.byref(cfg), ctypes.byref(router), _ptr(x), _ptr(Wr), _ptr(W_gate_up), _ptr(W_down),
+        _ptr(fwd_ws), _bytes(fwd_ws, fwd_ws_bytes), _ptr(dout), _ptr(dx), _ptr(dWr),
+        _ptr(dlogit_bias), _ptr(dW_gate_up), _ptr(dW_down), _ptr(ws), _bytes(ws, ws_bytes),
+        _stream(stream))
+    return _check(s, "moe_backward_scored", raise_on_error)
+
+
+def moe_update_balance_bias(counts, rate, balance_bias, imbalance=None, layers=None, E=None,
+                            stream=None, raise_on_error=True):
+    """``counts`` [layers, E] or [E] int32, ``balance_bias`` of the same shape
+    fp32, ``imbalance`` [layers] fp32 or None (``layers`` and ``E`` are taken
+    from counts where they are not given)."""
+    if E is None:
+        E, layers = counts.shape[-1], counts.numel() // max(1, counts.shape[-1])
+        if counts.dtype != torch.int32 or balance_bias.dtype != torch.float32 \
+                or balance_bias.shape != counts.shape:
+            raise ValueError("counts are int32, the balance bias fp32 of the same shape")
+        if imbalance is not None and (imbalance.dtype != torch.float32
+                                      or imbalance.numel() != layers):
+            raise ValueError("the imbalance is fp32, one value a layer")
+    s = _lib.moe_update_balance_bias(_ptr(counts), int(layers), int(E), float(rate),
+                                     _ptr(balance_bias), _ptr(imbalance), _stream(stream))
+    return _check(s, "moe_update_balance_bias", raise_on_error)
+
+
+def adamw_list(tensors):
+    """The moe_adamw_tensor_t array of moe_adamw_step.  ``tensors``: dicts of
+    "param" and "grad" (bf16 or fp32), "exp_avg" and "exp_avg_sq" (fp32, or
+    float8_e4m3fn beside "exp_avg_scale" and "exp_avg_sq_scale", fp32, one for
+    256 elements), and optionally "master" (fp32) and "weight_decay".  It holds
+    addresses: keep the tensors alive, and build it once for buffers that stay
+    where they are."""
+    tensors = list(tensors)
+    arr = (moe_adamw_tensor_t * max(1, len(tensors)))()
+    arr.count = len(tensors)
+    types = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32, torch.float8_e4m3fn: MOE_E4M3}
+    for a, t in zip(arr, tensors):
+        p, g, m, v = t["param"], t["grad"], t["exp_avg"], t["exp_avg_sq"]
+        master, scales = t.get("master"), [t.get("exp_avg_scale"), t.get("exp_avg_sq_scale")]
+        n, small = p.numel(), m.dtype == torch.float8_e4m3fn
+        if p.dtype not in types or g.dtype not in types or torch.float8_e4m3fn in (p.dtype, g.dtype):
+            raise TypeError(f"parameters and gradients are bf16 or fp32, not {p.dtype}, {g.dtype}")
+        if m.dtype != v.dtype or m.dtype not in (torch.float32, torch.float8_e4m3fn):
+            raise TypeError(f"both states are fp32 or float8_e4m3fn, not {m.dtype}, {v.dtype}")
+        if any(x.numel() != n for x in (g, m, v)):
+            raise ValueError("a gradient and its states have the parameter's size")
+        if master is not None and (p.dtype != torch.bfloat16 or master.dtype != torch.float32
+                                   or master.numel() != n):
+            raise ValueError("a master copy is an fp32 tensor of a bf16 parameter's size")
+        blocks = (n + ADAMW_BLOCK - 1) // ADAMW_BLOCK
+        if any((x is not None) != small or (small and (x.dtype != torch.float32
+                                                       or x.numel() != blocks)) for x in scales):
+            raise ValueError("8-bit states, and they alone, have an fp32 scale for 256 elements")
+        if any(x is not None and x.device != p.device for x in (g, m, v, master, *scales)):
+            raise ValueError("a parameter, its gradient and its states are on one device")
+        a.param, a.grad, a.exp_avg, a.exp_avg_sq = _ptr(p), _ptr(g), _ptr(m), _ptr(v)
+        a.exp_avg_scale, a.exp_avg_sq_scale, a.master = _ptr(scales[0]), _ptr(scales[1]), _ptr(master)
+        a.numel, a.weight_decay = n, float(t.get("weight_decay", 0.0))
+        a.param_dtype, a.grad_dtype, a.state_dtype = types[p.dtype], types[g.dtype], types[m.dtype]
+    return arr
+
+
+def adamw_hyper(lr, beta1=0.9, beta2=0.95, eps=1e-8, step=1, seed=0, max_norm=0.0,
+                stochastic=False, skip_nonfinite=False) -> moe_adamw_hyper_t:
+    return moe_adamw_hyper_t(float(lr), float(beta1), float(beta2), float(eps), int(step),
+                             int(seed) & (2 ** 64 - 1), float(max_norm), int(bool(stochastic)),
+                             int(bool(skip_nonfinite)), 0)
+
+
+def moe_adamw_scalars(hyper, raise_on_error=True) -> moe_adamw_scalars_t:
+    out = moe_adamw_scalars_t()
+    _check(_lib.moe_adamw_scalars(ctypes.byref(hyper), ctypes.byref(out)), "moe_adamw_scalars",
+           raise_on_error)
+    return out
+
+
+def moe_adamw_step(tensors, hyper, norm=None, scalars=None, n=None, stream=None,
+                   raise_on_error=True):
+    """``tensors``: from adamw_list (n defaults to its length); ``norm``: from
+    moe_clip_grad_norm, or None; ``scalars``: device memory with a
+    moe_adamw_scalars_t, or None."""
+    n = tensors.count if n is None else int(n)
+    s = _lib.moe_adamw_step(tensors, n, ctypes.byref(hyper), _ptr(norm), _ptr(scalars),
+                            _stream(stream))
+    return _check(s, "moe_adamw_step", raise_on_error)
+
+
 def moe_last_device_error(stream=None, raise_on_error=True):
     s = _lib.moe_last_device_error(_stream(stream))
     return _check(s, "moe_last_device_error", raise_on_error)
@@ -376,7 +577,9 @@ class MoELayer:
     """Weights of one MoE layer plus reusable workspaces; ``forward`` runs
     ``moe_forward`` on the given (default: current) stream.  Weights: Wr [E, d]
     fp32, W_gate_up [E, d, 2f] and W_down [E, f, d] in the activation dtype,
-    optional per-expert logit bias [E] fp32.
+    optional per-expert logit bias [E] fp32.  ``router``: other scores than
+    softmax and top-k alone (from ``router()``), with an optional balance bias [E] fp32, which
+    ``update_balance_bias`` moves.
 
     The workspace holds a call's intermediates (logits, routing, permuted
     rows), so two calls in flight at once must not share one: the layer keeps
@@ -397,7 +600,13 @@ class MoELayer:
     replays read ``x`` afresh)."""
 
     def __init__(self, Wr, W_gate_up, W_down, k, logit_bias=None, renormalize=True,
-                 scale_inputs=False):
+                 scale_inputs=False, router=None, balance_bias=None):
+        if balance_bias is not None:
+            if router is None:
+                raise ValueError("a balance bias needs a router (moe.router())")
+            if balance_bias.shape != Wr.shape[:1] or balance_bias.dtype != torch.float32 \
+                    or balance_bias.device != Wr.device:
+                raise ValueError(f"the balance bias is [{Wr.shape[0]}] fp32 on {Wr.device}")
         self.Wr, self.W_gate_up, self.W_down = Wr, W_gate_up, W_down
         self.logit_bias = logit_bias
         self.E, self.d = Wr.shape
@@ -406,6 +615,7 @@ class MoELayer:
         self.dtype = W_gate_up.dtype
         self.renormalize = renormalize
         self.scale_inputs = scale_inputs
+        self.router, self.balance_bias = router, balance_bias
         self._ws = {}  # stream handle -> workspace
         self._bwd_ws = {}  # the same for the backward pass
         self._tokens = {}  # stream handle -> tokens of its latest forward
@@ -470,15 +680,39 @@ class MoELayer:
         _record(side, given)
         ws = self._forward_ws(cfg, stream, key)
         self._forget(key)  # until all of its kernels are launched
-        moe_forward(cfg, x, self.Wr, self.logit_bias, self.W_gate_up, self.W_down, out, ws,
-                    stream=key)
+        if self.router is None:
+            moe_forward(cfg, x, self.Wr, self.logit_bias, self.W_gate_up, self.W_down, out, ws,
+                        stream=key)
+        else:
+            moe_forward_scored(cfg, self.router, x, self.Wr, self.logit_bias, self.balance_bias,
+                               self.W_gate_up, self.W_down, out, ws, stream=key)
         self._tokens[key] = cfg.T
         version = None if self._capturing(ws) else _version(x)
         if _ptr(out) != x.data_ptr():
-            self._forwards[key] = (ws, bytes(cfg), x.data_ptr(), version)
+            self._forwards[key] = (ws, self._modes(cfg), x.data_ptr(), version)
         return out
 
     __call__ = forward
+
+    def _modes(self, cfg):
+        return bytes(cfg) if self.router is None else bytes(cfg) + bytes(self.router)
+
+    def update_balance_bias(self, rate, imbalance=None, stream=None):
+        """Moves the balance bias by ``rate`` against the loads that the latest
+        ``forward`` on this stream dispatched; ``imbalance`` [1] fp32 (optional)
+        takes their largest over their mean."""
+        key = _stream(stream)
+        T, ws = self._tokens.get(key), self._ws.get(key)
+        if self.balance_bias is None or not T or ws is None:
+            raise RuntimeError("no balance bias, or no forward of any tokens on this stream")
+        if imbalance is not None and (imbalance.dtype != torch.float32 or imbalance.numel() != 1
+                                      or imbalance.device != self.Wr.device):
+            raise ValueError(f"the imbalance is one fp32 value on {self.Wr.device}")
+        side = self._other(stream, key)
+        _record(side, (self.balance_bias, imbalance))
+        at = moe_workspace_layout(self.config(T)).counts
+        moe_update_balance_bias(ws.data_ptr() + at, rate, self.balance_bias, imbalance, layers=1,
+                                E=self.E, stream=key)
 
     def backward(self, x, dout, grads=None, stream=None):
         """Gradients of <out, dout> for the latest ``forward(x)`` on this
@@ -514,15 +748,101 @@ class MoELayer:
                 raise ValueError(f"the gradient of {n} is {tuple(shape)} {dtype} on {x.device}")
         fwd_ws, ran, at, version = self._forwards.get(key, (None,) * 4)
         written = version is not None and _version(x) not in (None, version)
-        if T and (ran != bytes(cfg) or at != x.data_ptr() or written):
+        if T and (ran != self._modes(cfg) or at != x.data_ptr() or written):
             raise RuntimeError("x is not what the latest forward on this stream read, has been "
                                "written to since, or the layer has changed since")
         _record(side, (x, dout))
         if side is not None:
             _record(torch.cuda.current_stream() if made else side, grads.values())
-        ws = self._grown(self._bwd_ws, moe_backward_workspace_size(cfg), stream, key)
+        need = moe_backward_workspace_size(cfg) if self.router is None else \
+            moe_backward_scored_workspace_size(cfg, self.router)
+        ws = self._grown(self._bwd_ws, need, stream, key)
         self._capturing(ws, *(() if fwd_ws is None else (fwd_ws,)))
-        moe_backward(cfg, x, self.Wr, self.W_gate_up, self.W_down, fwd_ws, dout, grads["x"],
-                     grads["Wr"], grads.get("logit_bias"), grads["W_gate_up"], grads["W_down"], ws,
-                     stream=key)
+        args = (x, self.Wr, self.W_gate_up, self.W_down, fwd_ws, dout, grads["x"], grads["Wr"],
+                grads.get("logit_bias"), grads["W_gate_up"], grads["W_down"], ws)
+        if self.router is None:
+            moe_backward(cfg, *args, stream=key)
+        else:
+            moe_backward_scored(cfg, self.router, *args, stream=key)
         return grads
+
+
+class AdamW:
+    """moe_adamw_step for a list of parameters and of the gradient buffers that
+    a training loop keeps: their states, and the list of addresses, built once.
+
+    ``bits``: 32 or 8, of the states.  ``master``: fp32 copies of the bf16
+    parameters; without them the bf16 values are rounded stochastically.
+    ``max_norm``: the gradients count as clipped to this global norm (their
+    buffers keep what they hold), which ``norm`` has after a step; a step whose
+    norm is not finite is skipped.  ``weight_decay``: one number, or one a
+    parameter.  ``lr`` may be changed between steps.
+
+    In a captured graph (``capturable``) a step reads its number, lr and seed from
+    device memory: call ``advance()`` before every replay, on the replay's stream."""
+
+    def __init__(self, params, grads, lr, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.0, bits=32,
+                 master=True, max_norm=None, seed=0, capturable=False):
+        params, grads = list(params), list(grads)
+        if len(params) != len(grads) or not params:
+            raise ValueError(f"{len(params)} parameters but {len(grads)} gradients")
+        if bits not in (8, 32):
+            raise ValueError("states have 8 or 32 bits")
+        wd = list(weight_decay) if isinstance(weight_decay, (list, tuple)) \
+            else [weight_decay] * len(params)
+        if len(wd) != len(params):
+            raise ValueError(f"{len(wd)} weight decays for {len(params)} parameters")
+        self.lr, self.betas, self.eps, self.seed, self.steps = lr, betas, eps, int(seed), 0
+        self.max_norm, self.stochastic = max_norm, not master
+        self.tensors, device = [], params[0].device
+        for p, g, d in zip(params, grads, wd):
+            if p.device != device:
+                raise ValueError(f"parameters on {p.device} and {device}")
+            t = {"param": p, "grad": g, "weight_decay": d}
+            kind = torch.float32 if bits == 32 else torch.float8_e4m3fn
+            for n in ("exp_avg", "exp_avg_sq"):
+                t[n] = torch.zeros(p.numel(), dtype=torch.uint8 if bits == 8 else kind,
+                                   device=device).view(kind)
+                if bits == 8:
+                    t[n + "_scale"] = torch.zeros(-(-p.numel() // ADAMW_BLOCK), device=device)
+            if master and p.dtype == torch.bfloat16:
+                t["master"] = p.detach().float()
+            self.tensors.append(t)
+        self._list = adamw_list(self.tensors)
+        self.norm = self._ws = self._scalars = None
+        if max_norm is not None:
+            self._clip = grad_list(grads, [None] * len(grads))
+            self._ws = torch.empty(moe_clip_grad_norm_workspace_size(), dtype=torch.uint8,
+                                   device=device)
+            self.norm = torch.zeros((), device=device)
+        if capturable:
+            self._scalars = torch.zeros(ctypes.sizeof(moe_adamw_scalars_t), dtype=torch.uint8,
+                                        device=device)
+
+    def _hyper(self):
+        # (another seed every step: the one given, and the step's number)
+        return adamw_hyper(self.lr, *self.betas, self.eps, max(1, self.steps),
+                           (self.seed << 32) + self.steps, self.max_norm or 0.0, self.stochastic,
+                           skip_nonfinite=self.max_norm is not None)
+
+    def advance(self):
+        """Counts a step; capturable: what its replay reads, on the current stream."""
+        self.steps += 1
+        if self._scalars is not None:
+            raw = torch.frombuffer(bytearray(bytes(moe_adamw_scalars(self._hyper()))),
+                                   dtype=torch.uint8)
+            self._scalars.copy_(raw, non_blocking=True)
+
+    def step(self, stream=None):
+        """One step on the given (default: current) stream."""
+        side = stream if stream is None or isinstance(stream, torch.cuda.Stream) \
+            else torch.cuda.ExternalStream(int(stream))
+        with _allocating_on(side):
+            if self.tensors[0]["param"].is_cuda and torch.cuda.is_current_stream_capturing():
+                if self._scalars is None:
+                    raise RuntimeError("a step is captured with capturable=True")
+            else:
+                self.advance()
+            if self.max_norm is not None:
+                moe_clip_grad_norm(self._clip, self.max_norm, self.norm, self._ws)
+            moe_adamw_step(self._list, self._hyper(), self.norm, self._scalars)
