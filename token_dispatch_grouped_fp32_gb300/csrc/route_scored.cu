@@ -13,6 +13,8 @@
 // errors, about one token in 1,000 at E = 256) is decided again in fp64.
 #include <math.h>
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "once.h"
@@ -21,24 +23,30 @@ namespace moe {
 namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr uint32_t kNaNKey = 1u;  // below every number's key; 0: no expert, or one already taken
-
-// Order-preserving unsigned image of a value: a larger number has a larger key,
-// +0.0 and -0.0 the same, a NaN the lowest.
-__device__ __forceinline__ uint32_t key_of(float v) {
-    if (isnan(v)) return kNaNKey;
-    const uint32_t b = __float_as_uint(v == 0.f ? 0.f : v);
-    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-}
-__device__ __forceinline__ float value_of(uint32_t key) {  // (a NaN for kNaNKey)
-    return __uint_as_float((key & 0x80000000u) ? (key & 0x7FFFFFFFu) : ~key);
-}
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
     return v;
 }
+// The warp's largest number; NaN where no lane has one.
+__device__ __forceinline__ float warp_max(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+// 2^x and 1/x to 2 ulp and 1 ulp.
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
 
 struct SelectArgs {
     float *logits;  // [T][E]; written when nparts > 0, from the partial sums
@@ -47,371 +55,536 @@ struct SelectArgs {
     const float *logit_bias, *bias;
     int64_t T;
     int E, k, renorm, sigmoid;
-    // groups: lanes_per_group lanes share a group of `size` consecutive experts,
-    // `per` consecutive ones a lane, so that ids ascend with the lane
-    int G, Gk, top2, size, lanes_per_group, per;
+    // groups: 1 << shift lanes share a group of `size` consecutive experts, `per`
+    // consecutive ones a lane, so that ids ascend with the lane
+    int G, Gk, top2, size, shift, per;
     float scale;
+    int half;  // half the power of two that holds k slots
     int32_t *idx;
     float *w;
     unsigned *zero_word;
 };
 
-// What the decision in fp64 works on, a warp's share: q of the candidates, then their ids.
-struct Undecided {
-    double *q;
-    uint16_t *id;
-};
-
-__device__ __forceinline__ bool before(double a, double b) {  // by value alone; a NaN last
-    if (isnan(a) || isnan(b)) return !isnan(a) && isnan(b);
-    return a > b;
+// Sum and largest over the slots (lanes below 2 * half), in all lanes.
+__device__ __forceinline__ float slots_sum(float v, int half) {
+    for (int o = half; o >= 1; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    return __shfl_sync(kAll, v, 0);
+}
+__device__ __forceinline__ float slots_max(float v, int half) {
+    for (int o = half; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+    return __shfl_sync(kAll, v, 0);
 }
 
-struct Softmax {
-    float m;      // the largest logit
-    double z;     // sum of exp(L - m)
+// A candidate, or a slot of the selection.
+struct __align__(8) Ranked {
+    float q;
+    int id;
 };
+constexpr Ranked kNobody = {NAN, 0};
 
-__device__ __noinline__ double score64(float L, bool sigmoid, Softmax sm) {
-    if (sigmoid) return 1.0 / (1.0 + exp(-(double)L));
-    return sm.m == -INFINITY ? 0.0 : exp((double)L - (double)sm.m) / sm.z;
+// A warp's shared memory: candidates and slots, and for the tokens that they do
+// not settle the row of q, with a list of experts and their 64-bit values.
+struct Scratch {
+    Ranked *few, *slot;   // [32] each
+    long long *key;       // [E]
+    float *row;           // [E]
+    uint16_t *id;         // [E]
+};
+__host__ __device__ inline int scratch_bytes(int E) { return 512 + ((14 * E + 15) & ~15); }
+__device__ __forceinline__ Scratch scratch_of(unsigned char *smem, int wid, int E) {
+    unsigned char *p = smem + (size_t)wid * scratch_bytes(E);
+    return {reinterpret_cast<Ranked *>(p), reinterpret_cast<Ranked *>(p + 256),
+            reinterpret_cast<long long *>(p + 512), reinterpret_cast<float *>(p + 512 + 8 * E),
+            reinterpret_cast<uint16_t *>(p + 512 + 12 * E)};
 }
 
-// The selection in fp64, for a token that fp32 left open.  floor32: no expert
-// whose fp32 value is below it can be chosen; kept: the groups to choose from,
-// or, if `groups` is set, those are open as well.  Returns lane j's expert.
-__device__ __noinline__ int select64(const SelectArgs &a, const float *L, float m, float floor32,
-                                     const float *q32, unsigned kept, bool groups, Undecided u) {
-    const int lane = threadIdx.x & 31;
-    Softmax sm = {m, 1.0};
-    if (!a.sigmoid && m != -INFINITY) {
-        double z = 0.0;
-        for (int e = lane; e < a.E; e += 32) z += exp((double)L[e] - (double)m);
+// Order-preserving whole-number image of a 64-bit value (compared without the
+// slow fp64 pipe): -0.0 and 0.0 alike, a NaN below every number.
+constexpr long long kNaNKey = -0x7fffffffffffffffll;
+__device__ __forceinline__ long long key_of(double v) {
+    if (isnan(v)) return kNaNKey;
+    const long long b = __double_as_longlong(v + 0.0);
+    return b >= 0 ? b : (long long)(0x8000000000000000ull - (unsigned long long)b);
+}
+__device__ __forceinline__ double value_of(long long key) {
+    if (key == kNaNKey) return NAN;
+    return __longlong_as_double(
+        key >= 0 ? key : (long long)(0x8000000000000000ull - (unsigned long long)key));
+}
+
+// sum of exp(L - m) over a row
+__device__ __noinline__ double softmax_sum64(const float *L, int E, float m) {
+    double z = 0.0;
+    for (int e = threadIdx.x & 31; e < E; e += 32) z += exp((double)L[e] - (double)m);
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) z += __shfl_xor_sync(kAll, z, o);
-        sm.z = z;
-    }
-    // candidates, in ascending id
-    int n = 0;
-    for (int e0 = 0; e0 < a.E; e0 += 32) {
-        const int e = e0 + lane;
-        bool in = e < a.E;
-        if (in && !groups) in = ((kept >> (e / a.size)) & 1u) && !(q32[e] < floor32);
-        const unsigned b = __ballot_sync(kAll, in);
-        if (in) u.id[n + __popc(b & ((1u << lane) - 1u))] = (uint16_t)e;
-        n += __popc(b);
-    }
-    __syncwarp();
-    // one logit for all of them (a padded row's): one score
-    bool same = a.sigmoid;
+    for (int o = 16; o >= 1; o >>= 1) z += __shfl_xor_sync(kAll, z, o);
+    return z;
+}
+// q of one expert in fp64 (a lane's own); on_logits: the logit itself
+__device__ __noinline__ double value64(const SelectArgs &a, const float *L, int e, bool on_logits,
+                                       float m, double z) {
+    const double x = (double)L[e];
+    double s = x;
+    if (!on_logits)
+        s = a.sigmoid ? 1.0 / (1.0 + exp(-x)) : m == -INFINITY ? 0.0 : exp(x - (double)m) / z;
+    return a.bias ? s + (double)a.bias[e] : s;
+}
+
+// The 64-bit values of the n experts in u.id, to u.key.  One logit for all of them
+// (a padded row's): one score.
+__device__ __noinline__ void values64(const SelectArgs &a, const float *L, float m, bool on_logits,
+                                      int n, const Scratch &u) {
+    const int lane = threadIdx.x & 31;
+    const double z = a.sigmoid || on_logits || m == -INFINITY ? 1.0 : softmax_sum64(L, a.E, m);
     const float first = L[u.id[0]];
+    bool same = true;
     for (int p = lane; p < n; p += 32)
         same = same && __float_as_uint(L[u.id[p]]) == __float_as_uint(first);
     same = __all_sync(kAll, same);
-    const double s0 = same ? score64(first, true, sm) : 0.0;
+    double s0 = 0.0;
+    if (same) {
+        const double x = (double)first;
+        s0 = on_logits ? x
+             : a.sigmoid ? 1.0 / (1.0 + exp(-x))
+             : m == -INFINITY ? 0.0 : exp(x - (double)m) / z;
+    }
     for (int p = lane; p < n; p += 32) {
         const int e = u.id[p];
-        const double s = same ? s0 : score64(L[e], a.sigmoid, sm);
-        u.q[p] = a.bias ? s + (double)a.bias[e] : s;
+        u.key[p] = key_of(!same ? value64(a, L, e, on_logits, m, z)
+                          : a.bias ? s0 + (double)a.bias[e] : s0);
     }
     __syncwarp();
-    if (groups) {  // every expert is a candidate: p == e
-        double score = 0.0;
-        if (lane < a.G) {
-            double b1 = NAN, b2 = NAN;
-            for (int i = 0; i < a.size; ++i) {
-                const double v = u.q[lane * a.size + i];
-                if (i == 0) {
-                    b1 = v;
-                } else if (before(v, b1)) {
-                    b2 = b1;
-                    b1 = v;
-                } else if (i == 1 || before(v, b2)) {
-                    b2 = v;
-                }
-            }
-            score = a.top2 && a.size > 1 ? b1 + b2 : b1;
-        }
-        int ahead = 0;
-        for (int h = 0; h < a.G; ++h) {
-            const double o = __shfl_sync(kAll, score, h);
-            if (before(o, score) || (h < lane && !before(score, o))) ++ahead;
-        }
-        kept = __ballot_sync(kAll, lane < a.G && ahead < a.Gk);
-        for (int p = lane; p < n; p += 32) {
-            if (!((kept >> (u.id[p] / a.size)) & 1u)) u.id[p] = 0xFFFFu;
-            else if (!a.bias) u.q[p] = (double)L[u.id[p]];
-        }
-        __syncwarp();
-    }
-    int mine = 0;
-    for (int j = 0; j < a.k; ++j) {
-        double v = NAN;
-        int at = 0x7fffffff;
-        for (int p = lane; p < n; p += 32) {
-            if (u.id[p] == 0xFFFFu) continue;
-            if (at == 0x7fffffff || before(u.q[p], v)) {
-                v = u.q[p];
-                at = p;
-            }
-        }
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) {
-            const double ov = __shfl_xor_sync(kAll, v, o);
-            const int oat = __shfl_xor_sync(kAll, at, o);
-            if (oat != 0x7fffffff &&
-                (at == 0x7fffffff || before(ov, v) || (oat < at && !before(v, ov)))) {
-                v = ov;
-                at = oat;
-            }
-        }
-        if (lane == j) mine = u.id[at];
-        __syncwarp();
-        if (lane == 0) u.id[at] = 0xFFFFu;
-        __syncwarp();
-    }
-    return mine;
 }
 
-// One warp per token.  VPL: values a lane has room for (>= a.per).  EXACT: the
-// ranking is that of the logits themselves (no bias, and no group sums), which
-// fp32 settles; otherwise shared memory holds the fp64 decision's candidates.
+// The experts for which in(e) holds, in ascending order, to u.id.
+template <typename F> __device__ __forceinline__ int list_experts(int E, const Scratch &u, F in) {
+    const int lane = threadIdx.x & 31;
+    int n = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+        const bool is = in(e0 + lane);
+        const unsigned b = __ballot_sync(kAll, is);
+        if (is) u.id[n + __popc(b & ((1u << lane) - 1u))] = (uint16_t)(e0 + lane);
+        n += __popc(b);
+    }
+    __syncwarp();
+    return n;
+}
+
+// Which groups stay, decided in fp64 where fp32 left it open: `sure` do, and of the
+// groups in `near` the best `need`.  Masks: bit g << shift.  u.row: every
+// q; floor32 (a group's lanes): only its values from there up can be of its score.
+__device__ __noinline__ unsigned groups64(const SelectArgs &a, const float *L, float m,
+                                          bool on_logits, unsigned sure, unsigned near, int need,
+                                          float floor32, const Scratch &u) {
+    const int lane = threadIdx.x & 31, shift = a.shift;
+    const int n = list_experts(a.E, u, [&](int e) {
+        const int g = min(e, a.E - 1) / a.size;
+        const float f = __shfl_sync(kAll, floor32, g << shift);
+        return e < a.E && ((near >> (g << shift)) & 1u) && !(u.row[e] < f);
+    });
+    values64(a, L, m, on_logits, n, u);
+    // lane g << shift: its group's score
+    const int mine = lane >> shift;
+    const bool is = ((near >> lane) & 1u) != 0;
+    long long key = kNaNKey;
+    if (is) {
+        int have = 0;
+        long long b1 = kNaNKey, b2 = kNaNKey;
+        for (int p = 0; p < n; ++p) {
+            if (u.id[p] / a.size != mine) continue;
+            const long long v = u.key[p];
+            ++have;
+            if (v > b1) {
+                b2 = b1;
+                b1 = v;
+            } else if (v > b2) {
+                b2 = v;
+            }
+        }
+        key = a.top2 && a.size > 1 ? key_of(value_of(b1) + value_of(b2)) : b1;
+    }
+    int ahead = 0;
+    for (int h = 0; h < a.G; ++h) {
+        const long long o = __shfl_sync(kAll, key, h << shift);
+        if (((near >> (h << shift)) & 1u) && (o > key || (o == key && h < mine))) ++ahead;
+    }
+    return sure | __ballot_sync(kAll, is && ahead < need);
+}
+
+// The k best of the n experts in u.id, by their 64-bit values: lane j's expert.
+__device__ __noinline__ int best64(const SelectArgs &a, const float *L, float m, bool on_logits,
+                                   int n, const Scratch &u) {
+    const int lane = threadIdx.x & 31;
+    values64(a, L, m, on_logits, n, u);
+    for (int p = lane; p < n; p += 32) {
+        const long long v = u.key[p];
+        int ahead = 0;
+        for (int o = 0; o < n; ++o) {
+            const long long w = u.key[o];
+            if (w > v || (w == v && o < p)) ++ahead;
+        }
+        if (ahead < a.k) u.slot[ahead].id = u.id[p];
+    }
+    __syncwarp();
+    return u.slot[lane].id;
+}
+
+// k rounds over the row in shared memory (NaN: not to be chosen, or taken), where
+// the candidates are more than a warp has lanes: lane j's expert and q, and the
+// largest that was left (NaN: none).  False where fewer than k are numbers.
+__device__ __noinline__ bool select_rounds(int E, int k, float *row, Ranked *mine, float *next) {
+    const int lane = threadIdx.x & 31;
+    for (int j = 0; j <= k; ++j) {
+        float v = NAN;
+        int at = 0;
+        for (int e = lane; e < E; e += 32) {
+            const float x = row[e];
+            if (x > v || (isnan(v) && !isnan(x))) {
+                v = x;
+                at = e;
+            }
+        }
+        const float top = warp_max(v);
+        if (j == k) {
+            *next = top;
+            break;
+        }
+        if (isnan(top)) return false;
+        const int e = (int)__reduce_min_sync(kAll, v == top ? (unsigned)at : 0xffffffffu);
+        if (lane == j) *mine = {top, e};
+        __syncwarp();
+        if (lane == 0) row[e] = NAN;
+        __syncwarp();
+    }
+    return true;
+}
+
+// A warp per token, several tokens one after the other where there are many.
+// VPL: values a lane has room for (>= a.per).  EXACT: the ranking is that of the
+// logits themselves (no bias, and no group sums).
+//
+// The k-th largest of the lanes' maxima is a bound that k values reach, and few
+// more (with k = 8 and 8 values a lane about 10, with k = 16 about 21): these
+// candidates are gathered in shared memory, one a lane, and each counts those ahead
+// of it, instead of k rounds of a warp maximum with its removal.
 template <int VPL, bool EXACT>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, VPL <= 8 ? 4 : VPL <= 16 ? 3 : VPL <= 32 ? 2 : 1)
 select_kernel(const __grid_constant__ SelectArgs a) {
     pdl_entry();
     if (a.zero_word != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *a.zero_word = 0u;
     extern __shared__ __align__(16) unsigned char smem[];
     const int lane = threadIdx.x & 31, warps = blockDim.x >> 5, wid = threadIdx.x >> 5;
-    const int64_t t = (int64_t)blockIdx.x * warps + wid;
-    if (t >= a.T) return;  // warp-uniform
     const int E = a.E;
-    float *L = a.logits + t * E;
-    const int group = lane / a.lanes_per_group, r = lane % a.lanes_per_group;
+    const int group = lane >> a.shift, r = lane & ((1 << a.shift) - 1);
     const int e0 = group * a.size + r * a.per;
     const int count = group < a.G ? max(0, min(a.per, a.size - r * a.per)) : 0;
+    const bool whole = VPL % 4 == 0 && a.per == VPL && (E & 3) == 0 && (a.size & 3) == 0;
+    const unsigned below = (1u << lane) - 1u;
+    const Scratch u = scratch_of(smem, wid, E);
+    u.few[lane] = kNobody;
+    u.slot[lane] = kNobody;
 
-    float v[VPL];
-    if (a.nparts > 0) {
-        const float *p = a.partial + t * E;
+    for (int64_t t = (int64_t)blockIdx.x * warps + wid; t < a.T; t += (int64_t)gridDim.x * warps) {
+        float *L = a.logits + t * E;
+        float v[VPL];  // NaN: no expert
+        if (a.nparts > 0) {
+            const float *p = a.partial + t * E;
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) v[i] = i < count ? p[e0 + i] : 0.f;
+            for (int i = 0; i < VPL; ++i) v[i] = i < count ? p[e0 + i] : NAN;
 #pragma unroll 4
-        for (int z = 1; z < a.nparts; ++z) {
-            p += a.T * E;
+            for (int z = 1; z < a.nparts; ++z) {
+                p += a.T * E;
 #pragma unroll
-            for (int i = 0; i < VPL; ++i)
-                if (i < count) v[i] += p[e0 + i];
-        }
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            if (i >= count) continue;
-            if (a.logit_bias) v[i] += a.logit_bias[e0 + i];
-            L[e0 + i] = v[i];
-        }
-        __syncwarp();
-    } else if (VPL % 4 == 0 && a.per == VPL && (E & 3) == 0 && (a.size & 3) == 0) {
-#pragma unroll
-        for (int i = 0; i + 3 < VPL; i += 4) {
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (i < count) x = *reinterpret_cast<const float4 *>(L + e0 + i);
-            v[i] = x.x;
-            v[i + 1] = x.y;
-            v[i + 2] = x.z;
-            v[i + 3] = x.w;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) v[i] = i < count ? L[e0 + i] : 0.f;
-    }
-
-    // softmax: the largest logit and the sum of the exponentials
-    float m = -INFINITY, z = 1.f;
-    if (!a.sigmoid) {
-        uint32_t top = 0u;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            if (i < count) top = max(top, key_of(v[i]));
-        top = __reduce_max_sync(kAll, top);
-        if (top > kNaNKey) m = value_of(top);
-        z = 0.f;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            if (i < count) z += expf(v[i] - m);
-        z = warp_sum(z);
-    }
-    uint32_t key[VPL];
-    float *q32 = nullptr;
-    Undecided und = {nullptr, nullptr};
-    if constexpr (EXACT) {
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) key[i] = i < count ? key_of(v[i]) : 0u;
-    } else {
-        // this warp's share of the shared memory: q in fp64, in fp32, ids
-        unsigned char *mine = smem + (size_t)wid * ((14 * E + 15) & ~15);
-        und.q = reinterpret_cast<double *>(mine);
-        q32 = reinterpret_cast<float *>(mine + 8 * E);
-        und.id = reinterpret_cast<uint16_t *>(mine + 12 * E);
-        const float inv = 1.f / z;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            key[i] = 0u;
-            if (i >= count) continue;
-            const float s = a.sigmoid ? 1.f / (1.f + expf(-v[i]))
-                                      : m == -INFINITY ? 0.f : expf(v[i] - m) * inv;
-            const float q = a.bias ? s + a.bias[e0 + i] : s;
-            q32[e0 + i] = q;
-            key[i] = key_of(q);
-        }
-    }
-    // How far two values of q have to be apart for fp32 to rank them.  Sigmoid:
-    // expf 2 ulp, the sum and the division half a one each: 3 * 2^-23 of s <= 1.
-    // Softmax: the difference L - m gives the exponential 2^-24 |L - m| of itself
-    // and x e^-x < 0.4, expf 2 ulp, the sum of VPL + 5 terms in series half an ulp
-    // each, the reciprocal and the product: below (VPL + 12) 2^-23 of the largest
-    // score 1/z.  q itself is rounded to 2^-24 of its size.  Twice that for two
-    // values, and some room.
-    const float unit = a.sigmoid ? 8.f * 0x1p-23f : 2.f * (VPL + 12) * 0x1p-23f / z;
-    auto open = [&](float hi, float lo) {  // also where either is a NaN or both are infinite
-        return !(hi - lo > unit + 0x1p-22f * fmaxf(fabsf(hi), fabsf(lo)));
-    };
-
-    bool groups_open = false;
-    unsigned kept = kAll;
-    if (a.Gk < a.G) {
-        uint32_t b1 = 0u, b2 = 0u;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            b2 = max(b2, min(b1, key[i]));
-            b1 = max(b1, key[i]);
-        }
-        for (int o = 1; o < a.lanes_per_group; o <<= 1) {
-            const uint32_t o1 = __shfl_xor_sync(kAll, b1, o), o2 = __shfl_xor_sync(kAll, b2, o);
-            b2 = max(max(b2, o2), min(b1, o1));
-            b1 = max(b1, o1);
-        }
-        uint32_t u = b1;
-        if constexpr (!EXACT)
-            if (a.top2 && b2 != 0u) u = key_of(value_of(b1) + value_of(b2));
-        int ahead = 0;
-        for (int h = 0; h < a.G; ++h) {
-            const uint32_t o = __shfl_sync(kAll, u, h * a.lanes_per_group);
-            if (o > u || (o == u && h < group)) ++ahead;
-        }
-        const bool stays = group < a.G && ahead < a.Gk;
-        if constexpr (!EXACT) {
-            const float lo = value_of(__reduce_min_sync(kAll, stays ? u : 0xffffffffu));
-            const float hi = value_of(__reduce_max_sync(kAll, stays || group >= a.G ? 0u : u));
-            // a sum has the errors of its two values and its own rounding
-            groups_open = a.top2 ? !(lo - hi > 2.f * unit + 0x1p-21f * fmaxf(fabsf(lo), fabsf(hi)))
-                                 : open(lo, hi);
-            kept = 0u;
-            for (int g = 0; g < a.G; ++g)
-                if (__shfl_sync(kAll, (int)stays, g * a.lanes_per_group)) kept |= 1u << g;
-        }
-        if (!stays)
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) key[i] = 0u;
-        // without a bias the order inside the groups is that of the logits
-        if constexpr (!EXACT)
-            if (!a.bias && stays)
-#pragma unroll
-                for (int i = 0; i < VPL; ++i) key[i] = i < count ? key_of(v[i]) : 0u;
-    }
-
-    // k rounds: the largest key of the warp, in the lowest lane that has it, at
-    // the lowest place there
-    uint32_t best = 0u;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) best = max(best, key[i]);
-    int my_e = 0;
-    uint32_t my_key = 0u;
-    for (int j = 0; j < a.k; ++j) {
-        const uint32_t top = __reduce_max_sync(kAll, best);
-        const int owner = __ffs(__ballot_sync(kAll, best == top)) - 1;
-        int e = 0;
-        if (lane == owner) {
-            int at = VPL - 1;
-#pragma unroll
-            for (int i = VPL - 2; i >= 0; --i)
-                if (key[i] == top) at = i;
-            e = e0 + at;
-            best = 0u;
+                for (int i = 0; i < VPL; ++i)
+                    if (i < count) v[i] += p[e0 + i];
+            }
 #pragma unroll
             for (int i = 0; i < VPL; ++i) {
-                if (i == at) key[i] = 0u;
-                best = max(best, key[i]);
+                if (i >= count) continue;
+                if (a.logit_bias) v[i] += a.logit_bias[e0 + i];
+                L[e0 + i] = v[i];
+            }
+        } else if (whole) {
+#pragma unroll
+            for (int i = 0; i + 3 < VPL; i += 4) {
+                float4 x = make_float4(NAN, NAN, NAN, NAN);
+                if (i < count) x = *reinterpret_cast<const float4 *>(L + e0 + i);
+                v[i] = x.x;
+                v[i + 1] = x.y;
+                v[i + 2] = x.z;
+                v[i + 3] = x.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) v[i] = i < count ? L[e0 + i] : NAN;
+        }
+        __syncwarp();  // (the row as written, and the last token's slots as read)
+
+        // softmax, where scores or their sum are needed: the largest logit m, and z
+        float m = -INFINITY, z = 1.f;
+        if (!a.sigmoid && (!EXACT || !a.renorm)) {
+            float top = v[0];
+#pragma unroll
+            for (int i = 1; i < VPL; ++i) top = fmaxf(top, v[i]);
+            top = warp_max(top);
+            if (!isnan(top)) m = top;
+            z = 0.f;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                if (i < count) z += exp2_fast((v[i] - m) * kLog2e);
+            z = warp_sum(z);
+        }
+        if constexpr (!EXACT) {
+            const float inv = m == -INFINITY ? 0.f : 1.f / z;
+            if (a.sigmoid) {
+#pragma unroll
+                for (int i = 0; i < VPL; ++i) v[i] = rcp_fast(1.f + exp2_fast(v[i] * -kLog2e));
+            } else {
+#pragma unroll
+                for (int i = 0; i < VPL; ++i)
+                    v[i] = m == -INFINITY && i < count ? 0.f : exp2_fast((v[i] - m) * kLog2e) * inv;
+            }
+            if (a.bias) {
+                if (whole && count == VPL) {
+#pragma unroll
+                    for (int i = 0; i + 3 < VPL; i += 4) {
+                        const float4 b = *reinterpret_cast<const float4 *>(a.bias + e0 + i);
+                        v[i] += b.x;
+                        v[i + 1] += b.y;
+                        v[i + 2] += b.z;
+                        v[i + 3] += b.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < VPL; ++i)
+                        if (i < count) v[i] += a.bias[e0 + i];
+                }
             }
         }
-        e = __shfl_sync(kAll, e, owner);
-        if (lane == j) {
-            my_e = e;
-            my_key = top;
-        }
-    }
-    if constexpr (!EXACT) {
-        const uint32_t next = __reduce_max_sync(kAll, best);  // the best that was left
-        bool undecided = groups_open;
-        float last = 0.f;
-        if (a.bias) {
-            const float mine = value_of(my_key), above = __shfl_up_sync(kAll, mine, 1);
-            last = __shfl_sync(kAll, mine, a.k - 1);
-            bool o = lane > 0 && lane < a.k && open(above, mine);
-            if (lane == 0 && next != 0u) o = open(last, value_of(next));
-            undecided |= __any_sync(kAll, o) != 0;
-        }
-        if (undecided) {
-            __syncwarp();
-            // no candidate: those that fp32 puts below the last chosen by more than
-            // the errors (a NaN there excludes none)
-            const float floor32 = last - (2.f * unit + 0x1p-21f * fabsf(last));
-            my_e = select64(a, L, m, floor32, q32, kept, groups_open, und);
-        }
-    }
+        // How far two values of q have to be apart for fp32 to rank them.  Sigmoid:
+        // the exponential 2 ulp and its argument's rounding, 2^-24 |L|, times s (1 - s)
+        // and |L| s (1 - s) < 0.3; the sum half an ulp, the reciprocal one: below
+        // 2^-22.  Softmax: the argument's two roundings give the exponential
+        // 2^-23 |L - m| of itself, and x e^-x < 0.4; the exponential 2 ulp, the sum of
+        // VPL + 5 terms in series half an ulp each, reciprocal and product: below
+        // (VPL + 12) 2^-23 of the largest score 1/z.  q itself is rounded to 2^-24 of
+        // its size.  Twice that for two values, and some room.
+        float unit = 0.f;
+        if constexpr (!EXACT)
+            unit = a.sigmoid ? 8.f * 0x1p-23f : 2.f * (VPL + 12) * 0x1p-23f * rcp_fast(z);
+        auto open = [&](float hi, float lo) {  // also where either is a NaN or both are infinite
+            return !(hi - lo > unit + 0x1p-22f * fmaxf(fabsf(hi), fabsf(lo)));
+        };
+        const bool exact = EXACT || !a.bias;  // v are logits, from the choice among the experts on
 
-    // the weights, a slot a lane
-    if (a.sigmoid || a.renorm) {
-        const bool slot = lane < a.k;
-        const float mine = slot ? L[my_e] : 0.f;
-        float s = 0.f;
-        if (a.sigmoid) s = slot ? 1.f / (1.f + expf(-mine)) : 0.f;
-        float sum = a.sigmoid && a.renorm ? warp_sum(s) : 1.f;
-        if (a.renorm && (!a.sigmoid || sum < 0x1p-100f)) {
-            // shares of exponentials, shifted by the largest chosen logit; so too
-            // sigmoids that underflow together, where 1 + exp(L) is 1
-            float top = slot ? mine : -INFINITY;
+        float best = NAN;
+        unsigned kept = kAll;
+        if (a.Gk < a.G) {
+            float score, floor32;
+            if (EXACT || !a.top2 || a.size == 1) {
+                best = v[0];
 #pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
-            s = !slot || top == -INFINITY ? 0.f : expf(mine - top);
-            sum = top == -INFINITY ? 1.f : warp_sum(s);
+                for (int i = 1; i < VPL; ++i) best = fmaxf(best, v[i]);
+                score = best;
+                for (int o = 1; o < (1 << a.shift); o <<= 1)
+                    score = fmaxf(score, __shfl_xor_sync(kAll, score, o));
+                floor32 = score;
+            } else {
+                float b1 = -INFINITY, b2 = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < VPL; ++i) {
+                    b2 = fmaxf(b2, v[i] > b1 ? b1 : v[i]);
+                    b1 = fmaxf(b1, v[i]);
+                }
+                best = b1;
+                for (int o = 1; o < (1 << a.shift); o <<= 1) {
+                    const float o1 = __shfl_xor_sync(kAll, b1, o), o2 = __shfl_xor_sync(kAll, b2, o);
+                    b2 = fmaxf(fmaxf(b2, o2), fminf(b1, o1));
+                    b1 = fmaxf(b1, o1);
+                }
+                // (no second number, or an excluded expert: left to groups64)
+                score = group < a.G && b2 > -INFINITY ? b1 + b2 : NAN;
+                floor32 = isnan(score) ? NAN : b2;
+            }
+            // the Gk-th largest score, and the groups that reach it or come near
+            const bool head = r == 0 && group < a.G;
+            float cur = head ? score : NAN, bound = NAN;
+            for (int j = 0; j < a.Gk;) {
+                const float top = warp_max(cur);
+                if (isnan(top)) break;
+                bound = top;
+                j += __popc(__ballot_sync(kAll, cur == top));
+                if (cur == top) cur = NAN;
+            }
+            // (a sum has the errors of its two values and its own rounding)
+            const float off = EXACT ? 0.f : 2.f * unit + 0x1p-21f * fabsf(bound);
+            const unsigned reach = __ballot_sync(kAll, head && !(score < bound - off));
+            if (__popc(reach) == a.Gk) {
+                kept = reach;
+            } else {
+#pragma unroll
+                for (int i = 0; i < VPL; ++i)
+                    if (i < count) u.row[e0 + i] = v[i];
+                __syncwarp();
+                const unsigned sure = __ballot_sync(kAll, head && score > bound + off);
+                if (!EXACT) floor32 -= unit + 0x1p-22f * fabsf(floor32);
+                kept = groups64(a, L, m, EXACT, sure, reach & ~sure, a.Gk - __popc(sure), floor32, u);
+            }
+            // without a bias the order inside the groups is that of the logits
+            if (!EXACT && !a.bias) {
+                best = NAN;
+#pragma unroll
+                for (int i = 0; i < VPL; ++i) {
+                    v[i] = i < count ? L[e0 + i] : NAN;
+                    best = fmaxf(best, v[i]);
+                }
+            }
+            if (((kept >> (group << a.shift)) & 1u) == 0u) {
+                best = NAN;
+#pragma unroll
+                for (int i = 0; i < VPL; ++i) v[i] = NAN;
+            }
+        } else {
+            best = v[0];
+#pragma unroll
+            for (int i = 1; i < VPL; ++i) best = fmaxf(best, v[i]);
+        }
+
+        // a bound that k values reach: the k-th largest distinct maximum of a lane
+        float bound = -INFINITY;
+        for (int j = 0; j < a.k; ++j) {
+            const float top = warp_max(best);
+            if (isnan(top)) {  // fewer lanes than that: every value
+                bound = -INFINITY;
+                break;
+            }
+            bound = top;
+            if (best == top) best = NAN;
+        }
+        // the values that the chosen ones are among, and those too near to rank
+        const float floor32 = exact ? bound : bound - (unit + 0x1p-21f * fabsf(bound));
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            const bool in = v[i] >= floor32;
+            const unsigned b = __ballot_sync(kAll, in);
+            if (b == 0u) continue;
+            const int at = n + __popc(b & below);
+            if (in && at < 32) u.few[at] = {v[i], e0 + i};
+            n += __popc(b);
+        }
+        __syncwarp();
+        Ranked mine = u.few[lane];
+        bool undecided;
+        if (n >= a.k && n <= 32) {
+            int ahead = 0;
+            for (int p = 0; p < n; p += 4) {  // (nobody: NaN, ahead of none)
+                const float4 x = *reinterpret_cast<const float4 *>(u.few + p);
+                const float4 y = *reinterpret_cast<const float4 *>(u.few + p + 2);
+                ahead += (x.x > mine.q) + (x.z > mine.q) + (y.x > mine.q) + (y.z > mine.q);
+            }
+            if (lane < n) u.slot[ahead] = mine;
+            __syncwarp();
+            u.few[lane] = kNobody;
+            const int id = mine.id;
+            mine = u.slot[lane];  // (equal values leave a slot after them empty)
+            const float above = __shfl_up_sync(kAll, mine.q, 1);
+            undecided = __any_sync(kAll, lane > 0 && lane <= a.k && lane < n &&
+                                             (exact ? isnan(mine.q) : open(above, mine.q)));
+            if (undecided) {
+                if (lane < n) u.id[lane] = (uint16_t)id;
+                __syncwarp();
+                // (in ascending order: equal values go to the lower place)
+                if (lane < n) {
+                    int place = 0;
+                    for (int p = 0; p < n; ++p) place += u.id[p] < id;
+                    u.row[place] = __int_as_float(id);
+                }
+                __syncwarp();
+                if (lane < n) u.id[lane] = (uint16_t)__float_as_int(u.row[lane]);
+                __syncwarp();
+                mine.id = best64(a, L, m, exact, n, u);
+                __syncwarp();
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                if (i < count) u.row[e0 + i] = v[i];
+            u.few[lane] = kNobody;
+            __syncwarp();
+            float next = NAN;
+            undecided = !select_rounds(E, a.k, u.row, &mine, &next);
+            if (!exact) {
+                const float above = __shfl_up_sync(kAll, mine.q, 1);
+                bool o = lane > 0 && lane < a.k && open(above, mine.q);
+                if (lane == a.k - 1 && !isnan(next)) o |= open(mine.q, next);
+                undecided |= __any_sync(kAll, o) != 0;
+            }
+            if (undecided) {  // (the rounds took values out of the row)
+#pragma unroll
+                for (int i = 0; i < VPL; ++i)
+                    if (i < count) u.row[e0 + i] = v[i];
+                __syncwarp();
+                const int c = list_experts(E, u, [&](int e) {
+                    return e < E && ((kept >> (min(e, E - 1) / a.size << a.shift)) & 1u) &&
+                           !(u.row[e] < floor32);
+                });
+                mine.id = best64(a, L, m, exact, c, u);
+                __syncwarp();
+            }
+        }
+        u.slot[lane] = kNobody;
+        const int my_e = mine.id;
+
+        // the weights, a slot a lane
+        const bool slot = lane < a.k;
+        const float logit = slot ? L[my_e] : -INFINITY;
+        float w;
+        if (a.sigmoid || a.renorm) {
+            float s = a.sigmoid ? rcp_fast(1.f + expf(-logit)) : 0.f;
+            float sum = 1.f;
+            if (a.sigmoid && a.renorm) sum = slots_sum(slot ? s : 0.f, a.half);
+            if (a.renorm && (!a.sigmoid || sum < 0x1p-100f)) {
+                // shares of exponentials, shifted by the largest chosen logit; so too
+                // sigmoids that underflow together, where 1 + exp(L) is 1
+                const float top = slots_max(logit, a.half);
+                s = !slot || top == -INFINITY ? 0.f : expf(logit - top);
+                sum = slots_sum(s, a.half);
+                if (top == -INFINITY) sum = 1.f;
+            }
+            w = a.scale * __fdividef(s, sum);
+        } else {
+            w = m == -INFINITY ? 0.f : a.scale * __fdividef(expf(logit - m), z);
         }
         if (slot) {
             a.idx[t * a.k + lane] = my_e;
-            a.w[t * a.k + lane] = a.scale * (s / sum);
+            a.w[t * a.k + lane] = w;
         }
-    } else if (lane < a.k) {
-        a.idx[t * a.k + lane] = my_e;
-        a.w[t * a.k + lane] = m == -INFINITY ? 0.f : a.scale * (expf(L[my_e] - m) / z);
     }
 }
 
 template <int VPL>
 cudaError_t launch_select_v(const SelectArgs &a, bool exact, cudaStream_t st) {
     const int threads = 256, warps = threads / 32;
-    const dim3 grid((unsigned)((a.T + warps - 1) / warps));
-    if (exact) return launch_pdl(select_kernel<VPL, true>, grid, dim3(threads), 0, st, a);
-    // the candidates' shared memory: 14 bytes an expert and warp
-    const size_t smem = (size_t)warps * ((14 * (size_t)a.E + 15) & ~(size_t)15);
+    const size_t smem = (size_t)warps * scratch_bytes(a.E);
+    // as many blocks as stay resident (8 of 32 registers a thread), then more tokens a warp
+    const int64_t blocks = (a.T + warps - 1) / warps;
+    const dim3 grid((unsigned)std::min<int64_t>(blocks, (int64_t)device_sm_count() * 8));
     if (smem > 48 * 1024) {
         static OncePerDevice once;
         const cudaError_t e = once([](int) {
-            return cudaFuncSetAttribute(select_kernel<VPL, false>,
-                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        8 * 14 * 1024);
+            const int most = 8 * scratch_bytes(1024);
+            const cudaError_t err = cudaFuncSetAttribute(
+                select_kernel<VPL, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+            return err != cudaSuccess
+                       ? err
+                       : cudaFuncSetAttribute(select_kernel<VPL, false>,
+                                              cudaFuncAttributeMaxDynamicSharedMemorySize, most);
         });
         if (e != cudaSuccess) return e;
     }
-    return launch_pdl(select_kernel<VPL, false>, grid, dim3(threads), smem, st, a);
+    return launch_pdl(exact ? select_kernel<VPL, true> : select_kernel<VPL, false>, grid,
+                      dim3(threads), smem, st, a);
 }
 
 // ------------------------- gradient to the logits --------------------------
@@ -605,10 +778,11 @@ cudaError_t launch_select(const Shape &s, const Router &r, float *logits, const 
     a.Gk = r.Gk < r.G ? r.Gk : 1;
     a.top2 = r.top2;
     a.size = s.E / a.G;
-    a.lanes_per_group = 32;
-    for (int g = 1; g < a.G; g <<= 1) a.lanes_per_group /= 2;
-    a.per = (a.size + a.lanes_per_group - 1) / a.lanes_per_group;
+    a.shift = 5;
+    for (int g = 1; g < a.G; g <<= 1) --a.shift;
+    a.per = (a.size + (1 << a.shift) - 1) >> a.shift;
     a.scale = r.scale;
+    for (int h = 1; h < s.k; h <<= 1) a.half = h;
     a.idx = idx;
     a.w = w;
     a.zero_word = zero_word;
