@@ -58,22 +58,12 @@ struct SelectArgs {
     // groups: 1 << shift lanes share a group of `size` consecutive experts, `per`
     // consecutive ones a lane, so that ids ascend with the lane
     int G, Gk, top2, size, shift, per;
+    int per_group;  // 2^20 / size, rounded up: e * per_group >> 20 is e's group
     float scale;
-    int half;  // half the power of two that holds k slots
     int32_t *idx;
     float *w;
     unsigned *zero_word;
 };
-
-// Sum and largest over the slots (lanes below 2 * half), in all lanes.
-__device__ __forceinline__ float slots_sum(float v, int half) {
-    for (int o = half; o >= 1; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
-    return __shfl_sync(kAll, v, 0);
-}
-__device__ __forceinline__ float slots_max(float v, int half) {
-    for (int o = half; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
-    return __shfl_sync(kAll, v, 0);
-}
 
 // A candidate, or a slot of the selection.
 struct __align__(8) Ranked {
@@ -85,17 +75,16 @@ constexpr Ranked kNobody = {NAN, 0};
 // A warp's shared memory: candidates and slots, and for the tokens that they do
 // not settle the row of q, with a list of experts and their 64-bit values.
 struct Scratch {
-    Ranked *few, *slot;   // [32] each
+    Ranked *slot;         // [32]
     long long *key;       // [E]
     float *row;           // [E]
     uint16_t *id;         // [E]
 };
-__host__ __device__ inline int scratch_bytes(int E) { return 512 + ((14 * E + 15) & ~15); }
-__device__ __forceinline__ Scratch scratch_of(unsigned char *smem, int wid, int E) {
-    unsigned char *p = smem + (size_t)wid * scratch_bytes(E);
-    return {reinterpret_cast<Ranked *>(p), reinterpret_cast<Ranked *>(p + 256),
-            reinterpret_cast<long long *>(p + 512), reinterpret_cast<float *>(p + 512 + 8 * E),
-            reinterpret_cast<uint16_t *>(p + 512 + 12 * E)};
+__host__ __device__ inline int scratch_bytes(int E) { return 256 + ((14 * E + 15) & ~15); }
+__device__ __forceinline__ Scratch scratch_of(unsigned char *p, int E) {
+    return {reinterpret_cast<Ranked *>(p), reinterpret_cast<long long *>(p + 256),
+            reinterpret_cast<float *>(p + 256 + 8 * E),
+            reinterpret_cast<uint16_t *>(p + 256 + 12 * E)};
 }
 
 // Order-preserving whole-number image of a 64-bit value (compared without the
@@ -130,17 +119,20 @@ __device__ __noinline__ double value64(const SelectArgs &a, const float *L, int 
     return a.bias ? s + (double)a.bias[e] : s;
 }
 
-// The 64-bit values of the n experts in u.id, to u.key.  One logit for all of them
+// The 64-bit values of the n experts in u.id, to u.key.  One logit for all of many
 // (a padded row's): one score.
 __device__ __noinline__ void values64(const SelectArgs &a, const float *L, float m, bool on_logits,
                                       int n, const Scratch &u) {
     const int lane = threadIdx.x & 31;
     const double z = a.sigmoid || on_logits || m == -INFINITY ? 1.0 : softmax_sum64(L, a.E, m);
-    const float first = L[u.id[0]];
-    bool same = true;
-    for (int p = lane; p < n; p += 32)
-        same = same && __float_as_uint(L[u.id[p]]) == __float_as_uint(first);
-    same = __all_sync(kAll, same);
+    bool same = n > 32;
+    float first = 0.f;
+    if (same) {
+        first = L[u.id[0]];
+        for (int p = lane; p < n; p += 32)
+            same = same && __float_as_uint(L[u.id[p]]) == __float_as_uint(first);
+        same = __all_sync(kAll, same);
+    }
     double s0 = 0.0;
     if (same) {
         const double x = (double)first;
@@ -156,10 +148,13 @@ __device__ __noinline__ void values64(const SelectArgs &a, const float *L, float
     __syncwarp();
 }
 
+__device__ __forceinline__ int group_of(const SelectArgs &a, int e) { return e * a.per_group >> 20; }
+
 // The experts for which in(e) holds, in ascending order, to u.id.
 template <typename F> __device__ __forceinline__ int list_experts(int E, const Scratch &u, F in) {
     const int lane = threadIdx.x & 31;
     int n = 0;
+#pragma unroll 8
     for (int e0 = 0; e0 < E; e0 += 32) {
         const bool is = in(e0 + lane);
         const unsigned b = __ballot_sync(kAll, is);
@@ -170,30 +165,26 @@ template <typename F> __device__ __forceinline__ int list_experts(int E, const S
     return n;
 }
 
-// Which groups stay, decided in fp64 where fp32 left it open: `sure` do, and of the
-// groups in `near` the best `need`.  Masks: bit g << shift.  u.row: every
-// q; floor32 (a group's lanes): only its values from there up can be of its score.
+// The best `need` of the groups in `near` (bit g), by their 64-bit scores.  u.row:
+// every q; floor32 (lane g: its group's): only values from there up can be of the
+// score.
 __device__ __noinline__ unsigned groups64(const SelectArgs &a, const float *L, float m,
-                                          bool on_logits, unsigned sure, unsigned near, int need,
-                                          float floor32, const Scratch &u) {
-    const int lane = threadIdx.x & 31, shift = a.shift;
+                                          bool on_logits, unsigned near, int need, float floor32,
+                                          const Scratch &u) {
+    const int lane = threadIdx.x & 31;
     const int n = list_experts(a.E, u, [&](int e) {
-        const int g = min(e, a.E - 1) / a.size;
-        const float f = __shfl_sync(kAll, floor32, g << shift);
-        return e < a.E && ((near >> (g << shift)) & 1u) && !(u.row[e] < f);
+        const int g = group_of(a, min(e, a.E - 1));
+        const float f = __shfl_sync(kAll, floor32, g);
+        return e < a.E && ((near >> g) & 1u) && !(u.row[e] < f);
     });
     values64(a, L, m, on_logits, n, u);
-    // lane g << shift: its group's score
-    const int mine = lane >> shift;
     const bool is = ((near >> lane) & 1u) != 0;
     long long key = kNaNKey;
     if (is) {
-        int have = 0;
         long long b1 = kNaNKey, b2 = kNaNKey;
         for (int p = 0; p < n; ++p) {
-            if (u.id[p] / a.size != mine) continue;
+            if (group_of(a, u.id[p]) != lane) continue;
             const long long v = u.key[p];
-            ++have;
             if (v > b1) {
                 b2 = b1;
                 b1 = v;
@@ -205,58 +196,182 @@ __device__ __noinline__ unsigned groups64(const SelectArgs &a, const float *L, f
     }
     int ahead = 0;
     for (int h = 0; h < a.G; ++h) {
-        const long long o = __shfl_sync(kAll, key, h << shift);
-        if (((near >> (h << shift)) & 1u) && (o > key || (o == key && h < mine))) ++ahead;
+        const long long o = __shfl_sync(kAll, key, h);
+        if (((near >> h) & 1u) && (o > key || (o == key && h < lane))) ++ahead;
     }
-    return sure | __ballot_sync(kAll, is && ahead < need);
+    return __ballot_sync(kAll, is && ahead < need);
 }
 
-// The k best of the n experts in u.id, by their 64-bit values: lane j's expert.
-__device__ __noinline__ int best64(const SelectArgs &a, const float *L, float m, bool on_logits,
-                                   int n, const Scratch &u) {
-    const int lane = threadIdx.x & 31;
-    values64(a, L, m, on_logits, n, u);
-    for (int p = lane; p < n; p += 32) {
-        const long long v = u.key[p];
-        int ahead = 0;
-        for (int o = 0; o < n; ++o) {
-            const long long w = u.key[o];
-            if (w > v || (w == v && o < p)) ++ahead;
+// How far two values of q have to be apart for fp32 to rank them.  Sigmoid: the
+// exponential 2 ulp and its argument's rounding, 2^-24 |L|, times s (1 - s), and
+// |L| s (1 - s) < 0.3; the sum half an ulp, the reciprocal one: below 2^-22 (two
+// values 4 * 2^-23).
+// Softmax: the argument's two roundings give the exponential 2^-23 |L - m| of
+// itself, and x e^-x < 0.4; the exponential 2 ulp, the sum of at most 37 terms in
+// series (`terms` of them a lane) half an ulp each, reciprocal and product: below
+// (terms + 12) 2^-23 of the largest score 1/z.  q itself is rounded to 2^-24 of its
+// size, and so is a sum of two.  With some room.
+__device__ __forceinline__ float unit_of(bool sigmoid, int terms, float z) {
+    return sigmoid ? 4.5f * 0x1p-23f : 2.f * (terms + 12) * 0x1p-23f * rcp_fast(z);
+}
+// (true also where either is a NaN or both are infinite)
+__device__ __forceinline__ bool too_near(float hi, float lo, float unit) {
+    return !(hi - lo > unit + 0x1.2p-23f * fmaxf(fabsf(hi), fabsf(lo)));
+}
+
+__device__ __forceinline__ float score32(float L, bool sigmoid, float m, float inv) {
+    if (sigmoid) return rcp_fast(1.f + exp2_fast(L * -kLog2e));
+    return m == -INFINITY ? 0.f : exp2_fast((L - m) * kLog2e) * inv;
+}
+
+// A token's weights and ids.  A lane with `chosen` has the expert `id`, its logit and
+// its slot; m, z: softmax without renormalisation.
+__device__ __forceinline__ void write_slots(const SelectArgs &a, int64_t t, bool chosen, int slot, int id,
+                                            float logit, float m, float z) {
+    float w;
+    if (a.sigmoid || a.renorm) {
+        float s = a.sigmoid ? rcp_fast(1.f + expf(-logit)) : 0.f;
+        float sum = 1.f;
+        if (a.sigmoid && a.renorm) sum = warp_sum(chosen ? s : 0.f);
+        if (a.renorm && (!a.sigmoid || sum < 0x1p-100f)) {
+            // shares of exponentials, shifted by the largest chosen logit; so too
+            // sigmoids that underflow together, where 1 + exp(L) is 1
+            const float top = warp_max(chosen ? logit : NAN);
+            s = !chosen || top == -INFINITY ? 0.f : expf(logit - top);
+            sum = warp_sum(s);
+            if (top == -INFINITY) sum = 1.f;
         }
-        if (ahead < a.k) u.slot[ahead].id = u.id[p];
+        w = a.scale * s * rcp_fast(sum);
+    } else {
+        w = m == -INFINITY ? 0.f : a.scale * expf(logit - m) * rcp_fast(z);
+    }
+    if (chosen) {
+        a.idx[t * a.k + slot] = id;
+        a.w[t * a.k + slot] = w;
+    }
+}
+
+// A token that the fast path below leaves open: ties, values or groups that fp32
+// cannot rank, NaN, or more candidates than a warp has lanes.  From the beginning, for any
+// sizes: candidates are ranked in fp32 where that settles them, else in fp64.
+__device__ __noinline__ void decide(const SelectArgs &a, int64_t t, unsigned char *smem) {
+    const int lane = threadIdx.x & 31, E = a.E;
+    const Scratch u = scratch_of(smem, E);
+    const float *L = a.logits + t * E;
+    const bool by_logits = !a.bias && (a.Gk == a.G || !a.top2);
+    __syncwarp();
+    float m = -INFINITY, z = 1.f;
+    if (!a.sigmoid) {
+        float top = NAN;
+        for (int e = lane; e < E; e += 32) top = fmaxf(top, L[e]);
+        top = warp_max(top);
+        if (!isnan(top)) m = top;
+        z = 0.f;
+#pragma unroll 4
+        for (int e = lane; e < E; e += 32) z += exp2_fast((L[e] - m) * kLog2e);
+        z = warp_sum(z);
+    }
+    const float unit = by_logits ? 0.f : unit_of(a.sigmoid, (E + 31) / 32, z);
+    const float inv = rcp_fast(z);
+    for (int e0 = lane; e0 < E; e0 += 256) {
+        float q[8], b[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int e = min(e0 + 32 * i, E - 1);
+            q[i] = L[e];
+            b[i] = a.bias ? a.bias[e] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (!by_logits) q[i] = score32(q[i], a.sigmoid, m, inv);
+            if (a.bias) q[i] += b[i];
+            if (e0 + 32 * i < E) u.row[e0 + 32 * i] = q[i];
+        }
     }
     __syncwarp();
-    return u.slot[lane].id;
-}
-
-// k rounds over the row in shared memory (NaN: not to be chosen, or taken), where
-// the candidates are more than a warp has lanes: lane j's expert and q, and the
-// largest that was left (NaN: none).  False where fewer than k are numbers.
-__device__ __noinline__ bool select_rounds(int E, int k, float *row, Ranked *mine, float *next) {
-    const int lane = threadIdx.x & 31;
-    for (int j = 0; j <= k; ++j) {
-        float v = NAN;
-        int at = 0;
-        for (int e = lane; e < E; e += 32) {
-            const float x = row[e];
-            if (x > v || (isnan(v) && !isnan(x))) {
-                v = x;
-                at = e;
+    unsigned kept = 1u;
+    if (a.Gk < a.G) {
+        float b1 = NAN, b2 = NAN, score = NAN, floor32 = NAN, mag = 0.f;
+        if (lane < a.G) {
+            for (int i = 0; i < a.size; ++i) {
+                const float x = u.row[lane * a.size + i];
+                b2 = fmaxf(b2, x > b1 ? b1 : isnan(b1) ? NAN : x);
+                b1 = fmaxf(b1, x);
             }
+            const bool sum = a.top2 && a.size > 1;
+            score = sum ? b1 + b2 : b1;
+            floor32 = isnan(score) ? NAN : sum ? b2 : b1;
+            if (!by_logits) floor32 -= unit + 0x1p-22f * fabsf(floor32);
+            mag = isnan(score) ? 0.f : fabsf(b1) + (sum ? fabsf(b2) : 0.f);
         }
-        const float top = warp_max(v);
-        if (j == k) {
-            *next = top;
-            break;
+        float cur = score, bound = NAN;  // the Gk-th largest score
+        for (int j = 0; j < a.Gk;) {
+            const float top = warp_max(cur);
+            if (isnan(top)) break;
+            bound = top;
+            j += __popc(__ballot_sync(kAll, cur == top));
+            if (cur == top) cur = NAN;
         }
-        if (isnan(top)) return false;
-        const int e = (int)__reduce_min_sync(kAll, v == top ? (unsigned)at : 0xffffffffu);
-        if (lane == j) *mine = {top, e};
-        __syncwarp();
-        if (lane == 0) row[e] = NAN;
+        const float off = by_logits ? 0.f : 2.f * unit + 0x1.2p-22f * warp_max(mag);
+        const unsigned reach = __ballot_sync(kAll, lane < a.G && !(score < bound - off));
+        kept = reach;
+        if (__popc(reach) != a.Gk) {
+            const unsigned sure = __ballot_sync(kAll, lane < a.G && score > bound + off);
+            kept = sure | groups64(a, L, m, by_logits, reach & ~sure, a.Gk - __popc(sure), floor32, u);
+        }
+        if (!by_logits && !a.bias) {  // the order inside the groups is that of the logits
+            for (int e = lane; e < E; e += 32) u.row[e] = L[e];
+            __syncwarp();
+        }
+    }
+    const bool exact = by_logits || !a.bias;
+    auto stays = [&](int e) { return e < E && ((kept >> group_of(a, min(e, E - 1))) & 1u); };
+    float best = NAN, bound = NAN;
+#pragma unroll 4
+    for (int e = lane; e < E; e += 32)
+        if (stays(e)) best = fmaxf(best, u.row[e]);
+    for (int j = 0; j < a.k; ++j) {
+        bound = warp_max(best);
+        if (best == bound) best = NAN;
+    }
+    if (isnan(bound)) bound = -INFINITY;  // fewer lanes than that: every value, and NaN
+    const float floor32 = exact ? bound : bound - (unit + 0x1p-21f * fabsf(bound));
+    const int n = list_experts(E, u, [&](int e) { return stays(e) && !(u.row[min(e, E - 1)] < floor32); });
+    u.slot[lane] = kNobody;
+    __syncwarp();
+    // (few candidates that are not logits: two of them are too near, mostly)
+    bool open = !exact && n <= 64;
+    for (int p = lane; p < n && !open; p += 32) {
+        const float q = u.row[u.id[p]];
+        int ahead = 0;
+        for (int o = 0; o < n; ++o) {
+            const float x = u.row[u.id[o]];
+            if (x > q || (x == q && o < p)) ++ahead;
+            if (!exact && o != p && x >= q) open |= too_near(x, q, unit);
+        }
+        // (only neighbours of the first k matter; a NaN is for the 64-bit keys)
+        if (isnan(q)) open = true;
+        else if (ahead < a.k) u.slot[ahead] = {q, u.id[p]};
+    }
+    open = __any_sync(kAll, open);
+    __syncwarp();
+    if (open) {
+        values64(a, L, m, exact, n, u);
+        for (int p = lane; p < n; p += 32) {
+            const long long v = u.key[p];
+            int ahead = 0;
+            for (int o = 0; o < n; ++o) {
+                const long long w = u.key[o];
+                if (w > v || (w == v && o < p)) ++ahead;
+            }
+            if (ahead < a.k) u.slot[ahead].id = u.id[p];
+        }
         __syncwarp();
     }
-    return true;
+    const bool chosen = lane < a.k;
+    const int id = chosen ? u.slot[lane].id : 0;
+    write_slots(a, t, chosen, lane, id, L[id], m, z);
+    __syncwarp();
 }
 
 // A warp per token, several tokens one after the other where there are many.
@@ -266,25 +381,31 @@ __device__ __noinline__ bool select_rounds(int E, int k, float *row, Ranked *min
 // The k-th largest of the lanes' maxima is a bound that k values reach, and few
 // more (with k = 8 and 8 values a lane about 10, with k = 16 about 21): these
 // candidates are gathered in shared memory, one a lane, and each counts those ahead
-// of it, instead of k rounds of a warp maximum with its removal.
-template <int VPL, bool EXACT>
-__global__ void __launch_bounds__(256, VPL <= 8 ? 4 : VPL <= 16 ? 3 : VPL <= 32 ? 2 : 1)
-select_kernel(const __grid_constant__ SelectArgs a) {
+// of it, instead of k rounds of a warp maximum with its removal.  What this leaves
+// open goes to decide(), after every 32 tokens: a call inside their loop cost it
+// spills (T = 131072, E = 128: 43 us to 62).  Blocks of one warp: what depends on the
+// token is uniform, which the compiler sees.
+template <int VPL, bool EXACT, bool GROUPS>
+__global__ void __launch_bounds__(32, VPL <= 8 ? 32 : 16)
+select_kernel(const SelectArgs a, const __grid_constant__ SelectArgs cold) {
     pdl_entry();
     if (a.zero_word != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *a.zero_word = 0u;
     extern __shared__ __align__(16) unsigned char smem[];
-    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5, wid = threadIdx.x >> 5;
+    const int lane = threadIdx.x;
     const int E = a.E;
-    const int group = lane >> a.shift, r = lane & ((1 << a.shift) - 1);
+    const int group = GROUPS ? lane >> a.shift : 0;
+    const int r = GROUPS ? lane & ((1 << a.shift) - 1) : lane;
     const int e0 = group * a.size + r * a.per;
     const int count = group < a.G ? max(0, min(a.per, a.size - r * a.per)) : 0;
     const bool whole = VPL % 4 == 0 && a.per == VPL && (E & 3) == 0 && (a.size & 3) == 0;
     const unsigned below = (1u << lane) - 1u;
-    const Scratch u = scratch_of(smem, wid, E);
-    u.few[lane] = kNobody;
-    u.slot[lane] = kNobody;
+    Ranked *few = reinterpret_cast<Ranked *>(smem);  // up to 32 VPL candidates
 
-    for (int64_t t = (int64_t)blockIdx.x * warps + wid; t < a.T; t += (int64_t)gridDim.x * warps) {
+    for (int64_t t0 = blockIdx.x; t0 < a.T; t0 += 32 * (int64_t)gridDim.x) {
+    unsigned left = 0u;  // of the tokens t0 + i * gridDim.x
+    for (int i32 = 0; i32 < 32; ++i32) {
+        const int64_t t = t0 + i32 * (int64_t)gridDim.x;
+        if (t >= a.T) break;
         float *L = a.logits + t * E;
         float v[VPL];  // NaN: no expert
         if (a.nparts > 0) {
@@ -318,7 +439,7 @@ select_kernel(const __grid_constant__ SelectArgs a) {
 #pragma unroll
             for (int i = 0; i < VPL; ++i) v[i] = i < count ? L[e0 + i] : NAN;
         }
-        __syncwarp();  // (the row as written, and the last token's slots as read)
+        __syncwarp();  // (the row as written, and the last token's candidates as read)
 
         // softmax, where scores or their sum are needed: the largest logit m, and z
         float m = -INFINITY, z = 1.f;
@@ -335,14 +456,13 @@ select_kernel(const __grid_constant__ SelectArgs a) {
             z = warp_sum(z);
         }
         if constexpr (!EXACT) {
-            const float inv = m == -INFINITY ? 0.f : 1.f / z;
             if (a.sigmoid) {
 #pragma unroll
-                for (int i = 0; i < VPL; ++i) v[i] = rcp_fast(1.f + exp2_fast(v[i] * -kLog2e));
-            } else {
+                for (int i = 0; i < VPL; ++i) v[i] = score32(v[i], true, 0.f, 0.f);
+            } else {  // (m == -INF, a row without scores: its NaN are for decide())
+                const float inv = rcp_fast(z);
 #pragma unroll
-                for (int i = 0; i < VPL; ++i)
-                    v[i] = m == -INFINITY && i < count ? 0.f : exp2_fast((v[i] - m) * kLog2e) * inv;
+                for (int i = 0; i < VPL; ++i) v[i] = exp2_fast((v[i] - m) * kLog2e) * inv;
             }
             if (a.bias) {
                 if (whole && count == VPL) {
@@ -361,26 +481,13 @@ select_kernel(const __grid_constant__ SelectArgs a) {
                 }
             }
         }
-        // How far two values of q have to be apart for fp32 to rank them.  Sigmoid:
-        // the exponential 2 ulp and its argument's rounding, 2^-24 |L|, times s (1 - s)
-        // and |L| s (1 - s) < 0.3; the sum half an ulp, the reciprocal one: below
-        // 2^-22.  Softmax: the argument's two roundings give the exponential
-        // 2^-23 |L - m| of itself, and x e^-x < 0.4; the exponential 2 ulp, the sum of
-        // VPL + 5 terms in series half an ulp each, reciprocal and product: below
-        // (VPL + 12) 2^-23 of the largest score 1/z.  q itself is rounded to 2^-24 of
-        // its size.  Twice that for two values, and some room.
-        float unit = 0.f;
-        if constexpr (!EXACT)
-            unit = a.sigmoid ? 8.f * 0x1p-23f : 2.f * (VPL + 12) * 0x1p-23f * rcp_fast(z);
-        auto open = [&](float hi, float lo) {  // also where either is a NaN or both are infinite
-            return !(hi - lo > unit + 0x1p-22f * fmaxf(fabsf(hi), fabsf(lo)));
-        };
-        const bool exact = EXACT || !a.bias;  // v are logits, from the choice among the experts on
+        const float unit = EXACT ? 0.f : unit_of(a.sigmoid, VPL, z);
+        const bool exact = EXACT || (GROUPS && !a.bias);  // v are logits, from here on
 
-        float best = NAN;
-        unsigned kept = kAll;
-        if (a.Gk < a.G) {
-            float score, floor32;
+        float best;
+        bool decided = true;
+        if constexpr (GROUPS) {
+            float score, mag = 0.f;
             if (EXACT || !a.top2 || a.size == 1) {
                 best = v[0];
 #pragma unroll
@@ -388,7 +495,7 @@ select_kernel(const __grid_constant__ SelectArgs a) {
                 score = best;
                 for (int o = 1; o < (1 << a.shift); o <<= 1)
                     score = fmaxf(score, __shfl_xor_sync(kAll, score, o));
-                floor32 = score;
+                if (!EXACT) mag = fabsf(score);
             } else {
                 float b1 = -INFINITY, b2 = -INFINITY;
 #pragma unroll
@@ -402,34 +509,19 @@ select_kernel(const __grid_constant__ SelectArgs a) {
                     b2 = fmaxf(fmaxf(b2, o2), fminf(b1, o1));
                     b1 = fmaxf(b1, o1);
                 }
-                // (no second number, or an excluded expert: left to groups64)
+                // (no second number, or an excluded expert: for decide())
                 score = group < a.G && b2 > -INFINITY ? b1 + b2 : NAN;
-                floor32 = isnan(score) ? NAN : b2;
+                if (!isnan(score)) mag = fabsf(b1) + fabsf(b2);
             }
-            // the Gk-th largest score, and the groups that reach it or come near
-            const bool head = r == 0 && group < a.G;
-            float cur = head ? score : NAN, bound = NAN;
-            for (int j = 0; j < a.Gk;) {
-                const float top = warp_max(cur);
-                if (isnan(top)) break;
-                bound = top;
-                j += __popc(__ballot_sync(kAll, cur == top));
-                if (cur == top) cur = NAN;
+            // a score that Gk groups reach: if no more come near it, they stay
+            float cur = score, bound = NAN;
+            for (int j = 0; j < a.Gk; ++j) {
+                bound = warp_max(cur);
+                if (cur == bound) cur = NAN;
             }
             // (a sum has the errors of its two values and its own rounding)
-            const float off = EXACT ? 0.f : 2.f * unit + 0x1p-21f * fabsf(bound);
-            const unsigned reach = __ballot_sync(kAll, head && !(score < bound - off));
-            if (__popc(reach) == a.Gk) {
-                kept = reach;
-            } else {
-#pragma unroll
-                for (int i = 0; i < VPL; ++i)
-                    if (i < count) u.row[e0 + i] = v[i];
-                __syncwarp();
-                const unsigned sure = __ballot_sync(kAll, head && score > bound + off);
-                if (!EXACT) floor32 -= unit + 0x1p-22f * fabsf(floor32);
-                kept = groups64(a, L, m, EXACT, sure, reach & ~sure, a.Gk - __popc(sure), floor32, u);
-            }
+            const float off = EXACT ? 0.f : 2.f * unit + 0x1.2p-22f * warp_max(mag);
+            decided = __popc(__ballot_sync(kAll, r == 0 && group < a.G && !(score < bound - off))) == a.Gk;
             // without a bias the order inside the groups is that of the logits
             if (!EXACT && !a.bias) {
                 best = NAN;
@@ -439,7 +531,7 @@ select_kernel(const __grid_constant__ SelectArgs a) {
                     best = fmaxf(best, v[i]);
                 }
             }
-            if (((kept >> (group << a.shift)) & 1u) == 0u) {
+            if (!(score >= bound)) {
                 best = NAN;
 #pragma unroll
                 for (int i = 0; i < VPL; ++i) v[i] = NAN;
@@ -451,16 +543,13 @@ select_kernel(const __grid_constant__ SelectArgs a) {
         }
 
         // a bound that k values reach: the k-th largest distinct maximum of a lane
-        float bound = -INFINITY;
+        float bound = NAN;
+#pragma unroll 4
         for (int j = 0; j < a.k; ++j) {
-            const float top = warp_max(best);
-            if (isnan(top)) {  // fewer lanes than that: every value
-                bound = -INFINITY;
-                break;
-            }
-            bound = top;
-            if (best == top) best = NAN;
+            bound = warp_max(best);
+            if (best == bound) best = NAN;
         }
+        if (isnan(bound)) bound = -INFINITY;  // fewer lanes than that: every value
         // the values that the chosen ones are among, and those too near to rank
         const float floor32 = exact ? bound : bound - (unit + 0x1p-21f * fabsf(bound));
         int n = 0;
@@ -468,123 +557,60 @@ select_kernel(const __grid_constant__ SelectArgs a) {
         for (int i = 0; i < VPL; ++i) {
             const bool in = v[i] >= floor32;
             const unsigned b = __ballot_sync(kAll, in);
-            if (b == 0u) continue;
-            const int at = n + __popc(b & below);
-            if (in && at < 32) u.few[at] = {v[i], e0 + i};
+            if (VPL > 8 && b == 0u) continue;
+            if (in) few[n + __popc(b & below)] = {v[i], e0 + i};
             n += __popc(b);
         }
+        decided = decided && n >= a.k && n <= 32;
         __syncwarp();
-        Ranked mine = u.few[lane];
-        bool undecided;
-        if (n >= a.k && n <= 32) {
-            int ahead = 0;
-            for (int p = 0; p < n; p += 4) {  // (nobody: NaN, ahead of none)
-                const float4 x = *reinterpret_cast<const float4 *>(u.few + p);
-                const float4 y = *reinterpret_cast<const float4 *>(u.few + p + 2);
-                ahead += (x.x > mine.q) + (x.z > mine.q) + (y.x > mine.q) + (y.z > mine.q);
-            }
-            if (lane < n) u.slot[ahead] = mine;
-            __syncwarp();
-            u.few[lane] = kNobody;
-            const int id = mine.id;
-            mine = u.slot[lane];  // (equal values leave a slot after them empty)
-            const float above = __shfl_up_sync(kAll, mine.q, 1);
-            undecided = __any_sync(kAll, lane > 0 && lane <= a.k && lane < n &&
-                                             (exact ? isnan(mine.q) : open(above, mine.q)));
-            if (undecided) {
-                if (lane < n) u.id[lane] = (uint16_t)id;
-                __syncwarp();
-                // (in ascending order: equal values go to the lower place)
-                if (lane < n) {
-                    int place = 0;
-                    for (int p = 0; p < n; ++p) place += u.id[p] < id;
-                    u.row[place] = __int_as_float(id);
-                }
-                __syncwarp();
-                if (lane < n) u.id[lane] = (uint16_t)__float_as_int(u.row[lane]);
-                __syncwarp();
-                mine.id = best64(a, L, m, exact, n, u);
-                __syncwarp();
-            }
-        } else {
+        const Ranked mine = lane < n ? few[lane] : kNobody;
+        // (loops of fixed length: with n for their limit, which is uniform but not
+        // known to be, each of their warp operations took three times the instructions)
+        unsigned ahead_of_me = 0u;  // (a NaN is ahead of none)
+        auto rank = [&](int p) {
+            const unsigned b = __ballot_sync(kAll, mine.q > __shfl_sync(kAll, mine.q, p));
+            if (lane == p) ahead_of_me = b;
+        };
 #pragma unroll
-            for (int i = 0; i < VPL; ++i)
-                if (i < count) u.row[e0 + i] = v[i];
-            u.few[lane] = kNobody;
-            __syncwarp();
-            float next = NAN;
-            undecided = !select_rounds(E, a.k, u.row, &mine, &next);
-            if (!exact) {
-                const float above = __shfl_up_sync(kAll, mine.q, 1);
-                bool o = lane > 0 && lane < a.k && open(above, mine.q);
-                if (lane == a.k - 1 && !isnan(next)) o |= open(mine.q, next);
-                undecided |= __any_sync(kAll, o) != 0;
-            }
-            if (undecided) {  // (the rounds took values out of the row)
+        for (int p = 0; p < 12; ++p) rank(p);
+        if (n > 12)
 #pragma unroll
-                for (int i = 0; i < VPL; ++i)
-                    if (i < count) u.row[e0 + i] = v[i];
-                __syncwarp();
-                const int c = list_experts(E, u, [&](int e) {
-                    return e < E && ((kept >> (min(e, E - 1) / a.size << a.shift)) & 1u) &&
-                           !(u.row[e] < floor32);
-                });
-                mine.id = best64(a, L, m, exact, c, u);
-                __syncwarp();
-            }
+            for (int p = 12; p < 32; ++p) rank(p);
+        const int ahead = __popc(ahead_of_me);
+        const bool chosen = lane < n && ahead < a.k;
+        // equal values have the same place
+        decided &= __popc(__reduce_or_sync(kAll, lane < n ? 1u << ahead : 0u)) == n;
+        if (!exact) {
+            __syncwarp();
+            if (lane < n) few[ahead] = mine;
+            __syncwarp();
+            const bool behind = chosen && ahead + 1 < n;
+            const float next = few[behind ? ahead + 1 : 0].q;
+            decided &= !__any_sync(kAll, behind && too_near(mine.q, next, unit));
         }
-        u.slot[lane] = kNobody;
-        const int my_e = mine.id;
-
-        // the weights, a slot a lane
-        const bool slot = lane < a.k;
-        const float logit = slot ? L[my_e] : -INFINITY;
-        float w;
-        if (a.sigmoid || a.renorm) {
-            float s = a.sigmoid ? rcp_fast(1.f + expf(-logit)) : 0.f;
-            float sum = 1.f;
-            if (a.sigmoid && a.renorm) sum = slots_sum(slot ? s : 0.f, a.half);
-            if (a.renorm && (!a.sigmoid || sum < 0x1p-100f)) {
-                // shares of exponentials, shifted by the largest chosen logit; so too
-                // sigmoids that underflow together, where 1 + exp(L) is 1
-                const float top = slots_max(logit, a.half);
-                s = !slot || top == -INFINITY ? 0.f : expf(logit - top);
-                sum = slots_sum(s, a.half);
-                if (top == -INFINITY) sum = 1.f;
-            }
-            w = a.scale * __fdividef(s, sum);
-        } else {
-            w = m == -INFINITY ? 0.f : a.scale * __fdividef(expf(logit - m), z);
-        }
-        if (slot) {
-            a.idx[t * a.k + lane] = my_e;
-            a.w[t * a.k + lane] = w;
-        }
+        if (decided) write_slots(a, t, chosen, ahead, mine.id,
+                                 exact ? mine.q : chosen ? L[mine.id] : 0.f, m, z);
+        if (!decided) left |= 1u << i32;
+    }
+    while (left) {
+        const int i = __ffs(left) - 1;
+        left &= left - 1u;
+        decide(cold, t0 + i * (int64_t)gridDim.x, smem);
+    }
     }
 }
 
-template <int VPL>
-cudaError_t launch_select_v(const SelectArgs &a, bool exact, cudaStream_t st) {
-    const int threads = 256, warps = threads / 32;
-    const size_t smem = (size_t)warps * scratch_bytes(a.E);
-    // as many blocks as stay resident (8 of 32 registers a thread), then more tokens a warp
-    const int64_t blocks = (a.T + warps - 1) / warps;
-    const dim3 grid((unsigned)std::min<int64_t>(blocks, (int64_t)device_sm_count() * 8));
-    if (smem > 48 * 1024) {
-        static OncePerDevice once;
-        const cudaError_t e = once([](int) {
-            const int most = 8 * scratch_bytes(1024);
-            const cudaError_t err = cudaFuncSetAttribute(
-                select_kernel<VPL, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-            return err != cudaSuccess
-                       ? err
-                       : cudaFuncSetAttribute(select_kernel<VPL, false>,
-                                              cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-        });
-        if (e != cudaSuccess) return e;
-    }
-    return launch_pdl(exact ? select_kernel<VPL, true> : select_kernel<VPL, false>, grid,
-                      dim3(threads), smem, st, a);
+template <int VPL, bool EXACT, bool GROUPS>
+cudaError_t launch_select_t(const SelectArgs &a, cudaStream_t st) {
+    const size_t smem = std::max<size_t>(scratch_bytes(a.E), sizeof(Ranked) * (32 * VPL + 4));
+    // as many blocks as stay resident, then more tokens a block
+    const dim3 grid((unsigned)std::min<int64_t>(a.T, (int64_t)device_sm_count() * 32));
+    return launch_pdl(select_kernel<VPL, EXACT, GROUPS>, grid, dim3(32), smem, st, a, a);
+}
+template <int VPL> cudaError_t launch_select_v(const SelectArgs &a, bool exact, cudaStream_t st) {
+    if (a.Gk < a.G)
+        return exact ? launch_select_t<VPL, true, true>(a, st) : launch_select_t<VPL, false, true>(a, st);
+    return exact ? launch_select_t<VPL, true, false>(a, st) : launch_select_t<VPL, false, false>(a, st);
 }
 
 // ------------------------- gradient to the logits --------------------------
@@ -778,11 +804,11 @@ cudaError_t launch_select(const Shape &s, const Router &r, float *logits, const 
     a.Gk = r.Gk < r.G ? r.Gk : 1;
     a.top2 = r.top2;
     a.size = s.E / a.G;
+    a.per_group = (1 << 20) / a.size + 1;  // (e < 1024: off by less than 1 / size)
     a.shift = 5;
     for (int g = 1; g < a.G; g <<= 1) --a.shift;
     a.per = (a.size + (1 << a.shift) - 1) >> a.shift;
     a.scale = r.scale;
-    for (int h = 1; h < s.k; h <<= 1) a.half = h;
     a.idx = idx;
     a.w = w;
     a.zero_word = zero_word;
@@ -794,7 +820,8 @@ cudaError_t launch_select(const Shape &s, const Router &r, float *logits, const 
     else if (a.per <= 8) e = launch_select_v<8>(a, exact, st);
     else if (a.per <= 16) e = launch_select_v<16>(a, exact, st);
     else if (a.per <= 32) e = launch_select_v<32>(a, exact, st);
-    else e = launch_select_v<64>(a, exact, st);  // E > 512, a number of groups between powers of two
+    else if (exact) e = launch_select_t<64, true, true>(a, st);  // few lanes a group: 9 to 31 groups
+    else e = launch_select_t<64, false, true>(a, st);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
