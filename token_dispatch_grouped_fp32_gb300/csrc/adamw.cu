@@ -27,7 +27,11 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBlock = 256;                // elements under one scale
-constexpr int kChunk = 64 * kBlock;        // elements a thread block takes at a time
+// Blocks a thread block takes at a time, one to eight a warp: as many as leave two
+// rounds of resident thread blocks (300 small tensors: 5.1 us with one, 10.3 with
+// eight; 64 M parameters, 8 bits: 180 us with one, 149 with eight).
+constexpr int kMostBlocks = 8 * kWarps;
+constexpr int64_t kRounds = 2 * 4 * 152;
 constexpr int kGrid = 152 * 8;
 constexpr int kTable = 300;                // tensors per launch
 constexpr int kMapped = 1024;              // chunks with a map of their own
@@ -43,7 +47,7 @@ struct Entry {
     uint8_t p_bf16, g_bf16, vec;
 };
 struct Table {
-    int n, chunks, mapped;
+    int n, chunks, mapped, chunk_blocks;
     uint16_t tensor_of[kMapped];
     Entry t[kTable];
 };
@@ -79,86 +83,163 @@ __device__ __forceinline__ uint32_t random_bits(Key k, int place) {
     return fold(fold(k.x + kK0 * (uint32_t)place, kK2) ^ k.y, kK1);
 }
 
-// fp32 to bf16, up or down by 16 random bits (NaN stays NaN)
-__device__ __forceinline__ uint32_t bf16_bits(float v, uint32_t u) {
-    const uint32_t b = __float_as_uint(v);
-    return isnan(v) ? 0x7fffu : (b + (u & 0xffffu)) >> 16;
+// Two fp32 values to bf16, up or down by 16 random bits each (the low ones of u and
+// w): the bits plus those, without their last 16; a NaN stays one.
+__device__ __forceinline__ uint32_t bf16_pair(float2 v, uint32_t u, uint32_t w) {
+    uint32_t d;
+    asm("cvt.rs.bf16x2.f32 %0, %1, %2, %3;"
+        : "=r"(d) : "f"(v.y), "f"(v.x), "r"(__byte_perm(u, w, 0x5410)));
+    return d;
 }
 
-// |y| <= 256 to a neighbouring e4m3 value, as a float: the low 20 mantissa bits
-// go, up or down by 16 random bits.  Below 2^-6 the steps are 2^-9 throughout,
-// those of the values from 2^-6 to 2^-5: with 2^-6 added, the same.
-__device__ __forceinline__ float to_e4m3(float y, uint32_t random20) {
-    const float low = fabsf(y) < 0x1p-6f ? copysignf(0x1p-6f, y) : 0.f;
-    const uint32_t z = (__float_as_uint(y + low) + random20) & ~0xFFFFFu;
-    return __uint_as_float(z) - low;
+// The largest magnitude of three; a NaN if one is.
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 
-template <typename T> struct Eight;  // eight consecutive elements as floats
-template <> struct Eight<float> {
-    static __device__ __forceinline__ void load(const float *p, float (&v)[8]) {
-        const float4 a = *reinterpret_cast<const float4 *>(p);
-        const float4 b = *reinterpret_cast<const float4 *>(p + 4);
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    }
-    static __device__ __forceinline__ void store(float *p, const float (&v)[8]) {
-        *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-        *reinterpret_cast<float4 *>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-    }
+// Two fp32 operations in one instruction, each rounded as its own.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 two(float v) { return make_float2(v, v); }
+
+// Root and reciprocal to 1 ulp.  FLUSH: squares below 2^-126 count as 0.
+template <bool FLUSH> __device__ __forceinline__ float root(float v) {
+    float r;
+    if constexpr (FLUSH) asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    else asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float reciprocal(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// Eight consecutive elements as they lie in memory, and as floats.
+template <typename T> struct Eight {
+    uint4 c;
+    __device__ __forceinline__ void load(const T *p) { c = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void store(T *p) const { stg16(p, c); }
 };
-template <> struct Eight<__nv_bfloat16> {
-    static __device__ __forceinline__ void load(const __nv_bfloat16 *p, float (&v)[8]) {
-        unpack16(*reinterpret_cast<const uint4 *>(p), v, static_cast<const __nv_bfloat16 *>(nullptr));
+template <> struct Eight<float> {
+    uint4 c, d;
+    __device__ __forceinline__ void load(const float *p) {
+        c = *reinterpret_cast<const uint4 *>(p);
+        d = *reinterpret_cast<const uint4 *>(p + 4);
     }
-    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&v)[8]) {
-        stg16(p, pack16(v, static_cast<const __nv_bfloat16 *>(nullptr)));
+    __device__ __forceinline__ void store(float *p) const {
+        stg16(p, c);
+        stg16(p + 4, d);
     }
 };
 template <> struct Eight<__nv_fp8_e4m3> {
-    static __device__ __forceinline__ float2 two(uint32_t c) {
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c & 0xffffu), __NV_E4M3);
-        return __half22float2(__half2(h));
-    }
-    static __device__ __forceinline__ uint32_t code(float a, float b) {
-        return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-    }
-    static __device__ __forceinline__ void load(const __nv_fp8_e4m3 *p, float (&v)[8]) {
-        const uint2 c = *reinterpret_cast<const uint2 *>(p);
-        float2 f = two(c.x);
-        v[0] = f.x; v[1] = f.y;
-        f = two(c.x >> 16);
-        v[2] = f.x; v[3] = f.y;
-        f = two(c.y);
-        v[4] = f.x; v[5] = f.y;
-        f = two(c.y >> 16);
-        v[6] = f.x; v[7] = f.y;
-    }
-    static __device__ __forceinline__ void store(__nv_fp8_e4m3 *p, const float (&v)[8]) {
-        *reinterpret_cast<uint2 *>(p) = make_uint2(code(v[0], v[1]) | code(v[2], v[3]) << 16,
-                                                   code(v[4], v[5]) | code(v[6], v[7]) << 16);
-    }
+    uint2 c;
+    __device__ __forceinline__ void load(const __nv_fp8_e4m3 *p) { c = *reinterpret_cast<const uint2 *>(p); }
+    __device__ __forceinline__ void store(__nv_fp8_e4m3 *p) const { *reinterpret_cast<uint2 *>(p) = c; }
 };
-
-// n of the lane's eight elements (all: a vector where the tensor allows it)
-template <typename T>
-__device__ __forceinline__ void load8(const T *p, int n, bool vec, float (&v)[8]) {
-    if (vec && n == 8) {
-        Eight<T>::load(p, v);
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < n ? (float)p[i] : 0.f;
+__device__ __forceinline__ float2 pair_of(uint32_t a, uint32_t b) {
+    return make_float2(__uint_as_float(a), __uint_as_float(b));
 }
-template <typename T>
-__device__ __forceinline__ void store8(T *p, int n, bool vec, const float (&v)[8]) {
-    if (vec && n == 8) {
-        Eight<T>::store(p, v);
-        return;
-    }
+__device__ __forceinline__ void unpack(const Eight<float> &e, float2 (&v)[4]) {
+    v[0] = pair_of(e.c.x, e.c.y);
+    v[1] = pair_of(e.c.z, e.c.w);
+    v[2] = pair_of(e.d.x, e.d.y);
+    v[3] = pair_of(e.d.z, e.d.w);
+}
+__device__ __forceinline__ void unpack(const Eight<__nv_bfloat16> &e, float2 (&v)[4]) {
+    const uint32_t w[4] = {e.c.x, e.c.y, e.c.z, e.c.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < n) p[i] = T(v[i]);
+    for (int i = 0; i < 4; ++i) v[i] = pair_of(w[i] << 16, w[i] & 0xffff0000u);
+}
+__device__ __forceinline__ float2 e4m3_pair(uint32_t c) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c & 0xffffu), __NV_E4M3);
+    return __half22float2(__half2(h));
+}
+__device__ __forceinline__ void unpack(const Eight<__nv_fp8_e4m3> &e, float2 (&v)[4]) {
+    v[0] = e4m3_pair(e.c.x);
+    v[1] = e4m3_pair(e.c.x >> 16);
+    v[2] = e4m3_pair(e.c.y);
+    v[3] = e4m3_pair(e.c.y >> 16);
+}
+__device__ __forceinline__ void pack(const float2 (&v)[4], Eight<float> *e) {
+    e->c = make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x),
+                      __float_as_uint(v[1].y));
+    e->d = make_uint4(__float_as_uint(v[2].x), __float_as_uint(v[2].y), __float_as_uint(v[3].x),
+                      __float_as_uint(v[3].y));
+}
+__device__ __forceinline__ void pack(const float2 (&v)[4], Eight<__nv_bfloat16> *e) {
+    __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&e->c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[i].x, v[i].y);
+}
+__device__ __forceinline__ uint32_t e4m3_code(float2 a, float2 b) {
+    return (uint32_t)__nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3) |
+           (uint32_t)__nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3) << 16;
+}
+__device__ __forceinline__ void pack(const float2 (&v)[4], Eight<__nv_fp8_e4m3> *e) {
+    e->c = make_uint2(e4m3_code(v[0], v[1]), e4m3_code(v[2], v[3]));
+}
+
+// ... n of them, an element at a time (0 for the others: the zero of every type)
+template <typename T> struct Bits;
+template <> struct Bits<float> { using U = uint32_t; };
+template <> struct Bits<__nv_bfloat16> { using U = uint16_t; };
+template <> struct Bits<__nv_fp8_e4m3> { using U = uint8_t; };
+template <typename T> __device__ __forceinline__ uint32_t some_word(const T *p, int n, int w) {
+    using U = typename Bits<T>::U;
+    constexpr int kIn = 4 / sizeof(T);
+    const U *q = reinterpret_cast<const U *>(p);
+    uint32_t x = 0u;
+#pragma unroll
+    for (int j = 0; j < kIn; ++j)
+        if (w * kIn + j < n) x |= (uint32_t)q[w * kIn + j] << (8 * sizeof(T) * j);
+    return x;
+}
+template <typename T> __device__ __forceinline__ void put_word(T *p, int n, int w, uint32_t x) {
+    using U = typename Bits<T>::U;
+    constexpr int kIn = 4 / sizeof(T);
+    U *q = reinterpret_cast<U *>(p);
+#pragma unroll
+    for (int j = 0; j < kIn; ++j)
+        if (w * kIn + j < n) q[w * kIn + j] = (U)(x >> (8 * sizeof(T) * j));
+}
+template <typename T> __device__ __forceinline__ void load_some(const T *p, int n, Eight<T> *e) {
+    e->c.x = some_word(p, n, 0);
+    e->c.y = some_word(p, n, 1);
+    if constexpr (sizeof(T) > 1) {
+        e->c.z = some_word(p, n, 2);
+        e->c.w = some_word(p, n, 3);
+    }
+    if constexpr (sizeof(T) == 4)
+        e->d = make_uint4(some_word(p, n, 4), some_word(p, n, 5), some_word(p, n, 6), some_word(p, n, 7));
+}
+template <typename T> __device__ __forceinline__ void store_some(T *p, int n, const Eight<T> &e) {
+    put_word(p, n, 0, e.c.x);
+    put_word(p, n, 1, e.c.y);
+    if constexpr (sizeof(T) > 1) {
+        put_word(p, n, 2, e.c.z);
+        put_word(p, n, 3, e.c.w);
+    }
+    if constexpr (sizeof(T) == 4) {
+        put_word(p, n, 4, e.d.x);
+        put_word(p, n, 5, e.d.y);
+        put_word(p, n, 6, e.d.z);
+        put_word(p, n, 7, e.d.w);
+    }
 }
 
 // 2^(e - 7) and its reciprocal for a block whose largest magnitude has these bits
@@ -168,110 +249,189 @@ __device__ __forceinline__ float scale_of(uint32_t largest, float *inverse) {
     return __uint_as_float(e << 23);
 }
 
+// 16 random bits (of a root: the high ones; else bits 8 to 23) as a float's bits in
+// [1, 2), in the middle of their step.
+template <bool ROOT> __device__ __forceinline__ uint32_t fraction(uint32_t u) {
+    return ((u >> (ROOT ? 9 : 1)) & 0x7FFF80u) | 0x3F800040u;
+}
+
 // A block's states to 8 bits, in place.  x: 0 beyond the tensor's end; u: the elements'
 // random bits.  ROOT: the roots, no positive one of which becomes zero.
 template <bool ROOT>
-__device__ __forceinline__ float quantise(float (&x)[8], uint32_t largest, const uint32_t (&u)[8]) {
+__device__ __forceinline__ float quantise(float2 (&x)[4], uint32_t largest, const uint32_t (&u)[8]) {
     float inv;
     const float scale = scale_of(largest, &inv);
     if (largest >= 0x7f800000u) {  // uniform: a NaN or an infinity in the block
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] *= inv;
+        for (int i = 0; i < 4; ++i) x[i] = mul2(x[i], two(inv));
         return scale;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t r = ROOT ? ((u[i] >> 12) & 0xFFFF0u) | 8u : ((u[i] >> 4) & 0xFFFF0u) | 8u;
-        const float y = to_e4m3(x[i] * inv, r);
-        x[i] = ROOT && x[i] > 0.f ? fmaxf(y, 0x1p-9f) : y;
+    for (int i = 0; i < 4; ++i) {
+        const float2 y = mul2(x[i], two(inv));
+        // to a neighbouring e4m3 value (|y| <= 256).  power: 2^e <= |y|, at least 2^-6, below
+        // which the steps are those from there up: a step is power / 8.  A random part
+        // of a step in (-1/2, 1/2), of 16 bits, is added, and the sum rounded to
+        // steps by adding and taking away 1.5 * 2^23 of them.
+        const float2 power = make_float2(
+            fmaxf(__uint_as_float(__float_as_uint(y.x) & 0x7f800000u), 0x1p-6f),
+            fmaxf(__uint_as_float(__float_as_uint(y.y) & 0x7f800000u), 0x1p-6f));
+        const float2 f = pair_of(fraction<ROOT>(u[2 * i]), fraction<ROOT>(u[2 * i + 1]));  // [1, 2)
+        const float2 magic = mul2(power, two(1.5f * 0x1p20f));
+        const float2 step = mul2(power, two(0x1p-3f));
+        const float2 shifted = fma2(step, two(-1.5f), y);
+        float2 q = add2(fma2(f, step, shifted), magic);
+        q = fma2(magic, two(-1.f), q);
+        if (ROOT) {  // (2^-9 if y is not 0)
+            const float2 least = make_float2(__saturatef(y.x * 0x1p126f), __saturatef(y.y * 0x1p126f));
+            const float2 l = mul2(least, two(0x1p-9f));
+            q = make_float2(fmaxf(q.x, l.x), fmaxf(q.y, l.y));
+        }
+        x[i] = q;
     }
     return scale;
 }
 
-// One block of 256 elements by a warp.
-template <typename TP, typename TG, bool MASTER, bool SMALL>
-__device__ __forceinline__ void step_block(const Entry &t, const Step &s, const moe_adamw_scalars_t &sc,
-                                           float coef, int64_t block) {
+// What a lane reads of a block of 256 elements.
+template <typename TP, typename TG, bool SMALL> struct Block {
     using TS = std::conditional_t<SMALL, __nv_fp8_e4m3, float>;
+    Eight<TP> p;
+    Eight<TG> g;
+    Eight<TS> m, v;
+};
+
+// The blocks b, b + kWarps, ... before `last` of a tensor, by a warp.  TP: the
+// stepped parameter's type (a master copy's: fp32).
+template <typename TP, typename TG, bool MASTER, bool SMALL>
+__device__ __forceinline__ void step_chunk(const Entry &t, const Step &s, const moe_adamw_scalars_t &sc,
+                                           float coef, int64_t first, int64_t last) {
+    using B = Block<TP, TG, SMALL>;
+    using TS = typename B::TS;
     const int lane = threadIdx.x & 31;
-    const int64_t at = block * kBlock + 8 * lane;
-    const int n = (int)max((int64_t)0, min((int64_t)8, t.numel - at));
-    const bool vec = t.vec;
-    float p[8], g[8], m[8], v[8];
-    if constexpr (MASTER) load8(t.master + at, n, vec, p);
-    else load8(static_cast<const TP *>(t.p) + at, n, vec, p);
-    load8(static_cast<const TG *>(t.g) + at, n, vec, g);
-    load8(static_cast<const TS *>(t.m) + at, n, vec, m);
-    load8(static_cast<const TS *>(t.v) + at, n, vec, v);
+    int64_t b = first + (threadIdx.x >> 5);
+    if (b >= last) return;
+    TP *const stepped = MASTER ? reinterpret_cast<TP *>(t.master) : static_cast<TP *>(t.p);
     const float decay = fmaf(-sc.lr, t.wd, 1.f);
-    if constexpr (SMALL) {
-        const float ms = t.ms[block], rs = t.rs[block];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            m[i] *= ms;
-            const float r = v[i] * rs;
-            v[i] = __fmul_rn(r, r);
-        }
+    const bool round_p = sizeof(TP) == 2 && s.stochastic;
+    // the key and the scales of block b + i kWarps, in lane i (a scale that each block
+    // waited for itself cost a round to memory: 187 us to X for 64 M bf16 parameters)
+    const int64_t mine = b + lane * kWarps;
+    float ms = 0.f, rs = 0.f;
+    if (SMALL && mine < last) {
+        ms = t.ms[mine];
+        rs = t.rs[mine];
     }
-    uint32_t top_m = 0u;
-    float r[8], top_v = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float gi = g[i] * coef;
-        m[i] = __fadd_rn(__fmul_rn(m[i], s.b1), __fmul_rn(gi, s.c1));
-        v[i] = __fadd_rn(__fmul_rn(v[i], s.b2), __fmul_rn(__fmul_rn(gi, gi), s.c2));
-        r[i] = __fsqrt_rn(v[i]);
-        p[i] = fmaf(-sc.step_size, __fdividef(m[i], fmaf(r[i], sc.inv_sqrt_bc2, s.eps)), p[i] * decay);
-        if constexpr (SMALL) {
-            top_m = max(top_m, __float_as_uint(m[i]) & 0x7fffffffu);
-            top_v = v[i] > top_v || isnan(v[i]) ? v[i] : top_v;
-        }
-    }
-    Key key = {0u, 0u};
-    uint32_t u[8];
-    const bool round = SMALL || (sizeof(TP) == 2 && !MASTER && s.stochastic);
-    if (round) {
-        key = block_key(t.block0 + block, sc.seed_lo, sc.seed_hi);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) u[i] = random_bits(key, 8 * lane + i);
-    }
-    if constexpr (MASTER) store8(t.master + at, n, vec, p);
-    if (sizeof(TP) == 2 && !MASTER && s.stochastic) {
-        uint16_t *o = static_cast<uint16_t *>(t.p) + at;
-        if (vec && n == 8) {
-            uint32_t h[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) h[i] = bf16_bits(p[i], u[i]);
-            stg16(o, make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16,
-                                h[6] | h[7] << 16));
+    Key keys = {0u, 0u};
+    if (SMALL || round_p) keys = block_key(t.block0 + b + lane * kWarps, sc.seed_lo, sc.seed_hi);
+
+    // (whole: vectors)
+    auto fetch = [&](B &r, int64_t block, bool whole) {
+        const int64_t at = block * kBlock + 8 * lane;
+        if (whole) {
+            r.p.load(stepped + at);
+            r.g.load(static_cast<const TG *>(t.g) + at);
+            r.m.load(static_cast<const TS *>(t.m) + at);
+            r.v.load(static_cast<const TS *>(t.v) + at);
         } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < n) o[i] = (uint16_t)bf16_bits(p[i], u[i]);
+            const int n = (int)max((int64_t)0, min((int64_t)8, t.numel - at));
+            load_some(stepped + at, n, &r.p);
+            load_some(static_cast<const TG *>(t.g) + at, n, &r.g);
+            load_some(static_cast<const TS *>(t.m) + at, n, &r.m);
+            load_some(static_cast<const TS *>(t.v) + at, n, &r.v);
         }
-    } else {
-        store8(static_cast<TP *>(t.p) + at, n, vec, p);
+    };
+    const int64_t full = t.vec ? t.numel / kBlock : 0;
+    for (int i = 0; b < last; ++i, b += kWarps) {
+        B now;
+        fetch(now, b, b < full);
+
+        float2 p[4], g[4], m[4], v[4], r[4];
+        unpack(now.p, p);
+        unpack(now.g, g);
+        unpack(now.m, m);
+        unpack(now.v, v);
+        if constexpr (SMALL) {
+            const float old_ms = __shfl_sync(kAll, ms, i), old_rs = __shfl_sync(kAll, rs, i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                m[j] = mul2(m[j], two(old_ms));
+                v[j] = mul2(v[j], two(old_rs));
+                v[j] = mul2(v[j], v[j]);
+            }
+        }
+        float top_m = 0.f, top_v = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 gj = mul2(g[j], two(coef));
+            m[j] = add2(mul2(m[j], two(s.b1)), mul2(gj, two(s.c1)));
+            v[j] = add2(mul2(v[j], two(s.b2)), mul2(mul2(gj, gj), two(s.c2)));
+            r[j] = make_float2(root<SMALL>(v[j].x), root<SMALL>(v[j].y));
+            const float2 d = fma2(r[j], two(sc.inv_sqrt_bc2), two(s.eps));
+            const float2 q = mul2(m[j], make_float2(reciprocal(d.x), reciprocal(d.y)));
+            p[j] = fma2(two(-sc.step_size), q, mul2(p[j], two(decay)));
+            if constexpr (SMALL) {
+                top_m = max_abs(top_m, m[j].x, m[j].y);
+                top_v = max_abs(top_v, v[j].x, v[j].y);
+            }
+        }
+        uint32_t u[8];
+        if (SMALL || round_p) {
+            const Key key = {__shfl_sync(kAll, keys.x, i), __shfl_sync(kAll, keys.y, i)};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) u[j] = random_bits(key, 8 * lane + j);
+        }
+        Eight<TP> op;
+        if constexpr (sizeof(TP) == 2) {
+            if (round_p)
+                op.c = make_uint4(bf16_pair(p[0], u[0], u[1]), bf16_pair(p[1], u[2], u[3]),
+                                  bf16_pair(p[2], u[4], u[5]), bf16_pair(p[3], u[6], u[7]));
+            else
+                pack(p, &op);
+        } else {
+            pack(p, &op);
+        }
+        Eight<__nv_bfloat16> copy;  // MASTER
+        if constexpr (MASTER) pack(p, &copy);
+        if constexpr (SMALL) {
+            const uint32_t largest_m = __reduce_max_sync(kAll, __float_as_uint(top_m));
+            // (the root's order is its square's; correctly rounded, for its last bit)
+            const uint32_t largest_v = __reduce_max_sync(kAll, __float_as_uint(top_v));
+            const uint32_t largest_r = __float_as_uint(__fsqrt_rn(__uint_as_float(largest_v))) & 0x7fffffffu;
+            const float new_ms = quantise<false>(m, largest_m, u);
+            const float new_rs = quantise<true>(r, largest_r, u);
+            if (lane == i) {
+                ms = new_ms;
+                rs = new_rs;
+            }
+        }
+        Eight<TS> om, ov;
+        pack(m, &om);
+        if constexpr (SMALL) pack(r, &ov);
+        else pack(v, &ov);
+        const int64_t at = b * kBlock + 8 * lane;
+        if (b < full) {
+            op.store(stepped + at);
+            if constexpr (MASTER) copy.store(static_cast<__nv_bfloat16 *>(t.p) + at);
+            om.store(static_cast<TS *>(t.m) + at);
+            ov.store(static_cast<TS *>(t.v) + at);
+        } else {
+            const int n = (int)max((int64_t)0, min((int64_t)8, t.numel - at));
+            store_some(stepped + at, n, op);
+            if constexpr (MASTER) store_some(static_cast<__nv_bfloat16 *>(t.p) + at, n, copy);
+            store_some(static_cast<TS *>(t.m) + at, n, om);
+            store_some(static_cast<TS *>(t.v) + at, n, ov);
+        }
     }
     if constexpr (SMALL) {
-        top_m = __reduce_max_sync(kAll, top_m);
-        // (the root's order is its square's)
-        const uint32_t top_r = __reduce_max_sync(kAll, __float_as_uint(__fsqrt_rn(top_v)) & 0x7fffffffu);
-        const float ms = quantise<false>(m, top_m, u);
-        const float rs = quantise<true>(r, top_r, u);
-        store8(static_cast<TS *>(t.m) + at, n, vec, m);
-        store8(static_cast<TS *>(t.v) + at, n, vec, r);
-        if (lane == 0) {
-            t.ms[block] = ms;
-            t.rs[block] = rs;
+        if (mine < last) {
+            t.ms[mine] = ms;
+            t.rs[mine] = rs;
         }
-    } else {
-        store8(static_cast<float *>(t.m) + at, n, vec, m);
-        store8(static_cast<float *>(t.v) + at, n, vec, v);
     }
 }
 
 template <bool SMALL>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, SMALL ? 4 : 3)
 adamw_kernel(const __grid_constant__ Table tab, const __grid_constant__ Step s) {
     pdl_wait();
     const moe_adamw_scalars_t sc = s.dev ? *s.dev : s.sc;
@@ -282,7 +442,6 @@ adamw_kernel(const __grid_constant__ Table tab, const __grid_constant__ Step s) 
         coef = s.max_norm / (norm + 1e-6f);
         coef = coef > 1.f ? 1.f : coef;  // a NaN norm stays NaN
     }
-    const int wid = threadIdx.x >> 5;
     for (int c = blockIdx.x; c < tab.chunks; c += gridDim.x) {
         int lo = 0, hi = tab.n - 1;
         if (tab.mapped) lo = hi = tab.tensor_of[c];
@@ -292,26 +451,23 @@ adamw_kernel(const __grid_constant__ Table tab, const __grid_constant__ Step s) 
         }
         const Entry &t = tab.t[lo];
         const int64_t blocks = (t.numel + kBlock - 1) / kBlock;
-        const int64_t all = (t.numel + kChunk - 1) / kChunk;
-        const int64_t first = (c - (t.end - all)) * (kChunk / kBlock);
-        const int64_t last = min(blocks, first + kChunk / kBlock);
-        const int kind = t.p_bf16 ? (t.master ? 2 : 1) : 0;
-        for (int64_t b = first + wid; b < last; b += kWarps) {
-            if (kind == 0) {
-                if (t.g_bf16) step_block<float, __nv_bfloat16, false, SMALL>(t, s, sc, coef, b);
-                else step_block<float, float, false, SMALL>(t, s, sc, coef, b);
-            } else if (kind == 1) {
-                if (t.g_bf16) step_block<__nv_bfloat16, __nv_bfloat16, false, SMALL>(t, s, sc, coef, b);
-                else step_block<__nv_bfloat16, float, false, SMALL>(t, s, sc, coef, b);
-            } else {
-                if (t.g_bf16) step_block<__nv_bfloat16, __nv_bfloat16, true, SMALL>(t, s, sc, coef, b);
-                else step_block<__nv_bfloat16, float, true, SMALL>(t, s, sc, coef, b);
-            }
+        const int64_t all = (blocks + tab.chunk_blocks - 1) / tab.chunk_blocks;
+        const int64_t first = (c - (t.end - all)) * tab.chunk_blocks;
+        const int64_t last = min(blocks, first + tab.chunk_blocks);
+        if (!t.p_bf16) {
+            if (t.g_bf16) step_chunk<float, __nv_bfloat16, false, SMALL>(t, s, sc, coef, first, last);
+            else step_chunk<float, float, false, SMALL>(t, s, sc, coef, first, last);
+        } else if (!t.master) {
+            if (t.g_bf16) step_chunk<__nv_bfloat16, __nv_bfloat16, false, SMALL>(t, s, sc, coef, first, last);
+            else step_chunk<__nv_bfloat16, float, false, SMALL>(t, s, sc, coef, first, last);
+        } else {
+            if (t.g_bf16) step_chunk<float, __nv_bfloat16, true, SMALL>(t, s, sc, coef, first, last);
+            else step_chunk<float, float, true, SMALL>(t, s, sc, coef, first, last);
         }
     }
 }
 
-int64_t chunks_of(int64_t numel) { return (numel + kChunk - 1) / kChunk; }
+int64_t blocks_of(int64_t numel) { return (numel + kBlock - 1) / kBlock; }
 
 bool vectors(const moe_adamw_tensor_t &t) {
     const uintptr_t all = reinterpret_cast<uintptr_t>(t.param) | reinterpret_cast<uintptr_t>(t.grad) |
@@ -323,7 +479,7 @@ bool vectors(const moe_adamw_tensor_t &t) {
 
 }  // namespace
 
-int64_t adamw_chunk() { return kChunk; }
+int64_t adamw_chunk() { return kWarps * kBlock; }
 
 cudaError_t launch_adamw(const moe_adamw_tensor_t *ts, int64_t n, const moe_adamw_scalars_t &sc,
                          const moe_adamw_scalars_t *dev, const moe_adamw_hyper_t &h,
@@ -341,6 +497,10 @@ cudaError_t launch_adamw(const moe_adamw_tensor_t *ts, int64_t n, const moe_adam
     s.dev = dev;
     s.norm = norm;
     Table tab;
+    int64_t blocks = 0;
+    for (int64_t i = 0; i < n; ++i) blocks += blocks_of(ts[i].numel);
+    tab.chunk_blocks = kWarps;
+    while (tab.chunk_blocks < kMostBlocks && blocks > kRounds * tab.chunk_blocks) tab.chunk_blocks *= 2;
     for (const bool small : {false, true}) {
         int64_t block0 = 0, i = 0;
         while (i < n) {
@@ -349,10 +509,10 @@ cudaError_t launch_adamw(const moe_adamw_tensor_t *ts, int64_t n, const moe_adam
             for (; i < n && tab.n < kTable; ++i) {
                 const moe_adamw_tensor_t &t = ts[i];
                 const int64_t first = block0;
-                block0 += (t.numel + kBlock - 1) / kBlock;
+                block0 += blocks_of(t.numel);
                 if (t.numel == 0 || (t.state_dtype == MOE_E4M3) != small) continue;
                 const int from = end;
-                end += (int)chunks_of(t.numel);
+                end += (int)((blocks_of(t.numel) + tab.chunk_blocks - 1) / tab.chunk_blocks);
                 for (int c = from; c < end && c < kMapped; ++c) tab.tensor_of[c] = (uint16_t)tab.n;
                 tab.t[tab.n++] = {t.param, t.grad, t.exp_avg, t.exp_avg_sq, t.exp_avg_scale,
                                   t.exp_avg_sq_scale, t.master, t.numel, first, end, t.weight_decay,
