@@ -632,7 +632,8 @@ moe_status_t moe_update_balance_bias(const int32_t *counts, int64_t layers, int3
  * (at least 2^-126).  They are rounded stochastically: a state's change of a few
  * percent of itself, or less, is far below a step of e4m3, and would be lost
  * whole by rounding to the nearest.  An r above 0 is stored as at least the
- * smallest code, so that no later step divides by eps alone.  (Zeros in all bytes
+ * smallest code, so that no later step divides by eps alone (a v below 2^-126
+ * counts as 0).  (Zeros in all bytes
  * and scales are valid initial states of either kind.)
  * A block with a NaN or an infinity keeps NaN and the format's largest value
  * for those elements.

@@ -242,11 +242,16 @@ template <typename T> __device__ __forceinline__ void store_some(T *p, int n, co
     }
 }
 
-// 2^(e - 7) and its reciprocal for a block whose largest magnitude has these bits
-__device__ __forceinline__ float scale_of(uint32_t largest, float *inverse) {
-    const uint32_t e = max((largest >> 23) & 0xffu, 8u) - 7u;  // biased; at least 2^-126
-    *inverse = __uint_as_float((254u - e) << 23);
-    return __uint_as_float(e << 23);
+// The biased exponent of 2^(e - 7), at least that of 2^-126, for a block whose largest
+// magnitude has these bits; and for the roots of one whose largest value has.
+__device__ __forceinline__ uint32_t scale_exponent(uint32_t largest) {
+    return max(largest >> 23, 8u) - 7u;
+}
+__device__ __forceinline__ uint32_t root_scale_exponent(uint32_t largest) {
+    // half of v's exponent, rounded down; just below an even power the root, rounded
+    // to the nearest, is the next one.  (Below 2^-126 the roots are 0.)
+    const int e = (int)((largest + 1u) >> 23) - 127;
+    return largest < 0x00800000u ? 1u : (uint32_t)((e >> 1) + 127 - 7);
 }
 
 // 16 random bits (of a root: the high ones; else bits 8 to 23) as a float's bits in
@@ -255,13 +260,13 @@ template <bool ROOT> __device__ __forceinline__ uint32_t fraction(uint32_t u) {
     return ((u >> (ROOT ? 9 : 1)) & 0x7FFF80u) | 0x3F800040u;
 }
 
-// A block's states to 8 bits, in place.  x: 0 beyond the tensor's end; u: the elements'
-// random bits.  ROOT: the roots, no positive one of which becomes zero.
+// A block's states to 8 bits, in place, by a scale of biased exponent e.  x: 0 beyond
+// the tensor's end; u: the elements' random bits.  ROOT: the roots, no positive one
+// of which becomes zero.
 template <bool ROOT>
-__device__ __forceinline__ float quantise(float2 (&x)[4], uint32_t largest, const uint32_t (&u)[8]) {
-    float inv;
-    const float scale = scale_of(largest, &inv);
-    if (largest >= 0x7f800000u) {  // uniform: a NaN or an infinity in the block
+__device__ __forceinline__ float quantise(float2 (&x)[4], uint32_t e, bool finite, const uint32_t (&u)[8]) {
+    const float inv = __uint_as_float((254u - e) << 23), scale = __uint_as_float(e << 23);
+    if (!finite) {  // uniform: a NaN or an infinity in the block
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[i] = mul2(x[i], two(inv));
         return scale;
@@ -272,16 +277,16 @@ __device__ __forceinline__ float quantise(float2 (&x)[4], uint32_t largest, cons
         // to a neighbouring e4m3 value (|y| <= 256).  power: 2^e <= |y|, at least 2^-6, below
         // which the steps are those from there up: a step is power / 8.  A random part
         // of a step in (-1/2, 1/2), of 16 bits, is added, and the sum rounded to
-        // steps by adding and taking away 1.5 * 2^23 of them.
+        // steps by adding and taking away 1.5 * 2^23 of them.  (Four packed operations;
+        // by integer sums on the bits it took seven or eight of the ALU, which is
+        // what bounds this kernel.)
         const float2 power = make_float2(
             fmaxf(__uint_as_float(__float_as_uint(y.x) & 0x7f800000u), 0x1p-6f),
             fmaxf(__uint_as_float(__float_as_uint(y.y) & 0x7f800000u), 0x1p-6f));
         const float2 f = pair_of(fraction<ROOT>(u[2 * i]), fraction<ROOT>(u[2 * i + 1]));  // [1, 2)
-        const float2 magic = mul2(power, two(1.5f * 0x1p20f));
-        const float2 step = mul2(power, two(0x1p-3f));
-        const float2 shifted = fma2(step, two(-1.5f), y);
-        float2 q = add2(fma2(f, step, shifted), magic);
-        q = fma2(magic, two(-1.f), q);
+        const float2 part = fma2(f, two(0x1p-3f), two(-1.5f * 0x1p-3f));
+        const float2 sum = fma2(power, two(1.5f * 0x1p20f), fma2(part, power, y));
+        float2 q = fma2(power, two(-1.5f * 0x1p20f), sum);
         if (ROOT) {  // (2^-9 if y is not 0)
             const float2 least = make_float2(__saturatef(y.x * 0x1p126f), __saturatef(y.y * 0x1p126f));
             const float2 l = mul2(least, two(0x1p-9f));
@@ -394,11 +399,9 @@ __device__ __forceinline__ void step_chunk(const Entry &t, const Step &s, const 
         if constexpr (MASTER) pack(p, &copy);
         if constexpr (SMALL) {
             const uint32_t largest_m = __reduce_max_sync(kAll, __float_as_uint(top_m));
-            // (the root's order is its square's; correctly rounded, for its last bit)
             const uint32_t largest_v = __reduce_max_sync(kAll, __float_as_uint(top_v));
-            const uint32_t largest_r = __float_as_uint(__fsqrt_rn(__uint_as_float(largest_v))) & 0x7fffffffu;
-            const float new_ms = quantise<false>(m, largest_m, u);
-            const float new_rs = quantise<true>(r, largest_r, u);
+            const float new_ms = quantise<false>(m, scale_exponent(largest_m), largest_m < 0x7f800000u, u);
+            const float new_rs = quantise<true>(r, root_scale_exponent(largest_v), largest_v < 0x7f800000u, u);
             if (lane == i) {
                 ms = new_ms;
                 rs = new_rs;
