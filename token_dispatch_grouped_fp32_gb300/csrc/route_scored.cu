@@ -618,10 +618,12 @@ template <int VPL> cudaError_t launch_select_v(const SelectArgs &a, bool exact, 
 //   softmax:                dl[e]     = s_e (c g_e - S),  g_e = d_j where e = idx_j
 //   sigmoid, renormalised:  dl[idx_j] = w_j (d_j - S/c) (1 - s_j)
 //   sigmoid:                dl[idx_j] = w_j d_j (1 - s_j)
-// with S = sum_j w_j d_j.  A warp per token: its row's chosen entries in shared
-// memory, zero elsewhere, then written whole.  VEC: four columns a lane.
+// with S = sum_j w_j d_j.  LANES lanes per token: its row's chosen entries in shared
+// memory, zero elsewhere, then written whole, W columns a lane at a time (four where
+// E allows it).  The fewer lanes a token, the fewer steps its sums take; with
+// eight columns a lane T = 131072, E = 128 (softmax, all logits) takes 16 lanes, X us against
+// 34.7 with 32, bound by HBM.
 constexpr int kGradThreads = 256;
-constexpr int kGradWarps = kGradThreads / 32;
 
 struct GradArgs {
     const float *logits;
@@ -633,112 +635,132 @@ struct GradArgs {
     float *dl;
 };
 
-// DENSE: softmax that is not renormalised; NV: its columns a lane, as float4s or floats
-template <bool DENSE, bool VEC, int NV>
+template <int LANES> __device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+    for (int o = LANES / 2; o >= 1; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    return v;
+}
+
+template <int W> struct Columns;
+template <> struct Columns<4> { using V = float4; };
+template <> struct Columns<1> { using V = float; };
+
+// DENSE: softmax that is not renormalised, N times W columns a lane
+template <bool DENSE, int W, int LANES, int N>
 __global__ void __launch_bounds__(kGradThreads)
 logits_grad_kernel(const GradArgs a, DevStatus ds) {
     pdl_wait();
+    using V = typename Columns<W>::V;
     extern __shared__ __align__(16) float rows[];
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, E = a.E;
+    const int E = a.E, l = threadIdx.x % LANES, own = threadIdx.x / LANES;
     const int stride = (E + 3) & ~3;
-    float *row = rows + wid * stride;
-    for (int e = lane; e < stride; e += 32) row[e] = 0.f;
-    __syncwarp();
-    const int64_t t = (int64_t)blockIdx.x * kGradWarps + wid;
-    if (t >= a.T) return;
+    const int64_t t = (int64_t)blockIdx.x * (kGradThreads / LANES) + own;
+    const bool there = t < a.T;
+    float *row = rows + own * stride;
+    for (int c = W * l; c < E; c += W * LANES)
+#pragma unroll
+        for (int i = 0; i < W; ++i) row[c + i] = 0.f;
     const float *L = a.logits + t * E;
     float *o = a.dl + t * E;
-    int e = -1;
-    float wj = 0.f, dj = 0.f;
-    if (lane < a.k) {
-        e = a.idx[t * a.k + lane];
-        wj = a.w[t * a.k + lane];
-        dj = a.dw[t * a.k + lane];
-        if ((unsigned)e >= (unsigned)E) {
-            raise_error(ds, kErrBadRouting);
-            e = -1;
-            wj = dj = 0.f;
+    // the logits first: nothing waits for them but the last sums
+    float v[N][W];
+    if constexpr (DENSE) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int c = (l + LANES * n) * W;
+            if (there && c < E) {
+                *reinterpret_cast<V *>(v[n]) = *reinterpret_cast<const V *>(L + c);
+            } else {
+#pragma unroll
+                for (int i = 0; i < W; ++i) v[n][i] = -INFINITY;
+            }
         }
     }
-    const float S = warp_sum(wj * dj);
-    if constexpr (!DENSE) {
-        if (e >= 0) row[e] = a.f.chosen(wj, dj, S, a.f.sigmoid ? L[e] : 0.f);
-        __syncwarp();
-        if constexpr (VEC) {
-            for (int i = lane; i < E / 4; i += 32)
-                reinterpret_cast<float4 *>(o)[i] = reinterpret_cast<const float4 *>(row)[i];
-        } else {
-            for (int i = lane; i < E; i += 32) o[i] = row[i];
+    float S = 0.f;
+    int e[32 / LANES];  // this lane's slots l, l + LANES, ...
+    float wj[32 / LANES], dj[32 / LANES];
+#pragma unroll
+    for (int q = 0; q < 32 / LANES; ++q) {
+        const int j = l + LANES * q;
+        e[q] = -1;
+        wj[q] = dj[q] = 0.f;
+        if (there && j < a.k) {
+            e[q] = a.idx[t * a.k + j];
+            wj[q] = a.w[t * a.k + j];
+            dj[q] = a.dw[t * a.k + j];
+            if ((unsigned)e[q] >= (unsigned)E) {
+                raise_error(ds, kErrBadRouting);
+                e[q] = -1;
+                wj[q] = dj[q] = 0.f;
+            }
         }
+        S += wj[q] * dj[q];
+    }
+    S = lanes_sum<LANES>(S);
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < 32 / LANES; ++q)
+        if (e[q] >= 0)
+            row[e[q]] = DENSE ? a.f.scale * dj[q]
+                              : a.f.chosen(wj[q], dj[q], S, a.f.sigmoid ? L[e[q]] : 0.f);
+    __syncwarp();
+    if constexpr (!DENSE) {
+        if (there)
+            for (int c = W * l; c < E; c += W * LANES)
+                *reinterpret_cast<V *>(o + c) = *reinterpret_cast<const V *>(row + c);
     } else {
-        constexpr int W = VEC ? 4 : 1;
-        if (e >= 0) row[e] = a.f.scale * dj;
-        float v[NV][W];
         float m = -INFINITY, z = 0.f;
 #pragma unroll
-        for (int n = 0; n < NV; ++n) {
-            const int c = (lane + 32 * n) * W;
-            if constexpr (VEC) {
-                float4 x = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-                if (c < E) x = *reinterpret_cast<const float4 *>(L + c);
-                v[n][0] = x.x;
-                v[n][1] = x.y;
-                v[n][2] = x.z;
-                v[n][3] = x.w;
-            } else {
-                v[n][0] = c < E ? L[c] : -INFINITY;
-            }
+        for (int n = 0; n < N; ++n)
 #pragma unroll
             for (int i = 0; i < W; ++i) m = fmaxf(m, v[n][i]);
-        }
 #pragma unroll
-        for (int q = 16; q >= 1; q >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, q));
+        for (int q = LANES / 2; q >= 1; q >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, q));
+        if (m == -INFINITY) m = 0.f;  // all masked: exponentials of 0, and no scores
 #pragma unroll
-        for (int n = 0; n < NV; ++n)
+        for (int n = 0; n < N; ++n)
 #pragma unroll
             for (int i = 0; i < W; ++i) {
-                v[n][i] = m == -INFINITY ? 0.f : expf(v[n][i] - m);  // all masked: no scores
+                v[n][i] = exp2_fast((v[n][i] - m) * kLog2e);
                 z += v[n][i];
             }
-        z = warp_sum(z);
-        const float inv = m == -INFINITY ? 0.f : 1.f / z;
-        __syncwarp();
+        z = lanes_sum<LANES>(z);
+        const float inv = z > 0.f || isnan(z) ? 1.f / z : 0.f;
+        if (!there) return;
 #pragma unroll
-        for (int n = 0; n < NV; ++n) {
-            const int c = (lane + 32 * n) * W;
+        for (int n = 0; n < N; ++n) {
+            const int c = (l + LANES * n) * W;
             if (c >= E) continue;
-            if constexpr (VEC) {
-                const float4 g = *reinterpret_cast<const float4 *>(row + c);
-                *reinterpret_cast<float4 *>(o + c) =
-                    make_float4(v[n][0] * inv * (g.x - S), v[n][1] * inv * (g.y - S),
-                                v[n][2] * inv * (g.z - S), v[n][3] * inv * (g.w - S));
-            } else {
-                o[c] = v[n][0] * inv * (row[c] - S);
-            }
+            float g[W];
+            *reinterpret_cast<V *>(g) = *reinterpret_cast<const V *>(row + c);
+#pragma unroll
+            for (int i = 0; i < W; ++i) g[i] = v[n][i] * inv * (g[i] - S);
+            *reinterpret_cast<V *>(o + c) = *reinterpret_cast<const V *>(g);
         }
     }
 }
 
-template <bool DENSE, bool VEC, int NV>
+template <bool DENSE, int W, int LANES, int N>
 cudaError_t launch_grad(const GradArgs &a, const DevStatus &ds, cudaStream_t st) {
-    const dim3 grid((unsigned)((a.T + kGradWarps - 1) / kGradWarps));
-    const size_t smem = sizeof(float) * kGradWarps * (size_t)((a.E + 3) & ~3);
-    return launch_pdl(logits_grad_kernel<DENSE, VEC, NV>, grid, dim3(kGradThreads), smem, st, a, ds);
+    constexpr int kTokens = kGradThreads / LANES;
+    const dim3 grid((unsigned)((a.T + kTokens - 1) / kTokens));
+    const size_t smem = sizeof(float) * kTokens * (size_t)((a.E + 3) & ~3);
+    return launch_pdl(logits_grad_kernel<DENSE, W, LANES, N>, grid, dim3(kGradThreads), smem, st, a, ds);
 }
 
-template <bool VEC>
-cudaError_t launch_grad_any(const GradArgs &a, bool dense, const DevStatus &ds, cudaStream_t st) {
-    if (!dense) return launch_grad<false, VEC, 1>(a, ds, st);
-    const int n = (a.E + (VEC ? 127 : 31)) / (VEC ? 128 : 32);
-    if (n <= 1) return launch_grad<true, VEC, 1>(a, ds, st);
-    if (n <= 2) return launch_grad<true, VEC, 2>(a, ds, st);
-    if (n <= 4) return launch_grad<true, VEC, 4>(a, ds, st);
-    if (VEC || n <= 8) return launch_grad<true, VEC, 8>(a, ds, st);
-    if constexpr (!VEC) {
-        if (n <= 16) return launch_grad<true, VEC, 16>(a, ds, st);
-        return launch_grad<true, VEC, 32>(a, ds, st);
+template <bool DENSE> cudaError_t launch_grad_any(const GradArgs &a, const DevStatus &ds, cudaStream_t st) {
+    if (a.E % 4 == 0) {  // two float4 a lane, and from E = 257 on more
+        if (a.E <= 64) return launch_grad<DENSE, 4, 8, 2>(a, ds, st);
+        if (a.E <= 128) return launch_grad<DENSE, 4, 16, 2>(a, ds, st);
+        if (a.E <= 256 || !DENSE) return launch_grad<DENSE, 4, 32, 2>(a, ds, st);
+        if (a.E <= 512) return launch_grad<DENSE, 4, 32, 4>(a, ds, st);
+        return launch_grad<DENSE, 4, 32, 8>(a, ds, st);
     }
-    return cudaErrorInvalidValue;
+    if (a.E <= 64) return launch_grad<DENSE, 1, 8, 8>(a, ds, st);
+    if (a.E <= 128) return launch_grad<DENSE, 1, 16, 8>(a, ds, st);
+    if (a.E <= 256 || !DENSE) return launch_grad<DENSE, 1, 32, 8>(a, ds, st);
+    if (a.E <= 512) return launch_grad<DENSE, 1, 32, 16>(a, ds, st);
+    return launch_grad<DENSE, 1, 32, 32>(a, ds, st);
 }
 
 // ------------------------------ balance bias -------------------------------
@@ -829,8 +851,7 @@ cudaError_t launch_logits_grad(const Shape &s, const ScoreGrad &f, const float *
                                const int32_t *idx, const float *w, const float *dw, float *dlogits,
                                const DevStatus &ds, cudaStream_t st) {
     const GradArgs a = {logits, idx, w, dw, s.T, s.E, s.k, f, dlogits};
-    const cudaError_t e = (s.E & 3) == 0 ? launch_grad_any<true>(a, f.dense, ds, st)
-                                         : launch_grad_any<false>(a, f.dense, ds, st);
+    const cudaError_t e = f.dense ? launch_grad_any<true>(a, ds, st) : launch_grad_any<false>(a, ds, st);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
