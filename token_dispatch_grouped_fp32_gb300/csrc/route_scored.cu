@@ -600,6 +600,244 @@ select_kernel(const SelectArgs a, const __grid_constant__ SelectArgs cold) {
     }
 }
 
+// Long batches: LANES lanes a token, 32 / LANES tokens a warp, N float4 of values a
+// lane, k <= 8, no groups.  The same steps as above, at a fraction of the
+// instructions a token, since a step of a reduction, a vote or a rank serves all of a
+// warp's tokens: the bound from the maxima of half a lane's values each, candidates
+// counted and placed by a prefix sum over the lanes, and two or four of them a lane.
+constexpr int kManyK = 8, kManyFew = 32;
+
+struct Segment {  // a token's shared memory; 200 words apart: no bank conflicts
+    Ranked few[kManyFew];     // candidates, NaN behind them
+    Ranked sorted[kManyFew];  // by rank; NaN where equal values leave a gap
+    uint32_t pad[72];
+};
+static_assert(sizeof(Segment) % 128 == 32, "");
+
+template <int LANES, bool MAX> __device__ __forceinline__ float segment_all(float v) {
+#pragma unroll
+    for (int o = LANES / 2; o >= 1; o >>= 1) {
+        const float u = __shfl_xor_sync(kAll, v, o);
+        v = MAX ? fmaxf(v, u) : v + u;
+    }
+    return v;
+}
+
+template <int LANES, int N, bool EXACT>
+__global__ void __launch_bounds__(32, 24)
+select_many_kernel(const SelectArgs a, const __grid_constant__ SelectArgs cold) {
+    pdl_entry();
+    if (a.zero_word != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *a.zero_word = 0u;
+    extern __shared__ __align__(16) unsigned char smem[];
+    constexpr int kTokens = 32 / LANES, V = 4 * N;
+    const int lane = threadIdx.x, seg = lane / LANES, l = lane % LANES, E = a.E;
+    Segment &s = reinterpret_cast<Segment *>(smem)[seg];
+
+    const int64_t stride = (int64_t)gridDim.x * kTokens;
+    for (int64_t t0 = (int64_t)blockIdx.x * kTokens; t0 < a.T; t0 += LANES * stride) {
+        unsigned left = 0u;  // bit LANES * seg + i: token t0 + i * stride + seg
+        for (int i = 0; i < LANES; ++i) {
+            const int64_t t = t0 + i * stride + seg;
+            if (t - seg >= a.T) break;
+            const bool there = t < a.T;
+            float *L = a.logits + t * E;
+            float v[V];  // NaN: no expert
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                const int e = 4 * (l + LANES * n);
+                float4 x = make_float4(NAN, NAN, NAN, NAN);
+                if (there && e < E) {
+                    if (a.nparts > 0) {
+                        const float *p = a.partial + t * E + e;
+                        x = *reinterpret_cast<const float4 *>(p);
+                        for (int z = 1; z < a.nparts; ++z) {
+                            const float4 y = *reinterpret_cast<const float4 *>(p + z * a.T * E);
+                            x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+                        }
+                        if (a.logit_bias) {
+                            const float4 y = *reinterpret_cast<const float4 *>(a.logit_bias + e);
+                            x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+                        }
+                        *reinterpret_cast<float4 *>(L + e) = x;
+                    } else {
+                        x = *reinterpret_cast<const float4 *>(L + e);
+                    }
+                }
+                v[4 * n] = x.x;
+                v[4 * n + 1] = x.y;
+                v[4 * n + 2] = x.z;
+                v[4 * n + 3] = x.w;
+            }
+            __syncwarp();  // (the last token's shared memory as read)
+#pragma unroll
+            for (int c = 2 * l; c < kManyFew; c += 2 * LANES) {
+                const float4 none = make_float4(NAN, 0.f, NAN, 0.f);
+                *reinterpret_cast<float4 *>(s.few + c) = none;
+                *reinterpret_cast<float4 *>(s.sorted + c) = none;
+            }
+
+            float m = -INFINITY, z = 1.f;
+            if (!a.sigmoid && (!EXACT || !a.renorm)) {
+                float top = v[0];
+#pragma unroll
+                for (int j = 1; j < V; ++j) top = fmaxf(top, v[j]);
+                top = segment_all<LANES, true>(top);
+                if (!isnan(top)) m = top;
+                z = 0.f;
+#pragma unroll
+                for (int n = 0; n < N; ++n)
+                    if (4 * (l + LANES * n) < E)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) z += exp2_fast((v[4 * n + j] - m) * kLog2e);
+                z = segment_all<LANES, false>(z);
+            }
+            if constexpr (!EXACT) {
+                if (a.sigmoid) {
+#pragma unroll
+                    for (int j = 0; j < V; ++j) v[j] = score32(v[j], true, 0.f, 0.f);
+                } else {
+                    const float inv = rcp_fast(z);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) v[j] = exp2_fast((v[j] - m) * kLog2e) * inv;
+                }
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    const int e = 4 * (l + LANES * n);
+                    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (e < E) x = __ldg(reinterpret_cast<const float4 *>(a.bias + e));
+                    v[4 * n] += x.x;
+                    v[4 * n + 1] += x.y;
+                    v[4 * n + 2] += x.z;
+                    v[4 * n + 3] += x.w;
+                }
+            }
+            const float unit = EXACT ? 0.f : unit_of(a.sigmoid, V, z);
+
+            float b0 = v[0], b1 = v[V / 2], bound = NAN;
+#pragma unroll
+            for (int j = 1; j < V / 2; ++j) {
+                b0 = fmaxf(b0, v[j]);
+                b1 = fmaxf(b1, v[V / 2 + j]);
+            }
+#pragma unroll
+            for (int j = 0; j < kManyK; ++j) {
+                if (j >= a.k) break;
+                bound = segment_all<LANES, true>(fmaxf(b0, b1));
+                if (b0 == bound) b0 = NAN;
+                if (b1 == bound) b1 = NAN;
+            }
+            if (isnan(bound)) bound = -INFINITY;
+            const float floor32 = EXACT ? bound : bound - (unit + 0x1p-21f * fabsf(bound));
+            int mine = 0;
+#pragma unroll
+            for (int j = 0; j < V; ++j) mine += v[j] >= floor32;
+            int upto = mine;  // with the lanes below
+#pragma unroll
+            for (int o = 1; o < LANES; o <<= 1) {
+                const int u = __shfl_up_sync(kAll, upto, o, LANES);
+                if (l >= o) upto += u;
+            }
+            const int n = __shfl_sync(kAll, upto, LANES - 1, LANES);
+            int at = upto - mine;
+            __syncwarp();
+            if (n <= kManyFew) {
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    if (v[j] >= floor32) s.few[at++] = {v[j], 4 * (l + LANES * (j / 4)) + j % 4};
+            }
+            __syncwarp();
+            // ranks, by the values behind each: by the sign of a difference, two a packed sum
+            constexpr int kHold = kManyFew / LANES;  // candidates a lane: 4, or 2
+            Ranked c[kHold];
+            int behind[kHold];
+#pragma unroll
+            for (int j = 0; j < kHold; ++j) {
+                c[j] = s.few[l + LANES * j];
+                behind[j] = 0;
+            }
+            auto rank = [&](int p, int j) {
+                const float4 x = *reinterpret_cast<const float4 *>(s.few + p);  // (q, id) twice
+                const float2 d = add2(make_float2(x.x, x.z), make_float2(-c[j].q, -c[j].q));
+                behind[j] += (int)(__float_as_uint(d.x) >> 31) + (int)(__float_as_uint(d.y) >> 31);
+            };
+#pragma unroll
+            for (int p = 0; p < 16; p += 2) {
+                rank(p, 0);
+                rank(p, 1);
+            }
+            if (__any_sync(kAll, n > 16)) {  // (uniform)
+#pragma unroll
+                for (int p = 0; p < kManyFew; p += 2)
+#pragma unroll
+                    for (int j = p < 16 ? 2 : 0; j < kHold; ++j) rank(p, j);
+            }
+#pragma unroll
+            for (int j = 0; j < kHold; ++j)
+                if (l + LANES * j < n && n <= kManyFew) s.sorted[n - 1 - behind[j]] = c[j];
+            __syncwarp();
+            const bool slot = l < a.k;
+            const Ranked chosen = s.sorted[l];
+            const float q = chosen.q, next = s.sorted[l + 1].q;
+            const bool bad = there && slot &&
+                             (n > kManyFew || isnan(q) ||
+                              (l + 1 < n && (EXACT ? !(q > next) : too_near(q, next, unit))));
+            unsigned open = __ballot_sync(kAll, bad);
+#pragma unroll
+            for (int o = LANES / 2; o >= 1; o >>= 1) open |= open >> o;  // each segment's any, in its bit 0
+            open &= LANES == 8 ? 0x01010101u : 0x00010001u;
+            left |= open << i;
+
+            const bool write = there && slot && ((open >> (LANES * seg)) & 1u) == 0u;
+            const int id = write ? chosen.id : 0;
+            const float logit = !write ? -INFINITY : EXACT ? q : L[id];
+            float w;
+            if (a.sigmoid || a.renorm) {
+                float x = a.sigmoid ? rcp_fast(1.f + expf(-logit)) : 0.f;
+                float sum = 1.f;
+                if (a.sigmoid && a.renorm) sum = segment_all<LANES, false>(slot ? x : 0.f);
+                if (a.renorm && __any_sync(kAll, !a.sigmoid || (write && sum < 0x1p-100f))) {
+                    // (as in write_slots; for all of the warp's tokens, if one needs it)
+                    const float top = segment_all<LANES, true>(logit);
+                    const bool here = !a.sigmoid || sum < 0x1p-100f;
+                    const float y = !write || top == -INFINITY ? 0.f : expf(logit - top);
+                    const float shares = segment_all<LANES, false>(y);
+                    if (here) {
+                        x = y;
+                        sum = top == -INFINITY ? 1.f : shares;
+                    }
+                }
+                w = a.scale * x * rcp_fast(sum);
+            } else {
+                w = m == -INFINITY ? 0.f : a.scale * expf(logit - m) * rcp_fast(z);
+            }
+            if (write) {
+                a.idx[t * a.k + l] = id;
+                a.w[t * a.k + l] = w;
+            }
+        }
+        while (left) {
+            const int bit = __ffs(left) - 1;
+            left &= left - 1u;
+            decide(cold, t0 + bit % LANES * stride + bit / LANES, smem);
+        }
+    }
+}
+
+template <int LANES, int N>
+cudaError_t launch_many(const SelectArgs &a, bool exact, cudaStream_t st) {
+    constexpr int kTokens = 32 / LANES;
+    const size_t smem = std::max<size_t>(scratch_bytes(a.E), sizeof(Segment) * kTokens);
+    const dim3 grid((unsigned)std::min<int64_t>((a.T + kTokens - 1) / kTokens,
+                                                (int64_t)device_sm_count() * 24));
+    return launch_pdl(exact ? select_many_kernel<LANES, N, true> : select_many_kernel<LANES, N, false>,
+                      grid, dim3(32), smem, st, a, a);
+}
+// From this many tokens on (measured below).
+constexpr int64_t kManyTokens = 16384;
+bool takes_many(const SelectArgs &a) {
+    return a.Gk == a.G && a.k <= kManyK && a.E % 4 == 0 && a.E >= 32 && a.E <= 256 && a.T >= kManyTokens;
+}
+
 template <int VPL, bool EXACT, bool GROUPS>
 cudaError_t launch_select_t(const SelectArgs &a, cudaStream_t st) {
     const size_t smem = std::max<size_t>(scratch_bytes(a.E), sizeof(Ranked) * (32 * VPL + 4));
@@ -836,7 +1074,12 @@ cudaError_t launch_select(const Shape &s, const Router &r, float *logits, const 
     a.zero_word = zero_word;
     const bool exact = !bias && (a.Gk == a.G || !a.top2);
     cudaError_t e;
-    if (a.per <= 1) e = launch_select_v<1>(a, exact, st);
+    if (takes_many(a)) {
+        if (a.E <= 64) e = launch_many<8, 2>(a, exact, st);
+        else if (a.E <= 128) e = launch_many<8, 4>(a, exact, st);
+        else e = launch_many<16, 4>(a, exact, st);
+    }
+    else if (a.per <= 1) e = launch_select_v<1>(a, exact, st);
     else if (a.per <= 2) e = launch_select_v<2>(a, exact, st);
     else if (a.per <= 4) e = launch_select_v<4>(a, exact, st);
     else if (a.per <= 8) e = launch_select_v<8>(a, exact, st);
