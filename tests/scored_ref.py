@@ -62,6 +62,22 @@ def select(L, bias, k, sigmoid, G, Gk, top2):
     return ranked(order[ids], ids)[:k]
 
 
+def select_many(L, bias, k, sigmoid, G, Gk, top2):
+    """The same for a batch [T, E] of finite logits, in torch on its device."""
+    T, E = L.shape
+    L = L.double()
+    s = 1.0 / (1.0 + torch.exp(-L)) if sigmoid else torch.softmax(L, -1)
+    q = s if bias is None else s + bias.double()
+    order = L if bias is None else q
+    if Gk < G:
+        best = torch.sort((q if top2 else order).view(T, G, -1), dim=-1, descending=True).values
+        u = best[..., :2].sum(-1) if top2 else best[..., 0]
+        kept = torch.sort(u, dim=-1, descending=True, stable=True).indices[:, :Gk]
+        there = torch.zeros(T, G, dtype=torch.bool, device=L.device).scatter_(1, kept, True)
+        order = order.masked_fill(~there.repeat_interleave(E // G, 1), float("-inf"))
+    return torch.sort(order, dim=-1, descending=True, stable=True).indices[:, :k]
+
+
 def weights(L, idx, sigmoid, renorm, scale):
     """torch, 64 bits, differentiable in L [T, E]."""
     s = torch.sigmoid(L) if sigmoid else torch.softmax(L, -1)
