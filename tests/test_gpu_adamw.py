@@ -83,10 +83,15 @@ def reference(e, h, coef=1.0):
     return dict(p=new, m=m, v=v, m_tol=8 * U * mag + 2.0 ** -149, p_tol=tol)
 
 
+def power(e):
+    """2^e, exactly (ldexp and exp2 are not, on the GPU)."""
+    return ((e.long() + 1023) << 52).view(torch.float64)
+
+
 def step_of(x, scale):
     """Distance of x's neighbours in e4m3 times scale (both per element)."""
     e = (torch.frexp(x.abs() / scale).exponent - 1).clamp(min=-6)
-    return torch.ldexp(scale, e - 3)
+    return scale * power(e - 3)
 
 
 def verify(before, after, h, coef=1.0, stochastic=False):
@@ -309,6 +314,58 @@ def test_repeats_and_seeds(moe):
     # the numbers go by the block's place in the list, whatever the launches
     assert not torch.equal(go(5, (1, 0, 2))[0], a[0]) and torch.equal(go(5, (1, 0, 2))[2], a[2])
     assert all(not torch.equal(x, y) for x, y in zip(a, go(5 + (1 << 32))))
+
+
+M32 = 0xFFFFFFFF
+CONST = (0x9E3779B1, 0xD6E8FEB9, 0xA24BAED5, 0xCA5A8263)
+
+
+def fold(a, c):
+    """High and low words of the 32-bit product, xor'ed."""
+    a = a & M32
+    hi = (a * (c >> 16) + ((a * (c & 0xFFFF)) >> 16)) >> 16
+    return (hi ^ (a * (c & 0xFFFF) + (((a * (c >> 16)) & 0xFFFF) << 16))) & M32
+
+
+def random_bits(block, seed):
+    x = fold(block + CONST[0], CONST[1])
+    x = fold(x ^ (seed & M32), CONST[2])
+    x = fold(x + (seed >> 32) + (block >> 32), CONST[3])
+    y = fold(x ^ CONST[0], CONST[3])
+    place = torch.arange(256, device="cuda") * CONST[0]
+    return fold(fold(x[:, None] + place, CONST[2]) ^ y[:, None], CONST[1]).view(-1)
+
+
+@pytest.mark.parametrize("seed", [0, 12345, (7 << 32) + 99])
+def test_the_random_numbers(moe, seed):
+    """Bits 0 to 15 round a bf16 parameter, 8 to 23 m and 16 to 31 r: away from
+    zero where the part of a step that is lost, plus the bits' part, reaches one.
+    (But for values whose fp32 rounding decides: under 1 in 10,000.)"""
+    skip, n = 700, 50_000
+    es = [entry(skip, 1), entry(n, 2, p=BF, g=F32, bits=8)]
+    before = copy(es[1])
+    run(moe, es, seed=seed, stochastic=True)
+    r = reference(before, HYPER)
+    blocks = torch.arange(-(-n // 256), device="cuda") + -(-skip // 256)
+    u = random_bits(blocks, seed)[:n]
+
+    def check(got, x, step, bits):
+        low = torch.floor(x.abs() / step)
+        up = (x.abs() / step - low + (bits.double() + 0.5) / 65536) >= 1
+        want = torch.copysign((low + up) * step, x)
+        assert float((got != want).double().mean()) < 1e-4
+        assert float(up.double().mean()) > 0.2
+    p = r["p"]
+    e = (torch.frexp(p.abs()).exponent - 1).clamp(min=-126)
+    check(es[1]["param"].double(), p, power(e - 7), u & 0xFFFF)
+    for name, x, bits in (("exp_avg", r["m"], (u >> 8) & 0xFFFF), ("exp_avg_sq", r["v"].sqrt(), u >> 16)):
+        s = es[1][name + "_scale"].double().repeat_interleave(256)[:n]
+        got = es[1][name].double() * s
+        if name == "exp_avg_sq":  # (the smallest code instead of zero)
+            keep = x > 2.0 ** -9 * s
+            check(got[keep], x[keep], step_of(x, s)[keep], bits[keep])
+        else:
+            check(got, x, step_of(x, s), bits)
 
 
 def test_streams_and_graph(moe):

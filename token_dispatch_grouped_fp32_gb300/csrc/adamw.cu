@@ -261,15 +261,19 @@ __device__ __forceinline__ float quantise(float2 (&x)[4], uint32_t e, bool finit
         const float2 y = mul2(x[i], two(inv));
         // to a neighbouring e4m3 value (|y| <= 256).  power: 2^e <= |y|, at least 2^-6, below
         // which the steps are those from there up: a step is power / 8.  A random part
-        // of a step in (-1/2, 1/2), of 16 bits, is added, and the sum rounded to
-        // steps by adding and taking away 1.5 * 2^23 of them.  (Four packed operations;
-        // by integer sums on the bits it took seven or eight of the ALU, which is
-        // what bounds this kernel.)
+        // of a step in (-1/2, 1/2), of 16 bits, is added to the magnitude, and the sum
+        // rounded to steps by adding and taking away 1.5 * 2^23 of them.  (Four packed
+        // operations; by integer sums on the bits it took seven or eight of the ALU,
+        // which is what bounds this kernel.)
         const float2 power = make_float2(
             fmaxf(__uint_as_float(__float_as_uint(y.x) & 0x7f800000u), 0x1p-6f),
             fmaxf(__uint_as_float(__float_as_uint(y.y) & 0x7f800000u), 0x1p-6f));
         const float2 f = pair_of(fraction<ROOT>(u[2 * i]), fraction<ROOT>(u[2 * i + 1]));  // [1, 2)
-        const float2 part = fma2(f, two(0x1p-3f), two(-1.5f * 0x1p-3f));
+        float2 part = fma2(f, two(0x1p-3f), two(-1.5f * 0x1p-3f));
+        if (!ROOT) {  // away from zero by the same numbers on either side
+            part.x = __uint_as_float(__float_as_uint(part.x) ^ (__float_as_uint(y.x) & 0x80000000u));
+            part.y = __uint_as_float(__float_as_uint(part.y) ^ (__float_as_uint(y.y) & 0x80000000u));
+        }
         const float2 sum = fma2(power, two(1.5f * 0x1p20f), fma2(part, power, y));
         float2 q = fma2(power, two(-1.5f * 0x1p20f), sum);
         if (ROOT) {  // (2^-9 if y is not 0)

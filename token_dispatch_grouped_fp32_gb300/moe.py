@@ -496,34 +496,42 @@ def adamw_list(tensors):
     256 elements), and optionally "master" (fp32) and "weight_decay".  It holds
     addresses: keep the tensors alive, and build it once for buffers that stay
     where they are."""
-    tensors = list(tensors)
-    arr = (moe_adamw_tensor_t * max(1, len(tensors)))()
-    arr.count = len(tensors)
-    types = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32, torch.float8_e4m3fn: MOE_E4M3}
-    for a, t in zip(arr, tensors):
-        p, g, m, v = t["param"], t["grad"], t["exp_avg"], t["exp_avg_sq"]
-        master, scales = t.get("master"), [t.get("exp_avg_scale"), t.get("exp_avg_sq_scale")]
-        n, small = p.numel(), m.dtype == torch.float8_e4m3fn
-        if p.dtype not in types or g.dtype not in types or torch.float8_e4m3fn in (p.dtype, g.dtype):
-            raise TypeError(f"parameters and gradients are bf16 or fp32, not {p.dtype}, {g.dtype}")
-        if m.dtype != v.dtype or m.dtype not in (torch.float32, torch.float8_e4m3fn):
-            raise TypeError(f"both states are fp32 or float8_e4m3fn, not {m.dtype}, {v.dtype}")
-        if any(x.numel() != n for x in (g, m, v)):
-            raise ValueError("a gradient and its states have the parameter's size")
-        if master is not None and (p.dtype != torch.bfloat16 or master.dtype != torch.float32
-                                   or master.numel() != n):
-            raise ValueError("a master copy is an fp32 tensor of a bf16 parameter's size")
-        blocks = (n + ADAMW_BLOCK - 1) // ADAMW_BLOCK
-        if any((x is not None) != small or (small and (x.dtype != torch.float32
-                                                       or x.numel() != blocks)) for x in scales):
-            raise ValueError("8-bit states, and they alone, have an fp32 scale for 256 elements")
-        if any(x is not None and x.device != p.device for x in (g, m, v, master, *scales)):
-            raise ValueError("a parameter, its gradient and its states are on one device")
-        a.param, a.grad, a.exp_avg, a.exp_avg_sq = _ptr(p), _ptr(g), _ptr(m), _ptr(v)
-        a.exp_avg_scale, a.exp_avg_sq_scale, a.master = _ptr(scales[0]), _ptr(scales[1]), _ptr(master)
-        a.numel, a.weight_decay = n, float(t.get("weight_decay", 0.0))
-        a.param_dtype, a.grad_dtype, a.state_dtype = types[p.dtype], types[g.dtype], types[m.dtype]
+    rows = [_adamw_row(**t) for t in tensors]
+    arr = (moe_adamw_tensor_t * max(1, len(rows)))(*rows)
+    arr.count = len(rows)
     return arr
+
+
+_ADAMW_TYPES = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}
+_STATE_TYPES = {torch.float32: MOE_F32, torch.float8_e4m3fn: MOE_E4M3}
+
+
+def _adamw_row(param, grad, exp_avg, exp_avg_sq, exp_avg_scale=None, exp_avg_sq_scale=None,
+               master=None, weight_decay=0.0):
+    n, kinds = param.numel(), (param.dtype, grad.dtype)
+    kind, state = [_ADAMW_TYPES.get(k) for k in kinds], _STATE_TYPES.get(exp_avg.dtype)
+    if None in kind:
+        raise TypeError(f"parameters and gradients are bf16 or fp32, not {kinds}")
+    if state is None or exp_avg_sq.dtype != exp_avg.dtype:
+        raise TypeError(f"both states are fp32 or float8_e4m3fn, not {exp_avg.dtype}, "
+                        f"{exp_avg_sq.dtype}")
+    if not grad.numel() == exp_avg.numel() == exp_avg_sq.numel() == n:
+        raise ValueError("a gradient and its states have the parameter's size")
+    others = [grad, exp_avg, exp_avg_sq]
+    if master is not None:
+        if kinds[0] != torch.bfloat16 or master.dtype != torch.float32 or master.numel() != n:
+            raise ValueError("a master copy is an fp32 tensor of a bf16 parameter's size")
+        others.append(master)
+    scales = [s for s in (exp_avg_scale, exp_avg_sq_scale) if s is not None]
+    if len(scales) != (2 if state == MOE_E4M3 else 0) or any(
+            s.dtype != torch.float32 or s.numel() != -(-n // ADAMW_BLOCK) for s in scales):
+        raise ValueError("8-bit states, and they alone, have an fp32 scale for 256 elements")
+    device = param.device
+    for x in others + scales:
+        if x.device != device:
+            raise ValueError("a parameter, its gradient and its states are on one device")
+    return (_ptr(param), _ptr(grad), _ptr(exp_avg), _ptr(exp_avg_sq), _ptr(exp_avg_scale),
+            _ptr(exp_avg_sq_scale), _ptr(master), n, kind[0], kind[1], state, float(weight_decay))
 
 
 def adamw_hyper(lr, beta1=0.9, beta2=0.95, eps=1e-8, step=1, seed=0, max_norm=0.0,
