@@ -6,8 +6,14 @@
 // The tensors are cut into blocks of 256 elements, the unit of an 8-bit state's
 // scale: a warp takes one, eight consecutive elements a lane, so that the block's
 // largest magnitudes are two warp reductions and every access is a vector.  Chunks
-// of 64 such blocks are dealt to the thread blocks; the tensors' addresses
+// of 8 to 64 such blocks are dealt to the thread blocks; the tensors' addresses
 // travel as kernel parameters, as in clip.cu.
+//
+// fp32 states are bound by HBM (64 M bf16 parameters: 213 us, 0.98 of the copy
+// rate).  8-bit states by the instructions of two roundings an element: 144 us
+// (0.66; fp32 parameters, which move more, 163: 0.93).  A ring of asynchronous copies
+// into shared memory took 148 to 155 us, values of the next block held in registers
+// 161 to 205, and a prefetch into L2 158: the loads are not what it waits for.
 //
 // m and v are formed by rounded products and sums in a fixed order (no fused
 // multiply-adds): a scale is a power of two that depends on the last bit of the
@@ -239,10 +245,10 @@ __device__ __forceinline__ uint32_t root_scale_exponent(uint32_t largest) {
     return largest < 0x00800000u ? 1u : (uint32_t)((e >> 1) + 127 - 7);
 }
 
-// 16 random bits (of a root: the high ones; else bits 8 to 23) as a float's bits in
-// [1, 2), in the middle of their step.
-template <bool ROOT> __device__ __forceinline__ uint32_t fraction(uint32_t u) {
-    return ((u >> (ROOT ? 9 : 1)) & 0x7FFF80u) | 0x3F800040u;
+// 16 random bits (of a root: the high ones; else bits 8 to 23) as the bits of
+// 2^23 + their number, in one instruction.
+template <bool ROOT> __device__ __forceinline__ uint32_t number(uint32_t u) {
+    return __byte_perm(u, 0x4B000000u, ROOT ? 0x7432 : 0x7421);
 }
 
 // A block's states to 8 bits, in place, by a scale of biased exponent e.  x: 0 beyond
@@ -261,15 +267,16 @@ __device__ __forceinline__ float quantise(float2 (&x)[4], uint32_t e, bool finit
         const float2 y = mul2(x[i], two(inv));
         // to a neighbouring e4m3 value (|y| <= 256).  power: 2^e <= |y|, at least 2^-6, below
         // which the steps are those from there up: a step is power / 8.  A random part
-        // of a step in (-1/2, 1/2), of 16 bits, is added to the magnitude, and the sum
+        // of a step in [-1/2, 1/2), of 16 bits, is added to the magnitude (on average
+        // 2^-17 of a step less than nothing), and the sum
         // rounded to steps by adding and taking away 1.5 * 2^23 of them.  (Four packed
         // operations; by integer sums on the bits it took seven or eight of the ALU,
         // which is what bounds this kernel.)
         const float2 power = make_float2(
             fmaxf(__uint_as_float(__float_as_uint(y.x) & 0x7f800000u), 0x1p-6f),
             fmaxf(__uint_as_float(__float_as_uint(y.y) & 0x7f800000u), 0x1p-6f));
-        const float2 f = pair_of(fraction<ROOT>(u[2 * i]), fraction<ROOT>(u[2 * i + 1]));  // [1, 2)
-        float2 part = fma2(f, two(0x1p-3f), two(-1.5f * 0x1p-3f));
+        const float2 f = pair_of(number<ROOT>(u[2 * i]), number<ROOT>(u[2 * i + 1]));
+        float2 part = fma2(f, two(0x1p-19f), two(-16.0625f));  // of power: -1/16 to 1/16
         if (!ROOT) {  // away from zero by the same numbers on either side
             part.x = __uint_as_float(__float_as_uint(part.x) ^ (__float_as_uint(y.x) & 0x80000000u));
             part.y = __uint_as_float(__float_as_uint(part.y) ^ (__float_as_uint(y.y) & 0x80000000u));
@@ -308,7 +315,7 @@ __device__ __forceinline__ void step_chunk(const Entry &t, const Step &s, const 
     const float decay = fmaf(-sc.lr, t.wd, 1.f);
     const bool round_p = sizeof(TP) == 2 && s.stochastic;
     // the key and the scales of block b + i kWarps, in lane i (a scale that each block
-    // waited for itself cost a round to memory: 187 us to X for 64 M bf16 parameters)
+    // waited for itself cost a round to memory: 64 M bf16 parameters 187 us, so 155)
     const int64_t mine = b + lane * kWarps;
     float ms = 0.f, rs = 0.f;
     if (SMALL && mine < last) {
@@ -422,6 +429,9 @@ __device__ __forceinline__ void step_chunk(const Entry &t, const Step &s, const 
     }
 }
 
+// Blocks an SM: with 8-bit states four (three took 156 us for 64 M parameters, five,
+// for which registers spill, 163, four 146); with fp32 states three (213 us against
+// 236 with four, whose accesses are spread over more of the memory's rows).
 template <bool SMALL>
 __global__ void __launch_bounds__(kThreads, SMALL ? 4 : 3)
 adamw_kernel(const __grid_constant__ Table tab, const __grid_constant__ Step s) {
