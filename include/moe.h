@@ -509,7 +509,7 @@ moe_status_t moe_clip_grad_norm(const moe_grad_t *grads, int64_t n, float max_no
  * 0; scores that fp32 cannot hold keep their shares.  A logit of +inf is not
  * supported with softmax scores.
  * Limits: 1 <= groups <= 32, E a multiple of groups, 1 <= topk_groups <=
- * groups, k <= topk_groups * E / groups, weight_scale > 0 and finite.
+ * groups, k <= topk_groups * E / groups, 2^-100 <= weight_scale <= 2^100.
  */
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_t;
 typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } moe_group_score_t;
@@ -633,8 +633,8 @@ moe_status_t moe_update_balance_bias(const int32_t *counts, int64_t layers, int3
  * percent of itself, or less, is far below a step of e4m3, and would be lost
  * whole by rounding to the nearest.  An r above 0 is stored as at least the
  * smallest code, so that no later step divides by eps alone (a v below 2^-126
- * counts as 0).  (Zeros in all bytes
- * and scales are valid initial states of either kind.)
+ * counts as 0, and eps = 0 then divides by 0).  (Zeros in all bytes and scales are
+ * valid initial states of either kind.)
  * A block with a NaN or an infinity keeps NaN and the format's largest value
  * for those elements.
  *
@@ -657,7 +657,7 @@ typedef struct {
 } moe_adamw_tensor_t;
 
 typedef struct {
-    double lr, beta1, beta2, eps;  /* lr, eps >= 0; 0 <= beta < 1 */
+    double lr, beta1, beta2, eps;  /* lr >= 0; 0 <= beta < 1; eps 0 or >= 2^-126 */
     int64_t step;                  /* >= 1 */
     uint64_t seed;
     float max_norm;                /* >= 0; read when `norm` is given */

@@ -2,6 +2,8 @@
 each call here returns before it touches a device."""
 import ctypes
 import math
+import weakref
+from types import SimpleNamespace
 
 import pytest
 import torch
@@ -214,7 +216,7 @@ def test_adamw_list_refuses(moe):
         return d
     assert moe.adamw_list([t(), t(master=torch.zeros(300))]).count == 2
     e4 = torch.zeros(300).to(torch.float8_e4m3fn)
-    two = dict(exp_avg=e4, exp_avg_sq=e4, exp_avg_scale=torch.zeros(2), exp_avg_sq_scale=torch.zeros(2))
+    two = dict(exp_avg=e4, exp_avg_sq=e4.clone(), exp_avg_scale=torch.zeros(2), exp_avg_sq_scale=torch.zeros(2))
     assert moe.adamw_list([t(**two)])[0].state_dtype == moe.MOE_E4M3
     for bad in (dict(p=torch.float16), dict(grad=torch.zeros(300).double()), dict(exp_avg=e4),
                 dict(exp_avg=torch.zeros(300, dtype=torch.bfloat16),
@@ -238,6 +240,97 @@ def test_adamw_class_refuses(moe):
                 dict(weight_decay=[0.1, 0.2]), dict(grads=[torch.zeros(299)])):
         with pytest.raises(ValueError):
             moe.AdamW(**{**dict(params=p, grads=g, lr=1e-3), **bad})
+
+
+def _plain(**kw):
+    z = lambda: torch.zeros(300)
+    return {**dict(param=z(), grad=z(), exp_avg=z(), exp_avg_sq=z()), **kw}
+
+
+def test_adamw_list_refuses_overlapping_tensors(moe):
+    a, b = _plain(), _plain()
+    moe.adamw_list([a, b])
+    moe.adamw_list([a, {**b, "grad": a["grad"]}])  # read only
+    buf = torch.zeros(600)
+    moe.adamw_list([{**a, "param": buf[:300]}, {**b, "param": buf[300:]}])
+    for bad in ([a, a], [a, {**b, "param": a["param"]}], [a, {**b, "exp_avg_sq": a["exp_avg"]}],
+                [{**a, "param": buf[:300]}, {**b, "param": buf[299:599]}]):
+        with pytest.raises(ValueError):
+            moe.adamw_list(bad)
+    with pytest.raises(ValueError):
+        moe.AdamW([buf, buf], [torch.zeros(600)] * 2, lr=1e-3)
+    m = lambda: torch.zeros(300, device="meta")
+    with pytest.raises(ValueError):
+        moe.adamw_list([a, dict(param=m(), grad=m(), exp_avg=m(), exp_avg_sq=m())])
+
+
+class _Elsewhere(torch.Tensor):
+    device = property(lambda self: torch.device("cuda", 1))
+
+
+def test_tensors_off_the_current_gpu_are_refused(moe, monkeypatch):
+    launched = []
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(moe, "_stream", lambda s: 0)
+    monkeypatch.setattr(moe, "_lib", SimpleNamespace(
+        moe_adamw_step=lambda *a: launched.append(a) or 0))
+    hyper = moe.adamw_hyper(1e-3)
+    with pytest.raises(ValueError):  # host memory
+        moe.moe_adamw_step(moe.adamw_list([_plain()]), hyper)
+    with pytest.raises(ValueError):
+        moe.AdamW([torch.zeros(300)], [torch.zeros(300)], lr=1e-3).step()
+    there = moe.adamw_list([{n: x.as_subclass(_Elsewhere) for n, x in _plain().items()}])
+    with pytest.raises(ValueError):
+        moe.moe_adamw_step(there, hyper)
+    assert not launched
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    moe.moe_adamw_step(there, hyper)
+    assert len(launched) == 1
+
+
+@pytest.mark.parametrize("hyper,ok", [(dict(eps=0.0), True), (dict(eps=2.0 ** -126), True),
+                                      (dict(eps=2.0 ** -127), False), (dict(eps=1e-60), False),
+                                      (dict(lr=1e300), False), (dict(eps=1e300), False)])
+def test_adamw_hyperparameters_as_floats(moe, hyper, ok):
+    h = moe.adamw_hyper(**{**dict(lr=1e-3), **hyper})
+    if ok:
+        moe.moe_adamw_scalars(h)
+    else:
+        with pytest.raises(moe.MoEError):
+            moe.moe_adamw_scalars(h)
+
+
+@pytest.mark.parametrize("scale,ok", [(2.0 ** -100, True), (2.0 ** 100, True), (2.0 ** -101, False),
+                                      (1e-40, False), (2.0 ** 101, False)])
+def test_weight_scales(moe, scale, ok):
+    s = moe.moe_route_scored_from_logits(moe.config(0, 8, 16, 4, 8), moe.router(weight_scale=scale),
+                                         None, None, None, None, stream=0, raise_on_error=False)
+    assert (s == moe.MOE_OK) is ok
+
+
+def test_a_captured_balance_update_keeps_its_workspace(moe, monkeypatch):
+    class OnDevice(torch.Tensor):
+        is_cuda = property(lambda self: True)
+
+    capturing = [False]
+    monkeypatch.setattr(moe, "_stream", lambda s: 7 if s is None else int(s))
+    monkeypatch.setattr(moe, "_on_current", lambda device: None)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
+    empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: empty(*a, **kw).as_subclass(OnDevice))
+    monkeypatch.setattr(moe, "moe_forward_scored", lambda *a, **kw: None)
+    monkeypatch.setattr(moe, "moe_update_balance_bias", lambda *a, **kw: None)
+    bf = torch.bfloat16
+    lay = moe.MoELayer(torch.zeros(8, 64), torch.zeros(8, 64, 256, dtype=bf),
+                       torch.zeros(8, 128, 64, dtype=bf), 2, router=moe.router("sigmoid"),
+                       balance_bias=torch.zeros(8))
+    lay(torch.zeros(16, 64, dtype=bf))
+    capturing[0] = True
+    lay.update_balance_bias(1e-3)
+    capturing[0] = False
+    held = weakref.ref(next(iter(lay._ws.values())))
+    lay(torch.zeros(4000, 64, dtype=bf))
+    assert held() is not None
 
 
 def test_layer_refuses(moe):

@@ -175,8 +175,9 @@ moe_status_t check_router(const moe_router_t *router, const Shape &s, Router *r)
         set_error_message("k=%d exceeds the %d experts of %d groups", s.k, Gk * (s.E / G), Gk);
         return MOE_ERR_INVALID_ARG;
     }
-    if (!(router->weight_scale > 0.f) || !(router->weight_scale < INFINITY)) {
-        set_error_message("weight_scale %g is not a positive finite number",
+    // (1 / weight_scale, and products with it, stay normal numbers)
+    if (!(router->weight_scale >= 0x1p-100f && router->weight_scale <= 0x1p100f)) {
+        set_error_message("weight_scale %g is not between 2^-100 and 2^100",
                           (double)router->weight_scale);
         return MOE_ERR_INVALID_ARG;
     }

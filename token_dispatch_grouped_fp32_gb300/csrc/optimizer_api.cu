@@ -1,5 +1,6 @@
 // optimizer_api.cu -- the C ABI of AdamW and of the balance bias's update
 // (declared in include/moe.h): argument checks and launches.
+#include <cfloat>
 #include <cmath>
 
 #include "api.h"
@@ -16,7 +17,10 @@ moe_status_t invalid(const char *what) {
 
 moe_status_t check_hyper(const moe_adamw_hyper_t *h) {
     if (!h) return invalid("hyper is NULL");
-    if (!(h->lr >= 0.0) || !(h->eps >= 0.0) || !std::isfinite(h->lr) || !std::isfinite(h->eps) ||
+    // (as floats: finite, and eps no subnormal, which a reciprocal takes for 0)
+    const float lr = (float)h->lr, eps = (float)h->eps;
+    if (!(lr >= 0.f) || !(eps == 0.f || eps >= FLT_MIN) || !std::isfinite(lr) || !std::isfinite(eps) ||
+        (eps == 0.f && h->eps != 0.0) ||
         !(h->beta1 >= 0.0 && h->beta1 < 1.0) || !(h->beta2 >= 0.0 && h->beta2 < 1.0)) {
         set_error_message("lr %g, beta1 %g, beta2 %g or eps %g out of range", h->lr, h->beta1, h->beta2,
                           h->eps);

@@ -1,7 +1,6 @@
 // route_scored.cu -- the router with scores of its own: softmax or sigmoid of
 // the logits, a balance bias that acts on the choice and not on the weights,
-// groups of experts, top-k, renormalised and scaled weights; and the gradient
-// of those weights with respect to the logits.
+// groups of experts, top-k, renormalised and scaled weights.
 //
 //   s_e = exp(L_e) / sum_i exp(L_i)   or   1 / (1 + exp(-L_e))
 //   q_e = s_e + b_e           the choice is made on q (without b: on L, the same order)
@@ -25,7 +24,7 @@ namespace {
 // candidates are gathered in shared memory, one a lane, and each counts those ahead
 // of it, instead of k rounds of a warp maximum with its removal.  What this leaves
 // open goes to decide(), after every 32 tokens: a call inside their loop cost it
-// spills (T = 131072, E = 128: 43 us to 62).  Blocks of one warp: what depends on the
+// spills (then 62 us for T = 131072, E = 128 instead of 43).  Blocks of one warp: what depends on the
 // token is uniform, which the compiler sees.
 template <int VPL, bool EXACT, bool GROUPS>
 __global__ void __launch_bounds__(32, VPL <= 8 ? 32 : 16)
@@ -46,213 +45,213 @@ select_kernel(const SelectArgs a, const __grid_constant__ SelectArgs cold) {
     Pending &pend = *reinterpret_cast<Pending *>(smem + a.pending_at);
     int64_t t = blockIdx.x;
     while (t < a.T) {
-    const int64_t t0 = t;
-    unsigned left = 0u;  // of the tokens t0 + i * gridDim.x, those for decide()
-    int pending = 0;     // and for settle()
-    for (int i32 = 0; i32 < 32 && t < a.T && pending < kPending; ++i32, t += gridDim.x) {
-        float *L = a.logits + t * E;
-        float v[VPL];  // NaN: no expert
-        if (a.nparts > 0) {
-            const float *p = a.partial + t * E;
+        const int64_t t0 = t;
+        unsigned left = 0u;  // of the tokens t0 + i * gridDim.x, those for decide()
+        int pending = 0;     // and for settle()
+        for (int i32 = 0; i32 < 32 && t < a.T && pending < kPending; ++i32, t += gridDim.x) {
+            float *L = a.logits + t * E;
+            float v[VPL];  // NaN: no expert
+            if (a.nparts > 0) {
+                const float *p = a.partial + t * E;
 #pragma unroll
-            for (int i = 0; i < VPL; ++i) v[i] = i < count ? p[e0 + i] : NAN;
+                for (int i = 0; i < VPL; ++i) v[i] = i < count ? p[e0 + i] : NAN;
 #pragma unroll 4
-            for (int z = 1; z < a.nparts; ++z) {
-                p += a.T * E;
-#pragma unroll
-                for (int i = 0; i < VPL; ++i)
-                    if (i < count) v[i] += p[e0 + i];
-            }
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-                if (i >= count) continue;
-                if (a.logit_bias) v[i] += a.logit_bias[e0 + i];
-                L[e0 + i] = v[i];
-            }
-        } else if (whole) {
-#pragma unroll
-            for (int i = 0; i + 3 < VPL; i += 4) {
-                float4 x = make_float4(NAN, NAN, NAN, NAN);
-                if (i < count) x = *reinterpret_cast<const float4 *>(L + e0 + i);
-                v[i] = x.x;
-                v[i + 1] = x.y;
-                v[i + 2] = x.z;
-                v[i + 3] = x.w;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) v[i] = i < count ? L[e0 + i] : NAN;
-        }
-        __syncwarp();  // (the row as written, and the last token's candidates as read)
-
-        // softmax, where scores or their sum are needed: the largest logit m, and z
-        float m = -INFINITY, z = 1.f;
-        if (!a.sigmoid && (!EXACT || !a.renorm)) {
-            float top = v[0];
-#pragma unroll
-            for (int i = 1; i < VPL; ++i) top = fmaxf(top, v[i]);
-            top = warp_max(top);
-            if (!isnan(top)) m = top;
-            z = 0.f;
-#pragma unroll
-            for (int i = 0; i < VPL; ++i)
-                if (i < count) z += exp2_fast((v[i] - m) * kLog2e);
-            z = warp_sum(z);
-        }
-        if constexpr (!EXACT) {
-            if (a.sigmoid) {
-#pragma unroll
-                for (int i = 0; i < VPL; ++i) v[i] = score32(v[i], true, 0.f, 0.f);
-            } else {  // (m == -INF, a row without scores: its NaN are for decide())
-                const float inv = rcp_fast(z);
-#pragma unroll
-                for (int i = 0; i < VPL; ++i) v[i] = exp2_fast((v[i] - m) * kLog2e) * inv;
-            }
-            if (a.bias) {
-                if (whole && count == VPL) {
-#pragma unroll
-                    for (int i = 0; i + 3 < VPL; i += 4) {
-                        const float4 b = *reinterpret_cast<const float4 *>(a.bias + e0 + i);
-                        v[i] += b.x;
-                        v[i + 1] += b.y;
-                        v[i + 2] += b.z;
-                        v[i + 3] += b.w;
-                    }
-                } else {
+                for (int z = 1; z < a.nparts; ++z) {
+                    p += a.T * E;
 #pragma unroll
                     for (int i = 0; i < VPL; ++i)
-                        if (i < count) v[i] += a.bias[e0 + i];
+                        if (i < count) v[i] += p[e0 + i];
+                }
+#pragma unroll
+                for (int i = 0; i < VPL; ++i) {
+                    if (i >= count) continue;
+                    if (a.logit_bias) v[i] += a.logit_bias[e0 + i];
+                    L[e0 + i] = v[i];
+                }
+            } else if (whole) {
+#pragma unroll
+                for (int i = 0; i + 3 < VPL; i += 4) {
+                    float4 x = make_float4(NAN, NAN, NAN, NAN);
+                    if (i < count) x = *reinterpret_cast<const float4 *>(L + e0 + i);
+                    v[i] = x.x;
+                    v[i + 1] = x.y;
+                    v[i + 2] = x.z;
+                    v[i + 3] = x.w;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < VPL; ++i) v[i] = i < count ? L[e0 + i] : NAN;
+            }
+            __syncwarp();  // (the row as written, and the last token's candidates as read)
+
+            // softmax, where scores or their sum are needed: the largest logit m, and z
+            float m = -INFINITY, z = 1.f;
+            if (!a.sigmoid && (!EXACT || !a.renorm)) {
+                float top = v[0];
+#pragma unroll
+                for (int i = 1; i < VPL; ++i) top = fmaxf(top, v[i]);
+                top = warp_max(top);
+                if (!isnan(top)) m = top;
+                z = 0.f;
+#pragma unroll
+                for (int i = 0; i < VPL; ++i)
+                    if (i < count) z += exp2_fast((v[i] - m) * kLog2e);
+                z = warp_sum(z);
+            }
+            if constexpr (!EXACT) {
+                if (a.sigmoid) {
+#pragma unroll
+                    for (int i = 0; i < VPL; ++i) v[i] = score32(v[i], true, 0.f, 0.f);
+                } else {  // (m == -INF, a row without scores: its NaN are for decide())
+                    const float inv = rcp_fast(z);
+#pragma unroll
+                    for (int i = 0; i < VPL; ++i) v[i] = exp2_fast((v[i] - m) * kLog2e) * inv;
+                }
+                if (a.bias) {
+                    if (whole && count == VPL) {
+#pragma unroll
+                        for (int i = 0; i + 3 < VPL; i += 4) {
+                            const float4 b = *reinterpret_cast<const float4 *>(a.bias + e0 + i);
+                            v[i] += b.x;
+                            v[i + 1] += b.y;
+                            v[i + 2] += b.z;
+                            v[i + 3] += b.w;
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < VPL; ++i)
+                            if (i < count) v[i] += a.bias[e0 + i];
+                    }
                 }
             }
-        }
-        const float unit = EXACT ? 0.f : unit_of(a.sigmoid, VPL, z);
-        const bool exact = EXACT || (GROUPS && !a.bias);  // v are logits, from here on
+            const float unit = EXACT ? 0.f : unit_of(a.sigmoid, VPL, z);
+            const bool exact = EXACT || (GROUPS && !a.bias);  // v are logits, from here on
 
-        float best;
-        bool decided = true;
-        if constexpr (GROUPS) {
-            float score, mag = 0.f;
-            if (EXACT || !a.top2 || a.size == 1) {
+            float best;
+            bool decided = true;
+            if constexpr (GROUPS) {
+                float score, mag = 0.f;
+                if (EXACT || !a.top2 || a.size == 1) {
+                    best = v[0];
+#pragma unroll
+                    for (int i = 1; i < VPL; ++i) best = fmaxf(best, v[i]);
+                    score = best;
+                    for (int o = 1; o < (1 << a.shift); o <<= 1)
+                        score = fmaxf(score, __shfl_xor_sync(kAll, score, o));
+                    if (!EXACT) mag = fabsf(score);
+                } else {
+                    float b1 = -INFINITY, b2 = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < VPL; ++i) {
+                        b2 = fmaxf(b2, v[i] > b1 ? b1 : v[i]);
+                        b1 = fmaxf(b1, v[i]);
+                    }
+                    best = b1;
+                    for (int o = 1; o < (1 << a.shift); o <<= 1) {
+                        const float o1 = __shfl_xor_sync(kAll, b1, o), o2 = __shfl_xor_sync(kAll, b2, o);
+                        b2 = fmaxf(fmaxf(b2, o2), fminf(b1, o1));
+                        b1 = fmaxf(b1, o1);
+                    }
+                    // (no second number, or an excluded expert: for decide())
+                    score = group < a.G && b2 > -INFINITY ? b1 + b2 : NAN;
+                    if (!isnan(score)) mag = fabsf(b1) + fabsf(b2);
+                }
+                // a score that Gk groups reach: if no more come near it, they stay
+                float cur = score, bound = NAN;
+                for (int j = 0; j < a.Gk; ++j) {
+                    bound = warp_max(cur);
+                    if (cur == bound) cur = NAN;
+                }
+                // (a sum has the errors of its two values and its own rounding)
+                const float off = EXACT ? 0.f : 2.f * unit + 0x1.2p-22f * warp_max(mag);
+                decided = __popc(__ballot_sync(kAll, r == 0 && group < a.G && !(score < bound - off))) == a.Gk;
+                // without a bias the order inside the groups is that of the logits
+                if (!EXACT && !a.bias) {
+                    best = NAN;
+#pragma unroll
+                    for (int i = 0; i < VPL; ++i) {
+                        v[i] = i < count ? L[e0 + i] : NAN;
+                        best = fmaxf(best, v[i]);
+                    }
+                }
+                if (!(score >= bound)) {
+                    best = NAN;
+#pragma unroll
+                    for (int i = 0; i < VPL; ++i) v[i] = NAN;
+                }
+            } else {
                 best = v[0];
 #pragma unroll
                 for (int i = 1; i < VPL; ++i) best = fmaxf(best, v[i]);
-                score = best;
-                for (int o = 1; o < (1 << a.shift); o <<= 1)
-                    score = fmaxf(score, __shfl_xor_sync(kAll, score, o));
-                if (!EXACT) mag = fabsf(score);
-            } else {
-                float b1 = -INFINITY, b2 = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < VPL; ++i) {
-                    b2 = fmaxf(b2, v[i] > b1 ? b1 : v[i]);
-                    b1 = fmaxf(b1, v[i]);
-                }
-                best = b1;
-                for (int o = 1; o < (1 << a.shift); o <<= 1) {
-                    const float o1 = __shfl_xor_sync(kAll, b1, o), o2 = __shfl_xor_sync(kAll, b2, o);
-                    b2 = fmaxf(fmaxf(b2, o2), fminf(b1, o1));
-                    b1 = fmaxf(b1, o1);
-                }
-                // (no second number, or an excluded expert: for decide())
-                score = group < a.G && b2 > -INFINITY ? b1 + b2 : NAN;
-                if (!isnan(score)) mag = fabsf(b1) + fabsf(b2);
             }
-            // a score that Gk groups reach: if no more come near it, they stay
-            float cur = score, bound = NAN;
-            for (int j = 0; j < a.Gk; ++j) {
-                bound = warp_max(cur);
-                if (cur == bound) cur = NAN;
-            }
-            // (a sum has the errors of its two values and its own rounding)
-            const float off = EXACT ? 0.f : 2.f * unit + 0x1.2p-22f * warp_max(mag);
-            decided = __popc(__ballot_sync(kAll, r == 0 && group < a.G && !(score < bound - off))) == a.Gk;
-            // without a bias the order inside the groups is that of the logits
-            if (!EXACT && !a.bias) {
-                best = NAN;
-#pragma unroll
-                for (int i = 0; i < VPL; ++i) {
-                    v[i] = i < count ? L[e0 + i] : NAN;
-                    best = fmaxf(best, v[i]);
-                }
-            }
-            if (!(score >= bound)) {
-                best = NAN;
-#pragma unroll
-                for (int i = 0; i < VPL; ++i) v[i] = NAN;
-            }
-        } else {
-            best = v[0];
-#pragma unroll
-            for (int i = 1; i < VPL; ++i) best = fmaxf(best, v[i]);
-        }
 
-        // a bound that k values reach: the k-th largest distinct maximum of a lane
-        float bound = NAN;
+            // a bound that k values reach: the k-th largest distinct maximum of a lane
+            float bound = NAN;
 #pragma unroll 4
-        for (int j = 0; j < a.k; ++j) {
-            bound = warp_max(best);
-            if (best == bound) best = NAN;
-        }
-        if (isnan(bound)) bound = -INFINITY;  // fewer lanes than that: every value
-        // the values that the chosen ones are among, and those too near to rank
-        const float floor32 = exact ? bound : bound - (unit + 0x1p-21f * fabsf(bound));
-        int n = 0;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            const bool in = v[i] >= floor32;
-            const unsigned b = __ballot_sync(kAll, in);
-            if (VPL > 8 && b == 0u) continue;
-            if (in) few[n + __popc(b & below)] = {v[i], e0 + i};
-            n += __popc(b);
-        }
-        const bool listed = decided && n >= a.k && n <= 32;
-        decided = listed;
-        __syncwarp();
-        const Ranked mine = lane < n ? few[lane] : kNobody;
-        // (loops of fixed length: with n for their limit, which is uniform but not
-        // known to be, each of their warp operations took three times the instructions)
-        unsigned ahead_of_me = 0u;  // (a NaN is ahead of none)
-        auto rank = [&](int p) {
-            const unsigned b = __ballot_sync(kAll, mine.q > __shfl_sync(kAll, mine.q, p));
-            if (lane == p) ahead_of_me = b;
-        };
-#pragma unroll
-        for (int p = 0; p < 12; ++p) rank(p);
-        if (n > 12)
-#pragma unroll
-            for (int p = 12; p < 32; ++p) rank(p);
-        const int ahead = __popc(ahead_of_me);
-        const bool chosen = lane < n && ahead < a.k;
-        // equal values have the same place
-        decided &= __popc(__reduce_or_sync(kAll, lane < n ? 1u << ahead : 0u)) == n;
-        if (!exact) {
-            __syncwarp();
-            if (lane < n) few[ahead] = mine;
-            __syncwarp();
-            const bool behind = chosen && ahead + 1 < n;
-            const float next = few[behind ? ahead + 1 : 0].q;
-            decided &= !__any_sync(kAll, behind && too_near(mine.q, next, unit));
-        }
-        if (decided) write_slots(a, t, chosen, ahead, mine.id,
-                                 exact ? mine.q : chosen ? L[mine.id] : 0.f, m, z);
-        if (!decided && listed) {
-            pend.id[pending][lane] = (uint16_t)mine.id;
-            if (lane == 0) {
-                pend.t[pending] = t;
-                pend.n[pending] = n;
+            for (int j = 0; j < a.k; ++j) {
+                bound = warp_max(best);
+                if (best == bound) best = NAN;
             }
-            ++pending;
-        } else if (!decided) {
-            left |= 1u << i32;
+            if (isnan(bound)) bound = -INFINITY;  // fewer lanes than that: every value
+            // the values that the chosen ones are among, and those too near to rank
+            const float floor32 = exact ? bound : bound - (unit + 0x1p-21f * fabsf(bound));
+            int n = 0;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                const bool in = v[i] >= floor32;
+                const unsigned b = __ballot_sync(kAll, in);
+                if (VPL > 8 && b == 0u) continue;
+                if (in) few[n + __popc(b & below)] = {v[i], e0 + i};
+                n += __popc(b);
+            }
+            const bool listed = decided && n >= a.k && n <= 32;
+            decided = listed;
+            __syncwarp();
+            const Ranked mine = lane < n ? few[lane] : kNobody;
+            // (loops of fixed length: with n for their limit, which is uniform but not
+            // known to be, each of their warp operations took three times the instructions)
+            unsigned ahead_of_me = 0u;  // (a NaN is ahead of none)
+            auto rank = [&](int p) {
+                const unsigned b = __ballot_sync(kAll, mine.q > __shfl_sync(kAll, mine.q, p));
+                if (lane == p) ahead_of_me = b;
+            };
+#pragma unroll
+            for (int p = 0; p < 12; ++p) rank(p);
+            if (n > 12)
+#pragma unroll
+                for (int p = 12; p < 32; ++p) rank(p);
+            const int ahead = __popc(ahead_of_me);
+            const bool chosen = lane < n && ahead < a.k;
+            // equal values have the same place
+            decided &= __popc(__reduce_or_sync(kAll, lane < n ? 1u << ahead : 0u)) == n;
+            if (!exact) {
+                __syncwarp();
+                if (lane < n) few[ahead] = mine;
+                __syncwarp();
+                const bool behind = chosen && ahead + 1 < n;
+                const float next = few[behind ? ahead + 1 : 0].q;
+                decided &= !__any_sync(kAll, behind && too_near(mine.q, next, unit));
+            }
+            if (decided) write_slots(a, t, chosen, ahead, mine.id,
+                                     exact ? mine.q : chosen ? L[mine.id] : 0.f, m, z);
+            if (!decided && listed) {
+                pend.id[pending][lane] = (uint16_t)mine.id;
+                if (lane == 0) {
+                    pend.t[pending] = t;
+                    pend.n[pending] = n;
+                }
+                ++pending;
+            } else if (!decided) {
+                left |= 1u << i32;
+            }
         }
-    }
-    __syncwarp();
-    for (int i = 0; i < pending; ++i) settle(cold, pend, i, smem);
-    while (left) {
-        const int i = __ffs(left) - 1;
-        left &= left - 1u;
-        decide(cold, t0 + i * (int64_t)gridDim.x, smem);
-    }
+        __syncwarp();
+        for (int i = 0; i < pending; ++i) settle(cold, pend, i, smem);
+        while (left) {
+            const int i = __ffs(left) - 1;
+            left &= left - 1u;
+            decide(cold, t0 + i * (int64_t)gridDim.x, smem);
+        }
     }
 }
 

@@ -5,10 +5,15 @@ namespace moe {
 namespace {
 
 // Long batches: LANES lanes a token, 32 / LANES tokens a warp, N float4 of values a
-// lane, k <= 8, no groups.  The same steps as above, at a fraction of the
-// instructions a token, since a step of a reduction, a vote or a rank serves all of a
-// warp's tokens: the bound from the maxima of half or a quarter of a lane's values each, candidates
-// counted and placed by a prefix sum over the lanes, and two or four of them a lane.
+// lane, k <= 8.  The same steps as a warp's per token, at a fraction of the
+// instructions, since a step of a reduction, a vote or a rank serves all of a warp's
+// tokens: the bound from the maxima of a half or a quarter of a lane's values each,
+// candidates counted and placed by a prefix sum over the lanes, and four of them a
+// lane.  T = 131072, E = 128, k = 8, softmax: 32 us, 68 with a warp a token (its bytes
+// take 11); E = 256 with bias 47 and 80; E = 256, eight groups 90 and 108.  What is
+// left is instructions (0.8 of the issue slots); code that a token seldom needs is
+// kept out of the loop, which has to fit the instruction cache (49 us when it did
+// not, 26 with the present loop, for E = 64).
 constexpr int kManyK = 8, kManyFew = 32;
 constexpr int kGroupParts = 4;  // (fewer of the lanes have values then)
 
@@ -307,7 +312,8 @@ cudaError_t launch_many(const SelectArgs &a, bool exact, cudaStream_t st) {
                                      : select_many_kernel<LANES, N, false, false, GROUPS>);
     return launch_pdl(kernel, grid, dim3(32), smem, st, b, a);
 }
-// From this many tokens on; with groups of 256 experts from four times as many.
+// From this many tokens on (E = 128, k = 8: see the figures in select_takes_many);
+// with groups of 256 experts from four times as many.
 constexpr int64_t kManyTokens = 4096;
 
 }  // namespace

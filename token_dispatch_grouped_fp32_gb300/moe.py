@@ -489,20 +489,37 @@ def moe_update_balance_bias(counts, rate, balance_bias, imbalance=None, layers=N
     return _check(s, "moe_update_balance_bias", raise_on_error)
 
 
+def _on_current(device):
+    """Refuses tensors that the current device's kernels are not to touch."""
+    if device is not None and (device.type != "cuda"
+                               or device.index != torch.cuda.current_device()):
+        raise ValueError(f"the tensors are on {device}, not on the current GPU")
+
+
 def adamw_list(tensors):
     """The moe_adamw_tensor_t array of moe_adamw_step.  ``tensors``: dicts of
     "param" and "grad" (bf16 or fp32), "exp_avg" and "exp_avg_sq" (fp32, or
     float8_e4m3fn beside "exp_avg_scale" and "exp_avg_sq_scale", fp32, one for
-    256 elements), and optionally "master" (fp32) and "weight_decay".  It holds
+    256 elements), and optionally "master" (fp32) and "weight_decay".  All are on
+    one device, and none that a step writes overlaps another.  It holds
     addresses: keep the tensors alive, and build it once for buffers that stay
     where they are."""
+    tensors = list(tensors)
     rows = [_adamw_row(**t) for t in tensors]
+    devices = {t["param"].device for t in tensors}
+    if len(devices) > 1:
+        raise ValueError(f"the tensors are on one device, not on {devices}")
+    spans = sorted((x.data_ptr(), x.numel() * x.element_size()) for t in tensors
+                   for n, x in t.items() if n in _ADAMW_WRITTEN and x is not None and x.numel())
+    if any(a + size > b for (a, size), (b, _) in zip(spans, spans[1:])):
+        raise ValueError("two tensors that a step writes overlap")
     arr = (moe_adamw_tensor_t * max(1, len(rows)))(*rows)
-    arr.count = len(rows)
+    arr.count, arr.device = len(rows), devices.pop() if devices else None
     return arr
 
 
 _ADAMW_TYPES = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}
+_ADAMW_WRITTEN = ("param", "exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale", "master")
 _STATE_TYPES = {torch.float32: MOE_F32, torch.float8_e4m3fn: MOE_E4M3}
 
 
@@ -554,6 +571,7 @@ def moe_adamw_step(tensors, hyper, norm=None, scalars=None, n=None, stream=None,
     moe_clip_grad_norm, or None; ``scalars``: device memory with a
     moe_adamw_scalars_t, or None."""
     n = tensors.count if n is None else int(n)
+    _on_current(getattr(tensors, "device", None))
     s = _lib.moe_adamw_step(tensors, n, ctypes.byref(hyper), _ptr(norm), _ptr(scalars),
                             _stream(stream))
     return _check(s, "moe_adamw_step", raise_on_error)
@@ -716,8 +734,10 @@ class MoELayer:
         if imbalance is not None and (imbalance.dtype != torch.float32 or imbalance.numel() != 1
                                       or imbalance.device != self.Wr.device):
             raise ValueError(f"the imbalance is one fp32 value on {self.Wr.device}")
+        _on_current(self.Wr.device)
         side = self._other(stream, key)
         _record(side, (self.balance_bias, imbalance))
+        self._capturing(ws)
         at = moe_workspace_layout(self.config(T)).counts
         moe_update_balance_bias(ws.data_ptr() + at, rate, self.balance_bias, imbalance, layers=1,
                                 E=self.E, stream=key)
@@ -783,7 +803,7 @@ class AdamW:
     parameters; without them the bf16 values are rounded stochastically.
     ``max_norm``: the gradients count as clipped to this global norm (their
     buffers keep what they hold), which ``norm`` has after a step; a step whose
-    norm is not finite is skipped.  ``weight_decay``: one number, or one a
+    norm is not finite is counted, but leaves everything as it was.  ``weight_decay``: one number, or one a
     parameter.  ``lr`` may be changed between steps.
 
     In a captured graph (``capturable``) a step reads its number, lr and seed from
@@ -843,10 +863,13 @@ class AdamW:
 
     def step(self, stream=None):
         """One step on the given (default: current) stream."""
-        side = stream if stream is None or isinstance(stream, torch.cuda.Stream) \
-            else torch.cuda.ExternalStream(int(stream))
+        side = stream
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            side = torch.cuda.ExternalStream(int(stream)) if int(stream) \
+                else torch.cuda.default_stream()
         with _allocating_on(side):
-            if self.tensors[0]["param"].is_cuda and torch.cuda.is_current_stream_capturing():
+            _on_current(self._list.device)
+            if torch.cuda.is_current_stream_capturing():
                 if self._scalars is None:
                     raise RuntimeError("a step is captured with capturable=True")
             else:
