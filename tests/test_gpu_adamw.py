@@ -368,6 +368,41 @@ def test_the_random_numbers(moe, seed):
             check(got, x, step_of(x, s), bits)
 
 
+def test_the_moments_are_rounded_products_and_sums(moe):
+    """Bit for bit, whole blocks and the last one: 8-bit scales hang on the last bit."""
+    e = entry(1_000_003, 4, p=F32, g=F32)
+    b1, c1, b2, c2 = (torch.tensor(x, dtype=F32, device="cuda") for b in ("beta1", "beta2")
+                      for x in (HYPER[b], 1 - HYPER[b]))
+    m = e["exp_avg"] * b1 + e["grad"] * c1
+    v = e["exp_avg_sq"] * b2 + (e["grad"] * e["grad"]) * c2
+    run(moe, [e])
+    assert torch.equal(e["exp_avg"], m) and torch.equal(e["exp_avg_sq"], v)
+
+
+def test_a_random_part_is_centred_in_its_step(moe):
+    """The same for m alone, whose fp32 value two rounded products and a sum give:
+    only where the lost part and the bits' part sum to one (exactly: 2^-20 of all) may
+    either neighbour be taken.  (To 2^-20: a magnitude below 2^-6 of the scale may have
+    bits that its sum with the random part, a float below 2^-5, rounds away: 2^-30,
+    or 2^-21 of a step of 2^-9; the part itself is off by 2^-27 2^-6, 2^-24 of one.)
+    Half a number off would turn 2^-17 of them."""
+    n = 1 << 22
+    e = entry(n, 5, p=F32, g=F32, bits=8)
+    old = e["exp_avg"].float() * e["exp_avg_scale"].repeat_interleave(256)
+    b1, c1 = (torch.tensor(x, dtype=F32, device="cuda") for x in (HYPER["beta1"], 1 - HYPER["beta1"]))
+    m = old * b1 + e["grad"] * c1
+    run(moe, [e], seed=77)
+    s = e["exp_avg_scale"].double().repeat_interleave(256)
+    step = step_of(m.double(), s)
+    bits = (random_bits(torch.arange(n // 256, device="cuda"), 77) >> 8) & 0xFFFF
+    low = torch.floor(m.double().abs() / step)
+    part = m.double().abs() / step - low + (bits.double() + 0.5) / 65536
+    want = torch.copysign((low + (part >= 1)) * step, m.double())
+    off = e["exp_avg"].double() * s != want
+    assert not (off & ((part - 1).abs() > 2.0 ** -20)).any()
+    assert int(off.sum()) <= 16  # (4 expected)
+
+
 def test_streams_and_graph(moe):
     """Two lists on two streams at once; a captured step that is replayed with
     new scalars, equal to eager steps bit for bit."""

@@ -56,6 +56,7 @@ def test_without_groups(moe, T, k, E, biased, score):
 @pytest.mark.parametrize("T,E,k,G,Gk", [
     (4097, 32, 4, 8, 4), (5000, 64, 8, 8, 3), (4500, 128, 8, 4, 2), (4099, 128, 6, 8, 5),
     (4096, 128, 8, 2, 1), (16385, 256, 8, 8, 4), (16384, 256, 8, 4, 3), (17001, 256, 2, 8, 1),
+    (32768, 256, 8, 8, 4), (33001, 256, 8, 4, 3), (32769, 256, 2, 8, 1), (32790, 160, 8, 8, 4),
     (4097, 96, 4, 8, 4), (5003, 160, 6, 8, 3), (16390, 160, 8, 8, 4), (16384, 256, 8, 16, 8),
     (4096, 64, 8, 1, 1)])
 def test_with_groups(moe, T, E, k, G, Gk, biased, top2, score):

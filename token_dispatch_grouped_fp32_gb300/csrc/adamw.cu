@@ -60,6 +60,7 @@ struct Table {
 
 struct Step {
     float b1, c1, b2, c2, eps, max_norm;  // c1 = 1 - b1, c2 = 1 - b2
+    float minus_zero;
     int stochastic, skip_nonfinite;
     moe_adamw_scalars_t sc;
     const moe_adamw_scalars_t *dev;
@@ -267,8 +268,7 @@ __device__ __forceinline__ float quantise(float2 (&x)[4], uint32_t e, bool finit
         const float2 y = mul2(x[i], two(inv));
         // to a neighbouring e4m3 value (|y| <= 256).  power: 2^e <= |y|, at least 2^-6, below
         // which the steps are those from there up: a step is power / 8.  A random part
-        // of a step in [-1/2, 1/2), of 16 bits, is added to the magnitude (on average
-        // 2^-17 of a step less than nothing), and the sum
+        // of a step in (-1/2, 1/2), of 16 bits, is added to the magnitude, and the sum
         // rounded to steps by adding and taking away 1.5 * 2^23 of them.  (Four packed
         // operations; by integer sums on the bits it took seven or eight of the ALU,
         // which is what bounds this kernel.)
@@ -276,7 +276,9 @@ __device__ __forceinline__ float quantise(float2 (&x)[4], uint32_t e, bool finit
             fmaxf(__uint_as_float(__float_as_uint(y.x) & 0x7f800000u), 0x1p-6f),
             fmaxf(__uint_as_float(__float_as_uint(y.y) & 0x7f800000u), 0x1p-6f));
         const float2 f = pair_of(number<ROOT>(u[2 * i]), number<ROOT>(u[2 * i + 1]));
-        float2 part = fma2(f, two(0x1p-19f), two(-16.0625f));  // of power: -1/16 to 1/16
+        // (number + 1/2) 2^-19 - 1/16, to 2^-27: 2^23 and 1/2 do not fit one float, but
+        // 2^23 2^-19 (1 - 2^-24) lacks 2^-20
+        float2 part = fma2(f, two(0x1p-19f * (1.f - 0x1p-24f)), two(-16.0625f + 0x1p-19f));
         if (!ROOT) {  // away from zero by the same numbers on either side
             part.x = __uint_as_float(__float_as_uint(part.x) ^ (__float_as_uint(y.x) & 0x80000000u));
             part.y = __uint_as_float(__float_as_uint(part.y) ^ (__float_as_uint(y.y) & 0x80000000u));
@@ -341,6 +343,9 @@ __device__ __forceinline__ void step_chunk(const Entry &t, const Step &s, const 
             load_some(static_cast<const TS *>(t.v) + at, n, &r.v);
         }
     };
+    // a product that is rounded: the compiler fuses a packed product with the sum that
+    // takes it, for all its .rn, but not one that is a multiply-add itself
+    auto product = [&](float2 a, float b) { return fma2(a, two(b), two(s.minus_zero)); };
     const int64_t full = t.vec ? t.numel / kBlock : 0;
     for (int i = 0; b < last; ++i, b += kWarps) {
         B now;
@@ -364,8 +369,8 @@ __device__ __forceinline__ void step_chunk(const Entry &t, const Step &s, const 
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float2 gj = mul2(g[j], two(coef));
-            m[j] = add2(mul2(m[j], two(s.b1)), mul2(gj, two(s.c1)));
-            v[j] = add2(mul2(v[j], two(s.b2)), mul2(mul2(gj, gj), two(s.c2)));
+            m[j] = add2(product(m[j], s.b1), product(gj, s.c1));
+            v[j] = add2(product(v[j], s.b2), product(mul2(gj, gj), s.c2));
             r[j] = make_float2(root<SMALL>(v[j].x), root<SMALL>(v[j].y));
             const float2 d = fma2(r[j], two(sc.inv_sqrt_bc2), two(s.eps));
             const float2 q = mul2(m[j], make_float2(reciprocal(d.x), reciprocal(d.y)));
@@ -492,6 +497,7 @@ cudaError_t launch_adamw(const moe_adamw_tensor_t *ts, int64_t n, const moe_adam
     s.b2 = (float)h.beta2;
     s.c2 = (float)(1.0 - h.beta2);
     s.eps = (float)h.eps;
+    s.minus_zero = -0.f;
     s.max_norm = h.max_norm;
     s.stochastic = h.stochastic;
     s.skip_nonfinite = h.skip_nonfinite;

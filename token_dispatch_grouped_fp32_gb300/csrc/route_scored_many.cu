@@ -9,8 +9,8 @@ namespace {
 // instructions, since a step of a reduction, a vote or a rank serves all of a warp's
 // tokens: the bound from the maxima of a half or a quarter of a lane's values each,
 // candidates counted and placed by a prefix sum over the lanes, and four of them a
-// lane.  T = 131072, E = 128, k = 8, softmax: 32 us, 68 with a warp a token (its bytes
-// take 11); E = 256 with bias 47 and 80; E = 256, eight groups 90 and 108.  What is
+// lane.  T = 131072, k = 8, sigmoid with bias: E = 128 32 us, 60 with a warp a token
+// (its bytes take 11); E = 256 47 and 76; E = 128 in four groups 46 and 79.  What is
 // left is instructions (0.8 of the issue slots); code that a token seldom needs is
 // kept out of the loop, which has to fit the instruction cache (49 us when it did
 // not, 26 with the present loop, for E = 64).
@@ -312,8 +312,11 @@ cudaError_t launch_many(const SelectArgs &a, bool exact, cudaStream_t st) {
                                      : select_many_kernel<LANES, N, false, false, GROUPS>);
     return launch_pdl(kernel, grid, dim3(32), smem, st, b, a);
 }
-// From this many tokens on (E = 128, k = 8: see the figures in select_takes_many);
-// with groups of 256 experts from four times as many.
+// From this many tokens on, where there are several for each lane's place (T = 4096,
+// E = 128: 3.7 us and 4.6 with a warp a token; 2048: 2.8 and 2.7; E = 256 3.8 and 4.6,
+// 3.1 and 2.7).  Groups of 256 experts, whose lanes are fewer, from eight times as
+// many (eight groups by their maxima: T = 16384 11.1 and 11.0, 32768 17.0 and 19.1;
+// by the sum of two: 18.6 and 16.4, 26.8 and 27.0, 131072 91 and 100).
 constexpr int64_t kManyTokens = 4096;
 
 }  // namespace
@@ -326,7 +329,7 @@ bool select_takes_many(const SelectArgs &a, bool exact) {
     // that is that of the values in hand
     const int lanes = a.G <= 8 ? 8 / a.G : 0;
     return lanes > 0 && (a.G & (a.G - 1)) == 0 && a.size % (4 * lanes) == 0 && (exact || a.bias) && a.size > 1 &&
-           a.Gk * lanes * kGroupParts >= 2 * a.k && (a.E <= 128 || a.T >= 4 * kManyTokens);
+           a.Gk * lanes * kGroupParts >= 2 * a.k && (a.E <= 128 || a.T >= 8 * kManyTokens);
 }
 
 cudaError_t launch_select_many(const SelectArgs &a, bool exact, cudaStream_t st) {
