@@ -5,13 +5,13 @@
 //
 // The tensors are cut into blocks of 256 elements, the unit of an 8-bit state's
 // scale: a warp takes one, eight consecutive elements a lane, so that the block's
-// largest magnitudes are two warp reductions and every access is a vector.  Chunks
-// of 8 to 64 such blocks are dealt to the thread blocks; the tensors' addresses
+// largest magnitudes are two warp reductions and every access is a vector.  A
+// thread block takes a chunk of 8 to 256 such blocks; the tensors' addresses
 // travel as kernel parameters, as in clip.cu.
 //
-// fp32 states are bound by HBM (64 M bf16 parameters: 213 us, 0.98 of the copy
-// rate).  8-bit states by the instructions of two roundings an element: 144 us
-// (0.66; fp32 parameters, which move more, 163: 0.93).  A ring of asynchronous copies
+// fp32 states are bound by HBM (64 M bf16 parameters: 210 us, 0.99 of the copy
+// rate).  8-bit states by the instructions of two roundings an element: 127 us
+// (0.75; fp32 parameters, which move more, 155: 0.98; 1.4 G bf16 ones 0.83).  A ring of asynchronous copies
 // into shared memory took 148 to 155 us, values of the next block held in registers
 // 161 to 205, and a prefetch into L2 158: the loads are not what it waits for.
 //
@@ -33,12 +33,15 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBlock = 256;                // elements under one scale
-// Blocks a thread block takes at a time, one to eight a warp: as many as leave two
-// rounds of resident thread blocks (300 small tensors: 5.1 us with one, 10.3 with
-// eight; 64 M parameters, 8 bits: 180 us with one, 149 with eight).
-constexpr int kMostBlocks = 8 * kWarps;
-constexpr int64_t kRounds = 2 * 4 * 152;
-constexpr int kGrid = 152 * 8;
+// Blocks a chunk, one to 32 a warp.  Every chunk has to be found and its scales
+// read, and in the last round of chunks some multiprocessors have none: the first costs
+// blocks / chunk, the second a chunk, and their sum is least where the chunk
+// goes by the root of the blocks (8-bit states: 64 M parameters 131 us with chunks
+// of 64, 132 of 128, 141 of 256; 1.4 G 2741 of 64, 2607 of 256; 3 M in ragged tensors 10.9
+// of 8, 9.5 of 16).  A thread block for each: 64 M took 137 us with a grid of eight
+// an SM, which cannot even out what they take.
+constexpr int kMostBlocks = 32 * kWarps;
+constexpr int kSquare = 76;
 constexpr int kTable = 300;                // tensors per launch
 constexpr int kMapped = 1024;              // chunks with a map of their own
 
@@ -86,8 +89,10 @@ __device__ __forceinline__ Key block_key(int64_t block, uint32_t lo, uint32_t hi
     x = fold(x + hi + (uint32_t)((uint64_t)block >> 32), kK3);
     return {x, fold(x ^ kK0, kK3)};
 }
+// (with the highest bit of m's flipped, which costs nothing here)
+constexpr uint32_t kFlip = 0x00800000u;
 __device__ __forceinline__ uint32_t random_bits(Key k, int place) {
-    return fold(fold(k.x + kK0 * (uint32_t)place, kK2) ^ k.y, kK1);
+    return fold(fold(k.x + kK0 * (uint32_t)place, kK2) ^ k.y, kK1) ^ kFlip;
 }
 
 // Two fp32 values to bf16, up or down by 16 random bits each (the low ones of u and
@@ -103,6 +108,13 @@ __device__ __forceinline__ uint32_t bf16_pair(float2 v, uint32_t u, uint32_t w) 
 __device__ __forceinline__ float max_abs(float a, float b, float c) {
     float d;
     asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// The smallest magnitude of three.
+__device__ __forceinline__ float min_abs(float a, float b, float c) {
+    float d;
+    asm("min.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
 
@@ -247,25 +259,24 @@ __device__ __forceinline__ uint32_t root_scale_exponent(uint32_t largest) {
 }
 
 // 16 random bits (of a root: the high ones; else bits 8 to 23) as the bits of
-// 2^23 + their number, in one instruction.
+// 2^23 + their number.
 template <bool ROOT> __device__ __forceinline__ uint32_t number(uint32_t u) {
-    return __byte_perm(u, 0x4B000000u, ROOT ? 0x7432 : 0x7421);
+    return __byte_perm(u ^ kFlip, 0x4B000000u, ROOT ? 0x7432 : 0x7421);
+}
+// ... and as a signed fraction of 2^32, centred: 2^16 (number - 2^15 + 1/2).
+template <bool ROOT> __device__ __forceinline__ int centred(uint32_t u) {
+    return ROOT ? (int)((u & 0xffff0000u) ^ (0x80008000u ^ kFlip)) : (int)__byte_perm(u, 0x8000u, 0x2154);
 }
 
-// A block's states to 8 bits, in place, by a scale of biased exponent e.  x: 0 beyond
-// the tensor's end; u: the elements' random bits.  ROOT: the roots, no positive one
-// of which becomes zero.
-template <bool ROOT>
-__device__ __forceinline__ float quantise(float2 (&x)[4], uint32_t e, bool finite, const uint32_t (&u)[8]) {
-    const float inv = __uint_as_float((254u - e) << 23), scale = __uint_as_float(e << 23);
-    if (!finite) {  // uniform: a NaN or an infinity in the block
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = mul2(x[i], two(inv));
-        return scale;
-    }
+// (a block with magnitudes below the normal ones; apart, for its registers)
+struct Values {
+    float2 x[4];
+    uint32_t u[8];
+};
+template <bool ROOT> __device__ __noinline__ Values small_ones(Values a) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float2 y = mul2(x[i], two(inv));
+        const float2 y = a.x[i];
         // to a neighbouring e4m3 value (|y| <= 256).  power: 2^e <= |y|, at least 2^-6, below
         // which the steps are those from there up: a step is power / 8.  A random part
         // of a step in (-1/2, 1/2), of 16 bits, is added to the magnitude, and the sum
@@ -275,7 +286,7 @@ __device__ __forceinline__ float quantise(float2 (&x)[4], uint32_t e, bool finit
         const float2 power = make_float2(
             fmaxf(__uint_as_float(__float_as_uint(y.x) & 0x7f800000u), 0x1p-6f),
             fmaxf(__uint_as_float(__float_as_uint(y.y) & 0x7f800000u), 0x1p-6f));
-        const float2 f = pair_of(number<ROOT>(u[2 * i]), number<ROOT>(u[2 * i + 1]));
+        const float2 f = pair_of(number<ROOT>(a.u[2 * i]), number<ROOT>(a.u[2 * i + 1]));
         // (number + 1/2) 2^-19 - 1/16, to 2^-27: 2^23 and 1/2 do not fit one float, but
         // 2^23 2^-19 (1 - 2^-24) lacks 2^-20
         float2 part = fma2(f, two(0x1p-19f * (1.f - 0x1p-24f)), two(-16.0625f + 0x1p-19f));
@@ -290,8 +301,37 @@ __device__ __forceinline__ float quantise(float2 (&x)[4], uint32_t e, bool finit
             const float2 l = mul2(least, two(0x1p-9f));
             q = make_float2(fmaxf(q.x, l.x), fmaxf(q.y, l.y));
         }
-        x[i] = q;
+        a.x[i] = q;
     }
+    return a;
+}
+
+// A block's states to 8 bits, in place, by a scale of biased exponent e.  x: 0 beyond
+// the tensor's end; u: the elements' random bits.
+// ROOT: the roots, no positive one of which becomes zero.
+template <bool ROOT>
+__device__ __forceinline__ float quantise(float2 (&x)[4], uint32_t e, bool finite, const uint32_t (&u)[8]) {
+    const float inv = __uint_as_float((254u - e) << 23), scale = __uint_as_float(e << 23);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = mul2(x[i], two(inv));
+    if (!finite) return scale;  // uniform: a NaN or an infinity in the block
+    float low = min_abs(x[0].x, x[0].y, x[1].x);
+    low = min_abs(low, x[1].y, x[2].x);
+    low = min_abs(low, x[2].y, x[3].x);
+    low = min_abs(low, low, x[3].y);
+    if (__all_sync(kAll, low >= 0x1p-6f)) {
+        // Normal numbers of e4m3, nineteen blocks of twenty: their last 20 bits are a part
+        // of a step, and a random one in (-1/2, 1/2) is added to them; the conversion
+        // rounds to the nearest.  (64 M bf16 parameters 137 us, by the way below alone 144.)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            x[i] = pair_of(__float_as_uint(x[i].x) + (uint32_t)(centred<ROOT>(u[2 * i]) >> 12),
+                           __float_as_uint(x[i].y) + (uint32_t)(centred<ROOT>(u[2 * i + 1]) >> 12));
+        return scale;
+    }
+    const Values a = small_ones<ROOT>({{x[0], x[1], x[2], x[3]}, {u[0], u[1], u[2], u[3], u[4], u[5], u[6], u[7]}});
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = a.x[i];
     return scale;
 }
 
@@ -317,7 +357,7 @@ __device__ __forceinline__ void step_chunk(const Entry &t, const Step &s, const 
     const float decay = fmaf(-sc.lr, t.wd, 1.f);
     const bool round_p = sizeof(TP) == 2 && s.stochastic;
     // the key and the scales of block b + i kWarps, in lane i (a scale that each block
-    // waited for itself cost a round to memory: 64 M bf16 parameters 187 us, so 155)
+    // waited for itself cost a round to memory: 64 M bf16 parameters 187 us, then 155)
     const int64_t mine = b + lane * kWarps;
     float ms = 0.f, rs = 0.f;
     if (SMALL && mine < last) {
@@ -386,44 +426,46 @@ __device__ __forceinline__ void step_chunk(const Entry &t, const Step &s, const 
 #pragma unroll
             for (int j = 0; j < 8; ++j) u[j] = random_bits(key, 8 * lane + j);
         }
+        // (each is stored as soon as it is known: registers)
+        const int64_t at = b * kBlock + 8 * lane;
+        const int n = (int)max((int64_t)0, min((int64_t)8, t.numel - at));
+        auto put = [&](auto *to, const auto &x) {
+            if (b < full) x.store(to + at);
+            else store_some(to + at, n, x);
+        };
         Eight<TP> op;
-        if constexpr (sizeof(TP) == 2) {
-            if (round_p)
+        if (sizeof(TP) == 2 && round_p) {
+            if constexpr (sizeof(TP) == 2)
                 op.c = make_uint4(bf16_pair(p[0], u[0], u[1]), bf16_pair(p[1], u[2], u[3]),
                                   bf16_pair(p[2], u[4], u[5]), bf16_pair(p[3], u[6], u[7]));
-            else
-                pack(p, &op);
         } else {
             pack(p, &op);
         }
-        Eight<__nv_bfloat16> copy;  // MASTER
-        if constexpr (MASTER) pack(p, &copy);
+        put(stepped, op);
+        if constexpr (MASTER) {
+            Eight<__nv_bfloat16> copy;
+            pack(p, &copy);
+            put(static_cast<__nv_bfloat16 *>(t.p), copy);
+        }
+        Eight<TS> state;
         if constexpr (SMALL) {
             const uint32_t largest_m = __reduce_max_sync(kAll, __float_as_uint(top_m));
             const uint32_t largest_v = __reduce_max_sync(kAll, __float_as_uint(top_v));
             const float new_ms = quantise<false>(m, scale_exponent(largest_m), largest_m < 0x7f800000u, u);
+            pack(m, &state);
+            put(static_cast<TS *>(t.m), state);
             const float new_rs = quantise<true>(r, root_scale_exponent(largest_v), largest_v < 0x7f800000u, u);
+            pack(r, &state);
+            put(static_cast<TS *>(t.v), state);
             if (lane == i) {
                 ms = new_ms;
                 rs = new_rs;
             }
-        }
-        Eight<TS> om, ov;
-        pack(m, &om);
-        if constexpr (SMALL) pack(r, &ov);
-        else pack(v, &ov);
-        const int64_t at = b * kBlock + 8 * lane;
-        if (b < full) {
-            op.store(stepped + at);
-            if constexpr (MASTER) copy.store(static_cast<__nv_bfloat16 *>(t.p) + at);
-            om.store(static_cast<TS *>(t.m) + at);
-            ov.store(static_cast<TS *>(t.v) + at);
         } else {
-            const int n = (int)max((int64_t)0, min((int64_t)8, t.numel - at));
-            store_some(stepped + at, n, op);
-            if constexpr (MASTER) store_some(static_cast<__nv_bfloat16 *>(t.p) + at, n, copy);
-            store_some(static_cast<TS *>(t.m) + at, n, om);
-            store_some(static_cast<TS *>(t.v) + at, n, ov);
+            pack(m, &state);
+            put(static_cast<TS *>(t.m), state);
+            pack(v, &state);
+            put(static_cast<TS *>(t.v), state);
         }
     }
     if constexpr (SMALL) {
@@ -434,9 +476,9 @@ __device__ __forceinline__ void step_chunk(const Entry &t, const Step &s, const 
     }
 }
 
-// Blocks an SM: with 8-bit states four (three took 156 us for 64 M parameters, five,
-// for which registers spill, 163, four 146); with fp32 states three (213 us against
-// 236 with four, whose accesses are spread over more of the memory's rows).
+// Blocks an SM: with 8-bit states four (64 M parameters 137 us; three took 152, and
+// five, for which registers spill, 153); with fp32 states three (213 us against 236
+// with four, whose accesses are spread over more of the memory's rows).
 template <bool SMALL>
 __global__ void __launch_bounds__(kThreads, SMALL ? 4 : 3)
 adamw_kernel(const __grid_constant__ Table tab, const __grid_constant__ Step s) {
@@ -449,28 +491,27 @@ adamw_kernel(const __grid_constant__ Table tab, const __grid_constant__ Step s) 
         coef = s.max_norm / (norm + 1e-6f);
         coef = coef > 1.f ? 1.f : coef;  // a NaN norm stays NaN
     }
-    for (int c = blockIdx.x; c < tab.chunks; c += gridDim.x) {
-        int lo = 0, hi = tab.n - 1;
-        if (tab.mapped) lo = hi = tab.tensor_of[c];
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (tab.t[mid].end > c) hi = mid; else lo = mid + 1;
-        }
-        const Entry &t = tab.t[lo];
-        const int64_t blocks = (t.numel + kBlock - 1) / kBlock;
-        const int64_t all = (blocks + tab.chunk_blocks - 1) / tab.chunk_blocks;
-        const int64_t first = (c - (t.end - all)) * tab.chunk_blocks;
-        const int64_t last = min(blocks, first + tab.chunk_blocks);
-        if (!t.p_bf16) {
-            if (t.g_bf16) step_chunk<float, __nv_bfloat16, false, SMALL>(t, s, sc, coef, first, last);
-            else step_chunk<float, float, false, SMALL>(t, s, sc, coef, first, last);
-        } else if (!t.master) {
-            if (t.g_bf16) step_chunk<__nv_bfloat16, __nv_bfloat16, false, SMALL>(t, s, sc, coef, first, last);
-            else step_chunk<__nv_bfloat16, float, false, SMALL>(t, s, sc, coef, first, last);
-        } else {
-            if (t.g_bf16) step_chunk<float, __nv_bfloat16, true, SMALL>(t, s, sc, coef, first, last);
-            else step_chunk<float, float, true, SMALL>(t, s, sc, coef, first, last);
-        }
+    const int c = blockIdx.x;
+    int lo = 0, hi = tab.n - 1;
+    if (tab.mapped) lo = hi = tab.tensor_of[c];
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (tab.t[mid].end > c) hi = mid; else lo = mid + 1;
+    }
+    const Entry &t = tab.t[lo];
+    const int64_t blocks = (t.numel + kBlock - 1) / kBlock;
+    const int64_t all = (blocks + tab.chunk_blocks - 1) / tab.chunk_blocks;
+    const int64_t first = (c - (t.end - all)) * tab.chunk_blocks;
+    const int64_t last = min(blocks, first + tab.chunk_blocks);
+    if (!t.p_bf16) {
+        if (t.g_bf16) step_chunk<float, __nv_bfloat16, false, SMALL>(t, s, sc, coef, first, last);
+        else step_chunk<float, float, false, SMALL>(t, s, sc, coef, first, last);
+    } else if (!t.master) {
+        if (t.g_bf16) step_chunk<__nv_bfloat16, __nv_bfloat16, false, SMALL>(t, s, sc, coef, first, last);
+        else step_chunk<__nv_bfloat16, float, false, SMALL>(t, s, sc, coef, first, last);
+    } else {
+        if (t.g_bf16) step_chunk<float, __nv_bfloat16, true, SMALL>(t, s, sc, coef, first, last);
+        else step_chunk<float, float, true, SMALL>(t, s, sc, coef, first, last);
     }
 }
 
@@ -508,7 +549,9 @@ cudaError_t launch_adamw(const moe_adamw_tensor_t *ts, int64_t n, const moe_adam
     int64_t blocks = 0;
     for (int64_t i = 0; i < n; ++i) blocks += blocks_of(ts[i].numel);
     tab.chunk_blocks = kWarps;
-    while (tab.chunk_blocks < kMostBlocks && blocks > kRounds * tab.chunk_blocks) tab.chunk_blocks *= 2;
+    while (tab.chunk_blocks < kMostBlocks &&
+           (int64_t)tab.chunk_blocks * tab.chunk_blocks * kSquare < blocks)
+        tab.chunk_blocks *= 2;
     for (const bool small : {false, true}) {
         int64_t block0 = 0, i = 0;
         while (i < n) {
@@ -530,7 +573,7 @@ cudaError_t launch_adamw(const moe_adamw_tensor_t *ts, int64_t n, const moe_adam
             tab.chunks = end;
             tab.mapped = end <= kMapped;
             const cudaError_t e = launch_pdl(small ? adamw_kernel<true> : adamw_kernel<false>,
-                                             dim3(std::min(kGrid, end)), dim3(kThreads), 0, st, tab, s);
+                                             dim3(end), dim3(kThreads), 0, st, tab, s);
             if (e != cudaSuccess) return e;
         }
     }
