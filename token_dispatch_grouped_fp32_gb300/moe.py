@@ -509,9 +509,17 @@ def adamw_list(tensors):
     devices = {t["param"].device for t in tensors}
     if len(devices) > 1:
         raise ValueError(f"the tensors are on one device, not on {devices}")
-    spans = sorted((x.data_ptr(), x.numel() * x.element_size()) for t in tensors
-                   for n, x in t.items() if n in _ADAMW_WRITTEN and x is not None and x.numel())
-    if any(a + size > b for (a, size), (b, _) in zip(spans, spans[1:])):
+    spans = []  # of what a step writes
+    for p, _, m, v, ms, rs, master, n, kind, _, state, _ in rows:
+        if n == 0:
+            continue
+        at = 4 if state == MOE_F32 else 1
+        spans += [(p, p + n * (4 if kind == MOE_F32 else 2)), (m, m + n * at), (v, v + n * at)]
+        spans += [(s, s + -(-n // ADAMW_BLOCK) * 4) for s in (ms, rs) if s is not None]
+        if master is not None:
+            spans.append((master, master + 4 * n))
+    spans.sort()
+    if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
         raise ValueError("two tensors that a step writes overlap")
     arr = (moe_adamw_tensor_t * max(1, len(rows)))(*rows)
     arr.count, arr.device = len(rows), devices.pop() if devices else None
@@ -519,7 +527,6 @@ def adamw_list(tensors):
 
 
 _ADAMW_TYPES = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}
-_ADAMW_WRITTEN = ("param", "exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale", "master")
 _STATE_TYPES = {torch.float32: MOE_F32, torch.float8_e4m3fn: MOE_E4M3}
 
 
