@@ -123,3 +123,20 @@ def test_captured_long_batch(moe):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(idx.long(), scored_ref.select_many(L, bias, 8, True, 1, 1, False))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("kind", ["none", "zero", "steps"])
+@pytest.mark.parametrize("T,E,k,G,Gk", [(300, 256, 8, 1, 1), (4200, 256, 8, 8, 4), (5000, 128, 8, 1, 1),
+                                        (300, 1000, 32, 1, 1), (300, 1000, 31, 20, 9), (4100, 60, 3, 1, 1),
+                                        (300, 33, 32, 1, 1), (300, 40, 5, 2, 1)])
+def test_padded_batches(moe, T, E, k, G, Gk, kind, score):
+    """Rows of equal logits, as tokens of zeros give: nothing but ties, which go to
+    the lowest ids, or the bias alone decides."""
+    L = logits(T, E, T + E)
+    L[T // 3:T // 2] = 0.0
+    L[T // 2:T // 2 + 20] = -0.0
+    L[T - 20:] = 1.75
+    L[T - 40:T - 20, ::2] = L[T - 40:T - 20, 1:2]
+    bias = {"none": None, "zero": torch.zeros(E, device="cuda"), "steps": steps_bias(E, E)}[kind]
+    check(moe, L, bias, k, score, G, Gk, kind != "none")

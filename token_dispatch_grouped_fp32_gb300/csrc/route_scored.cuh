@@ -61,7 +61,6 @@ __device__ __forceinline__ float rcp_fast(float x) {
 }
 constexpr float kLog2e = 1.4426950408889634f;
 
-
 // A candidate, or a slot of the selection.
 struct __align__(8) Ranked {
     float q;
@@ -98,10 +97,12 @@ __device__ __forceinline__ double value_of(long long key) {
         key >= 0 ? key : (long long)(0x8000000000000000ull - (unsigned long long)key));
 }
 
-// The code from here to write_chosen runs for a token in a thousand: mostly it is
-// read from memory for the one time that a multiprocessor runs it, so it is kept short, with
-// loops as they stand.
-__device__ __noinline__ double exp64(double x) { return exp(x); }
+// The code from here to write_chosen runs for a token in a thousand, and for those of a
+// padded batch, which are all ties: mostly it is read from memory for the one time that
+// a multiprocessor runs it, so it is kept short, with loops as they stand.
+
+// (a padded row's logits are alike, and most often 0)
+__device__ __noinline__ double exp64(double x) { return x == 0.0 ? 1.0 : exp(x); }
 
 // sum of exp(L - m) over a row
 __device__ __noinline__ double softmax_sum64(const float *L, int E, float m) {
@@ -179,9 +180,14 @@ __device__ __noinline__ unsigned groups64(const SelectArgs &a, const float *L, f
     long long key = kNaNKey;
     if (is) {
         long long b1 = kNaNKey, b2 = kNaNKey;
+        int p = 0, end = n;  // the first of the group's experts
 #pragma unroll 1
-        for (int p = 0; p < n; ++p) {
-            if (group_of(a, u.id[p]) != lane) continue;
+        while (p < end) {
+            const int mid = (p + end) >> 1;
+            if (u.id[mid] < lane * a.size) p = mid + 1; else end = mid;
+        }
+#pragma unroll 1
+        for (; p < n && u.id[p] < (lane + 1) * a.size; ++p) {
             const long long v = u.key[p];
             if (v > b1) {
                 b2 = b1;
@@ -263,9 +269,62 @@ __device__ __forceinline__ void softmax32(const float *L, int E, float *m, float
     *z = warp_sum(sum);
 }
 
+// Order-preserving whole-number image of a number, and back.
+__device__ __forceinline__ int key32(float v) {
+    const int b = __float_as_int(v + 0.f);
+    return b >= 0 ? b : (int)(0x80000000u - (unsigned)b);
+}
+__device__ __forceinline__ float value32(int key) {
+    return __int_as_float(key >= 0 ? key : (int)(0x80000000u - (unsigned)key));
+}
+__device__ __forceinline__ int largest(int v) { return __reduce_max_sync(kAll, v); }
+__device__ __forceinline__ long long largest(long long v) {
+    const int hi = __reduce_max_sync(kAll, (int)(v >> 32));
+    const unsigned lo = __reduce_max_sync(kAll, (int)(v >> 32) == hi ? (unsigned)v : 0u);
+    return (long long)(((unsigned long long)(unsigned)hi << 32) | lo);
+}
+// The `rounds` largest of more than 32 keys, one after the other, equal ones by id: the
+// first k to u.slot.  Lane r returns the r-th; *last: the last one.  The keys taken are
+// lost.  (Many candidates are ties, as in a padded row: ranking each against all
+// others took 577 us for T = 8192, E = 256, half of them padded; now 38.)
+template <typename K>
+__device__ __noinline__ K pick(int k, int n, int rounds, K *key, const Scratch &u, K *last) {
+    const int lane = threadIdx.x & 31;
+    constexpr K kTaken = sizeof(K) == 4 ? (K)INT32_MIN : (K)INT64_MIN;
+    K mine = kTaken, best = kTaken;
+    int at = 0;
+    auto scan = [&] {
+        best = kTaken;
+#pragma unroll 1
+        for (int p = lane; p < n; p += 32) {
+            const K v = key[p];
+            if (v > best) {
+                best = v;
+                at = p;
+            }
+        }
+    };
+    scan();
+#pragma unroll 1
+    for (int r = 0; r < rounds; ++r) {
+        const K top = largest(best);
+        const int p = __reduce_min_sync(kAll, best == top ? at : INT32_MAX);
+        if (lane == r) mine = top;
+        *last = top;
+        if ((p & 31) == lane) {
+            if (r < k) u.slot[r] = u.id[p];
+            key[p] = kTaken;
+            scan();
+        }
+        __syncwarp();
+    }
+    return mine;
+}
+
 // Ranks of the n experts in u.id by u.key, equal ones by id: the first k to u.slot.
 __device__ __forceinline__ void rank64(int k, int n, const Scratch &u) {
-    for (int p = threadIdx.x & 31; p < n; p += 32) {
+    const int p = threadIdx.x & 31;  // n <= 32
+    if (p < n) {
         const long long v = u.key[p];
         const int id = u.id[p];
         int ahead = 0;
@@ -363,26 +422,43 @@ __device__ __noinline__ void decide(const SelectArgs &a, int64_t t, unsigned cha
     const float floor32 = exact ? bound : bound - (unit + 0x1p-21f * fabsf(bound));
     const int n = list_experts(E, u, [&](int e) { return stays(e) && !(u.row[min(e, E - 1)] < floor32); });
     bool open = false;
-    {
+    if (n <= 32) {
+        const float q = lane < n ? u.row[u.id[lane]] : 0.f;
+        int ahead = 0;
+#pragma unroll 1
+        for (int o = 0; o < n; ++o) {
+            const float x = u.row[u.id[o]];
+            if (x > q || (x == q && o < lane)) ++ahead;
+            if (!exact && o != lane && x >= q) open |= too_near(x, q, unit);
+        }
+        open |= isnan(q);  // (for the 64-bit keys)
+        open &= lane < n;
+        if (lane < n && ahead < a.k) u.slot[ahead] = u.id[lane];
+    } else {
+        int *key = reinterpret_cast<int *>(u.key);
 #pragma unroll 1
         for (int p = lane; p < n; p += 32) {
             const float q = u.row[u.id[p]];
-            int ahead = 0;
-#pragma unroll 1
-            for (int o = 0; o < n; ++o) {
-                const float x = u.row[u.id[o]];
-                if (x > q || (x == q && o < p)) ++ahead;
-                if (!exact && o != p && x >= q) open |= too_near(x, q, unit);
-            }
-            if (isnan(q)) open = true;  // (for the 64-bit keys)
-            else if (ahead < a.k) u.slot[ahead] = u.id[p];
+            open |= isnan(q);
+            key[p] = key32(q);
         }
-        open = __any_sync(kAll, open);
         __syncwarp();
+        if (!__any_sync(kAll, open)) {
+            int last;
+            const int rounds = min(n, a.k + 1);
+            const int top = pick(a.k, n, rounds, key, u, &last);
+            const int next = __shfl_down_sync(kAll, top, 1);
+            if (!exact && lane + 1 < rounds)
+                open = too_near(value32(top), value32(lane == 31 ? last : next), unit);
+        }
     }
+    open = __any_sync(kAll, open);
+    __syncwarp();
     if (open) {
         values64(a, L, m, exact, n, u);
-        rank64(a.k, n, u);
+        long long last;
+        if (n <= 32) rank64(a.k, n, u);
+        else pick(a.k, n, a.k, u.key, u, &last);
     }
     write_chosen(a, t, L, m, z, u);
 }
