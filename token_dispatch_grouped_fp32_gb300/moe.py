@@ -162,6 +162,8 @@ def _status_name(status: int) -> str:
 # as plain ints, and the current stream is read as a raw handle where torch
 # has one (2.5 us less a call than through a Stream object).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+_started = False  # torch has brought up CUDA: the raw calls do
 
 
 def _ptr(t):
@@ -175,9 +177,14 @@ def _ptr(t):
 
 
 def _stream(stream):
+    global _started
     if stream is None:
+        if _started:
+            return _raw_stream(_raw_device())
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            device = torch.cuda.current_device()
+            _started = _raw_device is not None
+            return _raw_stream(device)
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -410,7 +417,7 @@ def router(score="softmax", groups: int = 1, topk_groups: int | None = None, gro
 def moe_route_scored(cfg, router, x, Wr, logit_bias, balance_bias, logits, topk_idx, topk_w, ws=None,
                      ws_bytes=None, stream=None, raise_on_error=True):
     s = _lib.moe_route_scored(
-        ctypes.byref(cfg), ctypes.byref(router), _ptr(x), _ptr(Wr), _ptr(logit_bias),
+        cfg, router, _ptr(x), _ptr(Wr), _ptr(logit_bias),
         _ptr(balance_bias), _ptr(logits), _ptr(topk_idx), _ptr(topk_w), _ptr(ws),
         _bytes(ws, ws_bytes), _stream(stream))
     return _check(s, "moe_route_scored", raise_on_error)
@@ -418,30 +425,28 @@ def moe_route_scored(cfg, router, x, Wr, logit_bias, balance_bias, logits, topk_
 
 def moe_route_scored_from_logits(cfg, router, logits, balance_bias, topk_idx, topk_w, stream=None,
                                  raise_on_error=True):
-    s = _lib.moe_route_scored_from_logits(ctypes.byref(cfg), ctypes.byref(router), _ptr(logits),
-                                          _ptr(balance_bias), _ptr(topk_idx), _ptr(topk_w),
-                                          _stream(stream))
+    s = _lib.moe_route_scored_from_logits(cfg, router, _ptr(logits), _ptr(balance_bias),
+                                          _ptr(topk_idx), _ptr(topk_w), _stream(stream))
     return _check(s, "moe_route_scored_from_logits", raise_on_error)
 
 
 def moe_route_scored_from_logits_backward(cfg, router, logits, topk_idx, topk_w, dtopk_w, dlogits,
                                           stream=None, raise_on_error=True):
     s = _lib.moe_route_scored_from_logits_backward(
-        ctypes.byref(cfg), ctypes.byref(router), _ptr(logits), _ptr(topk_idx), _ptr(topk_w),
+        cfg, router, _ptr(logits), _ptr(topk_idx), _ptr(topk_w),
         _ptr(dtopk_w), _ptr(dlogits), _stream(stream))
     return _check(s, "moe_route_scored_from_logits_backward", raise_on_error)
 
 
 def moe_route_scored_backward_workspace_size(cfg: moe_config_t, router: moe_router_t) -> int:
-    return int(_lib.moe_route_scored_backward_workspace_size(ctypes.byref(cfg),
-                                                             ctypes.byref(router)))
+    return int(_lib.moe_route_scored_backward_workspace_size(cfg, router))
 
 
 def moe_route_scored_backward(cfg, router, x, Wr, logits, topk_idx, topk_w, dtopk_w, dx_in, dlogits,
                               dWr, dlogit_bias, dx, ws, ws_bytes=None, stream=None,
                               raise_on_error=True):
     s = _lib.moe_route_scored_backward(
-        ctypes.byref(cfg), ctypes.byref(router), _ptr(x), _ptr(Wr), _ptr(logits), _ptr(topk_idx),
+        cfg, router, _ptr(x), _ptr(Wr), _ptr(logits), _ptr(topk_idx),
         _ptr(topk_w), _ptr(dtopk_w), _ptr(dx_in), _ptr(dlogits), _ptr(dWr), _ptr(dlogit_bias),
         _ptr(dx), _ptr(ws), _bytes(ws, ws_bytes), _stream(stream))
     return _check(s, "moe_route_scored_backward", raise_on_error)
@@ -450,21 +455,21 @@ def moe_route_scored_backward(cfg, router, x, Wr, logits, topk_idx, topk_w, dtop
 def moe_forward_scored(cfg, router, x, Wr, logit_bias, balance_bias, W_gate_up, W_down, out, ws,
                        ws_bytes=None, stream=None, raise_on_error=True):
     s = _lib.moe_forward_scored(
-        ctypes.byref(cfg), ctypes.byref(router), _ptr(x), _ptr(Wr), _ptr(logit_bias),
+        cfg, router, _ptr(x), _ptr(Wr), _ptr(logit_bias),
         _ptr(balance_bias), _ptr(W_gate_up), _ptr(W_down), _ptr(out), _ptr(ws),
         _bytes(ws, ws_bytes), _stream(stream))
     return _check(s, "moe_forward_scored", raise_on_error)
 
 
 def moe_backward_scored_workspace_size(cfg: moe_config_t, router: moe_router_t) -> int:
-    return int(_lib.moe_backward_scored_workspace_size(ctypes.byref(cfg), ctypes.byref(router)))
+    return int(_lib.moe_backward_scored_workspace_size(cfg, router))
 
 
 def moe_backward_scored(cfg, router, x, Wr, W_gate_up, W_down, fwd_ws, dout, dx, dWr, dlogit_bias,
                         dW_gate_up, dW_down, ws, fwd_ws_bytes=None, ws_bytes=None, stream=None,
                         raise_on_error=True):
     s = _lib.moe_backward_scored(
-        ctypes.byref(cfg), ctypes.byref(router), _ptr(x), _ptr(Wr), _ptr(W_gate_up), _ptr(W_down),
+        cfg, router, _ptr(x), _ptr(Wr), _ptr(W_gate_up), _ptr(W_down),
         _ptr(fwd_ws), _bytes(fwd_ws, fwd_ws_bytes), _ptr(dout), _ptr(dx), _ptr(dWr),
         _ptr(dlogit_bias), _ptr(dW_gate_up), _ptr(dW_down), _ptr(ws), _bytes(ws, ws_bytes),
         _stream(stream))
@@ -477,9 +482,10 @@ def moe_update_balance_bias(counts, rate, balance_bias, imbalance=None, layers=N
     fp32, ``imbalance`` [layers] fp32 or None (``layers`` and ``E`` are taken
     from counts where they are not given)."""
     if E is None:
-        E, layers = counts.shape[-1], counts.numel() // max(1, counts.shape[-1])
+        shape = counts.shape
+        E, layers = shape[-1], counts.numel() // max(1, shape[-1])
         if counts.dtype != torch.int32 or balance_bias.dtype != torch.float32 \
-                or balance_bias.shape != counts.shape:
+                or balance_bias.shape != shape:
             raise ValueError("counts are int32, the balance bias fp32 of the same shape")
         if imbalance is not None and (imbalance.dtype != torch.float32
                                       or imbalance.numel() != layers):
@@ -567,7 +573,7 @@ def adamw_hyper(lr, beta1=0.9, beta2=0.95, eps=1e-8, step=1, seed=0, max_norm=0.
 
 def moe_adamw_scalars(hyper, raise_on_error=True) -> moe_adamw_scalars_t:
     out = moe_adamw_scalars_t()
-    _check(_lib.moe_adamw_scalars(ctypes.byref(hyper), ctypes.byref(out)), "moe_adamw_scalars",
+    _check(_lib.moe_adamw_scalars(hyper, ctypes.byref(out)), "moe_adamw_scalars",
            raise_on_error)
     return out
 
@@ -579,7 +585,7 @@ def moe_adamw_step(tensors, hyper, norm=None, scalars=None, n=None, stream=None,
     moe_adamw_scalars_t, or None."""
     n = tensors.count if n is None else int(n)
     _on_current(getattr(tensors, "device", None))
-    s = _lib.moe_adamw_step(tensors, n, ctypes.byref(hyper), _ptr(norm), _ptr(scalars),
+    s = _lib.moe_adamw_step(tensors, n, hyper, _ptr(norm), _ptr(scalars),
                             _stream(stream))
     return _check(s, "moe_adamw_step", raise_on_error)
 
