@@ -515,6 +515,21 @@ adamw_kernel(const __grid_constant__ Table tab, const __grid_constant__ Step s) 
     }
 }
 
+// launch_pdl without its copy of the 28 KB of parameters (0.4 us a call).
+cudaError_t launch(void (*kernel)(Table, Step), int grid, Table &tab, Step &s, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    void *args[] = {&tab, &s};
+    return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(kernel), args);
+}
+
 int64_t blocks_of(int64_t numel) { return (numel + kBlock - 1) / kBlock; }
 
 bool vectors(const moe_adamw_tensor_t &t) {
@@ -572,8 +587,7 @@ cudaError_t launch_adamw(const moe_adamw_tensor_t *ts, int64_t n, const moe_adam
             if (tab.n == 0) continue;
             tab.chunks = end;
             tab.mapped = end <= kMapped;
-            const cudaError_t e = launch_pdl(small ? adamw_kernel<true> : adamw_kernel<false>,
-                                             dim3(end), dim3(kThreads), 0, st, tab, s);
+            const cudaError_t e = launch(small ? adamw_kernel<true> : adamw_kernel<false>, end, tab, s, st);
             if (e != cudaSuccess) return e;
         }
     }
