@@ -164,3 +164,33 @@ def test_a_captured_training_step(moe):
         for n in a:
             assert torch.equal(a[n], b[n]), (seed, n)
         assert torch.equal(opts[0].norm, opts[1].norm)
+
+
+@pytest.mark.parametrize("E,G,Gk,score", [(256, 1, 1, "sigmoid"), (256, 8, 4, "sigmoid"), (260, 1, 1, "softmax")])
+def test_logits_past_32_bit_offsets(moe, E, G, Gk, score):
+    """More than 2^31 logits: the last tokens as in a batch of their own, and their
+    gradient."""
+    T, k, tail = (1 << 31) // E + 4099, 8, 9000
+    g = torch.Generator(device="cuda").manual_seed(E)
+    L = torch.zeros(T, E, device="cuda")
+    for at in range(0, T, 1 << 21):
+        L[at:at + (1 << 21)].normal_(generator=g)
+    bias = torch.randn(E, generator=g, device="cuda") * 0.01
+    r = moe.router(score, G, Gk, "top2")
+    idx, w = torch.zeros(T, k, dtype=torch.int32, device="cuda"), torch.zeros(T, k, device="cuda")
+    moe.moe_route_scored_from_logits(moe.config(T, 8, E, k, 8, renormalize=False), r, L, bias, idx, w)
+    torch.cuda.synchronize()
+    last = L[T - tail:].clone()
+    want = scored_ref.select_many(last, bias, k, score == "sigmoid", G, Gk, True)
+    assert torch.equal(idx[T - tail:].long(), want.long())
+    dw = torch.zeros(T, k, device="cuda")
+    dw[T - tail:] = 1.0
+    dl = torch.ones(T, E, device="cuda")
+    moe.moe_route_scored_from_logits_backward(moe.config(T, 8, E, k, 8, renormalize=False), r, L, idx, w, dw, dl)
+    alone = torch.zeros(tail, E, device="cuda")
+    moe.moe_route_scored_from_logits_backward(
+        moe.config(tail, 8, E, k, 8, renormalize=False), r, last, idx[T - tail:].clone(), w[T - tail:].clone(),
+        dw[T - tail:].clone(), alone)
+    torch.cuda.synchronize()
+    assert moe.moe_last_device_error() == moe.MOE_OK
+    assert torch.equal(dl[T - tail:], alone) and not dl[:T - tail].any()
