@@ -64,7 +64,8 @@ def plain_layer(x, Wr, lb, Wgu, Wd, idx, score, renorm, scale_inputs):
     ("softmax", True, True)])
 @pytest.mark.parametrize("T,d,E,k,f,dtype", [
     (50, 64, 8, 2, 64, "f32"), (200, 64, 64, 4, 64, "bf16"), (1, 128, 16, 3, 72, "bf16"),
-    (1030, 128, 16, 2, 64, "bf16"), (40, 64, 4, 4, 64, "bf16"), (300, 72, 24, 3, 40, "f32")])
+    (1030, 128, 16, 2, 64, "bf16"), (40, 64, 4, 4, 64, "bf16"), (300, 72, 24, 3, 40, "f32"),
+    (4500, 64, 64, 8, 64, "bf16"), (4500, 64, 32, 8, 64, "f32")])
 def test_layer(moe, T, d, E, k, f, dtype, score, renorm, scale_inputs):
     dt = torch.bfloat16 if dtype == "bf16" else torch.float32
     layer, x, (Wr, Wgu, Wd, lb, bias) = layer_of(moe, T, d, E, k, f, dt, score, renorm, scale_inputs)

@@ -4,17 +4,17 @@
 namespace moe {
 namespace {
 
-// Long batches: LANES lanes a token, 32 / LANES tokens a warp, N float4 of values a
+// Long batches: eight lanes a token, four tokens a warp, N float4 of values a
 // lane, k <= 8.  The same steps as a warp's per token, at a fraction of the
 // instructions, since a step of a reduction, a vote or a rank serves all of a warp's
 // tokens: the bound from the maxima of a half or a quarter of a lane's values each,
 // candidates counted and placed by a prefix sum over the lanes, and four of them a
 // lane.  T = 131072, k = 8, sigmoid with bias: E = 128 32 us, 60 with a warp a token
 // (its bytes take 11); E = 256 47 and 76; E = 128 in four groups 46 and 79.  What is
-// left is instructions (0.8 of the issue slots); code that a token seldom needs is
+// left is instructions (0.66 of the issue slots); code that a token seldom needs is
 // kept out of the loop, which has to fit the instruction cache (49 us when it did
 // not, 26 with the present loop, for E = 64).
-constexpr int kManyK = 8, kManyFew = 32;
+constexpr int kLanes = 8, kManyK = 8, kManyFew = 32;
 constexpr int kGroupParts = 4;  // (fewer of the lanes have values then)
 
 struct Segment {  // a token's shared memory; 200 words apart: no bank conflicts
@@ -24,37 +24,37 @@ struct Segment {  // a token's shared memory; 200 words apart: no bank conflicts
 };
 static_assert(sizeof(Segment) % 128 == 32, "");
 
-template <int LANES, bool MAX> __device__ __forceinline__ float segment_all(float v) {
+template <bool MAX> __device__ __forceinline__ float segment_all(float v) {
 #pragma unroll
-    for (int o = LANES / 2; o >= 1; o >>= 1) {
+    for (int o = kLanes / 2; o >= 1; o >>= 1) {
         const float u = __shfl_xor_sync(kAll, v, o);
         v = MAX ? fmaxf(v, u) : v + u;
     }
     return v;
 }
 
-template <int LANES, int N, bool EXACT, bool SIGMOID, bool GROUPS>
+template <int N, bool EXACT, bool SIGMOID, bool GROUPS>
 __global__ void __launch_bounds__(32, N <= 4 ? 24 : 20)
 select_many_kernel(const SelectArgs a, const __grid_constant__ SelectArgs cold) {
     pdl_entry();
     if (a.zero_word != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *a.zero_word = 0u;
     extern __shared__ __align__(16) unsigned char smem[];
-    constexpr int kTokens = 32 / LANES, V = 4 * N, kParts = GROUPS ? kGroupParts : 2;
-    const int lane = threadIdx.x, seg = lane / LANES, l = lane % LANES, E = a.E;
+    constexpr int kTokens = 32 / kLanes, V = 4 * N, kParts = GROUPS ? kGroupParts : 2;
+    const int lane = threadIdx.x, seg = lane / kLanes, l = lane % kLanes, E = a.E;
     Segment &s = reinterpret_cast<Segment *>(smem)[seg];
-    // this lane's experts, four at a time: 4 (l + LANES n) on, or with groups, whose
+    // this lane's experts, four at a time: 4 (l + kLanes n) on, or with groups, whose
     // lanes follow one another, `per` consecutive ones
     const int mine0 = GROUPS ? l * a.per : 4 * l, mine_end = GROUPS ? mine0 + a.per : E;
-    constexpr int kNext = GROUPS ? 4 : 4 * LANES;
+    constexpr int kNext = GROUPS ? 4 : 4 * kLanes;
 
     const int64_t stride = (int64_t)gridDim.x * kTokens;
     Pending &pend = *reinterpret_cast<Pending *>(smem + a.pending_at);
     int64_t first = (int64_t)blockIdx.x * kTokens;
     while (first < a.T) {
         const int64_t t0 = first;
-        unsigned left = 0u;  // bit LANES * seg + i: token t0 + i * stride + seg is for decide()
+        unsigned left = 0u;  // bit kLanes * seg + i: token t0 + i * stride + seg is for decide()
         int pending = 0;     // and for settle()
-        for (int i = 0; i < LANES && first < a.T && pending <= kPending - kTokens; ++i, first += stride) {
+        for (int i = 0; i < kLanes && first < a.T && pending <= kPending - kTokens; ++i, first += stride) {
             const int64_t t = first + seg;
             const bool there = t < a.T;
             const float *L = a.logits + t * E;
@@ -71,7 +71,7 @@ select_many_kernel(const SelectArgs a, const __grid_constant__ SelectArgs cold) 
             }
             __syncwarp();  // (the last token's shared memory as read)
 #pragma unroll
-            for (int c = 2 * l; c < kManyFew; c += 2 * LANES) {
+            for (int c = 2 * l; c < kManyFew; c += 2 * kLanes) {
                 const float4 none = make_float4(NAN, 0.f, NAN, 0.f);
                 *reinterpret_cast<float4 *>(s.few + c) = none;
                 *reinterpret_cast<float4 *>(s.sorted + c) = none;
@@ -82,7 +82,7 @@ select_many_kernel(const SelectArgs a, const __grid_constant__ SelectArgs cold) 
                 float top = v[0];
 #pragma unroll
                 for (int j = 1; j < V; ++j) top = fmaxf(top, v[j]);
-                top = segment_all<LANES, true>(top);
+                top = segment_all<true>(top);
                 if (!isnan(top)) m = top;
                 z = 0.f;
 #pragma unroll
@@ -90,7 +90,7 @@ select_many_kernel(const SelectArgs a, const __grid_constant__ SelectArgs cold) 
                     if (mine0 + kNext * n < mine_end)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) z += exp2_fast((v[4 * n + j] - m) * kLog2e);
-                z = segment_all<LANES, false>(z);
+                z = segment_all<false>(z);
             }
             if constexpr (!EXACT) {
                 if (SIGMOID) {
@@ -138,18 +138,18 @@ select_many_kernel(const SelectArgs a, const __grid_constant__ SelectArgs cold) 
                         h2 = fmaxf(fmaxf(h2, o2), fminf(h1, o1));
                         h1 = fmaxf(h1, o1);
                     }
-                    score = h2 > -INFINITY ? h1 + h2 : NAN;  // (as above)
+                    score = h2 > -INFINITY ? h1 + h2 : NAN;  // (as in select_kernel)
                     mag = fabsf(h1) + fabsf(h2);
                 }
                 float cur = score;
                 for (int j = 0; j < a.Gk; ++j) {
-                    bound = segment_all<LANES, true>(cur);
+                    bound = segment_all<true>(cur);
                     if (cur == bound) cur = NAN;
                 }
                 const float off = EXACT ? 0.f
-                                        : 2.f * unit + 0x1.2p-22f * segment_all<LANES, true>(isnan(score) ? 0.f : mag);
+                                        : 2.f * unit + 0x1.2p-22f * segment_all<true>(isnan(score) ? 0.f : mag);
                 const unsigned reach = __ballot_sync(kAll, (l & (in_group - 1)) == 0 && !(score < bound - off));
-                groups_open = __popc((reach >> (LANES * seg)) & ((1u << LANES) - 1u)) != a.Gk;
+                groups_open = __popc((reach >> (kLanes * seg)) & ((1u << kLanes) - 1u)) != a.Gk;
                 if (!(score >= bound))
 #pragma unroll
                     for (int j = 0; j < V; ++j) v[j] = NAN;
@@ -169,7 +169,7 @@ select_many_kernel(const SelectArgs a, const __grid_constant__ SelectArgs cold) 
                 float top = fmaxf(part[0], part[1]);
 #pragma unroll
                 for (int p = 2; p < kParts; ++p) top = fmaxf(top, part[p]);
-                bound = segment_all<LANES, true>(top);
+                bound = segment_all<true>(top);
 #pragma unroll
                 for (int p = 0; p < kParts; ++p)
                     if (part[p] == bound) part[p] = NAN;
@@ -181,11 +181,11 @@ select_many_kernel(const SelectArgs a, const __grid_constant__ SelectArgs cold) 
             for (int j = 0; j < V; ++j) mine += v[j] >= floor32;
             int upto = mine;  // with the lanes below
 #pragma unroll
-            for (int o = 1; o < LANES; o <<= 1) {
-                const int u = __shfl_up_sync(kAll, upto, o, LANES);
+            for (int o = 1; o < kLanes; o <<= 1) {
+                const int u = __shfl_up_sync(kAll, upto, o, kLanes);
                 if (l >= o) upto += u;
             }
-            const int n = __shfl_sync(kAll, upto, LANES - 1, LANES);
+            const int n = __shfl_sync(kAll, upto, kLanes - 1, kLanes);
             int at = upto - mine;
             __syncwarp();
             if (n <= kManyFew) {
@@ -195,12 +195,12 @@ select_many_kernel(const SelectArgs a, const __grid_constant__ SelectArgs cold) 
             }
             __syncwarp();
             // ranks, by the values behind each: by the sign of a difference, two a packed sum
-            constexpr int kHold = kManyFew / LANES;  // candidates a lane: 4, or 2
+            constexpr int kHold = kManyFew / kLanes;  // candidates a lane
             Ranked c[kHold];
             int behind[kHold];
 #pragma unroll
             for (int j = 0; j < kHold; ++j) {
-                c[j] = s.few[l + LANES * j];
+                c[j] = s.few[l + kLanes * j];
                 behind[j] = 0;
             }
             auto rank = [&](int p, int j) {
@@ -226,7 +226,7 @@ select_many_kernel(const SelectArgs a, const __grid_constant__ SelectArgs cold) 
             }
 #pragma unroll
             for (int j = 0; j < kHold; ++j)
-                if (l + LANES * j < n && n <= kManyFew) s.sorted[n - 1 - behind[j]] = c[j];
+                if (l + kLanes * j < n && n <= kManyFew) s.sorted[n - 1 - behind[j]] = c[j];
             __syncwarp();
             const bool slot = l < a.k;
             const Ranked chosen = s.sorted[l];
@@ -236,17 +236,17 @@ select_many_kernel(const SelectArgs a, const __grid_constant__ SelectArgs cold) 
                               (l + 1 < n && (EXACT ? !(q > next) : too_near(q, next, unit))));
             unsigned open = __ballot_sync(kAll, bad);
 #pragma unroll
-            for (int o = LANES / 2; o >= 1; o >>= 1) open |= open >> o;  // each segment's any, in its bit 0
-            open &= LANES == 8 ? 0x01010101u : 0x00010001u;
+            for (int o = kLanes / 2; o >= 1; o >>= 1) open |= open >> o;  // each segment's any, in its bit 0
+            open &= 0x01010101u;
             if (open) {  // (uniform)
                 const unsigned many =
                     __ballot_sync(kAll, l == 0 && (groups_open || n < a.k || n > kManyFew));
                 left |= (open & many) << i;
                 const unsigned listed = open & ~many;
-                const int at_pend = pending + __popc(listed & ((1u << LANES * seg) - 1u));
-                if ((listed >> (LANES * seg)) & 1u) {
+                const int at_pend = pending + __popc(listed & ((1u << kLanes * seg) - 1u));
+                if ((listed >> (kLanes * seg)) & 1u) {
 #pragma unroll
-                    for (int c = l; c < kManyFew; c += LANES) pend.id[at_pend][c] = (uint16_t)s.few[c].id;
+                    for (int c = l; c < kManyFew; c += kLanes) pend.id[at_pend][c] = (uint16_t)s.few[c].id;
                     if (l == 0) {
                         pend.t[at_pend] = t;
                         pend.n[at_pend] = n;
@@ -255,20 +255,20 @@ select_many_kernel(const SelectArgs a, const __grid_constant__ SelectArgs cold) 
                 pending += __popc(listed);
             }
 
-            const bool write = there && slot && ((open >> (LANES * seg)) & 1u) == 0u;
+            const bool write = there && slot && ((open >> (kLanes * seg)) & 1u) == 0u;
             const int id = write ? chosen.id : 0;
             const float logit = !write ? -INFINITY : EXACT ? q : L[id];
             float w;
             if (SIGMOID || a.renorm) {
                 float x = SIGMOID ? rcp_fast(1.f + expf(-logit)) : 0.f;
                 float sum = 1.f;
-                if (SIGMOID && a.renorm) sum = segment_all<LANES, false>(slot ? x : 0.f);
+                if (SIGMOID && a.renorm) sum = segment_all<false>(slot ? x : 0.f);
                 if (a.renorm && __any_sync(kAll, !SIGMOID || (write && sum < 0x1p-100f))) {
                     // (as in write_slots; for all of the warp's tokens, if one needs it)
-                    const float top = segment_all<LANES, true>(logit);
+                    const float top = segment_all<true>(logit);
                     const bool here = !SIGMOID || sum < 0x1p-100f;
                     const float y = !write || top == -INFINITY ? 0.f : expf(logit - top);
-                    const float shares = segment_all<LANES, false>(y);
+                    const float shares = segment_all<false>(y);
                     if (here) {
                         x = y;
                         sum = top == -INFINITY ? 1.f : shares;
@@ -288,28 +288,28 @@ select_many_kernel(const SelectArgs a, const __grid_constant__ SelectArgs cold) 
         while (left) {
             const int bit = __ffs(left) - 1;
             left &= left - 1u;
-            decide(cold, t0 + bit % LANES * stride + bit / LANES, smem);
+            decide(cold, t0 + bit % kLanes * stride + bit / kLanes, smem);
         }
     }
 }
 
-template <int LANES, int N, bool GROUPS>
+template <int N, bool GROUPS>
 cudaError_t launch_many(const SelectArgs &a, bool exact, cudaStream_t st) {
-    constexpr int kTokens = 32 / LANES;
+    constexpr int kTokens = 32 / kLanes;
     SelectArgs b = a;
     if (GROUPS) {  // the lanes of a group, in a segment
         b.shift = 0;
-        while ((a.G << (b.shift + 1)) <= LANES) ++b.shift;
+        while ((a.G << (b.shift + 1)) <= kLanes) ++b.shift;
         b.per = a.size >> b.shift;
     }
     b.pending_at = std::max(scratch_bytes(a.E), (int)sizeof(Segment) * kTokens);
     const size_t smem = b.pending_at + sizeof(Pending);
     const dim3 grid((unsigned)std::min<int64_t>((a.T + kTokens - 1) / kTokens,
                                                 (int64_t)device_sm_count() * (N <= 4 ? 24 : 20)));
-    auto kernel = a.sigmoid ? (exact ? select_many_kernel<LANES, N, true, true, GROUPS>
-                                     : select_many_kernel<LANES, N, false, true, GROUPS>)
-                            : (exact ? select_many_kernel<LANES, N, true, false, GROUPS>
-                                     : select_many_kernel<LANES, N, false, false, GROUPS>);
+    auto kernel = a.sigmoid ? (exact ? select_many_kernel<N, true, true, GROUPS>
+                                     : select_many_kernel<N, false, true, GROUPS>)
+                            : (exact ? select_many_kernel<N, true, false, GROUPS>
+                                     : select_many_kernel<N, false, false, GROUPS>);
     return launch_pdl(kernel, grid, dim3(32), smem, st, b, a);
 }
 // From this many tokens on, where there are several for each lane's place (T = 4096,
@@ -334,10 +334,10 @@ bool select_takes_many(const SelectArgs &a, bool exact) {
 
 cudaError_t launch_select_many(const SelectArgs &a, bool exact, cudaStream_t st) {
     if (a.Gk < a.G)
-        return a.E <= 128 ? launch_many<8, 4, true>(a, exact, st) : launch_many<8, 8, true>(a, exact, st);
-    if (a.E <= 64) return launch_many<8, 2, false>(a, exact, st);
-    if (a.E <= 128) return launch_many<8, 4, false>(a, exact, st);
-    return launch_many<8, 8, false>(a, exact, st);
+        return a.E <= 128 ? launch_many<4, true>(a, exact, st) : launch_many<8, true>(a, exact, st);
+    if (a.E <= 64) return launch_many<2, false>(a, exact, st);
+    if (a.E <= 128) return launch_many<4, false>(a, exact, st);
+    return launch_many<8, false>(a, exact, st);
 }
 
 }  // namespace moe
