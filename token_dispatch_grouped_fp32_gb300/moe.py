@@ -515,17 +515,26 @@ def adamw_list(tensors):
     devices = {t["param"].device for t in tensors}
     if len(devices) > 1:
         raise ValueError(f"the tensors are on one device, not on {devices}")
-    spans = []  # of what a step writes
+    ends = {}  # of what a step writes, by its start
+    written = 0
     for p, _, m, v, ms, rs, master, n, kind, _, state, _ in rows:
         if n == 0:
             continue
-        at = 4 if state == MOE_F32 else 1
-        spans += [(p, p + n * (4 if kind == MOE_F32 else 2)), (m, m + n * at), (v, v + n * at)]
-        spans += [(s, s + -(-n // ADAMW_BLOCK) * 4) for s in (ms, rs) if s is not None]
+        ends[p] = p + (4 * n if kind == MOE_F32 else 2 * n)
+        at = 4 * n if state == MOE_F32 else n
+        ends[m] = m + at
+        ends[v] = v + at
+        written += 3
+        if state != MOE_F32:
+            blocks = -(-n // ADAMW_BLOCK)
+            ends[ms] = ms + 4 * blocks
+            ends[rs] = rs + 4 * blocks
+            written += 2
         if master is not None:
-            spans.append((master, master + 4 * n))
-    spans.sort()
-    if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+            ends[master] = master + 4 * n
+            written += 1
+    starts = sorted(ends)
+    if len(starts) != written or any(ends[a] > b for a, b in zip(starts, starts[1:])):
         raise ValueError("two tensors that a step writes overlap")
     arr = (moe_adamw_tensor_t * max(1, len(rows)))(*rows)
     arr.count, arr.device = len(rows), devices.pop() if devices else None
@@ -538,30 +547,32 @@ _STATE_TYPES = {torch.float32: MOE_F32, torch.float8_e4m3fn: MOE_E4M3}
 
 def _adamw_row(param, grad, exp_avg, exp_avg_sq, exp_avg_scale=None, exp_avg_sq_scale=None,
                master=None, weight_decay=0.0):
-    n, kinds = param.numel(), (param.dtype, grad.dtype)
-    kind, state = [_ADAMW_TYPES.get(k) for k in kinds], _STATE_TYPES.get(exp_avg.dtype)
-    if None in kind:
-        raise TypeError(f"parameters and gradients are bf16 or fp32, not {kinds}")
+    n, device = param.numel(), param.device
+    kind, grad_kind = _ADAMW_TYPES.get(param.dtype), _ADAMW_TYPES.get(grad.dtype)
+    state = _STATE_TYPES.get(exp_avg.dtype)
+    if kind is None or grad_kind is None:
+        raise TypeError(f"parameters and gradients are bf16 or fp32, not {param.dtype}, {grad.dtype}")
     if state is None or exp_avg_sq.dtype != exp_avg.dtype:
         raise TypeError(f"both states are fp32 or float8_e4m3fn, not {exp_avg.dtype}, "
                         f"{exp_avg_sq.dtype}")
-    if not grad.numel() == exp_avg.numel() == exp_avg_sq.numel() == n:
-        raise ValueError("a gradient and its states have the parameter's size")
-    others = [grad, exp_avg, exp_avg_sq]
-    if master is not None:
-        if kinds[0] != torch.bfloat16 or master.dtype != torch.float32 or master.numel() != n:
-            raise ValueError("a master copy is an fp32 tensor of a bf16 parameter's size")
-        others.append(master)
-    scales = [s for s in (exp_avg_scale, exp_avg_sq_scale) if s is not None]
-    if len(scales) != (2 if state == MOE_E4M3 else 0) or any(
-            s.dtype != torch.float32 or s.numel() != -(-n // ADAMW_BLOCK) for s in scales):
-        raise ValueError("8-bit states, and they alone, have an fp32 scale for 256 elements")
-    device = param.device
-    for x in others + scales:
+    for x in (grad, exp_avg, exp_avg_sq):
+        if x.numel() != n:
+            raise ValueError("a gradient and its states have the parameter's size")
         if x.device != device:
             raise ValueError("a parameter, its gradient and its states are on one device")
+    if master is not None and (kind != MOE_BF16 or master.dtype != torch.float32
+                               or master.numel() != n or master.device != device):
+        raise ValueError("a master copy is an fp32 tensor of a bf16 parameter's size")
+    if state == MOE_F32:
+        if exp_avg_scale is not None or exp_avg_sq_scale is not None:
+            raise ValueError("scales beside fp32 states")
+    else:
+        for s in (exp_avg_scale, exp_avg_sq_scale):
+            if s is None or s.dtype != torch.float32 or s.numel() != -(-n // ADAMW_BLOCK) \
+                    or s.device != device:
+                raise ValueError("8-bit states have an fp32 scale for 256 elements")
     return (_ptr(param), _ptr(grad), _ptr(exp_avg), _ptr(exp_avg_sq), _ptr(exp_avg_scale),
-            _ptr(exp_avg_sq_scale), _ptr(master), n, kind[0], kind[1], state, float(weight_decay))
+            _ptr(exp_avg_sq_scale), _ptr(master), n, kind, grad_kind, state, float(weight_decay))
 
 
 def adamw_hyper(lr, beta1=0.9, beta2=0.95, eps=1e-8, step=1, seed=0, max_norm=0.0,
