@@ -372,13 +372,26 @@ __device__ __noinline__ void decide(const SelectArgs &a, int64_t t, unsigned cha
     unsigned kept = 1u;
     if (a.Gk < a.G) {
         float b1 = NAN, b2 = NAN, score = NAN, floor32 = NAN, mag = 0.f;
-        if (lane < a.G) {
+        // a group's lanes share its experts, and lane g has its score
+        auto second = [](float x, float y) { return isnan(x) || isnan(y) ? NAN : fminf(x, y); };
+        const int g = lane >> a.shift, r = lane & ((1 << a.shift) - 1);
+        if (g < a.G) {
 #pragma unroll 1
-            for (int i = 0; i < a.size; ++i) {
-                const float x = u.row[lane * a.size + i];
-                b2 = fmaxf(b2, x > b1 ? b1 : isnan(b1) ? NAN : x);
+            for (int i = r * a.per; i < min(a.size, (r + 1) * a.per); ++i) {
+                const float x = u.row[g * a.size + i];
+                b2 = fmaxf(b2, second(x, b1));
                 b1 = fmaxf(b1, x);
             }
+        }
+#pragma unroll 1
+        for (int o = 1; o < (1 << a.shift); o <<= 1) {
+            const float o1 = __shfl_xor_sync(kAll, b1, o), o2 = __shfl_xor_sync(kAll, b2, o);
+            b2 = fmaxf(fmaxf(b2, o2), second(b1, o1));
+            b1 = fmaxf(b1, o1);
+        }
+        b1 = __shfl_sync(kAll, b1, lane << a.shift);
+        b2 = __shfl_sync(kAll, b2, lane << a.shift);
+        if (lane < a.G) {
             const bool sum = a.top2 && a.size > 1;
             score = sum ? b1 + b2 : b1;
             floor32 = isnan(score) ? NAN : sum ? b2 : b1;
