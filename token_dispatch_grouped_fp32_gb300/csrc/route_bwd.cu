@@ -151,12 +151,14 @@ __global__ void __launch_bounds__(kThreads) terms_kernel(TermsArgs a, DevStatus 
             float m = -INFINITY;
             for (int i = lane; i < a.E; i += 32) m = fmaxf(m, L[i]);
             m = warp_all<true>(m);
+            if (m == -INFINITY) m = 0.f;  // a row of -inf: scores of 0
             float z = 0.f;
             for (int i = lane; i < a.E; i += 32) {
                 row[i] = expf(L[i] - m);
                 z += row[i];
             }
-            const float inv = 1.f / warp_all<false>(z);
+            z = warp_all<false>(z);
+            const float inv = z != 0.f ? 1.f / z : 0.f;
             for (int i = lane; i < a.E; i += 32) row[i] *= inv * (0.f - S);
             __syncwarp();
             if (e >= 0) row[e] = expf(L[e] - m) * inv * (a.f.scale * dj - S);
@@ -363,13 +365,14 @@ few_experts_kernel(FewArgs a, DevStatus ds) {
                 p[e] = e < E ? a.logits[t * E + e] : -INFINITY;
                 m = fmaxf(m, p[e]);
             }
+            if (m == -INFINITY) m = 0.f;  // a row of -inf: scores of 0
 #pragma unroll
             for (int e = 0; e < EM; ++e) {
                 p[e] = e < E ? expf(p[e] - m) : 0.f;
                 z += p[e];
             }
         }
-        const float inv = 1.f / z;
+        const float inv = z != 0.f ? 1.f / z : 0.f;
 #pragma unroll
         for (int e = 0; e < EM; ++e) s_dl[i][e] = a.renorm ? 0.f : p[e] * inv * (0.f - S);
         for (int j = 0; j < k; ++j) {
