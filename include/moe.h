@@ -635,8 +635,11 @@ moe_status_t moe_update_balance_bias(const int32_t *counts, int64_t layers, int3
  * smallest code, so that no later step divides by eps alone (a v below 2^-126
  * counts as 0, and eps = 0 then divides by 0).  (Zeros in all bytes and scales are
  * valid initial states of either kind.)
- * A block with a NaN or an infinity keeps NaN and the format's largest value
- * for those elements.
+ * An element whose m or v is a NaN or infinite costs the others of its block
+ * nothing: the scales are those of the largest finite magnitudes.  A NaN is
+ * stored as NaN, an infinite m as the format's largest value, an infinite v as a
+ * negative NaN of r, which the next step reads as infinite (so, as with fp32
+ * states, a gradient whose square overflows leaves its parameter to the decay).
  *
  * Random numbers: 32 bits of every element, a function of `seed` (a caller takes
  * another each step), the number of its block of 256 elements counted over the

@@ -10,8 +10,8 @@
 // travel as kernel parameters, as in clip.cu.
 //
 // fp32 states are bound by HBM (64 M bf16 parameters: 210 us, 0.99 of the copy
-// rate).  8-bit states by the instructions of two roundings an element: 127 us
-// (0.75; fp32 parameters, which move more, 155: 0.98; 1.4 G bf16 ones 0.83).  A ring of asynchronous copies
+// rate).  8-bit states by the instructions of two roundings an element: 129 us
+// (0.74; fp32 parameters, which move more, 160: 0.95; 1.4 G bf16 ones 0.82).  A ring of asynchronous copies
 // into shared memory took 148 to 155 us, values of the next block held in registers
 // 161 to 205, and a prefetch into L2 158: the loads are not what it waits for.
 //
@@ -310,11 +310,10 @@ template <bool ROOT> __device__ __noinline__ Values small_ones(Values a) {
 // the tensor's end; u: the elements' random bits.
 // ROOT: the roots, no positive one of which becomes zero.
 template <bool ROOT>
-__device__ __forceinline__ float quantise(float2 (&x)[4], uint32_t e, bool finite, const uint32_t (&u)[8]) {
+__device__ __forceinline__ float quantise(float2 (&x)[4], uint32_t e, const uint32_t (&u)[8]) {
     const float inv = __uint_as_float((254u - e) << 23), scale = __uint_as_float(e << 23);
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = mul2(x[i], two(inv));
-    if (!finite) return scale;  // uniform: a NaN or an infinity in the block
     float low = min_abs(x[0].x, x[0].y, x[1].x);
     low = min_abs(low, x[1].y, x[2].x);
     low = min_abs(low, x[2].y, x[3].x);
@@ -335,6 +334,41 @@ __device__ __forceinline__ float quantise(float2 (&x)[4], uint32_t e, bool finit
     return scale;
 }
 
+// Eight states of a block with NaN or infinite ones to 8 bits: the scale is that of its
+// largest finite magnitude, and the others are rounded as they are without those.  A
+// NaN is stored as one, an infinite m as the largest value, an infinite root as kInfiniteRoot.
+constexpr uint8_t kInfiniteRoot = 0xff;  // a negative NaN
+template <bool ROOT>
+__device__ __forceinline__ float set_apart(const float (&x)[8], const uint32_t (&u)[8],
+                                           Eight<__nv_fp8_e4m3> *to) {
+    float top = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = isfinite(x[j]) ? fmaxf(top, fabsf(x[j])) : top;
+    const uint32_t e = scale_exponent(__reduce_max_sync(kAll, __float_as_uint(top)));
+    const float inv = __uint_as_float((254u - e) << 23);
+    float y[8];
+    Values a;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        y[j] = isfinite(x[j]) ? x[j] * inv : 0.f;
+        a.u[j] = u[j];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a.x[i] = make_float2(y[2 * i], y[2 * i + 1]);
+    a = small_ones<ROOT>(a);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        float &q = j & 1 ? a.x[j / 2].y : a.x[j / 2].x;
+        if (!isfinite(x[j])) q = ROOT ? NAN : x[j];
+    }
+    pack(a.x, to);
+    if (ROOT)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (isinf(x[j])) (j < 4 ? to->c.x : to->c.y) |= 0x80u << (8 * (j % 4));
+    return __uint_as_float(e << 23);
+}
+
 // What a lane reads of a block of 256 elements.
 template <typename TP, typename TG, bool SMALL> struct Block {
     using TS = std::conditional_t<SMALL, __nv_fp8_e4m3, float>;
@@ -342,6 +376,46 @@ template <typename TP, typename TG, bool SMALL> struct Block {
     Eight<TG> g;
     Eight<TS> m, v;
 };
+
+// A block of 8-bit states with one that is not finite: the same operations, apart from the
+// others for their registers (the branch there costs them 1 to 3 %; with the bad elements
+// handled where the others are, 6 to 8 % for more spills).  Returns the new scales.
+template <typename TP, typename TG, bool MASTER>
+__device__ __noinline__ float2 seldom_block(const Entry &t, const Step &s, float coef, int64_t b,
+                                            float ms, float rs, Key key) {
+    const moe_adamw_scalars_t sc = s.dev ? *s.dev : s.sc;
+    const int lane = threadIdx.x & 31;
+    const int64_t at = b * kBlock + 8 * lane;
+    const int n = (int)max((int64_t)0, min((int64_t)8, t.numel - at));
+    float m[8], r[8];
+    uint32_t u[8];
+#pragma unroll 1
+    for (int j = 0; j < 8; ++j) {
+        m[j] = r[j] = 0.f;
+        u[j] = random_bits(key, 8 * lane + j);
+        if (j >= n) continue;
+        const __nv_fp8_e4m3 *mp = static_cast<const __nv_fp8_e4m3 *>(t.m) + at + j;
+        const __nv_fp8_e4m3 *rp = static_cast<const __nv_fp8_e4m3 *>(t.v) + at + j;
+        const float root0 = __fmul_rn((float)*rp, rs);
+        const float v0 = rp->__x == kInfiniteRoot ? INFINITY : __fmul_rn(root0, root0);
+        const float g = __fmul_rn((float)static_cast<const TG *>(t.g)[at + j], coef);
+        m[j] = __fadd_rn(__fmul_rn(__fmul_rn((float)*mp, ms), s.b1), __fmul_rn(g, s.c1));
+        r[j] = root<true>(__fadd_rn(__fmul_rn(v0, s.b2), __fmul_rn(__fmul_rn(g, g), s.c2)));
+        TP *const p = (MASTER ? reinterpret_cast<TP *>(t.master) : static_cast<TP *>(t.p)) + at + j;
+        const float q = __fmul_rn(m[j], reciprocal(__fmaf_rn(r[j], sc.inv_sqrt_bc2, s.eps)));
+        const float x = __fmaf_rn(-sc.step_size, q, __fmul_rn((float)*p, fmaf(-sc.lr, t.wd, 1.f)));
+        if constexpr (sizeof(TP) == 4) *p = x;
+        else if (s.stochastic) *reinterpret_cast<uint16_t *>(p) = (uint16_t)bf16_pair(make_float2(x, x), u[j], u[j]);
+        else *p = __float2bfloat16_rn(x);
+        if constexpr (MASTER) static_cast<__nv_bfloat16 *>(t.p)[at + j] = __float2bfloat16_rn(x);
+    }
+    Eight<__nv_fp8_e4m3> to;
+    const float new_ms = set_apart<false>(m, u, &to);
+    store_some(static_cast<__nv_fp8_e4m3 *>(t.m) + at, n, to);
+    const float new_rs = set_apart<true>(r, u, &to);
+    store_some(static_cast<__nv_fp8_e4m3 *>(t.v) + at, n, to);
+    return make_float2(new_ms, new_rs);
+}
 
 // The blocks b, b + kWarps, ... before `last` of a tensor, by a warp.  TP: the
 // stepped parameter's type (a master copy's: fp32).
@@ -426,6 +500,21 @@ __device__ __forceinline__ void step_chunk(const Entry &t, const Step &s, const 
 #pragma unroll
             for (int j = 0; j < 8; ++j) u[j] = random_bits(key, 8 * lane + j);
         }
+        uint32_t largest_m = 0u, largest_v = 0u;
+        if constexpr (SMALL) {
+            largest_m = __reduce_max_sync(kAll, __float_as_uint(top_m));
+            largest_v = __reduce_max_sync(kAll, __float_as_uint(top_v));
+            if (max(largest_m, largest_v) >= 0x7f800000u) {  // (uniform) a NaN or an infinity
+                const Key key = {__shfl_sync(kAll, keys.x, i), __shfl_sync(kAll, keys.y, i)};
+                const float2 scales = seldom_block<TP, TG, MASTER>(t, s, coef, b, __shfl_sync(kAll, ms, i),
+                                                                   __shfl_sync(kAll, rs, i), key);
+                if (lane == i) {
+                    ms = scales.x;
+                    rs = scales.y;
+                }
+                continue;
+            }
+        }
         // (each is stored as soon as it is known: registers)
         const int64_t at = b * kBlock + 8 * lane;
         const int n = (int)max((int64_t)0, min((int64_t)8, t.numel - at));
@@ -449,12 +538,10 @@ __device__ __forceinline__ void step_chunk(const Entry &t, const Step &s, const 
         }
         Eight<TS> state;
         if constexpr (SMALL) {
-            const uint32_t largest_m = __reduce_max_sync(kAll, __float_as_uint(top_m));
-            const uint32_t largest_v = __reduce_max_sync(kAll, __float_as_uint(top_v));
-            const float new_ms = quantise<false>(m, scale_exponent(largest_m), largest_m < 0x7f800000u, u);
+            const float new_ms = quantise<false>(m, scale_exponent(largest_m), u);
             pack(m, &state);
             put(static_cast<TS *>(t.m), state);
-            const float new_rs = quantise<true>(r, root_scale_exponent(largest_v), largest_v < 0x7f800000u, u);
+            const float new_rs = quantise<true>(r, root_scale_exponent(largest_v), u);
             pack(r, &state);
             put(static_cast<TS *>(t.v), state);
             if (lane == i) {
