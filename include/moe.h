@@ -503,7 +503,7 @@ moe_status_t moe_clip_grad_norm(const moe_grad_t *grads, int64_t n, float max_no
  * their logits (the order of s as real numbers).  With one, and for sums of two, q
  * and u are compared as 64-bit values, however near they are in fp32.
  * Edges: a NaN q or u ranks below every number (a NaN logit makes all of a
- * softmax row NaN).  A logit of -inf has a score of 0, and still a q of b_e: to
+ * softmax row NaN, and all of its weights).  A logit of -inf has a score of 0, and still a q of b_e: to
  * exclude an expert from every choice give it a bias of -inf.  A row of -inf alone
  * has scores of 0.  Where all chosen scores are 0 their renormalised weights are
  * 0; scores that fp32 cannot hold keep their shares.  A logit of +inf is not

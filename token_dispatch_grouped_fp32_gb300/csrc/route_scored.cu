@@ -98,6 +98,19 @@ select_kernel(const SelectArgs a, const __grid_constant__ SelectArgs cold) {
                     if (i < count) z += exp2_fast((v[i] - m) * kLog2e);
                 z = warp_sum(z);
             }
+            // a NaN among softmax's logits makes every weight one: for decide(), as is a row
+            // of -INF (without an exact ranking both are, for their NaN in `unit`)
+            bool odd = false;
+            if (EXACT && !a.sigmoid) {
+                float sum = z;
+                if (a.renorm) {  // (no z; logits that overflow both ways go there too)
+                    sum = 0.f;
+#pragma unroll
+                    for (int i = 0; i < VPL; ++i)
+                        if (i < count) sum += v[i];
+                }
+                odd = __any_sync(kAll, isnan(sum));
+            }
             if constexpr (!EXACT) {
                 if (a.sigmoid) {
 #pragma unroll
@@ -204,7 +217,7 @@ select_kernel(const SelectArgs a, const __grid_constant__ SelectArgs cold) {
                 if (in) few[n + __popc(b & below)] = {v[i], e0 + i};
                 n += __popc(b);
             }
-            const bool listed = decided && n >= a.k && n <= 32;
+            const bool listed = decided && !odd && n >= a.k && n <= 32;
             decided = listed;
             __syncwarp();
             const Ranked mine = lane < n ? few[lane] : kNobody;

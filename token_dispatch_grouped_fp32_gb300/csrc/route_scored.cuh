@@ -230,7 +230,7 @@ __device__ __forceinline__ float score32(float L, bool sigmoid, float m, float i
 }
 
 // A token's weights and ids.  A lane with `chosen` has the expert `id`, its logit and
-// its slot; m, z: softmax without renormalisation.
+// its slot; m, z: softmax without renormalisation (m: a NaN where a logit of the row is one).
 __device__ __forceinline__ void write_slots(const SelectArgs &a, int64_t t, bool chosen, int slot, int id,
                                             float logit, float m, float z) {
     float w;
@@ -250,20 +250,25 @@ __device__ __forceinline__ void write_slots(const SelectArgs &a, int64_t t, bool
     } else {
         w = m == -INFINITY ? 0.f : a.scale * expf(logit - m) * rcp_fast(z);
     }
+    if (isnan(m)) w = NAN;
     if (chosen) {
         a.idx[t * a.k + slot] = id;
         a.w[t * a.k + slot] = w;
     }
 }
 
-// A row's largest logit and the sum of its exponentials.
+// A row's largest logit (a NaN where one is) and the sum of its exponentials.
 __device__ __forceinline__ void softmax32(const float *L, int E, float *m, float *z) {
     const int lane = threadIdx.x & 31;
     float top = NAN, sum = 0.f;
+    bool nan = false;
 #pragma unroll 1
-    for (int e = lane; e < E; e += 32) top = fmaxf(top, L[e]);
+    for (int e = lane; e < E; e += 32) {
+        top = fmaxf(top, L[e]);
+        nan |= isnan(L[e]);
+    }
     top = warp_max(top);
-    *m = isnan(top) ? -INFINITY : top;
+    *m = __any_sync(kAll, nan) ? NAN : top;
 #pragma unroll 1
     for (int e = lane; e < E; e += 32) sum += exp2_fast((L[e] - *m) * kLog2e);
     *z = warp_sum(sum);

@@ -92,6 +92,20 @@ select_many_kernel(const SelectArgs a, const __grid_constant__ SelectArgs cold) 
                         for (int j = 0; j < 4; ++j) z += exp2_fast((v[4 * n + j] - m) * kLog2e);
                 z = segment_all<false>(z);
             }
+            // a NaN among softmax's logits makes every weight one: for decide() (as is a row of
+            // -INF that is not renormalised, and sums that overflow both ways; without an exact
+            // ranking such rows are for their NaN in `unit`)
+            bool start_over = false;
+            if (EXACT && !SIGMOID) {
+                float2 sum = make_float2(z, 0.f);
+                if (a.renorm)  // (no z)
+#pragma unroll
+                    for (int j = 0; j < V; j += 4)
+                        if (mine0 + kNext * (j / 4) < mine_end)
+                            sum = add2(add2(sum, make_float2(v[j], v[j + 1])), make_float2(v[j + 2], v[j + 3]));
+                const unsigned odd = __ballot_sync(kAll, isnan(sum.x + sum.y) && there);
+                start_over = (odd >> (kLanes * seg)) & ((1u << kLanes) - 1u);
+            }
             if constexpr (!EXACT) {
                 if (SIGMOID) {
 #pragma unroll
@@ -115,7 +129,6 @@ select_many_kernel(const SelectArgs a, const __grid_constant__ SelectArgs cold) 
             const float unit = EXACT ? 0.f : unit_of(SIGMOID, V, z);
 
             float bound = NAN;
-            bool groups_open = false;
             if constexpr (GROUPS) {
                 const int in_group = 1 << a.shift;  // lanes
                 float score, mag = 0.f;
@@ -149,7 +162,7 @@ select_many_kernel(const SelectArgs a, const __grid_constant__ SelectArgs cold) 
                 const float off = EXACT ? 0.f
                                         : 2.f * unit + 0x1.2p-22f * segment_all<true>(isnan(score) ? 0.f : mag);
                 const unsigned reach = __ballot_sync(kAll, (l & (in_group - 1)) == 0 && !(score < bound - off));
-                groups_open = __popc((reach >> (kLanes * seg)) & ((1u << kLanes) - 1u)) != a.Gk;
+                start_over |= __popc((reach >> (kLanes * seg)) & ((1u << kLanes) - 1u)) != a.Gk;
                 if (!(score >= bound))
 #pragma unroll
                     for (int j = 0; j < V; ++j) v[j] = NAN;
@@ -232,7 +245,7 @@ select_many_kernel(const SelectArgs a, const __grid_constant__ SelectArgs cold) 
             const Ranked chosen = s.sorted[l];
             const float q = chosen.q, next = s.sorted[l + 1].q;
             const bool bad = there && slot &&
-                             (groups_open || n > kManyFew || isnan(q) ||
+                             (start_over || n > kManyFew || isnan(q) ||
                               (l + 1 < n && (EXACT ? !(q > next) : too_near(q, next, unit))));
             unsigned open = __ballot_sync(kAll, bad);
 #pragma unroll
@@ -240,7 +253,7 @@ select_many_kernel(const SelectArgs a, const __grid_constant__ SelectArgs cold) 
             open &= 0x01010101u;
             if (open) {  // (uniform)
                 const unsigned many =
-                    __ballot_sync(kAll, l == 0 && (groups_open || n < a.k || n > kManyFew));
+                    __ballot_sync(kAll, l == 0 && (start_over || n < a.k || n > kManyFew));
                 left |= (open & many) << i;
                 const unsigned listed = open & ~many;
                 const int at_pend = pending + __popc(listed & ((1u << kLanes * seg) - 1u));
