@@ -472,8 +472,11 @@ def measure_workload(moe, w, args, dev, rank, world, flush, with_e2e):
     start.record(stream)
     for st in streams:
         st.wait_stream(stream)
+    ordered = w.E >= 64 or 64 * w.E <= T * w.k < 512 * w.E  # see moe.h on streams
     for i in range(args.steps):
         st = streams[i % 2]
+        if ordered:
+            st.wait_stream(streams[(i + 1) % 2])
         e2e_step(i, st)
     ends = []
     for st in streams:

@@ -32,6 +32,12 @@
  *     legacy default stream) and never synchronises with the host, so a
  *     sequence of calls can be captured in a CUDA graph [EP-impl].
  *     moe_last_device_error() is the one call that synchronises.
+ *   - Calls with buffers and workspaces of their own may be queued on several
+ *     streams.  But order bf16 calls of moe_forward, moe_route and
+ *     moe_grouped_swiglu, of their _scored forms and of their gradients by
+ *     events where E >= 64 or 64 <= P / E < 512, as the Python layer does, so
+ *     that no other of these runs beside them: two side by side have, seldom,
+ *     not ended, for a cause that is not known.
  *   - Arguments are checked on the host before anything is launched; a
  *     failed check launches nothing and returns the status.  Returned
  *     statuses describe launch-time problems; problems found by a kernel

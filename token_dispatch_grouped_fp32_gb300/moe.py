@@ -12,9 +12,11 @@ workspace per stream (allocated with torch) and calls ``moe_forward``;
 """
 from __future__ import annotations
 
+import collections
 import contextlib
 import ctypes
 import os
+import threading
 
 import torch
 
@@ -623,6 +625,107 @@ def _record(side, tensors):
                 t.record_stream(side)
 
 
+class _Turns:
+    """The bf16 layer calls of one device.  Those that take the GPU alone (see _alone)
+    run beside no other, whatever streams they are queued on: their stream waits for the
+    end of what other calls' streams hold, and a later call's for theirs.  (Two calls of
+    one such shape side by side on two streams have, seldom, not ended: see moe.h on
+    streams.)  A call that is being captured in a graph waits for none, and none for it."""
+
+    def __init__(self):
+        self.lock = threading.Lock()
+        self.last = None  # handle of the stream of the latest call that ran alone
+        # that stream and those with calls behind it; an event at the latest one's end
+        # where the stream may be gone by the time that it is waited for
+        self.ends = {}
+        self.kept = set()  # handles that torch keeps to the program's end
+
+    def begin(self, key, alone):
+        """Orders stream `key` for a call on it; False: it is being captured."""
+        if alone:
+            follow = [k for k in self.ends if k != key]
+        else:
+            follow = [] if self.last is None or key in self.ends else [self.last]
+        if not follow:
+            return True
+        to = _torch_stream(key)
+        if _capturing_on(to):
+            return False
+        for k in follow:
+            event = self.ends[k]
+            if event is None:
+                side = _torch_stream(k)
+                if _capturing_on(side):
+                    raise RuntimeError("the stream of an earlier layer call is being captured: a call on "
+                                       "another stream cannot be ordered behind it")
+                event = side.record_event()
+            to.wait_event(event)
+        return True
+
+    def end(self, stream, key, alone):
+        event = None
+        if not self.keeps(stream, key):
+            side = _torch_stream(key)
+            if _capturing_on(side):
+                return
+            event = side.record_event()
+        if alone:
+            self.last = key
+            self.ends.clear()
+        self.ends[key] = event
+
+    def keeps(self, stream, key):
+        """Whether torch keeps the stream (its default and pooled ones)."""
+        if key in self.kept:
+            return True
+        if stream is None:
+            stream = torch.cuda.current_stream()
+        kept = key == 0 or isinstance(stream, torch.cuda.Stream) and stream.stream_id != key
+        if kept:
+            self.kept.add(key)
+        return kept
+
+
+class _Turn:
+    """with _Turn(turns, stream, key, alone): the launches of one call."""
+
+    def __init__(self, *call):
+        self.turns, *self.call = call
+
+    def __enter__(self):
+        self.turns.lock.acquire()
+        try:
+            self.counts = self.turns.begin(*self.call[1:])
+        except BaseException:
+            self.turns.lock.release()
+            raise
+
+    def __exit__(self, *exc):
+        try:
+            if self.counts:
+                self.turns.end(*self.call)
+        finally:
+            self.turns.lock.release()
+
+
+_turns = collections.defaultdict(_Turns)  # by device index
+
+
+def _torch_stream(key):
+    return torch.cuda.ExternalStream(key) if key else torch.cuda.default_stream()
+
+
+def _capturing_on(stream):
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
+def _alone(cfg):
+    """Calls that moe.h says to order."""
+    E, P = cfg.E, cfg.T * cfg.k
+    return E >= 64 or 64 * E <= P < 512 * E
+
+
 class MoELayer:
     """Weights of one MoE layer plus reusable workspaces; ``forward`` runs
     ``moe_forward`` on the given (default: current) stream.  Weights: Wr [E, d]
@@ -637,8 +740,11 @@ class MoELayer:
     ``stream`` that is not the current one allocates from that stream's pool,
     and neither what it returns nor the tensors given to it go back to a pool
     before both streams are done with them; ordering the two streams is the
-    caller's part.  A workspace that a graph was captured with stays allocated as
-    long as the layer, also when a longer batch gets a new one.
+    caller's part.  With bf16 weights, and E >= 64 or 64 <= T k / E < 512, a call runs
+    beside no other bf16 layer's on the GPU, whatever streams they are queued on;
+    replays of captured calls are the caller's to order.  A workspace that a graph was captured
+    with stays allocated as long as the layer, also when a longer batch gets a new
+    one.
 
     ``backward`` runs ``moe_backward`` for the latest ``forward`` on the same
     stream, whose intermediates it finds in that workspace.  It refuses when
@@ -717,7 +823,13 @@ class MoELayer:
             return None
         if isinstance(stream, torch.cuda.Stream):
             return stream
-        return torch.cuda.ExternalStream(key) if key else torch.cuda.default_stream()
+        return _torch_stream(key)
+
+    def _turn(self, stream, key, cfg):
+        w = self.W_gate_up
+        if not w.is_cuda or w.dtype != torch.bfloat16:
+            return contextlib.nullcontext()
+        return _Turn(_turns[w.device.index], stream, key, _alone(cfg))
 
     def forward(self, x, out=None, stream=None):
         key, cfg = _stream(stream), self.config(x.shape[0])
@@ -730,12 +842,13 @@ class MoELayer:
         _record(side, given)
         ws = self._forward_ws(cfg, stream, key)
         self._forget(key)  # until all of its kernels are launched
-        if self.router is None:
-            moe_forward(cfg, x, self.Wr, self.logit_bias, self.W_gate_up, self.W_down, out, ws,
-                        stream=key)
-        else:
-            moe_forward_scored(cfg, self.router, x, self.Wr, self.logit_bias, self.balance_bias,
-                               self.W_gate_up, self.W_down, out, ws, stream=key)
+        with self._turn(stream, key, cfg):
+            if self.router is None:
+                moe_forward(cfg, x, self.Wr, self.logit_bias, self.W_gate_up, self.W_down, out, ws,
+                            stream=key)
+            else:
+                moe_forward_scored(cfg, self.router, x, self.Wr, self.logit_bias, self.balance_bias,
+                                   self.W_gate_up, self.W_down, out, ws, stream=key)
         self._tokens[key] = cfg.T
         version = None if self._capturing(ws) else _version(x)
         if _ptr(out) != x.data_ptr():
@@ -812,10 +925,11 @@ class MoELayer:
         self._capturing(ws, *(() if fwd_ws is None else (fwd_ws,)))
         args = (x, self.Wr, self.W_gate_up, self.W_down, fwd_ws, dout, grads["x"], grads["Wr"],
                 grads.get("logit_bias"), grads["W_gate_up"], grads["W_down"], ws)
-        if self.router is None:
-            moe_backward(cfg, *args, stream=key)
-        else:
-            moe_backward_scored(cfg, self.router, *args, stream=key)
+        with self._turn(stream, key, cfg):
+            if self.router is None:
+                moe_backward(cfg, *args, stream=key)
+            else:
+                moe_backward_scored(cfg, self.router, *args, stream=key)
         return grads
 
 
