@@ -945,7 +945,11 @@ class AdamW:
     parameter.  ``lr`` may be changed between steps.
 
     In a captured graph (``capturable``) a step reads its number, lr and seed from
-    device memory: call ``advance()`` before every replay, on the replay's stream."""
+    device memory: call ``advance()`` before every replay, on the replay's stream.
+
+    A step's tensors, the given ones too, do not go back to a pool before the stream of
+    the step is done with them; ordering that stream behind what wrote them, and a graph's
+    replays, is the caller's part (keep the optimizer as long as a graph of its steps)."""
 
     def __init__(self, params, grads, lr, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.0, bits=32,
                  master=True, max_norm=None, seed=0, capturable=False):
@@ -984,6 +988,18 @@ class AdamW:
         if capturable:
             self._scalars = torch.zeros(ctypes.sizeof(moe_adamw_scalars_t), dtype=torch.uint8,
                                         device=device)
+        # streams that the memory of all of these does not go back to a pool before
+        self._streams = {_stream(None)} if device.type == "cuda" else set()
+
+    def _used_here(self):
+        """On the current stream: the tensors' memory stays until it is done with them."""
+        key = _stream(None)
+        if key not in self._streams:
+            here = torch.cuda.current_stream()
+            for t in self.tensors:
+                _record(here, t.values())
+            _record(here, (self.norm, self._ws, self._scalars))
+            self._streams.add(key)
 
     def _hyper(self):
         # (another seed every step: the one given, and the step's number)
@@ -995,6 +1011,7 @@ class AdamW:
         """Counts a step; capturable: what its replay reads, on the current stream."""
         self.steps += 1
         if self._scalars is not None:
+            self._used_here()
             raw = torch.frombuffer(bytearray(bytes(moe_adamw_scalars(self._hyper()))),
                                    dtype=torch.uint8)
             self._scalars.copy_(raw, non_blocking=True)
@@ -1007,6 +1024,7 @@ class AdamW:
                 else torch.cuda.default_stream()
         with _allocating_on(side):
             _on_current(self._list.device)
+            self._used_here()
             if torch.cuda.is_current_stream_capturing():
                 if self._scalars is None:
                     raise RuntimeError("a step is captured with capturable=True")
