@@ -42,7 +42,6 @@ constexpr int kBlock = 256;                // elements under one scale
 // an SM, which cannot even out what they take.
 constexpr int kMostBlocks = 32 * kWarps;
 constexpr int kSquare = 76;
-constexpr int kTable = 300;                // tensors per launch
 constexpr int kMapped = 1024;              // chunks with a map of their own
 
 struct Entry {
@@ -55,12 +54,6 @@ struct Entry {
     float wd;
     uint8_t p_bf16, g_bf16, vec;
 };
-struct Table {
-    int n, chunks, mapped, chunk_blocks;
-    uint16_t tensor_of[kMapped];
-    Entry t[kTable];
-};
-
 struct Step {
     float b1, c1, b2, c2, eps, max_norm;  // c1 = 1 - b1, c2 = 1 - b2
     float minus_zero;
@@ -69,6 +62,16 @@ struct Step {
     const moe_adamw_scalars_t *dev;
     const float *norm;
 };
+
+// Tensors per launch: what a kernel's parameters hold beside the rest.
+constexpr int kParameterBytes = 32764;
+constexpr int kTable = (kParameterBytes - (int)sizeof(Step) - 16 - 2 * kMapped) / (int)sizeof(Entry);
+struct Table {
+    int n, chunks, mapped, chunk_blocks;
+    uint16_t tensor_of[kMapped];
+    Entry t[kTable];
+};
+static_assert(sizeof(Table) + sizeof(Step) <= kParameterBytes, "");
 
 // ------------------------------ random bits --------------------------------
 // Words of a 32-bit product, xor'ed: the whole generator.  A block's two key words
@@ -602,7 +605,7 @@ adamw_kernel(const __grid_constant__ Table tab, const __grid_constant__ Step s) 
     }
 }
 
-// launch_pdl without its copy of the 28 KB of parameters (0.4 us a call).
+// launch_pdl without its copy of the 32 KB of parameters (0.4 us a call).
 cudaError_t launch(void (*kernel)(Table, Step), int grid, Table &tab, Step &s, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
