@@ -151,7 +151,7 @@ select_kernel(const SelectArgs a, const __grid_constant__ SelectArgs cold) {
                     score = best;
                     for (int o = 1; o < (1 << a.shift); o <<= 1)
                         score = fmaxf(score, __shfl_xor_sync(kAll, score, o));
-                    if (!EXACT) mag = fabsf(score);
+                    if (!EXACT) mag = size_of_score(score, score, 0.f);
                 } else {
                     float b1 = -INFINITY, b2 = -INFINITY;
 #pragma unroll
@@ -165,9 +165,10 @@ select_kernel(const SelectArgs a, const __grid_constant__ SelectArgs cold) {
                         b2 = fmaxf(fmaxf(b2, o2), fminf(b1, o1));
                         b1 = fmaxf(b1, o1);
                     }
-                    // (no second number, or an excluded expert: for decide())
-                    score = group < a.G && b2 > -INFINITY ? b1 + b2 : NAN;
-                    if (!isnan(score)) mag = fabsf(b1) + fabsf(b2);
+                    // (no second number, or an excluded expert: below every sum of two; decide()
+                    // knows more, where such groups are to be kept)
+                    score = group >= a.G ? NAN : b2 > -INFINITY ? b1 + b2 : -INFINITY;
+                    mag = size_of_score(score, b1, b2);
                 }
                 // a score that Gk groups reach: if no more come near it, they stay
                 float cur = score, bound = NAN;

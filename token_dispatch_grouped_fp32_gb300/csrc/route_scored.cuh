@@ -224,6 +224,11 @@ __device__ __forceinline__ bool too_near(float hi, float lo, float unit) {
     return !(hi - lo > unit + 0x1.2p-23f * fmaxf(fabsf(hi), fabsf(lo)));
 }
 
+// What the errors of a group's score b1 + b2 go by; an excluded group's, -INF, has none.
+__device__ __forceinline__ float size_of_score(float score, float b1, float b2) {
+    return score > -INFINITY ? fabsf(b1) + fabsf(b2) : 0.f;
+}
+
 __device__ __forceinline__ float score32(float L, bool sigmoid, float m, float inv) {
     if (sigmoid) return rcp_fast(1.f + exp2_fast(L * -kLog2e));
     return m == -INFINITY ? 0.f : exp2_fast((L - m) * kLog2e) * inv;
@@ -401,7 +406,7 @@ __device__ __noinline__ void decide(const SelectArgs &a, int64_t t, unsigned cha
             score = sum ? b1 + b2 : b1;
             floor32 = isnan(score) ? NAN : sum ? b2 : b1;
             if (!by_logits) floor32 -= unit + 0x1p-22f * fabsf(floor32);
-            mag = isnan(score) ? 0.f : fabsf(b1) + (sum ? fabsf(b2) : 0.f);
+            mag = size_of_score(score, b1, sum ? b2 : 0.f);
         }
         float cur = score, bound = NAN;  // the Gk-th largest score
 #pragma unroll 1

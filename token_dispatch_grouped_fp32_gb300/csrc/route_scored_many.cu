@@ -138,7 +138,7 @@ select_many_kernel(const SelectArgs a, const __grid_constant__ SelectArgs cold) 
                     for (int j = 1; j < V; ++j) score = fmaxf(score, v[j]);
                     for (int o = 1; o < in_group; o <<= 1)
                         score = fmaxf(score, __shfl_xor_sync(kAll, score, o));
-                    mag = fabsf(score);
+                    mag = size_of_score(score, score, 0.f);
                 } else {
                     float h1 = -INFINITY, h2 = -INFINITY;
 #pragma unroll
@@ -151,8 +151,8 @@ select_many_kernel(const SelectArgs a, const __grid_constant__ SelectArgs cold) 
                         h2 = fmaxf(fmaxf(h2, o2), fminf(h1, o1));
                         h1 = fmaxf(h1, o1);
                     }
-                    score = h2 > -INFINITY ? h1 + h2 : NAN;  // (as in select_kernel)
-                    mag = fabsf(h1) + fabsf(h2);
+                    score = h2 > -INFINITY ? h1 + h2 : -INFINITY;  // (as in select_kernel)
+                    mag = size_of_score(score, h1, h2);
                 }
                 float cur = score;
                 for (int j = 0; j < a.Gk; ++j) {
@@ -160,7 +160,7 @@ select_many_kernel(const SelectArgs a, const __grid_constant__ SelectArgs cold) 
                     if (cur == bound) cur = NAN;
                 }
                 const float off = EXACT ? 0.f
-                                        : 2.f * unit + 0x1.2p-22f * segment_all<true>(isnan(score) ? 0.f : mag);
+                                        : 2.f * unit + 0x1.2p-22f * segment_all<true>(mag);
                 const unsigned reach = __ballot_sync(kAll, (l & (in_group - 1)) == 0 && !(score < bound - off));
                 start_over |= __popc((reach >> (kLanes * seg)) & ((1u << kLanes) - 1u)) != a.Gk;
                 if (!(score >= bound))
