@@ -935,7 +935,9 @@ class MoELayer:
 
 class AdamW:
     """moe_adamw_step for a list of parameters and of the gradient buffers that
-    a training loop keeps: their states, and the list of addresses, built once.
+    a training loop keeps: their states, and the list of addresses, built once (about
+    3.5 us a tensor).  The steps read these buffers and nothing else: a parameter's
+    .grad is not looked at, so gradients that arrive in new tensors are copied there.
 
     ``bits``: 32 or 8, of the states.  ``master``: fp32 copies of the bf16
     parameters; without them the bf16 values are rounded stochastically.
