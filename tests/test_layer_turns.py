@@ -249,3 +249,15 @@ def test_other_calls_run_beside_none_that_runs_alone(world):
     small(x, rows(), stream=w.Stream(B))  # 6: on the stream of 2
     lay(x, rows(), stream=DEFAULT)        # 7: behind all
     assert latest(w, DEFAULT) == (7, set(range(7)))
+
+
+def test_streams_that_come_and_go_are_forgotten(world):
+    """... by a call now and then that follows all of them."""
+    w, small, x = world, layer(world, E=8), rows()
+    w.monkeypatch.setattr(w.moe._Turns, "keeps", lambda self, stream, key: False)
+    for i in range(1000):
+        small(x, rows(), stream=1000 + i)
+        assert len(w.moe._turns[0].ends) <= w.moe._MOST_STREAMS
+    lay = layer(w)
+    lay(x, rows(), stream=A)
+    assert latest(w, A) == (1000, set(range(1000)))

@@ -709,6 +709,7 @@ class _Turn:
 
 
 _turns = collections.defaultdict(_Turns)  # by device index
+_MOST_STREAMS = 64
 
 
 def _torch_stream(key):
@@ -829,7 +830,9 @@ class MoELayer:
         w = self.W_gate_up
         if not w.is_cuda or w.dtype != torch.bfloat16:
             return contextlib.nullcontext()
-        return _Turn(_turns[w.device.index], stream, key, _alone(cfg))
+        turns = _turns[w.device.index]
+        # (a call behind all streams also ends the record of them: streams that come and go)
+        return _Turn(turns, stream, key, _alone(cfg) or len(turns.ends) >= _MOST_STREAMS)
 
     def forward(self, x, out=None, stream=None):
         key, cfg = _stream(stream), self.config(x.shape[0])
